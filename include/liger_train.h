@@ -1,0 +1,84 @@
+/*
+ * liger_train.h -- C-ABI of libliger.so, second part: operators of a
+ * post-training step beside those of liger.h, whose conventions (status
+ * codes, dtypes, alignment, ownership of buffers, streams, threads) hold here
+ * too.
+ *
+ *   - block norms: the norm behind a block, its gate, the scaled residual sum
+ *     and the norm before the next block, forward and backward;
+ *   - SwiGLU with 8-bit activation checkpoints: the gate and up values kept
+ *     for the backward in 8 bits, elementwise and in FusedLinearSwiGLU;
+ *   - the label log-probabilities of a linear head, and the clipped policy
+ *     loss with a KL term from the hidden states, with its gradients.
+ *
+ * Every call here except liger_linear_logp_fwd and liger_linear_policy_fwd_bwd
+ * (which wait for their label scan) queues work only and can be captured in a
+ * CUDA graph after a first call on the device.
+ */
+#ifndef LIGER_TRAIN_H
+#define LIGER_TRAIN_H
+
+#include "liger.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* --------------------------------------------------------- block norms
+ * One pass over the rows between two blocks of a decoder: the norm behind the
+ * block just computed (post-norm), the block's gate, the residual sum and the
+ * norm before the next block (pre-norm).
+ *
+ * Forward, per row t of z (the block's output) and r (the residual stream),
+ * both [rows, cols]:
+ *     rz = 1 / sqrt(mean_j z[t,j]^2 + eps)
+ *     p[j] = z[t,j] rz w_post[j]                    (p = z when w_post is NULL)
+ *     h[t,j] = res_scale r[t,j] + block_scale g[j] p[j]
+ *     rh = 1 / sqrt(mean_j h[t,j]^2 + eps)
+ *     y[t,j] = h[t,j] rh w_pre[j]
+ *   with g = gate row t / (rows / gates), gate [gates, cols]: gates = 1 is one
+ *   learned gate per channel, gates = n one gate for each of n sequences of
+ *   rows / n rows; gates = 0 with gate NULL is no gate (g = 1).
+ *   rows must be a multiple of gates.
+ *   w_post [cols] or NULL (no post-norm; rstd_z is then not written);
+ *   w_pre [cols] or NULL (no pre-norm; y and rstd_h are then not written).
+ *   rstd_z, rstd_h: float [rows], each may be NULL (not stored).
+ *   All arithmetic is fp32 and h, y are rounded once, each from the unrounded
+ *   h (y is not formed from the stored h).
+ *   h may alias r, and y may alias z; no other overlap of inputs and outputs.
+ */
+int liger_block_norm_fwd(const void* z, const void* r, const void* w_post, const void* gate, const void* w_pre, void* h,
+                         void* y, float* rstd_z, float* rstd_h, int64_t rows, int64_t cols, int64_t gates,
+                         float res_scale, float block_scale, float eps, int dtype, void* stream);
+
+/* Bytes of workspace liger_block_norm_bwd needs (fp32 partial sums of the
+ * weight and gate gradients): an upper bound valid on any device,
+ * 3 * min(rows, 1024) * cols * 4. */
+size_t liger_block_norm_bwd_workspace(int64_t rows, int64_t cols, int64_t gates);
+
+/* Backward, from dh (the gradient of h that does not come through y; NULL: 0)
+ * and dy, with z, h, rstd_z, rstd_h as the forward read and wrote them:
+ *     u = dy w_pre,  s1 = sum_j u h
+ *     D = dh + rh u - rh^3 / cols s1 h               (D = dh without w_pre)
+ *     dr = res_scale D
+ *     q = block_scale g w_post,  s2 = sum_j q D z
+ *     dz = rz q D - rz^3 / cols s2 z                 (dz = block_scale g D without w_post)
+ *     dw_pre = sum_t dy h rh
+ *     dw_post = sum_t block_scale g D z rz
+ *     dgate[i] = sum over the rows of gate row i of block_scale D p
+ *   Required: z with w_post or gate; h, dy, rstd_h, dw_pre with w_pre; rstd_z,
+ *   dw_post with w_post; dgate with gate; dh without w_pre.
+ *   The sums over rows are reduced in a fixed order (deterministic run to run
+ *   on one device).  dr may alias dh, and dz may alias dy; no other overlap.
+ *   ws: at least liger_block_norm_bwd_workspace bytes, 16-byte aligned.
+ *   rows = 0 writes zeros to dw_post, dgate and dw_pre.
+ */
+int liger_block_norm_bwd(const void* dh, const void* dy, const void* z, const void* h, const void* w_post,
+                         const void* gate, const void* w_pre, const float* rstd_z, const float* rstd_h, void* dr,
+                         void* dz, void* dw_post, void* dgate, void* dw_pre, void* ws, size_t ws_bytes, int64_t rows,
+                         int64_t cols, int64_t gates, float res_scale, float block_scale, int dtype, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* LIGER_TRAIN_H */

@@ -1,0 +1,66 @@
+"""The C entry points of include/liger_train.h: all exported and bound, and their argument checks (host only: no CUDA call)."""
+import ctypes
+import os
+
+import pytest
+
+from transformer_rmsnorm_fwd_gb300 import _native, _train
+
+OK, ODD = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1008)   # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_native.LIB_PATH):
+        from transformer_rmsnorm_fwd_gb300 import build
+        build.build()
+    return _train._lib()
+
+
+def test_exports_every_declared_function(lib):
+    names = _train.header_functions()
+    assert names and set(names) == set(_train.SIGNATURES)
+    for n in names:
+        assert hasattr(lib, n), n
+    import transformer_rmsnorm_fwd_gb300 as L
+    for n in names:
+        assert hasattr(L, n.replace("_async", "")), n
+
+
+def _norm_fwd(lib, **kw):
+    a = dict(z=OK, r=OK, w_post=OK, gate=OK, w_pre=OK, h=OK, y=OK, rz=OK, rh=OK, rows=6, cols=64, gates=1, a=1.0, b=1.0,
+             eps=1e-6, dtype=1)
+    a.update(kw)
+    return lib.liger_block_norm_fwd(*a.values(), None)
+
+
+def _norm_bwd(lib, **kw):
+    a = dict(dh=OK, dy=OK, z=OK, h=OK, w_post=OK, gate=OK, w_pre=OK, rz=OK, rh=OK, dr=OK, dz=OK, dw_post=OK, dgate=OK,
+             dw_pre=OK, ws=OK, ws_bytes=1 << 30, rows=6, cols=64, gates=1, a=1.0, b=1.0, dtype=1)
+    a.update(kw)
+    return lib.liger_block_norm_bwd(*a.values(), None)
+
+
+def test_block_norm_fwd_checks(lib):
+    assert _norm_fwd(lib, dtype=2) == -3
+    assert _norm_fwd(lib, rows=-1) == -2 and _norm_fwd(lib, cols=0) == -2 and _norm_fwd(lib, gates=-1) == -2
+    assert _norm_fwd(lib, gates=4) == -2                    # 6 rows
+    assert _norm_fwd(lib, gates=0) == -1 and _norm_fwd(lib, gate=None) == -1
+    assert _norm_fwd(lib, eps=-1.0) == -2 and _norm_fwd(lib, eps=float("nan")) == -2
+    for k in ("z", "r", "h", "y"):
+        assert _norm_fwd(lib, **{k: None}) == -1
+    for k in ("z", "r", "h", "y", "w_post", "gate", "w_pre"):
+        assert _norm_fwd(lib, **{k: ODD}) == -4
+    assert _norm_fwd(lib, rows=0, z=None) == 0
+
+
+def test_block_norm_bwd_checks(lib):
+    assert _norm_bwd(lib, dtype=9) == -3 and _norm_bwd(lib, gates=5) == -2
+    for k in ("dy", "z", "h", "rz", "rh", "dr", "dz", "dw_post", "dgate", "dw_pre"):
+        assert _norm_bwd(lib, **{k: None}) == -1, k
+    assert _norm_bwd(lib, w_pre=None, dh=None) == -1
+    for k in ("dh", "dy", "z", "h", "dr", "dz", "dw_post", "dgate", "dw_pre"):
+        assert _norm_bwd(lib, **{k: ODD}) == -4, k
+    need = lib.liger_block_norm_bwd_workspace(6, 64, 1)
+    assert need == 3 * 6 * 64 * 4 and lib.liger_block_norm_bwd_workspace(1 << 20, 64, 1) == 3 * 1024 * 64 * 4
+    assert _norm_bwd(lib, ws_bytes=need - 1) == -6 and _norm_bwd(lib, ws=None) == -6 and _norm_bwd(lib, ws=ODD) == -6
