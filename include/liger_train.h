@@ -78,6 +78,53 @@ int liger_block_norm_bwd(const void* dh, const void* dy, const void* z, const vo
                          void* dz, void* dw_post, void* dgate, void* dw_pre, void* ws, size_t ws_bytes, int64_t rows,
                          int64_t cols, int64_t gates, float res_scale, float block_scale, int dtype, void* stream);
 
+/* ------------------------------------- SwiGLU with 8-bit checkpoints
+ * The checkpoint of a [rows, cols] tensor x that a backward will read: int8
+ * codes [rows, cols] and one scale byte for each group of 32 columns of a row
+ * (the last group of a row may be shorter), scales [rows, ceil(cols / 32)].
+ * For a group with m = max |x|:
+ *     E = floor(log2 m),  step = 2^(E - 6),  code = clamp(rint(x / step), -127, 127),
+ *     scale byte = E + 127,  x read back as code * step
+ *   (rint rounds halves to even).  The step is a power of two, so x / step and
+ *   code * step are exact: |x - read back| <= step / 2 (< step where |x| >
+ *   127.5 step), step <= m / 64.
+ *   m < 2^-111: codes 0 and scale byte 0 (the group reads back as zeros).
+ *   A group that holds an infinity or NaN: scale byte 255, all of the group
+ *   reads back as NaN.
+ * 1 + 1/32 bytes an element, against 2 (bf16) or 4.
+ */
+#define LIGER_CKPT8_GROUP 32
+
+/* Forward, elementwise on [rows, cols]: y = silu(gate) * up from the exact
+ * gate and up (as liger_swiglu_fwd), and the checkpoints of both.
+ *   gate, up, y: dtype, 16-byte aligned; y may alias gate or up.
+ *   gate8, up8: int8 codes, 16-byte aligned; gate_scale, up_scale: scale bytes. */
+int liger_swiglu_fwd_ckpt8(const void* gate, const void* up, void* y, int8_t* gate8, uint8_t* gate_scale, int8_t* up8,
+                           uint8_t* up_scale, int64_t rows, int64_t cols, int dtype, void* stream);
+
+/* Backward from the checkpoints: with g, u read back and s = sigmoid(g),
+ *     dup = dy g s,  dgate = dy u s (1 + g (1 - s))
+ *   dgate or dup may alias dy. */
+int liger_swiglu_bwd_ckpt8(const void* dy, const int8_t* gate8, const uint8_t* gate_scale, const int8_t* up8,
+                           const uint8_t* up_scale, void* dgate, void* dup, int64_t rows, int64_t cols, int dtype,
+                           void* stream);
+
+/* FusedLinearSwiGLU (liger_fused_linear_swiglu_fwd / _bwd) with the gate and
+ * up products kept in 8 bits: the forward's epilogue writes out and the
+ * checkpoints of g = X Wg^T and u = X Wu^T ([T, I], formed from the fp32
+ * products; 2.06 bytes an element against the 4 of _fwd_save), and the
+ * backward reads them instead of recomputing g and u (8 T H I flops).
+ * Arguments, shapes (bf16; H >= 64, H and I multiples of 8), workspace
+ * (liger_fused_linear_swiglu_workspace) and errors otherwise as
+ * liger_fused_linear_swiglu_fwd_save / _bwd_saved; codes 16-byte aligned. */
+int liger_fused_linear_swiglu_fwd_ckpt8(const void* X, const void* Wg, const void* Wu, void* out, int8_t* gate8,
+                                        uint8_t* gate_scale, int8_t* up8, uint8_t* up_scale, int64_t T, int64_t H,
+                                        int64_t I, int dtype, void* stream);
+int liger_fused_linear_swiglu_bwd_ckpt8(const void* X, const void* Wg, const void* Wu, const void* dH,
+                                        const int8_t* gate8, const uint8_t* gate_scale, const int8_t* up8,
+                                        const uint8_t* up_scale, void* dX, void* dWg, void* dWu, void* ws,
+                                        size_t ws_bytes, int64_t T, int64_t H, int64_t I, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -64,3 +64,35 @@ def test_block_norm_bwd_checks(lib):
     need = lib.liger_block_norm_bwd_workspace(6, 64, 1)
     assert need == 3 * 6 * 64 * 4 and lib.liger_block_norm_bwd_workspace(1 << 20, 64, 1) == 3 * 1024 * 64 * 4
     assert _norm_bwd(lib, ws_bytes=need - 1) == -6 and _norm_bwd(lib, ws=None) == -6 and _norm_bwd(lib, ws=ODD) == -6
+
+
+def test_swiglu_ckpt8_checks(lib):
+    for fn in (lib.liger_swiglu_fwd_ckpt8, lib.liger_swiglu_bwd_ckpt8):
+        good = [OK] * 7
+        assert fn(*good, 4, 64, 5, None) == -3
+        assert fn(*good, -1, 64, 1, None) == -2 and fn(*good, 4, -64, 1, None) == -2
+        assert fn(*([None] * 7), 0, 64, 1, None) == 0
+        for k in range(7):
+            assert fn(*[None if i == k else p for i, p in enumerate(good)], 4, 64, 1, None) == -1, k
+    # codes and tensors want 16 bytes, scale bytes none
+    for fn, wide in ((lib.liger_swiglu_fwd_ckpt8, (0, 1, 2, 3, 5)), (lib.liger_swiglu_bwd_ckpt8, (0, 1, 3, 5, 6))):
+        for k in wide:
+            assert fn(*[ODD if i == k else OK for i in range(7)], 4, 64, 1, None) == -4, k
+
+
+def test_linear_swiglu_ckpt8_checks(lib):
+    fwd = lambda *p, T=4, H=64, I=64, dt=1: lib.liger_fused_linear_swiglu_fwd_ckpt8(*p, T, H, I, dt, None)
+    ps = [OK] * 8
+    assert fwd(*ps, dt=0) == -3 and fwd(*ps, H=60) == -2 and fwd(*ps, I=12) == -2
+    for k in range(8):
+        assert fwd(*[None if i == k else OK for i in range(8)]) == -1, k
+    for k in (0, 1, 2, 3, 4, 6):
+        assert fwd(*[ODD if i == k else OK for i in range(8)]) == -4, k
+    need = lib.liger_fused_linear_swiglu_workspace(4, 64)
+    bwd = lambda *p, ws=OK, n=need, dt=1: lib.liger_fused_linear_swiglu_bwd_ckpt8(*p, ws, n, 4, 64, 64, dt, None)
+    ps = [OK] * 11
+    assert bwd(*ps, dt=0) == -3 and bwd(*ps, n=need - 1) == -6 and bwd(*ps, ws=None) == -6
+    for k in range(11):
+        assert bwd(*[None if i == k else OK for i in range(11)]) == -1, k
+    for k in (0, 1, 2, 3, 4, 6, 8, 9, 10):
+        assert bwd(*[ODD if i == k else OK for i in range(11)]) == -4, k

@@ -18,4 +18,6 @@ from ._native import (LIGER_BF16, LIGER_F32, LigerError,  # noqa: F401
                       liger_rmsnorm_bwd, liger_rmsnorm_bwd_noalloc, liger_rmsnorm_bwd_workspace, liger_rmsnorm_fwd,
                       liger_rmsnorm_qkv_rope_fwd, liger_rmsnorm_qkv_rope_workspace, liger_rope_bwd,
                       liger_rope_bwd_ex, liger_rope_fwd, liger_rope_fwd_ex, liger_swiglu_bwd, liger_swiglu_fwd, load)
-from ._train import (liger_block_norm_bwd, liger_block_norm_bwd_workspace, liger_block_norm_fwd)  # noqa: F401
+from ._train import (liger_block_norm_bwd, liger_block_norm_bwd_workspace, liger_block_norm_fwd,  # noqa: F401
+                     liger_ckpt8_empty, liger_fused_linear_swiglu_bwd_ckpt8, liger_fused_linear_swiglu_fwd_ckpt8,
+                     liger_swiglu_bwd_ckpt8, liger_swiglu_fwd_ckpt8)

@@ -20,6 +20,10 @@ SIGNATURES = {
     "liger_block_norm_fwd": ([_P] * 9 + [_I64] * 3 + [_F] * 3 + [_INT, _P], _INT),
     "liger_block_norm_bwd_workspace": ([_I64] * 3, _SZ),
     "liger_block_norm_bwd": ([_P] * 15 + [_SZ] + [_I64] * 3 + [_F] * 2 + [_INT, _P], _INT),
+    "liger_swiglu_fwd_ckpt8": ([_P] * 7 + [_I64] * 2 + [_INT, _P], _INT),
+    "liger_swiglu_bwd_ckpt8": ([_P] * 7 + [_I64] * 2 + [_INT, _P], _INT),
+    "liger_fused_linear_swiglu_fwd_ckpt8": ([_P] * 8 + [_I64] * 3 + [_INT, _P], _INT),
+    "liger_fused_linear_swiglu_bwd_ckpt8": ([_P] * 12 + [_SZ] + [_I64] * 3 + [_INT, _P], _INT),
 }
 
 _loaded = None
@@ -141,3 +145,76 @@ def liger_block_norm_bwd(dh, dy, z, h, dr, dz, ws, w_post=None, gate=None, w_pre
                                        _ptr(dw_pre), pws, nws, rows, cols, gates, res_scale, block_scale, _code(dr),
                                        _stream()))
     return dr, dz
+
+
+# ------------------------------------------------- SwiGLU with 8-bit checkpoints
+CKPT8_GROUP = 32    # columns of a row that share a scale byte
+
+
+def liger_ckpt8_empty(rows: int, cols: int, device="cuda"):
+    """An empty 8-bit checkpoint of a [rows, cols] tensor: int8 codes [rows, cols] and uint8 scales
+    [rows, ceil(cols / 32)]."""
+    import torch
+    return (torch.empty(rows, cols, dtype=torch.int8, device=device),
+            torch.empty(rows, -(-cols // CKPT8_GROUP), dtype=torch.uint8, device=device))
+
+
+def _ckpt(rows, cols, *pairs):
+    import torch
+    groups = -(-cols // CKPT8_GROUP)
+    for name, codes, scale in pairs:
+        _one(name + "8", codes, torch.int8, None)
+        _one(name + "_scale", scale, torch.uint8, None)
+        if codes.numel() != rows * cols or scale.numel() != rows * groups:
+            raise ValueError(f"the checkpoint of {name} must hold {rows} x {cols} codes and {rows} x {groups} scales")
+
+
+def liger_swiglu_fwd_ckpt8(gate, up, y, gate8, gate_scale, up8, up_scale):
+    """y = silu(gate) up, and the 8-bit checkpoints of gate and up (see liger_train.h); gate, up, y [..., cols]."""
+    shape, cols = tuple(gate.shape), gate.shape[-1]
+    rows = gate.numel() // cols if cols else 0
+    _same(gate, shape, gate=gate, up=up, y=y)
+    _ckpt(rows, cols, ("gate", gate8, gate_scale), ("up", up8, up_scale))
+    _check(_lib().liger_swiglu_fwd_ckpt8(_ptr(gate), _ptr(up), _ptr(y), _ptr(gate8), _ptr(gate_scale), _ptr(up8),
+                                         _ptr(up_scale), rows, cols, _code(gate), _stream()))
+    return y
+
+
+def liger_swiglu_bwd_ckpt8(dy, gate8, gate_scale, up8, up_scale, dgate, dup):
+    """dgate and dup from dy and the checkpoints that liger_swiglu_fwd_ckpt8 wrote."""
+    shape, cols = tuple(dy.shape), dy.shape[-1]
+    rows = dy.numel() // cols if cols else 0
+    _same(dy, shape, dy=dy, dgate=dgate, dup=dup)
+    _ckpt(rows, cols, ("gate", gate8, gate_scale), ("up", up8, up_scale))
+    _check(_lib().liger_swiglu_bwd_ckpt8(_ptr(dy), _ptr(gate8), _ptr(gate_scale), _ptr(up8), _ptr(up_scale), _ptr(dgate),
+                                         _ptr(dup), rows, cols, _code(dy), _stream()))
+    return dgate, dup
+
+
+def liger_fused_linear_swiglu_fwd_ckpt8(X, Wg, Wu, out, gate8, gate_scale, up8, up_scale):
+    """FusedLinearSwiGLU forward that keeps X Wg^T and X Wu^T in 8 bits."""
+    T, H = X.shape
+    I = Wg.shape[0]
+    _same(X, (T, H), X=X)
+    _same(X, (I, H), Wg=Wg, Wu=Wu)
+    _same(X, (T, I), out=out)
+    _ckpt(T, I, ("gate", gate8, gate_scale), ("up", up8, up_scale))
+    _check(_lib().liger_fused_linear_swiglu_fwd_ckpt8(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(out), _ptr(gate8),
+                                                      _ptr(gate_scale), _ptr(up8), _ptr(up_scale), T, H, I, _code(X),
+                                                      _stream()))
+    return out
+
+
+def liger_fused_linear_swiglu_bwd_ckpt8(X, Wg, Wu, dH, gate8, gate_scale, up8, up_scale, dX, dWg, dWu, ws):
+    """FusedLinearSwiGLU backward from the 8-bit checkpoints; ws as liger_fused_linear_swiglu_workspace says."""
+    T, H = X.shape
+    I = Wg.shape[0]
+    _same(X, (T, H), X=X, dX=dX)
+    _same(X, (I, H), Wg=Wg, Wu=Wu, dWg=dWg, dWu=dWu)
+    _same(X, (T, I), dH=dH)
+    _ckpt(T, I, ("gate", gate8, gate_scale), ("up", up8, up_scale))
+    pws, nws = _bytes(ws)
+    _check(_lib().liger_fused_linear_swiglu_bwd_ckpt8(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(dH), _ptr(gate8),
+                                                      _ptr(gate_scale), _ptr(up8), _ptr(up_scale), _ptr(dX), _ptr(dWg),
+                                                      _ptr(dWu), pws, nws, T, H, I, _code(X), _stream()))
+    return dX, dWg, dWu

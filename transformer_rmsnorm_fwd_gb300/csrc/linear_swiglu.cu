@@ -22,6 +22,7 @@
 //    operands MN-major.
 #include <atomic>
 
+#include "liger_train.h"
 #include "tc_gemm.cuh"
 
 namespace liger {
@@ -64,8 +65,14 @@ using namespace liger::tc;
 namespace liger {
 namespace {
 
+// 8-bit checkpoints of the gate and up products (null codes: none)
+struct Ckpt8 {
+    int8_t *g8, *u8;
+    uint8_t *g8s, *u8s;
+};
+
 int fwd_impl(const void* X, const void* Wg, const void* Wu, void* out, void* g_save, void* u_save, int64_t T,
-             int64_t H, int64_t I, int dtype, void* stream, const char* who) {
+             int64_t H, int64_t I, int dtype, void* stream, const char* who, const Ckpt8& q = Ckpt8{}) {
     using namespace tc;
     if (int rc = check_shapes(T, H, I, dtype, who)) return rc;
     if (T == 0) return LIGER_OK;
@@ -103,6 +110,17 @@ int fwd_impl(const void* X, const void* Wg, const void* Wu, void* out, void* g_s
         f.out = e.out + m0 * I;
         if (e.out2 != nullptr) f.out2 = e.out2 + m0 * I;
         if (e.out3 != nullptr) f.out3 = e.out3 + m0 * I;
+        if (q.g8 != nullptr) {
+            f.ldq = ceil_div(I, kCkptGroup);
+            f.g8 = q.g8 + m0 * I;
+            f.u8 = q.u8 + m0 * I;
+            f.g8s = q.g8s + m0 * f.ldq;
+            f.u8s = q.u8s + m0 * f.ldq;
+            if ((rc = launch_gemm<0, 0, EPI_SWIGLU_CKPT8, 1>(mX, mG, ml, ntile_n * BN, static_cast<int>(H), f,
+                                                             as_stream(stream), 0, &mX, &mU)))
+                return rc;
+            continue;
+        }
         if ((rc = launch_gemm<0, 0, EPI_SWIGLU, 1>(mX, mG, ml, ntile_n * BN, static_cast<int>(H), f, as_stream(stream),
                                                    0, &mX, &mU)))
             return rc;
@@ -178,6 +196,18 @@ extern "C" int liger_fused_linear_swiglu_fwd_save(const void* X, const void* Wg,
     return fwd_impl(X, Wg, Wu, out, g, u, T, H, I, dtype, stream, "fused_linear_swiglu_fwd_save");
 }
 
+extern "C" int liger_fused_linear_swiglu_fwd_ckpt8(const void* X, const void* Wg, const void* Wu, void* out,
+                                                   int8_t* gate8, uint8_t* gate_scale, int8_t* up8, uint8_t* up_scale,
+                                                   int64_t T, int64_t H, int64_t I, int dtype, void* stream) {
+    clear_error();
+    const char* who = "fused_linear_swiglu_fwd_ckpt8";
+    if (T > 0 && (!gate8 || !gate_scale || !up8 || !up_scale))
+        return fail(LIGER_ERR_NULL, "%s: the checkpoints are required", who);
+    if (!aligned16(gate8) || !aligned16(up8)) return fail(LIGER_ERR_ALIGN, "%s: codes must be 16-byte aligned", who);
+    return fwd_impl(X, Wg, Wu, out, nullptr, nullptr, T, H, I, dtype, stream, who,
+                    Ckpt8{gate8, up8, gate_scale, up_scale});
+}
+
 extern "C" size_t liger_fused_linear_swiglu_workspace(int64_t T, int64_t I) {
     if (T <= 0 || I <= 0) return 0;
     return 2 * ((static_cast<size_t>(T) * static_cast<size_t>(I) * 2 + 255) & ~static_cast<size_t>(255));
@@ -246,12 +276,14 @@ extern "C" int liger_fused_linear_swiglu_bwd(const void* X, const void* Wg, cons
     return grads_from_dgdu(X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st);
 }
 
-extern "C" int liger_fused_linear_swiglu_bwd_saved(const void* X, const void* Wg, const void* Wu, const void* dH,
-                                                   const void* g, const void* u, void* dX, void* dWg, void* dWu,
-                                                   void* ws, size_t ws_bytes, int64_t T, int64_t H, int64_t I,
-                                                   int dtype, void* stream) {
-    clear_error();
-    const char* who = "fused_linear_swiglu_bwd_saved";
+namespace liger {
+namespace {
+
+// The backward from kept g and u: dgdu(dG, dU) queues the elementwise SwiGLU backward from them.
+template <typename DgDu>
+int bwd_kept(const char* who, const void* X, const void* Wg, const void* Wu, const void* dH, const void* g, const void* u,
+             void* dX, void* dWg, void* dWu, void* ws, size_t ws_bytes, int64_t T, int64_t H, int64_t I, int dtype,
+             cudaStream_t st, DgDu dgdu) {
     if (int rc = check_shapes(T, H, I, dtype, who)) return rc;
     if (!Wg || !Wu || !dWg || !dWu || (T > 0 && (!X || !dH || !g || !u || !dX)))
         return fail(LIGER_ERR_NULL, "%s: null tensor pointer", who);
@@ -262,11 +294,10 @@ extern "C" int liger_fused_linear_swiglu_bwd_saved(const void* X, const void* Wg
     if (need > 0 && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255)))
         return fail(LIGER_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, need,
                     ws_bytes);
-    cudaStream_t st = as_stream(stream);
     if (T == 0) {
         const size_t wb = static_cast<size_t>(I * H) * 2;
         if (cudaMemsetAsync(dWg, 0, wb, st) != cudaSuccess || cudaMemsetAsync(dWu, 0, wb, st) != cudaSuccess)
-            return check_launch("fused_linear_swiglu_bwd_saved memset");
+            return check_launch("fused_linear_swiglu_bwd memset");
         return LIGER_OK;
     }
     int* d_err = nullptr;
@@ -274,7 +305,36 @@ extern "C" int liger_fused_linear_swiglu_bwd_saved(const void* X, const void* Wg
     __nv_bfloat16* dG = static_cast<__nv_bfloat16*>(ws);
     __nv_bfloat16* dU = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + need / 2);
     // 1. dG, dU from dh and the saved g, u (the elementwise SwiGLU backward)
-    if (int rc = liger_swiglu_bwd(dH, g, u, dG, dU, T * I, LIGER_BF16, stream)) return rc;
+    if (int rc = dgdu(dG, dU)) return rc;
     // 2-3. as in the backward with recompute
     return grads_from_dgdu(X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st);
+}
+
+}  // namespace
+}  // namespace liger
+
+extern "C" int liger_fused_linear_swiglu_bwd_saved(const void* X, const void* Wg, const void* Wu, const void* dH,
+                                                   const void* g, const void* u, void* dX, void* dWg, void* dWu,
+                                                   void* ws, size_t ws_bytes, int64_t T, int64_t H, int64_t I,
+                                                   int dtype, void* stream) {
+    clear_error();
+    return bwd_kept("fused_linear_swiglu_bwd_saved", X, Wg, Wu, dH, g, u, dX, dWg, dWu, ws, ws_bytes, T, H, I, dtype,
+                    as_stream(stream), [&](__nv_bfloat16* dG, __nv_bfloat16* dU) {
+                        return liger_swiglu_bwd(dH, g, u, dG, dU, T * I, LIGER_BF16, stream);
+                    });
+}
+
+extern "C" int liger_fused_linear_swiglu_bwd_ckpt8(const void* X, const void* Wg, const void* Wu, const void* dH,
+                                                   const int8_t* gate8, const uint8_t* gate_scale, const int8_t* up8,
+                                                   const uint8_t* up_scale, void* dX, void* dWg, void* dWu, void* ws,
+                                                   size_t ws_bytes, int64_t T, int64_t H, int64_t I, int dtype,
+                                                   void* stream) {
+    clear_error();
+    const char* who = "fused_linear_swiglu_bwd_ckpt8";
+    if (T > 0 && (!gate_scale || !up_scale)) return fail(LIGER_ERR_NULL, "%s: the checkpoints are required", who);
+    return bwd_kept(who, X, Wg, Wu, dH, gate8, up8, dX, dWg, dWu, ws, ws_bytes, T, H, I, dtype, as_stream(stream),
+                    [&](__nv_bfloat16* dG, __nv_bfloat16* dU) {
+                        return liger_swiglu_bwd_ckpt8(dH, gate8, gate_scale, up8, up_scale, dG, dU, T, I, LIGER_BF16,
+                                                      stream);
+                    });
 }

@@ -39,6 +39,7 @@
 
 #include <atomic>
 
+#include "ckpt8.cuh"
 #include "common.cuh"
 #include "mbarrier.cuh"
 
@@ -81,7 +82,8 @@ enum Epi : int {
     EPI_SWIGLU = 3,
     EPI_SWIGLU_BWD = 4,
     EPI_QKV_ROPE = 5,
-    EPI_SOFTMAX = 6
+    EPI_SOFTMAX = 6,
+    EPI_SWIGLU_CKPT8 = 7
 };
 
 // Tile order of the persistent loop: m fastest, n fastest, or groups of
@@ -167,6 +169,11 @@ struct EpiParams {
     int n_tab, tab_mod;
     int hd, nq, nk;
     __nv_bfloat16* out3;
+    // EPI_SWIGLU_CKPT8: out as EPI_SWIGLU, and the 8-bit checkpoints of g and u: codes [M, N]
+    // and one scale byte per 32 columns [M, ldq]
+    int8_t *g8, *u8;
+    uint8_t *g8s, *u8s;
+    int64_t ldq;
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -893,6 +900,57 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (EPI == EPI_SWIGLU && ep.out2 != nullptr)
                         store_block<4, false>(s_out3, lane, reinterpret_cast<uint8_t*>(ep.out3 + orow0 + c * 32),
                                               ep.ldo * 2, rows, nch);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) release_acc(as);
+            } else if (EPI == EPI_SWIGLU_CKPT8) {
+                const int o0 = ni * (BN / 2);   // first output (intermediate) column of the tile
+                const int64_t orow0 = static_cast<int64_t>(row - lane) * ep.ldo + o0;
+                // a chunk of 32 columns of this lane's row is one checkpoint group: its largest
+                // magnitude, scale byte and 32 codes need no other lane
+                auto keep = [&](const float(&v)[32], int c, int8_t* codes, uint8_t* scales) {
+                    const int left = ep.N - (o0 + c * 32);   // a multiple of 8
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = max(top, j < left ? mag_bits(v[j]) : 0u);
+                    const uint32_t sc = ckpt_scale(top);
+                    const float inv = ckpt_inv(sc);
+                    if (!row_ok || left <= 0) return;
+                    scales[static_cast<int64_t>(row) * ep.ldq + (o0 >> 5) + c] = static_cast<uint8_t>(sc);
+                    int8_t* dst = codes + static_cast<int64_t>(row) * ep.ldo + o0 + c * 32;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t k[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) k[e] = ckpt_code(v[g * 8 + e], inv);
+                        if (g * 8 < left)
+                            *reinterpret_cast<uint2*>(dst + g * 8) =
+                                make_uint2(ckpt_pack4(k[0], k[1], k[2], k[3]), ckpt_pack4(k[4], k[5], k[6], k[7]));
+                    }
+                };
+#pragma unroll 1
+                for (int c = 0; c < BN / 64; ++c) {
+                    const int nch = chunks_below(o0 + c * 32, ep.N, 8, 4);
+                    float gv[32], uv[32];
+                    tmem_ld32(taddr + c * 32, gv);
+                    tmem_ld32(taddr + BN / 2 + c * 32, uv);
+                    keep(gv, c, ep.g8, ep.g8s);
+                    keep(uv, c, ep.u8, ep.u8s);
+                    __syncwarp();   // the previous block's row runs have been read
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float a[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = gv[g * 8 + e];
+                            a[e] = x * __fdividef(1.0f, 1.0f + __expf(-x)) * uv[g * 8 + e];
+                        }
+                        sts16(sbuf + stage_slot<4>(lane, g), pack(a));
+                    }
+                    __syncwarp();
+                    store_block<4, false>(sbuf, lane, reinterpret_cast<uint8_t*>(ep.out + orow0 + c * 32), ep.ldo * 2,
+                                          rows, nch);
                 }
                 tc_fence_before();
                 __syncwarp();
