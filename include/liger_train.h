@@ -125,6 +125,77 @@ int liger_fused_linear_swiglu_bwd_ckpt8(const void* X, const void* Wg, const voi
                                         const uint8_t* up_scale, void* dX, void* dWg, void* dWu, void* ws,
                                         size_t ws_bytes, int64_t T, int64_t H, int64_t I, int dtype, void* stream);
 
+/* --------------------------------- label log-probabilities of a linear head
+ *     logp[t] = z_t[labels[t]] - log sum_v exp(z_t[v]),  z_t = W x_t
+ * of the tokens whose label is not ignore_index, 0 on the others: what a policy
+ * loss needs of the old and of the reference policy.  Forward only; the logits
+ * never reach device memory on the bf16 tensor-core path (H >= 64 and a
+ * multiple of 8, V >= 256); other cases run in fp32 with a [chunk x V] buffer.
+ *   X [T, H], W [V, H] in dtype, labels int64 [T], logp float [T].
+ *   ws: at least liger_linear_logp_workspace bytes, 256-byte aligned.
+ * liger_linear_logp_fwd waits for a scan of the labels: a label outside [0, V)
+ * that is not ignore_index returns LIGER_ERR_LABEL with nothing else queued,
+ * and only tokens that are not ignored go through the GEMM.  The _async form
+ * does not wait (it can be captured): it runs all tokens, and a bad label's
+ * logp is NaN. */
+size_t liger_linear_logp_workspace(int64_t T, int64_t H, int64_t V, int dtype);
+int liger_linear_logp_fwd(const void* X, const void* W, const int64_t* labels, int64_t T, int64_t H, int64_t V,
+                          int64_t ignore_index, float* logp, void* ws, size_t ws_bytes, int dtype, void* stream);
+int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* labels, int64_t T, int64_t H, int64_t V,
+                                int64_t ignore_index, float* logp, void* ws, size_t ws_bytes, int dtype, void* stream);
+
+/* ------------------------- clipped policy loss with a KL term of a linear head
+ * T tokens in B sequences, packed: sequence b is the tokens [cu_seqlens[b],
+ * cu_seqlens[b + 1]) (int32 [B + 1] on the device, not descending, within
+ * [0, T]); cu_seqlens NULL: B = 1, one sequence of all T tokens.  A token is
+ * valid if it lies in a sequence and its label is not ignore_index.  With lp =
+ * logp[t] as above, A the token's advantage and d = ref_logp[t] - lp, a valid
+ * token has
+ *     r = exp(lp - old_logp[t]),  kl = exp(d) - d - 1   (0 without ref_logp)
+ *     l = -min(r A, clamp(r, 1 - eps_low, 1 + eps_high) A) + beta kl
+ *     dl/dlp = -(r A, or 0 where A > 0 and r > 1 + eps_high or A < 0 and r < 1 - eps_low)
+ *              + beta (1 - exp(d))
+ *   (A = 0: no policy term), and
+ *     loss = sum over valid tokens of w l
+ *     reduction 0 (token mean):    w = 1 / number of valid tokens
+ *     reduction 1 (sum):           w = 1
+ *     reduction 2 (sequence mean): w = 1 / (B * valid tokens of the token's sequence)
+ *     D_t = grad_scale w dl/dlp (onehot(labels[t]) - softmax(z_t)),  dX = D W,  dW = D^T X
+ *   No valid token: loss 0 and zero gradients.
+ *   adv: float [B], or [T] with LIGER_POLICY_ADV_PER_TOKEN in flags.
+ *   old_logp float [T]; ref_logp float [T], may be NULL when beta is 0 (then no
+ *   kl).  Nothing of old_logp, ref_logp or a per-token adv is read at tokens that are
+ *   not valid.  0 <= eps_low <= 1, eps_high >= 0.
+ *   loss: one float; stats: two floats or NULL, the mean kl and the share of
+ *   clipped tokens over the valid tokens; logp: float [T] or NULL, 0 at tokens
+ *   that are not valid; dX [T, H], dW [V, H] in dtype, each may be NULL.  Rows
+ *   of dX of tokens that are not valid are written as +0.
+ *   Token chunks, the GEMM path by dtype and shape and chunk are as in
+ *   liger_linear_ce_fwd_bwd: per chunk the logits exist only in a [chunk x V]
+ *   workspace buffer.  ws: at least liger_linear_policy_workspace bytes,
+ *   256-byte aligned.
+ *   The call waits for a scan of the labels and sequences: a bad label returns
+ *   LIGER_ERR_LABEL, bad cu_seqlens LIGER_ERR_SHAPE, with nothing else queued,
+ *   and only valid tokens go through the GEMMs.  The _async form does not wait
+ *   (it can be captured in a CUDA graph): all tokens go through the GEMMs, a bad
+ *   label counts as ignored and bad cu_seqlens leave no valid token; either
+ *   makes the loss and stats NaN.
+ *   dW may differ between the two forms by rounding (the same sums over another
+ *   grouping of the tokens). */
+#define LIGER_POLICY_ADV_PER_TOKEN 1
+size_t liger_linear_policy_workspace(int64_t T, int64_t H, int64_t V, int64_t B, int64_t chunk, int dtype);
+int liger_linear_policy_fwd_bwd(const void* X, const void* W, const int64_t* labels, const int32_t* cu_seqlens,
+                                const float* old_logp, const float* ref_logp, const float* adv, int64_t T, int64_t H,
+                                int64_t V, int64_t B, int64_t ignore_index, int reduction, int flags, float eps_low,
+                                float eps_high, float beta, float grad_scale, float* loss, float* stats, float* logp,
+                                void* dX, void* dW, void* ws, size_t ws_bytes, int64_t chunk, int dtype, void* stream);
+int liger_linear_policy_fwd_bwd_async(const void* X, const void* W, const int64_t* labels, const int32_t* cu_seqlens,
+                                      const float* old_logp, const float* ref_logp, const float* adv, int64_t T,
+                                      int64_t H, int64_t V, int64_t B, int64_t ignore_index, int reduction, int flags,
+                                      float eps_low, float eps_high, float beta, float grad_scale, float* loss,
+                                      float* stats, float* logp, void* dX, void* dW, void* ws, size_t ws_bytes,
+                                      int64_t chunk, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -96,3 +96,49 @@ def test_linear_swiglu_ckpt8_checks(lib):
         assert bwd(*[None if i == k else OK for i in range(11)]) == -1, k
     for k in (0, 1, 2, 3, 4, 6, 8, 9, 10):
         assert bwd(*[ODD if i == k else OK for i in range(11)]) == -4, k
+
+
+def _logp(fn, **kw):
+    a = dict(X=OK, W=OK, labels=OK, T=4, H=64, V=300, ign=-100, logp=OK, ws=OK, n=1 << 30, dtype=1)
+    a.update(kw)
+    return fn(*a.values(), None)
+
+
+def _policy(fn, **kw):
+    a = dict(X=OK, W=OK, labels=OK, cu=OK, old=OK, ref=OK, adv=OK, T=4, H=64, V=300, B=2, ign=-100, reduction=0, flags=0,
+             lo=0.2, hi=0.2, beta=0.1, gs=1.0, loss=OK, stats=OK, logp=OK, dX=OK, dW=OK, ws=OK, n=1 << 40, chunk=0, dtype=1)
+    a.update(kw)
+    return fn(*a.values(), None)
+
+
+def test_logp_checks(lib):
+    for fn in (lib.liger_linear_logp_fwd, lib.liger_linear_logp_fwd_async):
+        assert _logp(fn, dtype=3) == -3 and _logp(fn, T=-1) == -2 and _logp(fn, V=0) == -2 and _logp(fn, H=0) == -2
+        assert _logp(fn, T=1 << 31) == -2 and _logp(fn, T=0, X=None) == 0
+        for k in ("X", "W", "labels", "logp"):
+            assert _logp(fn, **{k: None}) == -1, k
+        for k in ("X", "W"):
+            assert _logp(fn, **{k: ODD}) == -4, k
+        assert _logp(fn, labels=ctypes.c_void_p(0x1004)) == -4 and _logp(fn, logp=ctypes.c_void_p(0x1002)) == -4
+        need = lib.liger_linear_logp_workspace(4, 64, 300, 1)
+        assert need > 0 and _logp(fn, n=need - 1) == -6 and _logp(fn, ws=None) == -6 and _logp(fn, ws=ODD) == -6
+    assert lib.liger_linear_logp_workspace(4, 64, 300, 9) == 0 and lib.liger_linear_logp_workspace(-1, 64, 300, 1) == 0
+
+
+def test_policy_checks(lib):
+    nan = float("nan")
+    for fn in (lib.liger_linear_policy_fwd_bwd, lib.liger_linear_policy_fwd_bwd_async):
+        assert _policy(fn, dtype=3) == -3
+        for kw in (dict(T=-1), dict(H=0), dict(V=0), dict(B=0), dict(chunk=-1), dict(reduction=3), dict(reduction=-1),
+                   dict(flags=2), dict(lo=-0.1), dict(lo=1.1), dict(hi=-0.1), dict(lo=nan), dict(hi=nan), dict(beta=nan),
+                   dict(gs=nan), dict(T=1 << 31)):
+            assert _policy(fn, **kw) == -2, kw
+        for k in ("X", "W", "labels", "cu", "old", "ref", "adv", "loss"):
+            assert _policy(fn, **{k: None}) == -1, k
+        for k in ("X", "W", "dX", "dW"):
+            assert _policy(fn, **{k: ODD}) == -4, k
+        for k in ("cu", "old", "ref", "adv", "loss", "stats", "logp"):
+            assert _policy(fn, **{k: ctypes.c_void_p(0x1002)}) == -4, k
+        need = lib.liger_linear_policy_workspace(4, 64, 300, 2, 0, 1)
+        assert need > 0 and _policy(fn, n=need - 1) == -6 and _policy(fn, ws=None) == -6 and _policy(fn, ws=ODD) == -6
+    assert lib.liger_linear_policy_workspace(4, 64, 300, 0, 0, 1) == 0

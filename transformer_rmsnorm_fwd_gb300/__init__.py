@@ -20,4 +20,5 @@ from ._native import (LIGER_BF16, LIGER_F32, LigerError,  # noqa: F401
                       liger_rope_bwd_ex, liger_rope_fwd, liger_rope_fwd_ex, liger_swiglu_bwd, liger_swiglu_fwd, load)
 from ._train import (liger_block_norm_bwd, liger_block_norm_bwd_workspace, liger_block_norm_fwd,  # noqa: F401
                      liger_ckpt8_empty, liger_fused_linear_swiglu_bwd_ckpt8, liger_fused_linear_swiglu_fwd_ckpt8,
-                     liger_swiglu_bwd_ckpt8, liger_swiglu_fwd_ckpt8)
+                     liger_linear_logp_fwd, liger_linear_logp_workspace, liger_linear_policy_fwd_bwd,
+                     liger_linear_policy_workspace, liger_swiglu_bwd_ckpt8, liger_swiglu_fwd_ckpt8)

@@ -24,6 +24,13 @@ SIGNATURES = {
     "liger_swiglu_bwd_ckpt8": ([_P] * 7 + [_I64] * 2 + [_INT, _P], _INT),
     "liger_fused_linear_swiglu_fwd_ckpt8": ([_P] * 8 + [_I64] * 3 + [_INT, _P], _INT),
     "liger_fused_linear_swiglu_bwd_ckpt8": ([_P] * 12 + [_SZ] + [_I64] * 3 + [_INT, _P], _INT),
+    "liger_linear_logp_workspace": ([_I64] * 3 + [_INT], _SZ),
+    "liger_linear_logp_fwd": ([_P] * 3 + [_I64] * 4 + [_P] * 2 + [_SZ, _INT, _P], _INT),
+    "liger_linear_logp_fwd_async": ([_P] * 3 + [_I64] * 4 + [_P] * 2 + [_SZ, _INT, _P], _INT),
+    "liger_linear_policy_workspace": ([_I64] * 5 + [_INT], _SZ),
+    "liger_linear_policy_fwd_bwd": ([_P] * 7 + [_I64] * 5 + [_INT] * 2 + [_F] * 4 + [_P] * 6 + [_SZ, _I64, _INT, _P], _INT),
+    "liger_linear_policy_fwd_bwd_async": ([_P] * 7 + [_I64] * 5 + [_INT] * 2 + [_F] * 4 + [_P] * 6
+                                          + [_SZ, _I64, _INT, _P], _INT),
 }
 
 _loaded = None
@@ -218,3 +225,65 @@ def liger_fused_linear_swiglu_bwd_ckpt8(X, Wg, Wu, dH, gate8, gate_scale, up8, u
                                                       _ptr(gate_scale), _ptr(up8), _ptr(up_scale), _ptr(dX), _ptr(dWg),
                                                       _ptr(dWu), pws, nws, T, H, I, _code(X), _stream()))
     return dX, dWg, dWu
+
+
+# ------------------------------------------------------- heads: label log-probabilities, policy loss
+def _head(X, W, labels):
+    import torch
+    T, H = X.shape
+    V = W.shape[0]
+    _same(X, (T, H), X=X)
+    _same(X, (V, H), W=W)
+    _one("labels", labels, torch.int64, (T,))
+    return T, H, V
+
+
+def liger_linear_logp_workspace(T: int, H: int, V: int, dtype: int = LIGER_BF16) -> int:
+    return int(_lib().liger_linear_logp_workspace(T, H, V, dtype))
+
+
+def liger_linear_logp_fwd(X, W, labels, logp, ws, ignore_index: int = -100, wait: bool = True):
+    """logp[t] = log softmax(W x_t)[labels[t]], 0 where the label is ignore_index (see liger_train.h); wait=False calls
+    the _async form (no host wait: capturable in a CUDA graph; a bad label's logp is NaN)."""
+    T, H, V = _head(X, W, labels)
+    _rows(T, logp=logp)
+    pws, nws = _bytes(ws)
+    fn = _lib().liger_linear_logp_fwd if wait else _lib().liger_linear_logp_fwd_async
+    _check(fn(_ptr(X), _ptr(W), _ptr(labels), T, H, V, int(ignore_index), _ptr(logp), pws, nws, _code(X), _stream()))
+    return logp
+
+
+_REDUCTION = {"token_mean": 0, "sum": 1, "seq_mean": 2}
+
+
+def liger_linear_policy_workspace(T: int, H: int, V: int, B: int = 1, chunk: int = 0, dtype: int = LIGER_BF16) -> int:
+    return int(_lib().liger_linear_policy_workspace(T, H, V, B, chunk, dtype))
+
+
+def liger_linear_policy_fwd_bwd(X, W, labels, old_logp, adv, loss, dX, dW, ws, ref_logp=None, cu_seqlens=None, logp=None,
+                                stats=None, ignore_index: int = -100, reduction: str = "token_mean", eps_low: float = 0.2,
+                                eps_high: float = 0.2, beta: float = 0.0, grad_scale: float = 1.0,
+                                adv_per_token: bool = False, chunk: int = 0, wait: bool = True):
+    """Clipped policy loss with a KL term, and its gradients dX and dW (each may be None), from the hidden states X [T, H]
+    and the head W [V, H] (see liger_train.h).
+
+    labels int64 [T]; old_logp, ref_logp float32 [T]; adv float32, one per sequence ([B]) or, with adv_per_token, one per
+    token ([T]); cu_seqlens int32 [B + 1] or None (one sequence); reduction "token_mean", "seq_mean" or "sum"; stats
+    float32 [2] or None (mean KL, share of clipped tokens).  wait=False calls the _async form."""
+    import torch
+    T, H, V = _head(X, W, labels)
+    B = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    if cu_seqlens is not None:
+        _one("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    _rows(T, old_logp=old_logp, ref_logp=ref_logp, logp=logp)
+    _rows(T if adv_per_token else B, adv=adv)
+    _rows(1, loss=loss)
+    _rows(2, stats=stats)
+    _same(X, (T, H), dX=dX)
+    _same(X, (V, H), dW=dW)
+    pws, nws = _bytes(ws)
+    fn = _lib().liger_linear_policy_fwd_bwd if wait else _lib().liger_linear_policy_fwd_bwd_async
+    _check(fn(_ptr(X), _ptr(W), _ptr(labels), _ptr(cu_seqlens), _ptr(old_logp), _ptr(ref_logp), _ptr(adv), T, H, V, B,
+              int(ignore_index), _REDUCTION[reduction], 1 if adv_per_token else 0, eps_low, eps_high, beta, grad_scale,
+              _ptr(loss), _ptr(stats), _ptr(logp), _ptr(dX), _ptr(dW), pws, nws, int(chunk), _code(X), _stream()))
+    return loss, dX, dW

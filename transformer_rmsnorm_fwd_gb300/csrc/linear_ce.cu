@@ -33,6 +33,7 @@
 
 #include <atomic>
 
+#include "liger_train.h"
 #include "tc_gemm.cuh"
 
 namespace liger {
@@ -244,6 +245,11 @@ __global__ void scatter_rowvals(const float* __restrict__ lse_c, const float* __
         loss[t] = p < 0 ? 0.f : loss_c[p];
     }
     if (blockIdx.x == 0 && threadIdx.x == 0 && *core_err != 0) atomicExch(err, *core_err);
+}
+
+// the run's kernel error word into the entry point's header
+__global__ void take_err(const int* core_err, int* err) {
+    if (*core_err != 0) atomicExch(err, *core_err);
 }
 
 // Counts the labels that are not ignore_index and flags any outside [0, V).  With
@@ -467,6 +473,250 @@ __global__ void __launch_bounds__(kRowThreads) dlogits_f32(const int64_t* __rest
     for (int v = threadIdx.x; v < V; v += kRowThreads) z[v] = sc * (expf(z[v] - l) - (v == y ? 1.0f : 0.0f));
 }
 
+// ------------------------------------------------ policy loss and label log-probabilities
+// The same products with another loss on top (liger_train.h): a token's term depends on its label's
+// log-probability only, so D_t = c_t (softmax - onehot) with a scale c_t for each token in place of
+// the cross-entropy's one scale.
+struct Policy {
+    const float *old_logp, *ref_logp, *adv;   // [T] by original token; adv [B] or, per token, [T]
+    int adv_per_token, reduction;
+    float lo, hi, beta, grad_scale;           // the ratio is held to [lo, hi]
+    const int* seq;                           // [T] sequence of a token, -1: not valid
+    const int* n_seq;                         // [B] valid tokens of a sequence
+    const Hdr* hdr;                           // n_valid
+    int64_t B;
+    float* coef;                              // [tokens run] the scale c_t, in the order the GEMMs run them
+    float *term, *kl, *clip;                  // [T] w l, kl and 1 where clipped, by original token
+    float* logp;                              // [T] by original token, or NULL
+};
+
+// exp(d) - d - 1 without the cancellation of small d: its Taylor series (terms d^2 / 2! to d^9 / 9!,
+// the next one below 2^-24 of the sum for |d| < 0.5), else expm1
+__device__ __forceinline__ float kl_term(float d) {
+    if (fabsf(d) < 0.5f) {
+        float s = 1.f / 362880.f;
+        s = fmaf(s, d, 1.f / 40320.f);
+        s = fmaf(s, d, 1.f / 5040.f);
+        s = fmaf(s, d, 1.f / 720.f);
+        s = fmaf(s, d, 1.f / 120.f);
+        s = fmaf(s, d, 1.f / 24.f);
+        s = fmaf(s, d, 1.f / 6.f);
+        s = fmaf(s, d, 0.5f);
+        return s * d * d;
+    }
+    return expm1f(d) - d;
+}
+
+// The scale c_t of a valid token with label log-probability lp; writes its terms when `write`.
+// NaN in old_logp, ref_logp or adv makes them NaN.
+__device__ float policy_token(const Policy& p, int64_t t, float lp, bool write) {
+    const int b = p.seq[t];
+    const float A = p.adv[p.adv_per_token ? t : b];
+    const float r = expf(lp - p.old_logp[t]);
+    const bool stop = (A > 0.f && r > p.hi) || (A < 0.f && r < p.lo);
+    const float ra = A == 0.f ? 0.f : r * A;
+    float l = stop ? -(A > 0.f ? p.hi : p.lo) * A : -ra;
+    float slope = stop ? 0.f : -ra;
+    float kl = 0.f;
+    if (p.ref_logp != nullptr) {
+        const float d = p.ref_logp[t] - lp;
+        kl = kl_term(d);
+        if (p.beta != 0.f) {
+            l = fmaf(p.beta, kl, l);
+            slope = fmaf(-p.beta, expm1f(d), slope);
+        }
+    }
+    float wf = 1.f;
+    if (p.reduction == 0) wf = 1.f / static_cast<float>(p.hdr->n_valid);
+    if (p.reduction == 2) wf = 1.f / (static_cast<float>(p.B) * static_cast<float>(p.n_seq[b]));
+    if (write) {
+        p.term[t] = wf * l;
+        p.kl[t] = kl;
+        p.clip[t] = stop ? 1.f : 0.f;
+    }
+    return -(slope * wf) * p.grad_scale;
+}
+
+// One thread per token: its sequence (binary search in cu_seqlens), whether it is valid, and the label
+// that the later kernels index with (ignore_index where it is not valid); counts the valid tokens of
+// each sequence and of all.  bad: bit 0 a label outside [0, V), bit 1 bad cu_seqlens (then no token is
+// valid, which the first loop of every block finds by itself).  Without cu_seqlens one sequence.
+// logp, term, kl, clip become 0 where a token is not valid (logp NaN at a bad label if bad_nan).
+__global__ void __launch_bounds__(256) policy_scan(const int64_t* __restrict__ labels, const int32_t* __restrict__ cu,
+                                                   int64_t T, int64_t V, int64_t B, int64_t ignore, Hdr* hdr,
+                                                   int64_t* __restrict__ lab_out, int* __restrict__ seq, int* n_seq,
+                                                   float* logp, float* term, float* kl, float* clip, int bad_nan) {
+    __shared__ int cu_bad;
+    if (threadIdx.x == 0) cu_bad = 0;
+    __syncthreads();
+    if (cu != nullptr)
+        for (int64_t b = threadIdx.x; b < B; b += blockDim.x)
+            if (cu[b] < 0 || cu[b] > cu[b + 1] || cu[b + 1] > T) cu_bad = 1;
+    __syncthreads();
+    if (cu_bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hdr->bad, 2);
+    const int lane = threadIdx.x & 31;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * blockDim.x; t0 < T; t0 += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t t = t0 + threadIdx.x;
+        int s = -1;
+        int64_t y = ignore;
+        bool bad = false;
+        if (t < T && !cu_bad) {
+            y = labels[t];
+            s = 0;
+            if (cu != nullptr) {   // the last sequence that starts at or before t
+                int64_t lo = 0, hi = B;   // cu[lo] <= t < cu[hi] once both hold
+                if (t < cu[0] || t >= cu[B]) {
+                    s = -1;
+                } else {
+                    while (hi - lo > 1) {
+                        const int64_t mid = (lo + hi) >> 1;
+                        if (cu[mid] <= t) lo = mid;
+                        else hi = mid;
+                    }
+                    s = static_cast<int>(lo);
+                }
+            }
+            if (s < 0 || y == ignore) {
+                s = -1;
+                y = ignore;
+            } else if (y < 0 || y >= V) {
+                bad = true;
+                s = -1;
+                y = ignore;
+            }
+        }
+        if (t < T) {
+            lab_out[t] = y;
+            if (seq != nullptr) seq[t] = s;
+            if (s < 0) {
+                if (logp != nullptr) logp[t] = bad && bad_nan ? __int_as_float(0x7FC00000) : 0.f;
+                if (term != nullptr) term[t] = kl[t] = clip[t] = 0.f;
+            }
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&hdr->bad, 1);
+        // integer counts: the order of the atomics does not matter
+        const unsigned live = __ballot_sync(0xffffffffu, s >= 0);
+        if (live == 0) continue;
+        if (lane == 0) atomicAdd(&hdr->n_valid, static_cast<unsigned long long>(__popc(live)));
+        if (n_seq != nullptr) {
+            const unsigned mates = __match_any_sync(0xffffffffu, s);
+            if (s >= 0 && lane == __ffs(mates) - 1) atomicAdd(n_seq + s, __popc(mates));
+        }
+    }
+}
+
+// The row pass of the bf16 path: lse from the (m, s) partials, the token's terms and scale, and P
+// rewritten in place into the softmax part of D, c_t P exp(m_tile - lse).  P null: lse and logp only.
+// idx: original token of a row (null: t0 + row).
+__global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* __restrict__ labels, int64_t ignore,
+                                                                const float2* __restrict__ part, int nvt,
+                                                                const float* __restrict__ zlab, __nv_bfloat16* P,
+                                                                int64_t ldp, int V, const Policy pol,
+                                                                const int64_t* __restrict__ idx, int64_t t0,
+                                                                float* __restrict__ coef) {
+    extern __shared__ float fac[];   // [nvt]
+    __shared__ float red[32];
+    const int64_t row = blockIdx.x;
+    __nv_bfloat16* prow = P + row * ldp;
+    const int nv8 = (V + 7) / 8;
+    if (labels[row] == ignore) {
+        if (P != nullptr) {
+            for (int k = threadIdx.x; k < nv8; k += kRowThreads)
+                stg16(prow + static_cast<int64_t>(k) * 8, make_uint4(0, 0, 0, 0));
+            if (threadIdx.x == 0) coef[row] = 0.f;
+        }
+        return;
+    }
+    const float2* pr = part + row * nvt;
+    float m = -INFINITY;
+    for (int j = threadIdx.x; j < nvt; j += kRowThreads) m = fmaxf(m, pr[j].x);
+    m = block_reduce<kRowThreads>(m, true, red);
+    float s = 0.f;
+    for (int j = threadIdx.x; j < nvt; j += kRowThreads) {
+        const float2 p = pr[j];
+        s += p.y * expf(p.x - m);
+    }
+    s = block_reduce<kRowThreads>(s, false, red);
+    const float l = m + logf(s);
+    float lp = zlab[row] - l;
+    if (pol.hdr->err != 0) lp = __int_as_float(0x7FC00000);   // a GEMM gave up on a bounded wait
+    const int64_t t = idx != nullptr ? idx[row] : t0 + row;
+    if (pol.logp != nullptr && threadIdx.x == 0) pol.logp[t] = lp;
+    if (P == nullptr) return;
+    const float sc = policy_token(pol, t, lp, threadIdx.x == 0);
+    if (threadIdx.x == 0) coef[row] = sc;
+    for (int j = threadIdx.x; j < nvt; j += kRowThreads) fac[j] = sc * expf(pr[j].x - l);
+    __syncthreads();
+    for (int k = threadIdx.x; k < nv8; k += kRowThreads) {
+        const int col = k * 8;
+        const float f = fac[col / kVT];
+        float v[8];
+        unpack(ldg16(prow + col), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= f;
+        stg16(prow + col, pack(v));
+    }
+}
+
+// fp32 path: z row -> lse, the token's terms and scale, D in place (log-probability only: z is left)
+__global__ void __launch_bounds__(kRowThreads) policy_rows_f32(const int64_t* __restrict__ labels, int64_t ignore,
+                                                               float* Z, int64_t ldz, int V, int with_d, const Policy pol,
+                                                               const int64_t* __restrict__ idx, int64_t t0) {
+    __shared__ float red[32];
+    const int64_t row = blockIdx.x;
+    const int64_t y = labels[row];
+    float* z = Z + row * ldz;
+    if (y == ignore) {
+        if (with_d)
+            for (int v = threadIdx.x; v < V; v += kRowThreads) z[v] = 0.f;
+        return;
+    }
+    float m = -INFINITY;
+    for (int v = threadIdx.x; v < V; v += kRowThreads) m = fmaxf(m, z[v]);
+    m = block_reduce<kRowThreads>(m, true, red);
+    float s = 0.f;
+    for (int v = threadIdx.x; v < V; v += kRowThreads) s += expf(z[v] - m);
+    s = block_reduce<kRowThreads>(s, false, red);
+    const float l = m + logf(s);
+    const float lp = (z[y] - m) - logf(s);
+    const int64_t t = idx != nullptr ? idx[row] : t0 + row;
+    if (pol.logp != nullptr && threadIdx.x == 0) pol.logp[t] = lp;
+    if (!with_d) return;
+    __syncthreads();   // every thread has read z[y] before it is overwritten
+    const float sc = policy_token(pol, t, lp, threadIdx.x == 0);
+    for (int v = threadIdx.x; v < V; v += kRowThreads) z[v] = sc * (expf(z[v] - l) - (v == y ? 1.0f : 0.0f));
+}
+
+// loss and stats: fixed-order fp64 sums of the tokens' terms; NaN if a kernel recorded an error or the
+// scan found a bad label or bad sequences
+__global__ void __launch_bounds__(1024) policy_final(const float* __restrict__ term, const float* __restrict__ kl,
+                                                     const float* __restrict__ clip, int64_t T, const Hdr* hdr,
+                                                     float* loss, float* stats) {
+    __shared__ double red[3][32];
+    double s[3] = {0.0, 0.0, 0.0};
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+        s[0] += static_cast<double>(term[t]);
+        s[1] += static_cast<double>(kl[t]);
+        s[2] += static_cast<double>(clip[t]);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+        if ((threadIdx.x & 31) == 0) red[i][threadIdx.x >> 5] = s[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        double tot = 0.0;
+        for (int i = 0; i < 32; ++i) tot += red[threadIdx.x][i];
+        const double n = static_cast<double>(hdr->n_valid);
+        float r = static_cast<float>(threadIdx.x == 0 ? tot : n > 0.0 ? tot / n : 0.0);
+        if (hdr->err != 0 || hdr->bad != 0) r = __int_as_float(0x7fc00000);
+        if (threadIdx.x == 0) *loss = r;
+        else if (stats != nullptr) stats[threadIdx.x - 1] = r;
+    }
+}
+
 // loss = sum of the row terms (fixed order, fp64) / n_valid; NaN if a
 // tensor-core kernel recorded an error.
 // dev_denom 0: divide by denom; 1 (mean) / 2 (sum): the denominator from the device-side
@@ -586,6 +836,8 @@ struct Args {
     int dtype;
     cudaStream_t st;
     const float* scale_dev;   // non-null: the gradient scale is read from the device (no host wait)
+    const Policy* pol;        // non-null: the policy loss in place of the cross-entropy
+    const int64_t* idx;       // policy loss: original token of a row (null: the row itself)
 };
 
 template <typename TI>
@@ -607,8 +859,11 @@ int run_simt(const Args& a, const Layout& L, float scale) {
         const bool first = c == 0, last = c == L.nchunks - 1;
         if ((rc = simt<TI, TI, TI, 0>(cl, V, H, X + t0 * H, H, 1, W, 1, H, Z, (TI*)nullptr, V, nullptr, 0, a.st)))
             return rc;
-        dlogits_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, scale, a.scale_dev, lse + t0,
-                                                  lossrow + t0);
+        if (a.pol != nullptr)
+            policy_rows_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, 1, *a.pol, nullptr, t0);
+        else
+            dlogits_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, scale, a.scale_dev, lse + t0,
+                                                      lossrow + t0);
         if ((rc = check_launch("dlogits_f32"))) return rc;
         if (dX && (rc = simt<float, TI, TI, 1>(cl, H, V, Z, V, 1, W, H, 1, nullptr, dX + t0 * H, H, a.labels + t0,
                                                a.ignore, a.st)))
@@ -722,10 +977,17 @@ int run_tc(const Args& a, const Layout& L, float scale) {
         e.zlab = zlab + t0;
         if ((rc = launch_logits(Xc, cl, H, V, mW_k, e, L.ldp, L.nvt, a.st))) return rc;
         // 2. lse, loss terms, P -> D in place
-        dlogits_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
-                                                          zlab + t0, P, L.ldp, V, scale, a.scale_dev, lse + t0,
-                                                          lossrow + t0);
+        if (a.pol != nullptr)
+            policy_rows_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
+                                                                  zlab + t0, P, L.ldp, V, *a.pol,
+                                                                  a.idx != nullptr ? a.idx + t0 : nullptr, t0,
+                                                                  a.pol->coef + t0);
+        else
+            dlogits_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
+                                                              zlab + t0, P, L.ldp, V, scale, a.scale_dev, lse + t0,
+                                                              lossrow + t0);
         if ((rc = check_launch("dlogits_bf16"))) return rc;
+        if (a.pol != nullptr) e.tok_scale = a.pol->coef + t0;
         // 3. dX_c = D W, minus scale * W[label] in fp32
         if (a.dX && dx_slab(V) < V) {
             // over vocabulary slabs, summed in fp32; the last slab subtracts scale * W[label]
@@ -757,7 +1019,9 @@ int run_tc(const Args& a, const Layout& L, float scale) {
                 d.ld_corr = H;
                 d.corr_scale = scale;
                 d.scale_ptr = a.scale_dev;
-                if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1>(mDs_k, mWs_mn, cl, H, vl, d, a.st))) return rc;
+                rc = a.pol != nullptr ? launch_gemm<0, 1, EPI_ACCUM, 1, 1>(mDs_k, mWs_mn, cl, H, vl, d, a.st)
+                                      : launch_gemm<0, 1, EPI_ACCUM, 1>(mDs_k, mWs_mn, cl, H, vl, d, a.st);
+                if (rc) return rc;
             }
         } else if (a.dX) {
             EpiParams d = e;
@@ -772,7 +1036,9 @@ int run_tc(const Args& a, const Layout& L, float scale) {
             d.ld_corr = H;
             d.corr_scale = scale;
             d.scale_ptr = a.scale_dev;
-            if ((rc = launch_gemm<0, 1, EPI_STORE, 1>(mD_k, mW_mn, cl, H, V, d, a.st))) return rc;
+            rc = a.pol != nullptr ? launch_gemm<0, 1, EPI_STORE, 1, 1>(mD_k, mW_mn, cl, H, V, d, a.st)
+                                  : launch_gemm<0, 1, EPI_STORE, 1>(mD_k, mW_mn, cl, H, V, d, a.st);
+            if (rc) return rc;
         }
         // 4. dW (+)= D^T X_c, minus scale * X_t in fp32 for each token t labelled with the row
         if (a.dW) {
@@ -787,6 +1053,7 @@ int run_tc(const Args& a, const Layout& L, float scale) {
                 d.lstart = lstart + c * (V + 1);
             } else {
                 d.corr_src = X;                   // absolute token indices
+                if (a.pol != nullptr) d.tok_scale = a.pol->coef;
                 d.keys = keys;
                 d.lstart = lstart + (t0 / L.seg) * (V + 1);
                 d.nseg = static_cast<int>(ceil_div(static_cast<int64_t>(cl), static_cast<int64_t>(L.seg)));
@@ -808,7 +1075,9 @@ int run_tc(const Args& a, const Layout& L, float scale) {
             d.acc_read = first ? 0 : 1;
             d.acc_write = last ? 0 : 1;
             d.out_write = last ? 1 : 0;
-            if ((rc = launch_gemm<1, 1, EPI_ACCUM, 1>(mD_mn, mX_mn, V, H, cl, d, a.st))) return rc;
+            rc = a.pol != nullptr ? launch_gemm<1, 1, EPI_ACCUM, 1, 1>(mD_mn, mX_mn, V, H, cl, d, a.st)
+                                  : launch_gemm<1, 1, EPI_ACCUM, 1>(mD_mn, mX_mn, V, H, cl, d, a.st);
+            if (rc) return rc;
         }
     }
     return LIGER_OK;
@@ -848,6 +1117,7 @@ int run_compacted(const Args& a, int64_t n_valid, const CompactLayout& C, const 
     Args b = a;
     b.X = w8 + C.xc;
     b.labels = labc;
+    b.idx = idx;
     b.T = n_valid;
     b.dX = a.dX ? static_cast<void*>(w8 + C.dxc) : nullptr;
     b.ws = w8 + C.core;
@@ -856,6 +1126,10 @@ int run_compacted(const Args& a, int64_t n_valid, const CompactLayout& C, const 
         const int tgrid = static_cast<int>(std::min<int64_t>(a.T, 8 * sm_count()));
         scatter_rows<<<tgrid, 256, 0, a.st>>>(reinterpret_cast<const uint4*>(w8 + C.dxc), inv, a.T, hv,
                                               static_cast<uint4*>(a.dX));
+    }
+    if (a.pol != nullptr) {   // its row pass wrote the tokens' values in place already
+        take_err<<<1, 1, 0, a.st>>>(&hc->err, &reinterpret_cast<Hdr*>(w8 + tv.hdr)->err);
+        return check_launch("linear_policy scatter");
     }
     const int vgrid = static_cast<int>(std::min<int64_t>(ceil_div(a.T, int64_t{256}), 4 * sm_count()));
     scatter_rowvals<<<vgrid, 256, 0, a.st>>>(reinterpret_cast<const float*>(w8 + C.core + cv.lse),
@@ -1247,4 +1521,303 @@ extern "C" int liger_linear_ce_two_pass_fwd_bwd_async(const void* X, const void*
                                                       size_t ws_bytes, int64_t vchunk, int dtype, void* stream) {
     return linear_ce_two_pass_impl(X, W, labels, T, H, V, ignore_index, reduction, grad_scale, loss, dX, dW, ws,
                                    ws_bytes, vchunk, dtype, stream, false);
+}
+
+// ------------------------------------------------ policy loss and label log-probabilities
+namespace liger {
+namespace {
+
+// Workspace of the policy loss: the cross-entropy's, then its own per-token arrays.
+struct PolicyLayout {
+    Layout L;
+    size_t seq, n_seq, coef, term, kl, clip, total;
+};
+
+PolicyLayout policy_layout(int64_t T, int64_t H, int64_t V, int64_t B, int64_t chunk, int dtype) {
+    PolicyLayout P{};
+    P.L = layout(T, H, V, chunk, dtype);
+    size_t o = up256(P.L.tc ? compact_layout(T, H, V, chunk, dtype).total : P.L.total);
+    const size_t per_token = up256(sizeof(float) * static_cast<size_t>(std::max<int64_t>(T, 1)));
+    P.seq = o; o += per_token;
+    P.coef = o; o += per_token;
+    P.term = o; o += per_token;
+    P.kl = o; o += per_token;
+    P.clip = o; o += per_token;
+    P.n_seq = o; o = up256(o + sizeof(int) * static_cast<size_t>(B));
+    P.total = o;
+    return P;
+}
+
+// Workspace of the log-probabilities.  Tensor-core path: header, labels, z at the label, the row
+// partials of a chunk; then, for the form that drops ignored tokens, their X rows and index maps.
+struct LogpLayout {
+    bool tc;
+    int64_t C, nvt;
+    size_t hdr, labs, zlab, part, scr, total;
+    CompactLayout comp;
+};
+
+LogpLayout logp_layout(int64_t T, int64_t H, int64_t V, int dtype) {
+    LogpLayout P{};
+    P.tc = use_tc(H, V, dtype);
+    P.nvt = ceil_div(V, kVT);
+    P.C = P.tc ? kAutoChunkTC : std::max<int64_t>(128, (int64_t{1} << 26) / V);
+    P.C = std::max<int64_t>(1, std::min(P.C, T));
+    const size_t t = static_cast<size_t>(std::max<int64_t>(T, 1));
+    size_t o = 0;
+    P.hdr = o; o = up256(o + sizeof(Hdr));
+    P.labs = o; o = up256(o + sizeof(int64_t) * t);
+    P.zlab = o; o = up256(o + sizeof(float) * t);
+    P.part = o; o = up256(o + (P.tc ? sizeof(float2) * static_cast<size_t>(P.C * P.nvt) : 0));
+    P.scr = o; o = up256(o + (P.tc ? 0 : sizeof(float) * static_cast<size_t>(P.C * V)));
+    P.comp = compact_regions(o, 0, T, H, 2);
+    P.total = P.tc ? P.comp.total : o;
+    return P;
+}
+
+// Reads the header of the scan back and waits for it.
+int read_hdr(const char* who, const Hdr* hdr, Hdr* out, cudaStream_t st) {
+    Hdr* hp = nullptr;
+    if (int rc = pinned_hdr(&hp)) return rc;
+    if (cudaMemcpyAsync(hp, hdr, sizeof(Hdr), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return check_launch(who);
+    *out = *hp;
+    return LIGER_OK;
+}
+
+unsigned scan_grid(int64_t T) { return static_cast<unsigned>(std::min<int64_t>(ceil_div(T, 256), 4 * sm_count())); }
+
+// The log-probabilities of n rows at X with labels labs; idx: original token of a row (null: the row)
+int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* labs, const int64_t* idx, int64_t n, int H,
+                int V, int64_t ignore, float* logp, uint8_t* w8, const LogpLayout& L, cudaStream_t st) {
+    using namespace tc;
+    CUtensorMap mW_k;
+    int rc;
+    if ((rc = make_map(&mW_k, W, H, V, H, BK, B_BOX_ROWS))) return rc;
+    Policy pol{};
+    pol.logp = logp;
+    pol.hdr = reinterpret_cast<Hdr*>(w8 + L.hdr);
+    float2* part = reinterpret_cast<float2*>(w8 + L.part);
+    float* zlab = reinterpret_cast<float*>(w8 + L.zlab);
+    for (int64_t t0 = 0; t0 < n; t0 += L.C) {
+        const int cl = static_cast<int>(std::min(L.C, n - t0));
+        EpiParams e{};
+        e.err = &reinterpret_cast<Hdr*>(w8 + L.hdr)->err;
+        e.ignore_index = ignore;
+        e.labels = labs + t0;
+        e.M = cl;
+        e.N = V;
+        e.raster = RASTER_M_FASTEST;
+        e.hint_a = HINT_EVICT_LAST;
+        e.hint_b = HINT_EVICT_FIRST;
+        e.p_out = nullptr;
+        e.part = part;
+        e.nvt = static_cast<int>(L.nvt);
+        e.zlab = zlab + t0;
+        if ((rc = launch_logits(X + t0 * H, cl, H, V, mW_k, e, 0, L.nvt, st))) return rc;
+        policy_rows_bf16<<<cl, kRowThreads, 0, st>>>(labs + t0, ignore, part, static_cast<int>(L.nvt), zlab + t0, nullptr,
+                                                     0, V, pol, idx != nullptr ? idx + t0 : nullptr, t0, nullptr);
+        if ((rc = check_launch("linear_logp rows"))) return rc;
+    }
+    return LIGER_OK;
+}
+
+template <typename TI>
+int run_logp_simt(const void* X, const void* W, const int64_t* labs, int64_t T, int H, int V, int64_t ignore, float* logp,
+                  uint8_t* w8, const LogpLayout& L, cudaStream_t st) {
+    float* Z = reinterpret_cast<float*>(w8 + L.scr);
+    Policy pol{};
+    pol.logp = logp;
+    for (int64_t t0 = 0; t0 < T; t0 += L.C) {
+        const int cl = static_cast<int>(std::min(L.C, T - t0));
+        if (int rc = simt<TI, TI, TI, 0>(cl, V, H, static_cast<const TI*>(X) + t0 * H, H, 1, static_cast<const TI*>(W), 1,
+                                         H, Z, static_cast<TI*>(nullptr), V, nullptr, 0, st))
+            return rc;
+        policy_rows_f32<<<cl, kRowThreads, 0, st>>>(labs + t0, ignore, Z, V, V, 0, pol, nullptr, t0);
+        if (int rc = check_launch("linear_logp rows")) return rc;
+    }
+    return LIGER_OK;
+}
+
+bool head_shape_ok(int64_t T, int64_t H, int64_t V) {
+    return T >= 0 && H > 0 && V > 0 && H <= (1 << 30) && V <= (1 << 30) && T <= (int64_t{1} << 31) - 1;
+}
+
+int logp_impl(const char* who, const void* X, const void* W, const int64_t* labels, int64_t T, int64_t H, int64_t V,
+              int64_t ignore, float* logp, void* ws, size_t ws_bytes, int dtype, void* stream, bool sync) {
+    clear_error();
+    if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
+    if (!head_shape_ok(T, H, V))
+        return fail(LIGER_ERR_SHAPE, "%s: T=%lld H=%lld V=%lld", who, (long long)T, (long long)H, (long long)V);
+    if (T == 0) return LIGER_OK;
+    if (!X || !W || !labels || !logp) return fail(LIGER_ERR_NULL, "%s: X, W, labels, logp required", who);
+    if (!aligned16(X) || !aligned16(W) || (reinterpret_cast<uintptr_t>(logp) & 3) ||
+        (reinterpret_cast<uintptr_t>(labels) & 7))
+        return fail(LIGER_ERR_ALIGN, "%s: X and W must be 16-byte aligned, labels 8, logp 4", who);
+    const LogpLayout L = logp_layout(T, H, V, dtype);
+    if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255))
+        return fail(LIGER_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, L.total,
+                    ws_bytes);
+    cudaStream_t st = as_stream(stream);
+    uint8_t* w8 = static_cast<uint8_t*>(ws);
+    Hdr* hdr = reinterpret_cast<Hdr*>(w8 + L.hdr);
+    int64_t* labs = reinterpret_cast<int64_t*>(w8 + L.labs);
+    if (cudaMemsetAsync(hdr, 0, sizeof(Hdr), st) != cudaSuccess) return check_launch("linear_logp memset");
+    // the waiting form leaves logp alone until it knows that the labels are good
+    policy_scan<<<scan_grid(T), 256, 0, st>>>(labels, nullptr, T, V, 1, ignore, hdr, labs, nullptr, nullptr,
+                                              sync ? nullptr : logp, nullptr, nullptr, nullptr, 1);
+    if (int rc = check_launch("linear_logp scan")) return rc;
+    int64_t n = T;
+    if (sync) {
+        Hdr h{};
+        if (int rc = read_hdr("linear_logp scan", hdr, &h, st)) return rc;
+        if (h.bad) return fail(LIGER_ERR_LABEL, "%s: a label is outside [0, %lld) and is not %lld", who, (long long)V,
+                               (long long)ignore);
+        n = static_cast<int64_t>(h.n_valid);
+        if (n < T && cudaMemsetAsync(logp, 0, sizeof(float) * static_cast<size_t>(T), st) != cudaSuccess)
+            return check_launch("linear_logp memset");
+        if (n == 0) return LIGER_OK;
+    }
+    if (!L.tc)
+        return dtype == LIGER_F32
+                   ? run_logp_simt<float>(X, W, labs, T, (int)H, (int)V, ignore, logp, w8, L, st)
+                   : run_logp_simt<__nv_bfloat16>(X, W, labs, T, (int)H, (int)V, ignore, logp, w8, L, st);
+    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16*>(X), *w = static_cast<const __nv_bfloat16*>(W);
+    const int64_t* idx = nullptr;
+    if (n < T) {   // only the tokens that are not ignored, in order
+        int* cnt = reinterpret_cast<int*>(w8 + L.comp.cnt);
+        int64_t* at = reinterpret_cast<int64_t*>(w8 + L.comp.idx);
+        int64_t* labc = reinterpret_cast<int64_t*>(w8 + L.comp.labc);
+        __nv_bfloat16* xc = reinterpret_cast<__nv_bfloat16*>(w8 + L.comp.xc);
+        const int64_t nb = ceil_div(T, static_cast<int64_t>(kCompactBlock));
+        compact_count<<<static_cast<unsigned>(nb), kCompactBlock, 0, st>>>(labs, T, ignore, cnt);
+        compact_scan<<<1, 1024, 0, st>>>(cnt, nb);
+        compact_index<<<static_cast<unsigned>(nb), kCompactBlock, 0, st>>>(labs, T, ignore, cnt, at,
+                                                                           reinterpret_cast<int*>(w8 + L.comp.inv), labc);
+        gather_rows<<<static_cast<int>(std::min<int64_t>(n, 8 * sm_count())), 256, 0, st>>>(
+            static_cast<const uint4*>(X), at, n, H * 2 / 16, reinterpret_cast<uint4*>(xc));
+        if (int rc = check_launch("linear_logp compaction")) return rc;
+        x = xc;
+        labs = labc;
+        idx = at;
+    }
+    return run_logp_tc(x, w, labs, idx, n, (int)H, (int)V, ignore, logp, w8, L, st);
+}
+
+int policy_impl(const char* who, const void* X, const void* W, const int64_t* labels, const int32_t* cu,
+                const float* old_logp, const float* ref_logp, const float* adv, int64_t T, int64_t H, int64_t V, int64_t B,
+                int64_t ignore, int reduction, int flags, float eps_low, float eps_high, float beta, float grad_scale,
+                float* loss, float* stats, float* logp, void* dX, void* dW, void* ws, size_t ws_bytes, int64_t chunk,
+                int dtype, void* stream, bool sync) {
+    clear_error();
+    if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
+    if (!head_shape_ok(T, H, V) || chunk < 0 || B < 1 || B > (1 << 30) || reduction < 0 || reduction > 2 ||
+        (flags & ~LIGER_POLICY_ADV_PER_TOKEN))
+        return fail(LIGER_ERR_SHAPE, "%s: T=%lld H=%lld V=%lld B=%lld chunk=%lld reduction=%d flags=%d", who, (long long)T,
+                    (long long)H, (long long)V, (long long)B, (long long)chunk, reduction, flags);
+    if (!cu && B != 1) return fail(LIGER_ERR_NULL, "%s: cu_seqlens is required with B=%lld", who, (long long)B);
+    if (!(eps_low >= 0.f && eps_low <= 1.f) || !(eps_high >= 0.f) || !(beta == beta) || !(grad_scale == grad_scale))
+        return fail(LIGER_ERR_SHAPE, "%s: eps_low=%g (0 to 1) eps_high=%g (>= 0) beta=%g grad_scale=%g", who, eps_low,
+                    eps_high, beta, grad_scale);
+    if (!W || !loss || (T > 0 && (!X || !labels || !old_logp || !adv || (beta != 0.f && !ref_logp))))
+        return fail(LIGER_ERR_NULL, "%s: X, W, labels, old_logp, adv, loss (and ref_logp with beta) required", who);
+    const auto off = [](const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; };
+    if (off(X, 16) || off(W, 16) || off(dX, 16) || off(dW, 16) || off(labels, 8) || off(cu, 4) || off(old_logp, 4) ||
+        off(ref_logp, 4) || off(adv, 4) || off(loss, 4) || off(stats, 4) || off(logp, 4))
+        return fail(LIGER_ERR_ALIGN, "%s: X, W, dX, dW must be 16-byte aligned, labels 8, the others 4", who);
+    const PolicyLayout PL = policy_layout(T, H, V, B, chunk, dtype);
+    if (!ws || ws_bytes < PL.total || (reinterpret_cast<uintptr_t>(ws) & 255))
+        return fail(LIGER_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, PL.total,
+                    ws_bytes);
+    cudaStream_t st = as_stream(stream);
+    uint8_t* w8 = static_cast<uint8_t*>(ws);
+    Hdr* hdr = reinterpret_cast<Hdr*>(w8 + PL.L.hdr);
+    int64_t* labs = reinterpret_cast<int64_t*>(w8 + PL.L.labs);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(w8 + at); };
+    int *seq = reinterpret_cast<int*>(w8 + PL.seq), *n_seq = reinterpret_cast<int*>(w8 + PL.n_seq);
+    if (cudaMemsetAsync(hdr, 0, sizeof(Hdr), st) != cudaSuccess ||
+        cudaMemsetAsync(n_seq, 0, sizeof(int) * static_cast<size_t>(B), st) != cudaSuccess)
+        return check_launch("linear_policy memset");
+    int64_t n = T;
+    if (T > 0) {
+        policy_scan<<<scan_grid(T), 256, 0, st>>>(labels, cu, T, V, B, ignore, hdr, labs, seq, n_seq, sync ? nullptr : logp,
+                                                  f32(PL.term), f32(PL.kl), f32(PL.clip), 0);
+        if (int rc = check_launch("linear_policy scan")) return rc;
+    }
+    if (sync && T > 0) {
+        Hdr h{};
+        if (int rc = read_hdr("linear_policy scan", hdr, &h, st)) return rc;
+        if (h.bad & 2) return fail(LIGER_ERR_SHAPE, "%s: cu_seqlens descends or leaves [0, %lld]", who, (long long)T);
+        if (h.bad) return fail(LIGER_ERR_LABEL, "%s: a label is outside [0, %lld) and is not %lld", who, (long long)V,
+                               (long long)ignore);
+        n = static_cast<int64_t>(h.n_valid);
+        if (logp && n < T && cudaMemsetAsync(logp, 0, sizeof(float) * static_cast<size_t>(T), st) != cudaSuccess)
+            return check_launch("linear_policy memset");
+    }
+    if (n == 0) {   // nothing to learn from
+        const size_t esz = dtype == LIGER_F32 ? 4 : 2;
+        bool ok = cudaMemsetAsync(loss, 0, sizeof(float), st) == cudaSuccess;
+        if (stats) ok = ok && cudaMemsetAsync(stats, 0, 2 * sizeof(float), st) == cudaSuccess;
+        if (dX) ok = ok && cudaMemsetAsync(dX, 0, static_cast<size_t>(T * H) * esz, st) == cudaSuccess;
+        if (dW) ok = ok && cudaMemsetAsync(dW, 0, static_cast<size_t>(V * H) * esz, st) == cudaSuccess;
+        return ok ? LIGER_OK : check_launch("linear_policy memset");
+    }
+    const Policy pol{old_logp, ref_logp, adv, flags & LIGER_POLICY_ADV_PER_TOKEN, reduction, 1.f - eps_low, 1.f + eps_high,
+                     beta, grad_scale, seq, n_seq, hdr, B, f32(PL.coef), f32(PL.term), f32(PL.kl), f32(PL.clip), logp};
+    const Args a{X, W, labs, T, H, V, ignore, reduction, grad_scale, loss, dX, dW, w8, dtype, st, nullptr, &pol, nullptr};
+    int rc;
+    if (PL.L.tc) rc = n < T ? run_tc_compact(a, n, chunk, 0.f) : run_tc(a, PL.L, 0.f);
+    else rc = dtype == LIGER_F32 ? run_simt<float>(a, PL.L, 0.f) : run_simt<__nv_bfloat16>(a, PL.L, 0.f);
+    if (rc) return rc;
+    policy_final<<<1, 1024, 0, st>>>(f32(PL.term), f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
+    return check_launch("linear_policy");
+}
+
+}  // namespace
+}  // namespace liger
+
+extern "C" size_t liger_linear_logp_workspace(int64_t T, int64_t H, int64_t V, int dtype) {
+    if (!head_shape_ok(T, H, V) || (dtype != LIGER_F32 && dtype != LIGER_BF16)) return 0;
+    return logp_layout(T, H, V, dtype).total;
+}
+
+extern "C" int liger_linear_logp_fwd(const void* X, const void* W, const int64_t* labels, int64_t T, int64_t H, int64_t V,
+                                     int64_t ignore_index, float* logp, void* ws, size_t ws_bytes, int dtype,
+                                     void* stream) {
+    return logp_impl("linear_logp", X, W, labels, T, H, V, ignore_index, logp, ws, ws_bytes, dtype, stream, true);
+}
+
+extern "C" int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* labels, int64_t T, int64_t H,
+                                           int64_t V, int64_t ignore_index, float* logp, void* ws, size_t ws_bytes,
+                                           int dtype, void* stream) {
+    return logp_impl("linear_logp_async", X, W, labels, T, H, V, ignore_index, logp, ws, ws_bytes, dtype, stream, false);
+}
+
+extern "C" size_t liger_linear_policy_workspace(int64_t T, int64_t H, int64_t V, int64_t B, int64_t chunk, int dtype) {
+    if (!head_shape_ok(T, H, V) || B < 1 || chunk < 0 || (dtype != LIGER_F32 && dtype != LIGER_BF16)) return 0;
+    return policy_layout(T, H, V, B, chunk, dtype).total;
+}
+
+extern "C" int liger_linear_policy_fwd_bwd(const void* X, const void* W, const int64_t* labels, const int32_t* cu_seqlens,
+                                           const float* old_logp, const float* ref_logp, const float* adv, int64_t T,
+                                           int64_t H, int64_t V, int64_t B, int64_t ignore_index, int reduction, int flags,
+                                           float eps_low, float eps_high, float beta, float grad_scale, float* loss,
+                                           float* stats, float* logp, void* dX, void* dW, void* ws, size_t ws_bytes,
+                                           int64_t chunk, int dtype, void* stream) {
+    return policy_impl("linear_policy", X, W, labels, cu_seqlens, old_logp, ref_logp, adv, T, H, V, B, ignore_index,
+                       reduction, flags, eps_low, eps_high, beta, grad_scale, loss, stats, logp, dX, dW, ws, ws_bytes,
+                       chunk, dtype, stream, true);
+}
+
+extern "C" int liger_linear_policy_fwd_bwd_async(const void* X, const void* W, const int64_t* labels,
+                                                 const int32_t* cu_seqlens, const float* old_logp, const float* ref_logp,
+                                                 const float* adv, int64_t T, int64_t H, int64_t V, int64_t B,
+                                                 int64_t ignore_index, int reduction, int flags, float eps_low,
+                                                 float eps_high, float beta, float grad_scale, float* loss, float* stats,
+                                                 float* logp, void* dX, void* dW, void* ws, size_t ws_bytes, int64_t chunk,
+                                                 int dtype, void* stream) {
+    return policy_impl("linear_policy_async", X, W, labels, cu_seqlens, old_logp, ref_logp, adv, T, H, V, B, ignore_index,
+                       reduction, flags, eps_low, eps_high, beta, grad_scale, loss, stats, logp, dX, dW, ws, ws_bytes,
+                       chunk, dtype, stream, false);
 }

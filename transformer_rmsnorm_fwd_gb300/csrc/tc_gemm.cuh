@@ -125,6 +125,9 @@ struct EpiParams {
     int64_t ld_corr;
     float corr_scale;
     const float* scale_ptr;             // non-null: corr_scale is read from here (set on the device)
+    // TOKSCALE kernels: a scale for each token in place of corr_scale (the token is the row, or
+    // the key's t)
+    const float* tok_scale;
     // The keys may come in nseg sorted segments with one start table each,
     // lstride ints apart (nseg 0 counts as 1).
     const unsigned long long* keys;
@@ -461,7 +464,7 @@ __device__ __forceinline__ uint4 pack_bf8(const float* f) {
 // one-time attribute set in one unit never stands in for another's.
 namespace {
 
-template <int A_MN, int B_MN, int EPI, int PAIR = 0>
+template <int A_MN, int B_MN, int EPI, int PAIR = 0, int TOKSCALE = 0>
 __global__ void __launch_bounds__(THREADS, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2, int M, int N,
@@ -712,7 +715,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int row = (mhi ? mi - ep.msplit_mt : mi) * Cfg::TM + static_cast<int>(crank) * BM + rl;
             const int n0 = ni * BN;
             const bool row_ok = row < (mhi ? ep.M2 : ep.M);
-            const float cscale = ep.scale_ptr != nullptr ? *ep.scale_ptr : ep.corr_scale;
+            const float cscale = TOKSCALE ? (row_ok && ep.keys == nullptr ? ep.tok_scale[row] : 0.f)
+                                          : ep.scale_ptr != nullptr ? *ep.scale_ptr : ep.corr_scale;
             // EPI_ACCUM: everything that does not depend on the accumulator is fetched
             // before waiting for it (label range, first 32 columns of the fp32 sum)
             int k_lo = 0, k_hi = 0;
@@ -1147,8 +1151,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         for (int kk = lo; kk < hi; ++kk) {
                             const int64_t t = static_cast<int64_t>(ep.keys[kk] & 0xFFFFFFFFull);
-                            sub_scaled32(v, ep.corr_src + t * ep.ld_corr + n0 + c * 32, cscale,
-                                         ep.N - (n0 + c * 32));
+                            sub_scaled32(v, ep.corr_src + t * ep.ld_corr + n0 + c * 32,
+                                         TOKSCALE ? ep.tok_scale[t] : cscale, ep.N - (n0 + c * 32));
                         }
                     }
                     if (lrow != nullptr) sub_scaled32(v, lrow + c * 32, cscale, ep.N - (n0 + c * 32));
@@ -1242,12 +1246,12 @@ int make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, i
 // 256 x 256 tiles.  grid_limit = 0: one block per SM (pairs: as many as fit).
 namespace {
 
-template <int A_MN, int B_MN, int EPI, int PAIR = 0>
+template <int A_MN, int B_MN, int EPI, int PAIR = 0, int TOKSCALE = 0>
 int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int K, const EpiParams& ep,
                 cudaStream_t st, int grid_limit = 0, const CUtensorMap* ma2 = nullptr,
                 const CUtensorMap* mb2 = nullptr) {
     using Cfg = TileCfg<PAIR>;
-    auto kern = tc_gemm_kernel<A_MN, B_MN, EPI, PAIR>;
+    auto kern = tc_gemm_kernel<A_MN, B_MN, EPI, PAIR, TOKSCALE>;
     // per instantiation and device: function attributes belong to each device's context.
     // units_of[dev] = 0 until the attribute is set; threads that race here all set the
     // same attribute and store the same count (published with release / acquire).
