@@ -10,8 +10,11 @@
 //    one running sum serves both.  Rows are split into units that never cross a
 //    gate row; per-unit partial rows go to the workspace and are added in a
 //    fixed order.
+#include <atomic>
+
 #include "common.cuh"
 #include "liger_train.h"
+#include "mbarrier.cuh"
 
 namespace liger {
 namespace {
@@ -99,6 +102,374 @@ __global__ void __launch_bounds__(256) block_norm_fwd_generic(FwdP p) {
     }
 }
 
+// ------------------------------------------------------- forward, rows in registers
+// VEC consecutive elements of a row as one thread holds them: a 16-byte vector, or one element
+// where the rows are no whole vectors.
+template <typename T, int VEC> struct Frag {
+    static_assert(VEC == Vec<T>::N, "whole vectors or single elements");
+    uint4 u;
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const T* p) { u = ldg16(p); }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const { unpack(u, f); }
+    static __device__ __forceinline__ void put(T* p, const float (&f)[VEC]) { stg16(p, pack(f)); }
+};
+template <typename T> struct Frag<T, 1> {
+    float v;
+    __device__ __forceinline__ void zero() { v = 0.f; }
+    __device__ __forceinline__ void load(const T* p) { v = ldf(p); }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = v; }
+    static __device__ __forceinline__ void put(T* p, const float (&f)[1]) { stf(p, f[0]); }
+};
+
+// A team of `tw` warps holds a row in registers (VPT fragments per thread), a block `teams` of them;
+// a team keeps its columns' weights in registers over its rows and has its next row's loads in
+// flight while it works on one.  The two row sums go over the team by shuffles and one named
+// barrier each; the exchange buffers alternate, so that a buffer is written again only after a
+// barrier that follows every read of it.
+template <typename T, int VEC, int VPT>
+__global__ void __launch_bounds__(512) block_norm_fwd_team(FwdP p, int tw) {
+    __shared__ float red[2][16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int team = warp / tw, wt = warp - team * tw, teams = (blockDim.x >> 5) / tw;
+    const int tt = wt * 32 + lane, nt = tw * 32;   // thread of the team, threads of the team
+    const int nfrag = p.cols / VEC;
+    const T *z = static_cast<const T*>(p.z), *r = static_cast<const T*>(p.r);
+    const T *wp = static_cast<const T*>(p.w_post), *wn = static_cast<const T*>(p.w_pre);
+    T *h = static_cast<T*>(p.h), *y = static_cast<T*>(p.y);
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    Frag<T, VEC> fp[VPT], fn[VPT], fg[VPT];
+    bool live[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = j * nt + tt;
+        live[j] = c < nfrag;
+        fp[j].zero();
+        fn[j].zero();
+        fg[j].zero();
+        if (live[j] && wp != nullptr) fp[j].load(wp + static_cast<int64_t>(c) * VEC);
+        if (live[j] && wn != nullptr) fn[j].load(wn + static_cast<int64_t>(c) * VEC);
+    }
+    int turn = 0;
+    auto team_sum = [&](float v) {
+        v = warp_sum(v);
+        if (tw == 1) return v;
+        float* sh = red[turn & 1] + team * tw;
+        ++turn;
+        if (lane == 0) sh[wt] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(nt) : "memory");
+        float t = 0.f;
+        for (int i = 0; i < tw; ++i) t += sh[i];
+        return t;
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * teams + team;
+    Frag<T, VEC> nz[VPT], nr[VPT];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            nz[j].zero();
+            nr[j].zero();
+            if (live[j]) {
+                const int64_t o = row * p.cols + static_cast<int64_t>(j * nt + tt) * VEC;
+                nz[j].load(z + o);
+                nr[j].load(r + o);
+            }
+        }
+    };
+    if (t < p.rows) fetch(t);
+    int64_t gate_row = -1;
+    for (; t < p.rows; t += step) {
+        Frag<T, VEC> cz[VPT], cr[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) cz[j] = nz[j], cr[j] = nr[j];
+        if (t + step < p.rows) fetch(t + step);   // rows of other teams are never written before they are read
+        if (p.gate != nullptr && t / p.per_gate != gate_row) {
+            gate_row = t / p.per_gate;
+            const T* g = static_cast<const T*>(p.gate) + gate_row * p.cols;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (live[j]) fg[j].load(g + static_cast<int64_t>(j * nt + tt) * VEC);
+        }
+        float rz = 1.f;
+        if (wp != nullptr) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                float f[VEC];
+                cz[j].get(f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) ss = fmaf(f[e], f[e], ss);
+            }
+            rz = 1.0f / sqrtf(team_sum(ss) * inv + p.eps);
+            if (p.rstd_z != nullptr && tt == 0) p.rstd_z[t] = rz;
+        }
+        const int64_t o = t * p.cols;
+        float hv[VPT][VEC];
+        float ss = 0.f;
+        const float bz = p.b * rz;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float fz[VEC], fr[VEC], w[VEC];
+            cz[j].get(fz);
+            cr[j].get(fr);
+            if (wp != nullptr) {
+                fp[j].get(w);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) fz[e] *= w[e];
+            }
+            if (p.gate != nullptr) {
+                fg[j].get(w);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) fz[e] *= w[e];
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                hv[j][e] = fmaf(bz, fz[e], p.a * fr[e]);
+                ss = fmaf(hv[j][e], hv[j][e], ss);
+            }
+            if (live[j]) Frag<T, VEC>::put(h + o + static_cast<int64_t>(j * nt + tt) * VEC, hv[j]);
+        }
+        if (wn == nullptr) continue;
+        const float rh = 1.0f / sqrtf(team_sum(ss) * inv + p.eps);
+        if (p.rstd_h != nullptr && tt == 0) p.rstd_h[t] = rh;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float w[VEC];
+            fn[j].get(w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) hv[j][e] = hv[j][e] * rh * w[e];
+            if (live[j]) Frag<T, VEC>::put(y + o + static_cast<int64_t>(j * nt + tt) * VEC, hv[j]);
+        }
+    }
+}
+
+// ------------------------------------------------------- forward, rows staged by bulk copies
+// 1 / sqrt(x) for x > 0: the hardware approximation and one Newton step (within an ulp or so; the
+// correctly rounded square root and division are a long serial chain between two barriers)
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float r = rsqrtf(x);
+    const float e = fmaf(-x * r, r, 1.f);
+    const float n = fmaf(0.5f * r, e, r);
+    return isfinite(n) ? n : r;   // x = 0, infinity or NaN: what rsqrt says
+}
+
+// The same team per row, with the rows of z and r brought into a ring of `nst` slots per team by
+// bulk copies, so that several rows per team are in flight without registers.  A slot is read into
+// registers at once and is free again after the next team barrier.  Every wait is bounded; on
+// expiry the team records it, waits (bounded) for its copies and writes NaN into the rows it did
+// not finish.  Streaming stores and issuing the next copy only after the sums measured 0.95 of the
+// copy rate at 4096 bf16 columns, against 0.93 with the copy first and 0.91 with plain stores (other
+// widths: within 0.01).
+// GATE: 0 none, 1 one gate row (folded into the post-norm's weights once), 2 several (read anew
+// where a row's gate differs from that of the team's row before).
+template <typename T, int VPT, int GATE, int NT, int MB, int ONE>
+__global__ void __launch_bounds__(NT, MB) block_norm_fwd_ring(FwdP p, int tw, int nst, int* err) {
+    constexpr int VEC = Vec<T>::N;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ __align__(16) float red[2][NT / 32 + 4][4];   // rows of 4: a team starts on a multiple of 4 warps or is a warp alone
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (ONE) tw = blockDim.x >> 5;
+    const int team = ONE ? 0 : warp / tw, wt = warp - team * tw, teams = ONE ? 1 : (blockDim.x >> 5) / tw;
+    const int tt = wt * 32 + lane, nt = tw * 32;
+    const int nvec = p.cols / VEC;
+    const uint32_t rb = static_cast<uint32_t>(p.cols) * sizeof(T);
+    const uint8_t* ring = sm + static_cast<size_t>(team) * nst * 2 * rb;
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(teams) * nst * 2 * rb) + 8u * team * nst;
+    const T *z = static_cast<const T*>(p.z), *r = static_cast<const T*>(p.r);
+    const T *wp = static_cast<const T*>(p.w_post), *wn = static_cast<const T*>(p.w_pre);
+    T *h = static_cast<T*>(p.h), *y = static_cast<T*>(p.y);
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * teams + team;
+    auto issue = [&](int64_t row, int s) {
+        const uint32_t bar = bars + 8u * s, dst = smem_u32(ring + static_cast<size_t>(s) * 2 * rb);
+        mbar_expect_tx(bar, 2 * rb);
+        bulk_g2s(dst, z + row * p.cols, rb, bar);
+        bulk_g2s(dst + rb, r + row * p.cols, rb, bar);
+    };
+    for (int i = threadIdx.x; i < 2 * (NT / 32 + 4) * 4; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    mbar_init_fence();
+    __syncthreads();
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t + s * step < p.rows) issue(t + s * step, s);
+    // wq = block_scale w_post (and the one gate row) in fp32, wn as stored
+    float wq[VPT][VEC];
+    uint4 fn[VPT];
+    bool live[VPT];
+    auto gate_in = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int64_t c = static_cast<int64_t>(j * nt + tt) * VEC;
+            float f[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) wq[j][e] = p.b;
+            if (!live[j]) continue;
+            if (wp != nullptr) {
+                unpack(ldg16(wp + c), f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) wq[j][e] *= f[e];
+            }
+            if (GATE != 0) {
+                unpack(ldg16(static_cast<const T*>(p.gate) + row * p.cols + c), f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) wq[j][e] *= f[e];
+            }
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        live[j] = j * nt + tt < nvec;
+        fn[j] = make_uint4(0, 0, 0, 0);
+        if (live[j] && wn != nullptr) fn[j] = ldg16(wn + static_cast<int64_t>(j * nt + tt) * VEC);
+    }
+    if (GATE != 2) gate_in(0);
+    int turn = 0;
+    // Team-wide sum in two halves: gather() brings the warps' sums together and says whether every
+    // thread of the team got its row (one team barrier), total() adds them up.
+    const int at0 = ONE ? 0 : team * ((tw + 3) & ~3);
+    auto gather = [&](float& v, bool& ok) {
+        v = warp_sum(v);
+        if (!ONE && tw == 1) {
+            ok = __all_sync(0xffffffffu, ok);
+            return;
+        }
+        if (lane == 0) (&red[turn][0][0])[at0 + wt] = v;
+        if (ONE) {
+            ok = __syncthreads_and(ok ? 1 : 0) != 0;
+        } else {
+            uint32_t all;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 q, %3, 0;\n\t"
+                "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(all)
+                : "r"(team + 1), "r"(nt), "r"(ok ? 1u : 0u)
+                : "memory");
+            ok = all != 0;
+        }
+    };
+    auto total = [&](float v) {
+        if (!ONE && tw == 1) return v;
+        const float4* q = reinterpret_cast<const float4*>(&red[turn][0][0] + at0);   // slots past the team's warps hold 0
+        turn ^= 1;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < (NT / 32 + 3) / 4; ++w)
+            if (w * 4 < tw) {
+                const float4 a = q[w];
+                s += (a.x + a.y) + (a.z + a.w);
+            }
+        return s;
+    };
+    // the gate row of row t, kept without a division: t = gate * per_gate + rem
+    int64_t gate_row = 0, rem = 0, step_gates = 0, step_rem = 0;
+    if (GATE == 2) {
+        gate_row = t / p.per_gate;
+        rem = t - gate_row * p.per_gate;
+        step_gates = step / p.per_gate;
+        step_rem = step - step_gates * p.per_gate;
+    }
+    bool new_gate = true;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (; t < p.rows; t += step) {
+        uint4 cz[VPT], cr[VPT];
+        if (GATE == 2) {   // its loads run while the row is waited for
+            if (new_gate) gate_in(gate_row);
+            rem += step_rem;
+            const int64_t on = step_gates + (rem >= p.per_gate ? 1 : 0);
+            if (rem >= p.per_gate) rem -= p.per_gate;
+            gate_row += on;
+            new_gate = on != 0;
+        }
+        ok = mbar_wait(bars + 8u * s, ph);
+        const uint8_t* slot = ring + static_cast<size_t>(s) * 2 * rb;
+        float sz = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            cz[j] = cr[j] = make_uint4(0, 0, 0, 0);
+            if (live[j] && ok) {
+                cz[j] = *reinterpret_cast<const uint4*>(slot + static_cast<size_t>(j * nt + tt) * 16);
+                cr[j] = *reinterpret_cast<const uint4*>(slot + rb + static_cast<size_t>(j * nt + tt) * 16);
+            }
+            float f[VEC];
+            unpack(cz[j], f);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sz = fmaf(f[e], f[e], sz);
+        }
+        gather(sz, ok);
+        if (!ok) break;
+        const float tz = total(sz);
+        if (tt == 0 && t + nst * step < p.rows) {   // every thread of the team has read the slot
+            fence_proxy_async_smem();
+            issue(t + nst * step, s);
+        }
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+        float rz = 1.f;
+        if (wp != nullptr) {
+            rz = inv_sqrt(fmaf(tz, inv, p.eps));
+            if (p.rstd_z != nullptr && tt == 0) p.rstd_z[t] = rz;
+        }
+        const int64_t o = t * p.cols;
+        float hv[VPT][VEC];
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float fz[VEC], fr[VEC];
+            unpack(cz[j], fz);
+            unpack(cr[j], fr);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                hv[j][e] = fmaf(fz[e] * wq[j][e], rz, p.a * fr[e]);
+                ss = fmaf(hv[j][e], hv[j][e], ss);
+            }
+            if (live[j]) stg16_cs(h + o + static_cast<int64_t>(j * nt + tt) * VEC, pack(hv[j]));
+        }
+        if (wn == nullptr) continue;
+        bool same = true;
+        gather(ss, same);
+        const float rh = inv_sqrt(fmaf(total(ss), inv, p.eps));
+        if (p.rstd_h != nullptr && tt == 0) p.rstd_h[t] = rh;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float w[VEC];
+            unpack(fn[j], w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) hv[j][e] = hv[j][e] * rh * w[e];
+            if (live[j]) stg16_cs(y + o + static_cast<int64_t>(j * nt + tt) * VEC, pack(hv[j]));
+        }
+    }
+    if (ok) return;
+    if (tt == 0) {
+        atomicExch(err, 1);
+        int64_t row = t;
+        for (int i = 0; i < nst && row < p.rows; ++i, row += step) {   // the copies in flight
+            mbar_wait(bars + 8u * s, ph);
+            if (++s == nst) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    const float nan = __int_as_float(0x7FC00000);
+    for (; t < p.rows; t += step) {
+        for (int v = tt; v < nvec; v += nt) {
+            stg16(h + t * p.cols + static_cast<int64_t>(v) * VEC, nan16<T>());
+            if (wn != nullptr) stg16(y + t * p.cols + static_cast<int64_t>(v) * VEC, nan16<T>());
+        }
+        if (tt == 0 && wp != nullptr && p.rstd_z != nullptr) p.rstd_z[t] = nan;
+        if (tt == 0 && wn != nullptr && p.rstd_h != nullptr) p.rstd_h[t] = nan;
+    }
+}
+
 // The block's partial rows live in the workspace; each element of them belongs to one thread.
 template <typename T>
 __global__ void __launch_bounds__(256) block_norm_bwd_generic(BwdP p) {
@@ -177,6 +548,327 @@ __global__ void __launch_bounds__(256) block_norm_bwd_generic(BwdP p) {
             }
         }
         __syncthreads();
+    }
+}
+
+// ------------------------------------------------------- backward, rows staged by bulk copies
+// A block per unit of rows; a team of `tw` warps takes every teams-th row of it, its rows of dh, dy,
+// z, h (those that the call has) brought into the team's ring of `nst` slots by bulk copies.  Each
+// thread owns VPT 16-byte column vectors: the weights and its share of the column sums S = sum D z rz
+// and sum dy h rh stay in fp32 registers over the rows.
+// D needs the row sum s1 and dz the row sum s2 of q D z, but with c1 = rh^3 / cols s1
+//     s2 = sum (dh + rh u) q z - c1 sum h q z,
+// so the three sums are formed in one pass over the row and reduced together: one team barrier a row,
+// whose values stay in registers across it, and the slot is free at once for the next copies.
+// Arithmetic on column pairs with the packed fp32x2 instructions.
+// WHOLE 0: the block's rows share one gate row (or there is none).  WHOLE 1 (one team): the block
+// takes whole gate rows; as one ends its dgate is written, and sum block_scale g S is kept.
+// ONE: a single team, known at compile time (its strides and widths are then constants: 0.97 of the
+// copy rate against 0.92 at 4096 bf16 columns).
+// Every wait is bounded; on expiry the block records it, waits (bounded) for its copies and writes
+// NaN into the rows and sums it did not finish.
+template <typename T, int VPT, int WHOLE, int NT, int ONE>
+__global__ void __launch_bounds__(NT, 1) block_norm_bwd_ring(BwdP p, int tw, int nst, int* err) {
+    constexpr int VEC = Vec<T>::N, NP = VEC / 2;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ __align__(16) float red[2][3][(NT / 32 + 3) / 4 * 4 + 4];
+    __shared__ int failed;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (ONE) tw = blockDim.x >> 5;
+    const int team = ONE ? 0 : warp / tw, wt = warp - team * tw, teams = ONE ? 1 : (blockDim.x >> 5) / tw;
+    const int tt = wt * 32 + lane, nt = tw * 32;
+    const int nvec = p.cols / VEC;
+    const uint32_t rb = static_cast<uint32_t>(p.cols) * sizeof(T);
+    const T *dh = static_cast<const T*>(p.dh), *dy = static_cast<const T*>(p.dy), *z = static_cast<const T*>(p.z),
+            *h = static_cast<const T*>(p.h);
+    const T *wp = static_cast<const T*>(p.w_post), *wn = static_cast<const T*>(p.w_pre), *gate = static_cast<const T*>(p.gate);
+    const bool post = wp != nullptr, pre = wn != nullptr, need_z = post || gate != nullptr, has_dh = dh != nullptr;
+    // offsets of the streams in a slot
+    uint32_t off = 0;
+    const uint32_t o_dh = off; off += has_dh ? rb : 0;
+    const uint32_t o_dy = off; off += pre ? rb : 0;
+    const uint32_t o_h = off; off += pre ? rb : 0;
+    const uint32_t o_z = off; off += need_z ? rb : 0;
+    const uint32_t slot_bytes = off;
+    const uint8_t* ring = sm + static_cast<size_t>(team) * nst * slot_bytes;
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(teams) * nst * slot_bytes) + 8u * team * nst;
+    int64_t u0, t1;   // the block's rows
+    int64_t gate_row = 0;
+    if (WHOLE) {
+        u0 = blockIdx.x * p.gates_per_block * p.per_gate;
+        t1 = min(p.rows, u0 + p.gates_per_block * p.per_gate);
+        gate_row = blockIdx.x * p.gates_per_block;
+    } else {
+        gate_row = blockIdx.x / p.splits;
+        u0 = gate_row * p.per_gate + (blockIdx.x - gate_row * p.splits) * p.unit_rows;
+        t1 = min(u0 + p.unit_rows, (gate_row + 1) * p.per_gate);
+    }
+    const int64_t t0 = u0 + team;   // the team's rows: t0, t0 + teams, ...
+    auto issue = [&](int64_t t, int s) {
+        const uint32_t bar = bars + 8u * s, dst = smem_u32(ring + static_cast<size_t>(s) * slot_bytes);
+        mbar_expect_tx(bar, slot_bytes);
+        if (has_dh) bulk_g2s(dst + o_dh, dh + t * p.cols, rb, bar);
+        if (pre) bulk_g2s(dst + o_dy, dy + t * p.cols, rb, bar);
+        if (pre) bulk_g2s(dst + o_h, h + t * p.cols, rb, bar);
+        if (need_z) bulk_g2s(dst + o_z, z + t * p.cols, rb, bar);
+    };
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    if (threadIdx.x == 0) failed = 0;
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    mbar_init_fence();
+    __syncthreads();
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t0 + static_cast<int64_t>(s) * teams < t1) issue(t0 + static_cast<int64_t>(s) * teams, s);
+    // q = block_scale g w_post and w_pre in fp32; sums
+    float2 q[VPT][NP], wf[VPT][NP], S[VPT][NP], Sn[VPT][NP], Sp[WHOLE ? VPT : 1][NP];
+    bool live[VPT];
+    const float2 zero2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * nt + tt;
+        live[j] = v < nvec;
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            wf[j][e] = S[j][e] = Sn[j][e] = zero2;
+            if (WHOLE) Sp[j][e] = zero2;
+        }
+        if (live[j] && pre) unpack2(ldg16(wn + static_cast<int64_t>(v) * VEC), wf[j]);
+    }
+    auto gate_in = [&]() {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int64_t c = static_cast<int64_t>(j * nt + tt) * VEC;
+            float2 f[NP];
+#pragma unroll
+            for (int e = 0; e < NP; ++e) q[j][e] = make_float2(p.b, p.b);
+            if (!live[j]) continue;
+            if (post) {
+                unpack2(ldg16(wp + c), f);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) q[j][e] = __fmul2_rn(q[j][e], f[e]);
+            }
+            if (gate != nullptr) {
+                unpack2(ldg16(gate + gate_row * p.cols + c), f);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) q[j][e] = __fmul2_rn(q[j][e], f[e]);
+            }
+        }
+    };
+    gate_in();
+    int64_t gate_end = WHOLE ? (gate_row + 1) * p.per_gate : 0;   // first row past the current gate row
+    // a gate row ends: its gradient, and its share of dw_post
+    auto flush = [&]() {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (!live[j]) continue;
+            const int64_t c = static_cast<int64_t>(j * nt + tt) * VEC;
+            float2 g[NP], w[NP];
+            unpack2(ldg16(gate + gate_row * p.cols + c), g);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) w[e] = make_float2(1.f, 1.f);
+            if (post) unpack2(ldg16(wp + c), w);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const float2 bs = __fmul2_rn(make_float2(p.b, p.b), S[j][e]);
+                Sp[WHOLE ? j : 0][e] = __ffma2_rn(g[e], bs, Sp[WHOLE ? j : 0][e]);
+                w[e] = __fmul2_rn(w[e], bs);
+                S[j][e] = zero2;
+            }
+            stg16(static_cast<T*>(p.dgate) + gate_row * p.cols + c, pack2(w));
+        }
+    };
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    int s = 0, turn = 0;
+    uint32_t ph = 0;
+    int64_t t = t0;
+    bool ok = true;
+    // the next row's scales, fetched a row ahead
+    float rzn = post && t < t1 ? p.rstd_z[t] : 1.f, rhn = pre && t < t1 ? p.rstd_h[t] : 0.f;
+    for (; t < t1; t += teams) {
+        const float rz = rzn, rh = rhn;
+        const bool more = t + teams < t1;
+        rzn = post && more ? p.rstd_z[t + teams] : 1.f;
+        rhn = pre && more ? p.rstd_h[t + teams] : 0.f;
+        if (WHOLE && t >= gate_end) {
+            flush();
+            ++gate_row;
+            gate_end += p.per_gate;
+            gate_in();
+        }
+        ok = mbar_wait(bars + 8u * s, ph);
+        const uint8_t* slot = ring + static_cast<size_t>(s) * slot_bytes;
+        uint4 cd[VPT], cy[VPT], ch[VPT], cz[VPT];
+        float2 a1 = zero2, a2 = zero2, a3 = zero2;
+        const float2 rh2 = make_float2(rh, rh), rz2 = make_float2(rz, rz);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const size_t at = static_cast<size_t>(j * nt + tt) * 16;
+            cd[j] = cy[j] = ch[j] = cz[j] = make_uint4(0, 0, 0, 0);
+            if (live[j] && ok) {
+                if (has_dh) cd[j] = *reinterpret_cast<const uint4*>(slot + o_dh + at);
+                if (pre) cy[j] = *reinterpret_cast<const uint4*>(slot + o_dy + at);
+                if (pre) ch[j] = *reinterpret_cast<const uint4*>(slot + o_h + at);
+                if (need_z) cz[j] = *reinterpret_cast<const uint4*>(slot + o_z + at);
+            }
+            float2 fd[NP], fy[NP], fh[NP], fz[NP];
+            unpack2(cd[j], fd);
+            unpack2(cy[j], fy);
+            unpack2(ch[j], fh);
+            unpack2(cz[j], fz);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const float2 yh = __fmul2_rn(fy[e], fh[e]);
+                a1 = __ffma2_rn(wf[j][e], yh, a1);
+                Sn[j][e] = __ffma2_rn(yh, rh2, Sn[j][e]);
+                const float2 v = __ffma2_rn(rh2, __fmul2_rn(fy[e], wf[j][e]), fd[e]);
+                const float2 qz = __fmul2_rn(q[j][e], fz[e]);
+                a2 = __ffma2_rn(v, qz, a2);
+                a3 = __ffma2_rn(fh[e], qz, a3);
+            }
+        }
+        float sums[3] = {a1.x + a1.y, a2.x + a2.y, a3.x + a3.y};
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) sums[k] += __shfl_xor_sync(0xffffffffu, sums[k], o);
+        const int at = ONE ? 0 : team * ((tw + 3) & ~3);
+        if (!ONE && tw == 1) {
+            ok = __all_sync(0xffffffffu, ok);
+        } else {
+            if (lane == 0)
+#pragma unroll
+                for (int k = 0; k < 3; ++k) red[turn][k][at + wt] = sums[k];
+            if (ONE) {
+                ok = __syncthreads_and(ok ? 1 : 0) != 0;
+            } else {
+                uint32_t all;
+                asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 q, %3, 0;\n\t"
+                "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(all)
+                : "r"(team + 1), "r"(nt), "r"(ok ? 1u : 0u)
+                : "memory");
+                ok = all != 0;
+            }
+        }
+        if (!ok) break;
+        if (ONE || tw > 1) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {   // entries past the team's warps hold 0
+                const float4* r4 = reinterpret_cast<const float4*>(red[turn][k] + at);
+                float a = 0.f;
+#pragma unroll
+                for (int w = 0; w < (NT / 32 + 3) / 4; ++w)
+                    if (ONE || w * 4 < tw) {
+                        const float4 f = r4[w];
+                        a += (f.x + f.y) + (f.z + f.w);
+                    }
+                sums[k] = a;
+            }
+            turn ^= 1;   // this buffer is written again only after the next barrier
+        }
+        if (tt == 0 && t + static_cast<int64_t>(nst) * teams < t1) {   // every thread of the team has the row's values
+            fence_proxy_async_smem();
+            issue(t + static_cast<int64_t>(nst) * teams, s);
+        }
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+        const float c1 = rh * rh * rh * inv * sums[0];
+        const float c2 = post ? rz * rz * rz * inv * (sums[1] - c1 * sums[2]) : 0.f;
+        const float2 nc1 = make_float2(-c1, -c1), nc2 = make_float2(-c2, -c2), ra = make_float2(p.a, p.a);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (!live[j]) continue;
+            float2 fd[NP], fy[NP], fh[NP], fz[NP], od[NP], oz[NP];
+            unpack2(cd[j], fd);
+            unpack2(cy[j], fy);
+            unpack2(ch[j], fh);
+            unpack2(cz[j], fz);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                float2 D = __ffma2_rn(rh2, __fmul2_rn(fy[e], wf[j][e]), fd[e]);
+                D = __ffma2_rn(nc1, fh[e], D);
+                od[e] = __fmul2_rn(ra, D);
+                const float2 Dr = __fmul2_rn(D, rz2);
+                oz[e] = __ffma2_rn(nc2, fz[e], __fmul2_rn(q[j][e], Dr));
+                S[j][e] = __ffma2_rn(Dr, fz[e], S[j][e]);
+            }
+            const int64_t at = t * p.cols + static_cast<int64_t>(j * nt + tt) * VEC;
+            stg16_cs(static_cast<T*>(p.dr) + at, pack2(od));
+            stg16_cs(static_cast<T*>(p.dz) + at, pack2(oz));
+        }
+    }
+    float* ps = p.part_s != nullptr ? p.part_s + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    float* pp = p.part_pre != nullptr ? p.part_pre + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    if (!ok) {
+        if (tt == 0) {
+            failed = 1;
+            atomicExch(err, 1);
+            // the team's copies in flight: rows t, t + teams, ..., the first in slot s
+            int64_t row = t;
+            for (int i = 0; i < nst && row < t1; ++i, row += teams) {
+                mbar_wait(bars + 8u * s, ph);
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        for (int64_t row = t; row < t1; row += teams)
+            for (int v = tt; v < nvec; v += nt) {
+                stg16(static_cast<T*>(p.dr) + row * p.cols + static_cast<int64_t>(v) * VEC, nan16<T>());
+                stg16(static_cast<T*>(p.dz) + row * p.cols + static_cast<int64_t>(v) * VEC, nan16<T>());
+            }
+        if (WHOLE)
+            for (int64_t gi = gate_row; gi * p.per_gate < t1; ++gi)
+                for (int v = tt; v < nvec; v += nt)
+                    stg16(static_cast<T*>(p.dgate) + gi * p.cols + static_cast<int64_t>(v) * VEC, nan16<T>());
+    } else if (WHOLE) {
+        flush();
+    }
+    // the block's partial rows: the teams' sums in the order of the teams, through the ring's memory
+    // once no copy is in flight (every team has waited for all its rows, or for its copies above)
+    __syncthreads();
+    const bool bad = failed != 0;
+    float2* acc = reinterpret_cast<float2*>(sm);   // per column vector: NP of S, NP of Sn
+    for (int k = 0; k < teams; ++k) {
+        if (team == k) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (!live[j]) continue;
+                const int v = j * nt + tt;
+                const int64_t c = static_cast<int64_t>(v) * VEC;
+                float2 s2[NP], n2[NP];
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    s2[e] = WHOLE ? Sp[WHOLE ? j : 0][e] : S[j][e];
+                    n2[e] = Sn[j][e];
+                    if (k > 0) {
+                        s2[e] = __fadd2_rn(acc[v * 2 * NP + e], s2[e]);
+                        n2[e] = __fadd2_rn(acc[v * 2 * NP + NP + e], n2[e]);
+                    }
+                    if (k + 1 < teams) {
+                        acc[v * 2 * NP + e] = s2[e];
+                        acc[v * 2 * NP + NP + e] = n2[e];
+                    }
+                }
+                if (k + 1 == teams) {
+#pragma unroll
+                    for (int e = 0; e < NP; e += 2) {
+                        const float2 so[2] = {s2[e], s2[e + 1]}, no[2] = {n2[e], n2[e + 1]};
+                        if (ps != nullptr) stg16(ps + c + 2 * e, bad ? nan16<float>() : pack2(so));
+                        if (pp != nullptr) stg16(pp + c + 2 * e, bad ? nan16<float>() : pack2(no));
+                    }
+                }
+            }
+        }
+        if (k + 1 < teams) __syncthreads();
     }
 }
 
@@ -267,8 +959,102 @@ int launch_sums(const SumP& s, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ launches
+// Resident blocks per SM of a kernel, asked once per device.
+template <typename K>
+int resident(K kern, int threads, size_t smem, std::atomic<int> (&cache)[64]) {
+    int dev = 0;
+    const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+    int n = known ? cache[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) n = 1;
+        if (known) cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <typename T, int VEC, int VPT>
+int launch_fwd_team(const FwdP& p, int tw, cudaStream_t st) {
+    static std::atomic<int> cache[17][64];   // per team width: the block's threads follow from it
+    const int teams = std::max(1, 8 / tw), threads = teams * tw * 32;
+    auto k = block_norm_fwd_team<T, VEC, VPT>;
+    const int64_t grid = std::min<int64_t>(ceil_div(p.rows, teams), static_cast<int64_t>(sm_count()) * resident(k, threads, 0, cache[tw]));
+    k<<<static_cast<unsigned>(grid), threads, 0, st>>>(p, tw);
+    return check_launch("block_norm_fwd_team");
+}
+
+template <typename T, int VPT, int GATE, int NT, int MB, int ONE>
+int launch_fwd_ring(const FwdP& p, int tw, cudaStream_t st) {
+    // per device: shared memory allowed, resident blocks per SM by (team width, ring) as last asked
+    const int teams = std::max(1, NT / 32 / tw), threads = teams * tw * 32;
+    const size_t slot = static_cast<size_t>(teams) * (2 * static_cast<size_t>(p.cols) * sizeof(T) + 8);
+    auto k = block_norm_fwd_ring<T, VPT, GATE, NT, MB, ONE>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(3 * slot)) != cudaSuccess)
+        return check_launch("block_norm_fwd_ring attribute");
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 2 * slot);
+    per_sm = std::max(1, per_sm);
+    // Two slots where that holds about 52 KB of rows on an SM, else three: less in flight leaves the
+    // memory idle, and more was slower (4096 bf16 columns: 64 KB 0.94 of the copy rate, 96 KB 0.84;
+    // 3000: 48 KB 0.90, 72 KB 0.96).
+    const int nst = per_sm * 2 * slot >= 52 * 1024 ? 2 : 3;
+    if (nst == 3) {
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 3 * slot);
+        per_sm = std::max(1, per_sm);
+    }
+    const int64_t grid = std::min<int64_t>(ceil_div(p.rows, teams), static_cast<int64_t>(sm_count()) * per_sm);
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    k<<<static_cast<unsigned>(grid), threads, nst * slot, st>>>(p, tw, nst, err);
+    return check_launch("block_norm_fwd_ring");
+}
+
+template <typename T, int VPT, int NT, int MB, int ONE>
+int launch_fwd_ring(const FwdP& p, int tw, cudaStream_t st) {
+    if (p.gate == nullptr) return launch_fwd_ring<T, VPT, 0, NT, MB, ONE>(p, tw, st);
+    if (p.per_gate == p.rows) return launch_fwd_ring<T, VPT, 1, NT, MB, ONE>(p, tw, st);
+    return launch_fwd_ring<T, VPT, 2, NT, MB, ONE>(p, tw, st);
+}
+
+template <typename T, int VPT, int NT, int MB>
+int launch_fwd_ring(const FwdP& p, int nvec, cudaStream_t st) {
+    const int tw = static_cast<int>(ceil_div(nvec, 32 * VPT));
+    if (NT / 32 / tw > 1) return launch_fwd_ring<T, VPT, NT, MB, 0>(p, tw, st);
+    return launch_fwd_ring<T, VPT, NT, MB, 1>(p, tw, st);
+}
+
+// Which kernel: by the row's 16-byte vectors, and whether there are rows enough that a team takes
+// several.  Fractions of the measured copy rate with many rows, bf16 unless said:
+//   ring, 1 vector a thread  256 columns 0.92, 512 0.94, 1024 0.94, 2048 0.91 (2 vectors: 0.87 and less)
+//         2 vectors          1536 columns 0.93, 320 0.84 (1 vector, two half-empty warps a row: 0.60),
+//                            4096 0.94, fp32 1024 0.94, fp32 4096 (512 threads) 0.97
+//         2, 384 threads     5120 0.90, 6144 0.93
+//         4 vectors          7168 1.00, 8192 0.96 (2 vectors, 512 threads: 0.96, 0.94), 16384 0.76
+//   registers               0.67 to 0.87 over the same widths; first to finish when a team has one row
 template <typename T>
 int launch_fwd(const FwdP& p, cudaStream_t st) {
+    constexpr int EPV = Vec<T>::N;
+    constexpr bool F32 = sizeof(T) == 4;
+    if (p.cols % EPV == 0) {
+        const int nvec = p.cols / EPV;
+        const int64_t few = static_cast<int64_t>(sm_count()) * std::max(1, 512 / std::max(nvec, 32));
+        if (p.rows <= few && nvec <= 512) return launch_fwd_team<T, EPV, 1>(p, (nvec + 31) / 32, st);
+        if (p.rows > few) {
+            const bool whole = nvec % 32 == 0 && 8 % (nvec / 32) == 0;   // one vector a thread fills the block's warps
+            if (nvec <= 32 || (!F32 && nvec <= 256 && whole)) return launch_fwd_ring<T, 1, 256, 2>(p, nvec, st);
+            if (nvec <= 512) return launch_fwd_ring<T, 2, 256, 2>(p, nvec, st);
+            if (nvec <= 768) return launch_fwd_ring<T, 2, 384, 2>(p, nvec, st);
+            if (nvec <= 1024 && F32) return launch_fwd_ring<T, 2, 512, 1>(p, nvec, st);
+            if (nvec <= 1024) return launch_fwd_ring<T, 4, 256, 1>(p, nvec, st);
+            if (nvec <= 1536) return launch_fwd_ring<T, 4, 384, 1>(p, nvec, st);
+            if (nvec <= 2048) return launch_fwd_ring<T, 4, 512, 1>(p, nvec, st);
+        }
+        if (nvec <= 1024) return launch_fwd_team<T, EPV, 2>(p, (nvec + 63) / 64, st);
+        if (nvec <= 2048) return launch_fwd_team<T, EPV, 4>(p, (nvec + 127) / 128, st);
+    } else {
+        if (p.cols <= 128) return launch_fwd_team<T, 1, 4>(p, 1, st);
+        if (p.cols <= 2048) return launch_fwd_team<T, 1, 4>(p, (p.cols + 127) / 128, st);
+        if (p.cols <= 4096) return launch_fwd_team<T, 1, 8>(p, (p.cols + 255) / 256, st);
+    }
     const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(sm_count()) * 8);
     block_norm_fwd_generic<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
     return check_launch("block_norm_fwd");
@@ -291,15 +1077,69 @@ int64_t split_rows(BwdP& p, int64_t want) {
     return ceil_div(p.gates, p.gates_per_block);
 }
 
+// The ring kernel for rows of nvec vectors, `slot` bytes a row of all streams; grid: the partial rows written.
+template <typename T, int VPT, int WHOLE, int NT, int ONE>
+int launch_bwd_ring(const BwdP& p, int nvec, size_t slot, int64_t grid, int teams, int per_sm, cudaStream_t st) {
+    const int tw = static_cast<int>(ceil_div(nvec, 32 * VPT));
+    auto k = block_norm_bwd_ring<T, VPT, WHOLE, NT, ONE>;
+    // about 128 KB of rows in flight on an SM (4096 bf16 columns, 32 KB a row, 1 vector a thread: 3 slots
+    // 0.96 of the copy rate, 4 0.97, 8 0.91); one slot if no more fit (the copy of the next row then overlaps the second
+    // half of a row's work only)
+    size_t nst = std::max<size_t>(1, std::min<size_t>(8, (128u * 1024u) / (per_sm * teams * slot)));
+    if (nst == 1 && 2 * teams * slot <= 220u * 1024u) nst = 2;
+    // the sums of the teams go through the ring's memory at the end: 16 bytes a vector and element pair
+    const size_t sums = teams > 1 ? static_cast<size_t>(nvec) * Vec<T>::N * 8 : 0;
+    const size_t smem = std::max(teams * nst * (slot + 8), sums);
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return check_launch("block_norm_bwd_ring attribute");
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    k<<<static_cast<unsigned>(grid), teams * tw * 32, smem, st>>>(p, tw, static_cast<int>(nst), err);
+    return check_launch("block_norm_bwd_ring");
+}
+
+// Splits the rows and launches: 256 threads' worth of teams where a row takes less.
+template <typename T, int VPT, int NT>
+int launch_bwd_ring(BwdP& p, int nvec, size_t slot, int64_t& grid, cudaStream_t st) {
+    const int tw = static_cast<int>(ceil_div(nvec, 32 * VPT));
+    const int teams = std::max(1, 8 / tw);
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block_norm_bwd_ring<T, VPT, 0, NT, 0>, teams * tw * 32, teams * slot);
+    per_sm = std::max(1, per_sm);
+    grid = split_rows(p, static_cast<int64_t>(sm_count()) * per_sm);
+    if (p.splits == 0) return launch_bwd_ring<T, VPT, 1, NT, 1>(p, nvec, slot, grid, 1, per_sm, st);
+    if (teams == 1) return launch_bwd_ring<T, VPT, 0, NT, 1>(p, nvec, slot, grid, 1, per_sm, st);
+    return launch_bwd_ring<T, VPT, 0, NT, 0>(p, nvec, slot, grid, teams, per_sm, st);
+}
+
 template <typename T>
 int launch_bwd(BwdP p, void* dw_post, void* dw_pre, float* ws, cudaStream_t st) {
-    const int64_t grid = split_rows(p, static_cast<int64_t>(sm_count()) * 4);
-    const int64_t room = std::min<int64_t>(p.rows, kMaxParts) * p.cols;
+    constexpr int EPV = Vec<T>::N;
     const bool need_s = p.w_post != nullptr || p.gate != nullptr;
+    const int64_t room = std::min<int64_t>(p.rows, kMaxParts) * p.cols;
     p.part_pre = p.w_pre != nullptr ? ws : nullptr;
     p.part_s = need_s ? ws + room : nullptr;
-    block_norm_bwd_generic<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
-    if (int rc = check_launch("block_norm_bwd")) return rc;
+    int64_t grid = 0;
+    const int streams = (p.dh != nullptr ? 1 : 0) + (p.w_pre != nullptr ? 2 : 0) + (need_s ? 1 : 0);
+    const size_t slot = static_cast<size_t>(streams) * p.cols * sizeof(T);
+    const int nvec = p.cols % EPV == 0 ? p.cols / EPV : 0;
+    int rc;
+    constexpr bool F32 = sizeof(T) == 4;
+    // By the row's 16-byte vectors; fractions of the measured copy rate with many rows, bf16 unless said:
+    // 1 a thread 2048 columns 0.93 (2: 0.87), 1024 0.89, 512 0.90, 256 0.86; 2 a thread 4096 0.97
+    // (1, 512 threads: 0.90 to 0.93), 5120 0.95, fp32 4096 0.94, fp32 1024 0.90 (1: 0.84); 4 a thread 8192
+    // 0.96, fp32 8192 0.94, 16384 0.42 (its sums spill).
+    if (nvec == 0 || nvec > 2048 || slot > 200u * 1024u) {
+        grid = split_rows(p, static_cast<int64_t>(sm_count()) * 4);
+        block_norm_bwd_generic<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
+        rc = check_launch("block_norm_bwd");
+    } else if (!F32 && nvec <= 256) rc = launch_bwd_ring<T, 1, 256>(p, nvec, slot, grid, st);
+    else if (nvec <= 512) rc = launch_bwd_ring<T, 2, 256>(p, nvec, slot, grid, st);
+    else if (nvec <= 768) rc = launch_bwd_ring<T, 2, 384>(p, nvec, slot, grid, st);
+    else if (F32 && nvec <= 1024) rc = launch_bwd_ring<T, 2, 512>(p, nvec, slot, grid, st);
+    else if (nvec <= 1024) rc = launch_bwd_ring<T, 4, 256>(p, nvec, slot, grid, st);
+    else rc = launch_bwd_ring<T, 4, 512>(p, nvec, slot, grid, st);
+    if (rc) return rc;
     const SumP s{p.part_s, p.part_pre, p.w_post, p.gate, dw_post, p.gate != nullptr ? p.dgate : nullptr, dw_pre, grid,
                  p.gates, p.splits, p.cols, p.b};
     return launch_sums<T>(s, st);
