@@ -170,9 +170,9 @@ int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* lab
  *   clipped tokens over the valid tokens; logp: float [T] or NULL, 0 at tokens
  *   that are not valid; dX [T, H], dW [V, H] in dtype, each may be NULL.  Rows
  *   of dX of tokens that are not valid are written as +0.
- *   Token chunks, the GEMM path by dtype and shape and chunk are as in
- *   liger_linear_ce_fwd_bwd: per chunk the logits exist only in a [chunk x V]
- *   workspace buffer.  ws: at least liger_linear_policy_workspace bytes,
+ *   Token chunks and the GEMM path by dtype and shape are as in
+ *   liger_linear_ce_fwd_bwd, but chunk 0 is min(T, 8192) on the tensor-core
+ *   path: per chunk the logits exist only in a [chunk x V] workspace buffer.  ws: at least liger_linear_policy_workspace bytes,
  *   256-byte aligned.
  *   The call waits for a scan of the labels and sequences: a bad label returns
  *   LIGER_ERR_LABEL, bad cu_seqlens LIGER_ERR_SHAPE, with nothing else queued,

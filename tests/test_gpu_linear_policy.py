@@ -251,7 +251,9 @@ def test_non_finite_inputs_reach_the_loss(L):
 
 @pytest.mark.parametrize("wait", [True, False])
 @pytest.mark.parametrize("T,H,V,dt", [(1, 64, 256, "bf16"), (1, 512, 5000, "bf16"), (300, 320, 2037, "bf16"), (77, 40, 300, "bf16"),
-                                      (65, 33, 100, "f32"), (1, 3, 2, "f32"), (9000, 64, 300, "bf16")])
+                                      (65, 33, 100, "f32"), (1, 3, 2, "f32"), (9000, 64, 300, "bf16"),
+                                      (2, 128, 300, "bf16"), (3, 72, 1003, "bf16"), (4, 4096, 5001, "bf16"), (5, 256, 257, "bf16"),
+                                      (8, 520, 70001, "bf16"), (9, 520, 2000, "bf16"), (6, 16384, 300, "bf16")])
 def test_logp(L, T, H, V, dt, wait):
     for masked in (0.0, 0.4, 2.0):
         i = _inputs(T, H, V, dt, [0, T], seed=T, masked=masked)

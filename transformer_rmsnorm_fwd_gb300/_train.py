@@ -12,7 +12,7 @@ import os
 import re
 
 from . import _native
-from ._native import _F, _I64, _INT, _P, _SZ, LIGER_BF16, LIGER_F32, _check, _ptr, _stream
+from ._native import _F, _I64, _INT, _P, _SZ, LIGER_BF16, LIGER_F32, _check, _ptr
 
 HEADER = os.path.join(os.path.dirname(_native.PKG), "include", "liger_train.h")
 
@@ -34,6 +34,7 @@ SIGNATURES = {
 }
 
 _loaded = None
+torch = None        # imported with the library, on the first call
 
 
 def header_functions() -> list:
@@ -44,65 +45,79 @@ def header_functions() -> list:
 
 
 def _lib():
-    global _loaded
+    global _loaded, torch
     if _loaded is None:
+        import torch as t
         lib = _native.load()
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
+        torch = t
         _loaded = lib
     return _loaded
 
 
-def _code(t):
-    import torch
-    if t.dtype is torch.bfloat16:
+def _code(dtype):
+    if dtype is torch.bfloat16:
         return LIGER_BF16
-    if t.dtype is torch.float32:
+    if dtype is torch.float32:
         return LIGER_F32
-    raise TypeError(f"unsupported dtype {t.dtype}: float32 or bfloat16")
+    raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
 
 
-def _same(ref, shape, **named):
-    """The tensors that are given are contiguous, on the current device, of ref's dtype and of this shape."""
-    for name, t in named.items():
-        if t is not None:
-            _one(name, t, ref.dtype, shape)
-
-
-def _one(name, t, dtype, shape):
-    import torch
-    if not t.is_cuda or not t.is_contiguous() or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on the current device")
+def _raise(dev, dtype, shape, t):
+    """Says what is wrong with a tensor that a check below did not let pass."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"tensors must be contiguous CUDA tensors on the current device (got one on {t.device}, "
+                         f"strides {tuple(t.stride())})")
     if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+    raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _bytes(ws):
+# The checks are written for calls of a few microseconds: one pass over the attributes, and words only on failure.
+def _like(dev, dtype, shape, *ts):
+    """Those of the tensors that are given are contiguous, on device dev, of this dtype and shape."""
+    for t in ts:
+        if t is not None and (t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+            _raise(dev, dtype, shape, t)
+
+
+def _hold(dev, dtype, n, *ts):
+    """As _like, for any shape of n elements."""
+    for t in ts:
+        if t is not None and (t.get_device() != dev or t.dtype is not dtype or t.numel() != n or not t.is_contiguous()):
+            _raise(dev, dtype, (n,), t)
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _bytes(dev, ws):
     """Pointer and size of a workspace tensor (or None)."""
     if ws is None:
         return None, 0
-    _one("ws", ws, ws.dtype, None)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _raise(dev, ws.dtype, ws.shape, ws)
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 # -------------------------------------------------------------- block norms
-def _norm_shapes(z, gate):
-    shape = tuple(z.shape)
+def _norm_sizes(dev, ref, gate, w_post, w_pre):
+    """shape, rows, cols, gates of the rows `ref` and its checked weights and gate."""
+    shape = ref.shape
     cols = shape[-1]
-    rows = z.numel() // cols if cols else 0
-    gates = 0 if gate is None else gate.numel() // cols if cols else 0
-    return shape, rows, cols, gates
-
-
-def _gate(gate, ref, cols, gates):
+    rows = ref.numel() // cols if cols else 0
+    _like(dev, ref.dtype, shape[-1:], w_post, w_pre)
+    gates = 0
     if gate is not None:
-        _one("gate", gate, ref.dtype, None)
-        if gates < 1 or gate.shape[-1] != cols or gate.dim() > 2:
+        if gate.dim() not in (1, 2) or gate.shape[-1] != cols or gate.numel() == 0:
             raise ValueError(f"gate must be [cols] or [gates, cols] with cols = {cols}, not {tuple(gate.shape)}")
+        _like(dev, ref.dtype, gate.shape, gate)
+        gates = gate.numel() // cols
+    return shape, rows, cols, gates
 
 
 def liger_block_norm_fwd(z, r, h, y=None, w_post=None, gate=None, w_pre=None, rstd_z=None, rstd_h=None,
@@ -111,24 +126,15 @@ def liger_block_norm_fwd(z, r, h, y=None, w_post=None, gate=None, w_pre=None, rs
 
     z, r, h, y [..., cols]; w_post, w_pre [cols] or None; gate None, [cols] or [gates, cols] (gate row i for the i-th
     run of rows / gates rows); rstd_z, rstd_h float32, one per row, or None.  h may be r, and y may be z."""
-    shape, rows, cols, gates = _norm_shapes(z, gate)
-    _same(z, shape, z=z, r=r, h=h, y=y)
-    _same(z, (cols,), w_post=w_post, w_pre=w_pre)
-    _gate(gate, z, cols, gates)
-    _rows(rows, rstd_z=rstd_z, rstd_h=rstd_h)
-    _check(_lib().liger_block_norm_fwd(_ptr(z), _ptr(r), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(h), _ptr(y),
-                                       _ptr(rstd_z), _ptr(rstd_h), rows, cols, gates, res_scale, block_scale, eps,
-                                       _code(z), _stream()))
+    lib = _loaded or _lib()
+    dev, dt = torch.cuda.current_device(), z.dtype
+    shape, rows, cols, gates = _norm_sizes(dev, z, gate, w_post, w_pre)
+    _like(dev, dt, shape, z, r, h, y)
+    _hold(dev, torch.float32, rows, rstd_z, rstd_h)
+    _check(lib.liger_block_norm_fwd(_ptr(z), _ptr(r), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(h), _ptr(y),
+                                    _ptr(rstd_z), _ptr(rstd_h), rows, cols, gates, res_scale, block_scale, eps, _code(dt),
+                                    _raw_stream(dev)))
     return h, y
-
-
-def _rows(rows, **named):
-    import torch
-    for name, t in named.items():
-        if t is not None:
-            _one(name, t, torch.float32, None)
-            if t.numel() != rows:
-                raise ValueError(f"{name} must hold {rows} values, not {t.numel()}")
 
 
 def liger_block_norm_bwd_workspace(rows: int, cols: int, gates: int = 0) -> int:
@@ -139,18 +145,19 @@ def liger_block_norm_bwd(dh, dy, z, h, dr, dz, ws, w_post=None, gate=None, w_pre
                          dw_post=None, dgate=None, dw_pre=None, res_scale: float = 1.0, block_scale: float = 1.0):
     """Backward of liger_block_norm_fwd (see liger_train.h): dh or None, and dy, give dr, dz and the gradients of the
     weights and of the gate that the forward had.  dr may be dh, and dz may be dy."""
-    shape, rows, cols, gates = _norm_shapes(dr, gate)
-    _same(dr, shape, dh=dh, dy=dy, z=z, h=h, dr=dr, dz=dz)
-    _same(dr, (cols,), w_post=w_post, w_pre=w_pre, dw_post=dw_post, dw_pre=dw_pre)
-    _gate(gate, dr, cols, gates)
-    if dgate is not None:
-        _one("dgate", dgate, dr.dtype, None if gate is None else tuple(gate.shape))
-    _rows(rows, rstd_z=rstd_z, rstd_h=rstd_h)
-    pws, nws = _bytes(ws)
-    _check(_lib().liger_block_norm_bwd(_ptr(dh), _ptr(dy), _ptr(z), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
-                                       _ptr(rstd_z), _ptr(rstd_h), _ptr(dr), _ptr(dz), _ptr(dw_post), _ptr(dgate),
-                                       _ptr(dw_pre), pws, nws, rows, cols, gates, res_scale, block_scale, _code(dr),
-                                       _stream()))
+    lib = _loaded or _lib()
+    dev, dt = torch.cuda.current_device(), dr.dtype
+    shape, rows, cols, gates = _norm_sizes(dev, dr, gate, w_post, w_pre)
+    _like(dev, dt, shape, dh, dy, z, h, dr, dz)
+    _like(dev, dt, shape[-1:], dw_post, dw_pre)
+    if gate is not None:
+        _like(dev, dt, gate.shape, dgate)
+    _hold(dev, torch.float32, rows, rstd_z, rstd_h)
+    pws, nws = _bytes(dev, ws)
+    _check(lib.liger_block_norm_bwd(_ptr(dh), _ptr(dy), _ptr(z), _ptr(h), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+                                    _ptr(rstd_z), _ptr(rstd_h), _ptr(dr), _ptr(dz), _ptr(dw_post), _ptr(dgate),
+                                    _ptr(dw_pre), pws, nws, rows, cols, gates, res_scale, block_scale, _code(dt),
+                                    _raw_stream(dev)))
     return dr, dz
 
 
@@ -161,80 +168,81 @@ CKPT8_GROUP = 32    # columns of a row that share a scale byte
 def liger_ckpt8_empty(rows: int, cols: int, device="cuda"):
     """An empty 8-bit checkpoint of a [rows, cols] tensor: int8 codes [rows, cols] and uint8 scales
     [rows, ceil(cols / 32)]."""
-    import torch
+    _lib()
     return (torch.empty(rows, cols, dtype=torch.int8, device=device),
             torch.empty(rows, -(-cols // CKPT8_GROUP), dtype=torch.uint8, device=device))
 
 
-def _ckpt(rows, cols, *pairs):
-    import torch
-    groups = -(-cols // CKPT8_GROUP)
-    for name, codes, scale in pairs:
-        _one(name + "8", codes, torch.int8, None)
-        _one(name + "_scale", scale, torch.uint8, None)
-        if codes.numel() != rows * cols or scale.numel() != rows * groups:
-            raise ValueError(f"the checkpoint of {name} must hold {rows} x {cols} codes and {rows} x {groups} scales")
+def _ckpt(dev, rows, cols, gate8, gate_scale, up8, up_scale):
+    _hold(dev, torch.int8, rows * cols, gate8, up8)
+    _hold(dev, torch.uint8, rows * -(-cols // CKPT8_GROUP), gate_scale, up_scale)
 
 
 def liger_swiglu_fwd_ckpt8(gate, up, y, gate8, gate_scale, up8, up_scale):
     """y = silu(gate) up, and the 8-bit checkpoints of gate and up (see liger_train.h); gate, up, y [..., cols]."""
-    shape, cols = tuple(gate.shape), gate.shape[-1]
+    lib = _loaded or _lib()
+    dev, dt, shape = torch.cuda.current_device(), gate.dtype, gate.shape
+    cols = shape[-1]
     rows = gate.numel() // cols if cols else 0
-    _same(gate, shape, gate=gate, up=up, y=y)
-    _ckpt(rows, cols, ("gate", gate8, gate_scale), ("up", up8, up_scale))
-    _check(_lib().liger_swiglu_fwd_ckpt8(_ptr(gate), _ptr(up), _ptr(y), _ptr(gate8), _ptr(gate_scale), _ptr(up8),
-                                         _ptr(up_scale), rows, cols, _code(gate), _stream()))
+    _like(dev, dt, shape, gate, up, y)
+    _ckpt(dev, rows, cols, gate8, gate_scale, up8, up_scale)
+    _check(lib.liger_swiglu_fwd_ckpt8(_ptr(gate), _ptr(up), _ptr(y), _ptr(gate8), _ptr(gate_scale), _ptr(up8),
+                                      _ptr(up_scale), rows, cols, _code(dt), _raw_stream(dev)))
     return y
 
 
 def liger_swiglu_bwd_ckpt8(dy, gate8, gate_scale, up8, up_scale, dgate, dup):
     """dgate and dup from dy and the checkpoints that liger_swiglu_fwd_ckpt8 wrote."""
-    shape, cols = tuple(dy.shape), dy.shape[-1]
+    lib = _loaded or _lib()
+    dev, dt, shape = torch.cuda.current_device(), dy.dtype, dy.shape
+    cols = shape[-1]
     rows = dy.numel() // cols if cols else 0
-    _same(dy, shape, dy=dy, dgate=dgate, dup=dup)
-    _ckpt(rows, cols, ("gate", gate8, gate_scale), ("up", up8, up_scale))
-    _check(_lib().liger_swiglu_bwd_ckpt8(_ptr(dy), _ptr(gate8), _ptr(gate_scale), _ptr(up8), _ptr(up_scale), _ptr(dgate),
-                                         _ptr(dup), rows, cols, _code(dy), _stream()))
+    _like(dev, dt, shape, dy, dgate, dup)
+    _ckpt(dev, rows, cols, gate8, gate_scale, up8, up_scale)
+    _check(lib.liger_swiglu_bwd_ckpt8(_ptr(dy), _ptr(gate8), _ptr(gate_scale), _ptr(up8), _ptr(up_scale), _ptr(dgate),
+                                      _ptr(dup), rows, cols, _code(dt), _raw_stream(dev)))
     return dgate, dup
 
 
 def liger_fused_linear_swiglu_fwd_ckpt8(X, Wg, Wu, out, gate8, gate_scale, up8, up_scale):
     """FusedLinearSwiGLU forward that keeps X Wg^T and X Wu^T in 8 bits."""
+    lib = _loaded or _lib()
+    dev, dt = torch.cuda.current_device(), X.dtype
     T, H = X.shape
     I = Wg.shape[0]
-    _same(X, (T, H), X=X)
-    _same(X, (I, H), Wg=Wg, Wu=Wu)
-    _same(X, (T, I), out=out)
-    _ckpt(T, I, ("gate", gate8, gate_scale), ("up", up8, up_scale))
-    _check(_lib().liger_fused_linear_swiglu_fwd_ckpt8(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(out), _ptr(gate8),
-                                                      _ptr(gate_scale), _ptr(up8), _ptr(up_scale), T, H, I, _code(X),
-                                                      _stream()))
+    _like(dev, dt, (T, H), X)
+    _like(dev, dt, (I, H), Wg, Wu)
+    _like(dev, dt, (T, I), out)
+    _ckpt(dev, T, I, gate8, gate_scale, up8, up_scale)
+    _check(lib.liger_fused_linear_swiglu_fwd_ckpt8(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(out), _ptr(gate8), _ptr(gate_scale),
+                                                   _ptr(up8), _ptr(up_scale), T, H, I, _code(dt), _raw_stream(dev)))
     return out
 
 
 def liger_fused_linear_swiglu_bwd_ckpt8(X, Wg, Wu, dH, gate8, gate_scale, up8, up_scale, dX, dWg, dWu, ws):
     """FusedLinearSwiGLU backward from the 8-bit checkpoints; ws as liger_fused_linear_swiglu_workspace says."""
+    lib = _loaded or _lib()
+    dev, dt = torch.cuda.current_device(), X.dtype
     T, H = X.shape
     I = Wg.shape[0]
-    _same(X, (T, H), X=X, dX=dX)
-    _same(X, (I, H), Wg=Wg, Wu=Wu, dWg=dWg, dWu=dWu)
-    _same(X, (T, I), dH=dH)
-    _ckpt(T, I, ("gate", gate8, gate_scale), ("up", up8, up_scale))
-    pws, nws = _bytes(ws)
-    _check(_lib().liger_fused_linear_swiglu_bwd_ckpt8(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(dH), _ptr(gate8),
-                                                      _ptr(gate_scale), _ptr(up8), _ptr(up_scale), _ptr(dX), _ptr(dWg),
-                                                      _ptr(dWu), pws, nws, T, H, I, _code(X), _stream()))
+    _like(dev, dt, (T, H), X, dX)
+    _like(dev, dt, (I, H), Wg, Wu, dWg, dWu)
+    _like(dev, dt, (T, I), dH)
+    _ckpt(dev, T, I, gate8, gate_scale, up8, up_scale)
+    pws, nws = _bytes(dev, ws)
+    _check(lib.liger_fused_linear_swiglu_bwd_ckpt8(_ptr(X), _ptr(Wg), _ptr(Wu), _ptr(dH), _ptr(gate8), _ptr(gate_scale),
+                                                   _ptr(up8), _ptr(up_scale), _ptr(dX), _ptr(dWg), _ptr(dWu), pws, nws, T,
+                                                   H, I, _code(dt), _raw_stream(dev)))
     return dX, dWg, dWu
 
 
 # ------------------------------------------------------- heads: label log-probabilities, policy loss
-def _head(X, W, labels):
-    import torch
+def _head(dev, X, W, labels):
     T, H = X.shape
     V = W.shape[0]
-    _same(X, (T, H), X=X)
-    _same(X, (V, H), W=W)
-    _one("labels", labels, torch.int64, (T,))
+    _like(dev, X.dtype, (T, H), X)
+    _like(dev, X.dtype, (V, H), W)
+    _like(dev, torch.int64, (T,), labels)
     return T, H, V
 
 
@@ -245,11 +253,14 @@ def liger_linear_logp_workspace(T: int, H: int, V: int, dtype: int = LIGER_BF16)
 def liger_linear_logp_fwd(X, W, labels, logp, ws, ignore_index: int = -100, wait: bool = True):
     """logp[t] = log softmax(W x_t)[labels[t]], 0 where the label is ignore_index (see liger_train.h); wait=False calls
     the _async form (no host wait: capturable in a CUDA graph; a bad label's logp is NaN)."""
-    T, H, V = _head(X, W, labels)
-    _rows(T, logp=logp)
-    pws, nws = _bytes(ws)
-    fn = _lib().liger_linear_logp_fwd if wait else _lib().liger_linear_logp_fwd_async
-    _check(fn(_ptr(X), _ptr(W), _ptr(labels), T, H, V, int(ignore_index), _ptr(logp), pws, nws, _code(X), _stream()))
+    lib = _loaded or _lib()
+    dev = torch.cuda.current_device()
+    T, H, V = _head(dev, X, W, labels)
+    _hold(dev, torch.float32, T, logp)
+    pws, nws = _bytes(dev, ws)
+    fn = lib.liger_linear_logp_fwd if wait else lib.liger_linear_logp_fwd_async
+    _check(fn(_ptr(X), _ptr(W), _ptr(labels), T, H, V, ignore_index, _ptr(logp), pws, nws, _code(X.dtype),
+              _raw_stream(dev)))
     return logp
 
 
@@ -270,20 +281,23 @@ def liger_linear_policy_fwd_bwd(X, W, labels, old_logp, adv, loss, dX, dW, ws, r
     labels int64 [T]; old_logp, ref_logp float32 [T]; adv float32, one per sequence ([B]) or, with adv_per_token, one per
     token ([T]); cu_seqlens int32 [B + 1] or None (one sequence); reduction "token_mean", "seq_mean" or "sum"; stats
     float32 [2] or None (mean KL, share of clipped tokens).  wait=False calls the _async form."""
-    import torch
-    T, H, V = _head(X, W, labels)
-    B = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    lib = _loaded or _lib()
+    dev, f32 = torch.cuda.current_device(), torch.float32
+    T, H, V = _head(dev, X, W, labels)
+    B = 1
     if cu_seqlens is not None:
-        _one("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
-    _rows(T, old_logp=old_logp, ref_logp=ref_logp, logp=logp)
-    _rows(T if adv_per_token else B, adv=adv)
-    _rows(1, loss=loss)
-    _rows(2, stats=stats)
-    _same(X, (T, H), dX=dX)
-    _same(X, (V, H), dW=dW)
-    pws, nws = _bytes(ws)
-    fn = _lib().liger_linear_policy_fwd_bwd if wait else _lib().liger_linear_policy_fwd_bwd_async
+        B = cu_seqlens.numel() - 1
+        _like(dev, torch.int32, (B + 1,), cu_seqlens)
+    _hold(dev, f32, T, old_logp, ref_logp, logp)
+    _hold(dev, f32, T if adv_per_token else B, adv)
+    _hold(dev, f32, 1, loss)
+    _hold(dev, f32, 2, stats)
+    _like(dev, X.dtype, (T, H), dX)
+    _like(dev, X.dtype, (V, H), dW)
+    pws, nws = _bytes(dev, ws)
+    fn = lib.liger_linear_policy_fwd_bwd if wait else lib.liger_linear_policy_fwd_bwd_async
     _check(fn(_ptr(X), _ptr(W), _ptr(labels), _ptr(cu_seqlens), _ptr(old_logp), _ptr(ref_logp), _ptr(adv), T, H, V, B,
-              int(ignore_index), _REDUCTION[reduction], 1 if adv_per_token else 0, eps_low, eps_high, beta, grad_scale,
-              _ptr(loss), _ptr(stats), _ptr(logp), _ptr(dX), _ptr(dW), pws, nws, int(chunk), _code(X), _stream()))
+              ignore_index, _REDUCTION[reduction], 1 if adv_per_token else 0, eps_low, eps_high, beta, grad_scale,
+              _ptr(loss), _ptr(stats), _ptr(logp), _ptr(dX), _ptr(dW), pws, nws, chunk, _code(X.dtype),
+              _raw_stream(dev)))
     return loss, dX, dW

@@ -963,6 +963,23 @@ int launch_sums(const SumP& s, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ launches
+// Lets a kernel have as much dynamic shared memory as the device gives, once per device (racing
+// threads set the same value).
+template <auto KERN>
+int allow_smem() {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("block_norm device");
+    if (done[dev].load(std::memory_order_acquire)) return LIGER_OK;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, KERN) != cudaSuccess ||
+        cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             max_smem_optin() - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess)
+        return check_launch("block_norm attribute");
+    done[dev].store(true, std::memory_order_release);
+    return LIGER_OK;
+}
+
 // Resident blocks per SM of a kernel, asked once per device.
 template <typename K>
 int resident(K kern, int threads, size_t smem, std::atomic<int> (&cache)[64]) {
@@ -988,12 +1005,10 @@ int launch_fwd_team(const FwdP& p, int tw, cudaStream_t st) {
 
 template <typename T, int VPT, int GATE, int NT, int MB, int ONE>
 int launch_fwd_ring(const FwdP& p, int tw, cudaStream_t st) {
-    // per device: shared memory allowed, resident blocks per SM by (team width, ring) as last asked
     const int teams = std::max(1, NT / 32 / tw), threads = teams * tw * 32;
     const size_t slot = static_cast<size_t>(teams) * (2 * static_cast<size_t>(p.cols) * sizeof(T) + 8);
-    auto k = block_norm_fwd_ring<T, VPT, GATE, NT, MB, ONE>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(3 * slot)) != cudaSuccess)
-        return check_launch("block_norm_fwd_ring attribute");
+    constexpr auto k = block_norm_fwd_ring<T, VPT, GATE, NT, MB, ONE>;
+    if (int rc = allow_smem<k>()) return rc;
     int per_sm = 0;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 2 * slot);
     per_sm = std::max(1, per_sm);
@@ -1085,7 +1100,7 @@ int64_t split_rows(BwdP& p, int64_t want) {
 template <typename T, int VPT, int WHOLE, int NT, int ONE>
 int launch_bwd_ring(const BwdP& p, int nvec, size_t slot, int64_t grid, int teams, int per_sm, cudaStream_t st) {
     const int tw = static_cast<int>(ceil_div(nvec, 32 * VPT));
-    auto k = block_norm_bwd_ring<T, VPT, WHOLE, NT, ONE>;
+    constexpr auto k = block_norm_bwd_ring<T, VPT, WHOLE, NT, ONE>;
     // about 128 KB of rows in flight on an SM (4096 bf16 columns, 32 KB a row, 1 vector a thread: 3 slots
     // 0.96 of the copy rate, 4 0.97, 8 0.91); one slot if no more fit (the copy of the next row then overlaps the second
     // half of a row's work only)
@@ -1094,8 +1109,7 @@ int launch_bwd_ring(const BwdP& p, int nvec, size_t slot, int64_t grid, int team
     // the sums of the teams go through the ring's memory at the end: 16 bytes a vector and element pair
     const size_t sums = teams > 1 ? static_cast<size_t>(nvec) * Vec<T>::N * 8 : 0;
     const size_t smem = std::max(teams * nst * (slot + 8), sums);
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return check_launch("block_norm_bwd_ring attribute");
+    if (int rc = allow_smem<k>()) return rc;
     int* err = nullptr;
     if (int rc = rmsnorm_err_word(&err)) return rc;
     k<<<static_cast<unsigned>(grid), teams * tw * 32, smem, st>>>(p, tw, static_cast<int>(nst), err);
@@ -1108,6 +1122,7 @@ int launch_bwd_ring(BwdP& p, int nvec, size_t slot, int64_t& grid, cudaStream_t 
     const int tw = static_cast<int>(ceil_div(nvec, 32 * VPT));
     const int teams = std::max(1, 8 / tw);
     int per_sm = 0;
+    if (int rc = allow_smem<block_norm_bwd_ring<T, VPT, 0, NT, 0>>()) return rc;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, block_norm_bwd_ring<T, VPT, 0, NT, 0>, teams * tw * 32, teams * slot);
     per_sm = std::max(1, per_sm);
     grid = split_rows(p, static_cast<int64_t>(sm_count()) * per_sm);

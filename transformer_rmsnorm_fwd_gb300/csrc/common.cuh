@@ -89,6 +89,25 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7]));
 }
 
+// Two products of packed bf16 pairs in fp32: (a.lo b.lo + c.x, a.hi b.hi + c.y), each
+// rounded once (the product of two bf16 values is exact in fp32).  The mixed-precision
+// fma takes the bf16 halves of the packed words as they are, so neither operand is
+// widened to fp32 by separate instructions first.
+__device__ __forceinline__ float2 fma_bf2(uint32_t a, uint32_t b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t"
+        "mov.b32 {al, ah}, %2;\n\t"
+        "mov.b32 {bl, bh}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %4;\n\t"
+        "fma.rn.f32.bf16 %1, ah, bh, %5;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(a), "r"(b), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ uint32_t word(const uint4& u, int e) {
+    return e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w;
+}
+
 // scalar access
 __device__ __forceinline__ float ldf(const float* p) { return *p; }
 __device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat162float(*p); }

@@ -706,14 +706,17 @@ __global__ void __launch_bounds__(1024) policy_final(const float* __restrict__ t
         if ((threadIdx.x & 31) == 0) red[i][threadIdx.x >> 5] = s[i];
     }
     __syncthreads();
-    if (threadIdx.x < 3) {
-        double tot = 0.0;
-        for (int i = 0; i < 32; ++i) tot += red[threadIdx.x][i];
+    if (threadIdx.x < 96) {   // one warp for each sum (fp64 adds are slow: five in a row, not 32)
+        const int i = threadIdx.x >> 5;
+        double tot = red[i][threadIdx.x & 31];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+        if ((threadIdx.x & 31) != 0) return;
         const double n = static_cast<double>(hdr->n_valid);
-        float r = static_cast<float>(threadIdx.x == 0 ? tot : n > 0.0 ? tot / n : 0.0);
+        float r = static_cast<float>(i == 0 ? tot : n > 0.0 ? tot / n : 0.0);
         if (hdr->err != 0 || hdr->bad != 0) r = __int_as_float(0x7fc00000);
-        if (threadIdx.x == 0) *loss = r;
-        else if (stats != nullptr) stats[threadIdx.x - 1] = r;
+        if (i == 0) *loss = r;
+        else if (stats != nullptr) stats[i - 1] = r;
     }
 }
 
@@ -907,14 +910,16 @@ int ensure_sort_attr() {
 // part and p_out set for row 0 of the chunk), in launches over rows_in_l2 rows: each
 // launch sweeps the whole vocabulary over its rows of X (an 8192-row chunk at hidden
 // 4096 takes two launches, reading W twice but each X row once)
+// Rows of X past cl up to x_rows (they are there, and are read, but give no output).
 int launch_logits(const __nv_bfloat16* Xc, int cl, int H, int V, const CUtensorMap& mW_k, const tc::EpiParams& e,
-                  int64_t ldp, int64_t nvt, cudaStream_t st) {
+                  int64_t ldp, int64_t nvt, cudaStream_t st, int64_t x_rows = 0) {
     using namespace tc;
     const int64_t sub = rows_in_l2(H, cl);
     for (int64_t s0 = 0; s0 < cl; s0 += sub) {
         const int sl = static_cast<int>(std::min<int64_t>(sub, cl - s0));
         CUtensorMap mX;
-        if (int rc = make_map(&mX, Xc + s0 * H, H, sl, H, BK, BM)) return rc;   // A (K-major)
+        // A (K-major)
+        if (int rc = make_map(&mX, Xc + s0 * H, H, std::max<int64_t>(sl, x_rows), H, BK, BM)) return rc;
         EpiParams f = e;
         f.M = sl;
         f.labels = e.labels + s0;
@@ -1533,8 +1538,16 @@ struct PolicyLayout {
     size_t seq, n_seq, coef, term, kl, clip, total;
 };
 
+// Tokens per chunk of the policy loss on the tensor-core path when the caller leaves it open: up to
+// 8192 at once, so that a batch of up to that needs no fp32 [V x H] sum of dW across chunks (reading
+// and writing it took 0.6 of 6.9 ms at 4096 x 4096 x 128256) and the dX tiles fill their waves better.
+int64_t policy_chunk(int64_t T, int64_t H, int64_t V, int64_t chunk, int dtype) {
+    return chunk > 0 || !use_tc(H, V, dtype) ? chunk : std::max<int64_t>(1, std::min<int64_t>(T, kAutoChunkTC));
+}
+
 PolicyLayout policy_layout(int64_t T, int64_t H, int64_t V, int64_t B, int64_t chunk, int dtype) {
     PolicyLayout P{};
+    chunk = policy_chunk(T, H, V, chunk, dtype);
     P.L = layout(T, H, V, chunk, dtype);
     size_t o = up256(P.L.tc ? compact_layout(T, H, V, chunk, dtype).total : P.L.total);
     const size_t per_token = up256(sizeof(float) * static_cast<size_t>(std::max<int64_t>(T, 1)));
@@ -1547,6 +1560,9 @@ PolicyLayout policy_layout(int64_t T, int64_t H, int64_t V, int64_t B, int64_t c
     P.total = o;
     return P;
 }
+
+constexpr int64_t kFewParts = 4 * 2048;   // partials of the few-token path
+constexpr int64_t kPadRows = 16;          // rows of X that a GEMM over fewer is given (see run_logp_tc)
 
 // Workspace of the log-probabilities.  Tensor-core path: header, labels, z at the label, the row
 // partials of a chunk; then, for the form that drops ignored tokens, their X rows and index maps.
@@ -1568,11 +1584,117 @@ LogpLayout logp_layout(int64_t T, int64_t H, int64_t V, int dtype) {
     P.hdr = o; o = up256(o + sizeof(Hdr));
     P.labs = o; o = up256(o + sizeof(int64_t) * t);
     P.zlab = o; o = up256(o + sizeof(float) * t);
-    P.part = o; o = up256(o + (P.tc ? sizeof(float2) * static_cast<size_t>(P.C * P.nvt) : 0));
+    // (few tokens: 4 tokens times at most 2048 blocks)
+    P.part = o; o = up256(o + (P.tc ? sizeof(float2) * static_cast<size_t>(std::max<int64_t>(P.C * P.nvt, kFewParts)) : 0));
     P.scr = o; o = up256(o + (P.tc ? 0 : sizeof(float) * static_cast<size_t>(P.C * V)));
-    P.comp = compact_regions(o, 0, T, H, 2);
+    P.comp = compact_regions(o, 0, std::max(T, kPadRows), H, 2);
     P.total = P.tc ? P.comp.total : o;
     return P;
+}
+
+// Logits of at most NT tokens, W read once: the tensor-core GEMM would spend a 256-row tile on
+// them (305 us for one token at 4096 x 128256, where reading W takes 155 us; 158 us here).
+// A warp takes R rows of W at a time, its lanes the rows' 16-byte vectors, 8 loads of a row in
+// flight (4 KB of it side by side: one row at a time 158 us, four rows with two loads each 174), the
+// tokens' vectors from shared memory; products of two bf16 values are exact in fp32.
+// Lane t keeps token t's running maximum and sum of exponentials over the warp's rows; the block
+// writes one (m, s) per token, as the GEMM's epilogue does per tile, and the logit at the label.
+// HBM-bound up to 4 tokens (167 us); 8 are bound by the multiply-adds (322 us).
+template <int NT, int R>
+__global__ void __launch_bounds__(256) logp_few(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
+                                                const int64_t* __restrict__ labels, int n, int H, int V,
+                                                float2* __restrict__ part, int nparts, float* __restrict__ zlab) {
+    extern __shared__ uint4 xs[];   // [NT][H / 8]
+    __shared__ float2 ms[8][NT];
+    const int nv = H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < NT * nv; i += 256)
+        xs[i] = i < n * nv ? ldg16(X + static_cast<int64_t>(i) * 8) : make_uint4(0, 0, 0, 0);
+    const int64_t y = lane < n ? labels[lane] : -1;
+    __syncthreads();
+    float m = -INFINITY, s = 0.f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * R;
+    for (int64_t v0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * R; v0 < V; v0 += step) {
+        const __nv_bfloat16* wr[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) wr[r] = W + min(v0 + r, static_cast<int64_t>(V) - 1) * H;
+        float2 acc[NT][R];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[t][r] = make_float2(0.f, 0.f);
+#pragma unroll 8
+        for (int j = lane; j < nv; j += 32) {
+            uint4 w[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) w[r] = ldg16_cs(wr[r] + static_cast<int64_t>(j) * 8);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint4 x = xs[t * nv + j];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][r] = fma_bf2(word(x, e), word(w[r], e), acc[t][r]);
+            }
+        }
+        float z[R];   // of this lane's token
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float v = warp_sum(acc[t][r].x + acc[t][r].y);
+                if (lane == t) z[r] = v;
+            }
+        if (lane < n) {
+            float top = m;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (v0 + r < V) top = fmaxf(top, z[r]);
+            float add = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (v0 + r < V) {
+                    add += expf(z[r] - top);
+                    if (v0 + r == y) zlab[lane] = z[r];
+                }
+            s = s * expf(m - top) + add;
+            m = top;
+        }
+    }
+    if (lane < NT) ms[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x < n) {
+        float top = -INFINITY, sum = 0.f;
+        for (int w = 0; w < 8; ++w) top = fmaxf(top, ms[w][threadIdx.x].x);
+        for (int w = 0; w < 8; ++w) {
+            const float2 p = ms[w][threadIdx.x];
+            if (p.y > 0.f) sum += p.y * expf(p.x - top);   // a warp without rows has s = 0
+        }
+        part[static_cast<int64_t>(threadIdx.x) * nparts + blockIdx.x] = make_float2(top, sum);
+    }
+}
+
+constexpr int kFewTokens = 4;
+constexpr size_t kFewSmem = 96u * 1024u;   // the tokens' vectors: two blocks per SM
+
+template <int NT, int R>
+int launch_logp_few(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* labs, int n, int H, int V, float2* part,
+                    float* zlab, int64_t most_parts, int& nparts, cudaStream_t st) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("logp_few device");
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(logp_few<NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewSmem)) !=
+            cudaSuccess)
+            return check_launch("logp_few attribute");
+        done[dev].store(true, std::memory_order_release);
+    }
+    const size_t smem = static_cast<size_t>(NT) * H * 2;
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, logp_few<NT, R>, 256, smem);
+    // every block has rows, and no more blocks than the workspace holds partials for
+    nparts = static_cast<int>(std::min<int64_t>({ceil_div(V, 8 * R), static_cast<int64_t>(sm_count()) * std::max(1, per_sm), most_parts}));
+    logp_few<NT, R><<<nparts, 256, smem, st>>>(X, W, labs, n, H, V, part, nparts, zlab);
+    return check_launch("logp_few");
 }
 
 // Reads the header of the scan back and waits for it.
@@ -1600,6 +1722,30 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
     pol.hdr = reinterpret_cast<Hdr*>(w8 + L.hdr);
     float2* part = reinterpret_cast<float2*>(w8 + L.part);
     float* zlab = reinterpret_cast<float*>(w8 + L.zlab);
+    if (n <= kFewTokens && kFewTokens * static_cast<size_t>(H) * 2 <= kFewSmem) {
+        int np = 0;
+        const int nn = static_cast<int>(n);
+        const int64_t most = kFewParts / kFewTokens;
+        rc = nn == 1   ? launch_logp_few<1, 1>(X, W, labs, nn, H, V, part, zlab, most, np, st)
+             : nn == 2 ? launch_logp_few<2, 1>(X, W, labs, nn, H, V, part, zlab, most, np, st)
+                       : launch_logp_few<4, 2>(X, W, labs, nn, H, V, part, zlab, most, np, st);
+        if (rc) return rc;
+        policy_rows_bf16<<<nn, kRowThreads, 0, st>>>(labs, ignore, part, np, zlab, nullptr, 0, V, pol, idx, 0, nullptr);
+        return check_launch("linear_logp rows");
+    }
+    int64_t x_rows = 0;
+    if (n < kPadRows) {
+        // Every CTA reads the same few lines of X at the same time; over one to fifteen rows they sit
+        // in so few L2 slices that this bounds the GEMM (9 tokens 206 us, 10 264 us, 16 181 us at 4096 x
+        // 128256), so X is read among rows of zeros.
+        __nv_bfloat16* pad = reinterpret_cast<__nv_bfloat16*>(w8 + L.comp.dxc);
+        const size_t row = static_cast<size_t>(H) * 2;
+        if (cudaMemsetAsync(pad, 0, kPadRows * row, st) != cudaSuccess ||
+            cudaMemcpyAsync(pad, X, n * row, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+            return check_launch("linear_logp rows of X");
+        X = pad;
+        x_rows = kPadRows;
+    }
     for (int64_t t0 = 0; t0 < n; t0 += L.C) {
         const int cl = static_cast<int>(std::min(L.C, n - t0));
         EpiParams e{};
@@ -1615,7 +1761,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
         e.part = part;
         e.nvt = static_cast<int>(L.nvt);
         e.zlab = zlab + t0;
-        if ((rc = launch_logits(X + t0 * H, cl, H, V, mW_k, e, 0, L.nvt, st))) return rc;
+        if ((rc = launch_logits(X + t0 * H, cl, H, V, mW_k, e, 0, L.nvt, st, x_rows))) return rc;
         policy_rows_bf16<<<cl, kRowThreads, 0, st>>>(labs + t0, ignore, part, static_cast<int>(L.nvt), zlab + t0, nullptr,
                                                      0, V, pol, idx != nullptr ? idx + t0 : nullptr, t0, nullptr);
         if ((rc = check_launch("linear_logp rows"))) return rc;
@@ -1727,6 +1873,7 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
         off(ref_logp, 4) || off(adv, 4) || off(loss, 4) || off(stats, 4) || off(logp, 4))
         return fail(LIGER_ERR_ALIGN, "%s: X, W, dX, dW must be 16-byte aligned, labels 8, the others 4", who);
     const PolicyLayout PL = policy_layout(T, H, V, B, chunk, dtype);
+    chunk = policy_chunk(T, H, V, chunk, dtype);
     if (!ws || ws_bytes < PL.total || (reinterpret_cast<uintptr_t>(ws) & 255))
         return fail(LIGER_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, PL.total,
                     ws_bytes);
