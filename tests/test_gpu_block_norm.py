@@ -57,7 +57,7 @@ def _forward(L, d, a, b, rows, in_place=False):
 
 
 SHAPES = [(1, 1), (1, 4096), (3, 64), (5, 33), (257, 1001), (64, 8192), (7, 520), (300, 4096), (2, 16384), (4, 20000),
-          (1000, 256), (33, 2050)]
+          (1000, 256), (33, 2050), (1, 65), (700, 129), (400, 1023), (301, 3001), (330, 4095), (200, 5003), (160, 8191), (400, 2047)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -176,7 +176,7 @@ def test_backward(L, rows, cols, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,gates", [(12, 3), (1200, 4), (1200, 100), (1500, 750), (2000, 2000), (3000, 1500), (640, 160)])
-@pytest.mark.parametrize("cols", [256, 77])
+@pytest.mark.parametrize("cols", [256, 77, 1500])
 def test_backward_gate_rows(L, rows, gates, cols, dtype):
     """Gate rows shared by many rows (their sums split over blocks), by two, by one."""
     _bwd_case(L, rows, cols, dtype, True, gates, True, 1.0, 0.5)

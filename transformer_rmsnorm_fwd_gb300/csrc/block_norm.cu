@@ -876,6 +876,376 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_ring(BwdP p, int tw, int
     }
 }
 
+// ------------------------------------------- rows that are no whole 16-byte vectors
+// The same rings for rows whose width is no multiple of a vector: rows then start anywhere, so a slot
+// takes the 16-byte aligned window around a row (the bytes of its neighbours in it are not looked at),
+// and threads take single elements from it, EPT fixed columns each.  Memory still moves in
+// bulk copies; the elements cost one shared-memory access each, which is what bounds these kernels.
+// The last row's window may end past the tensor: the copy stops at the last whole 16 bytes, and the
+// elements behind that come by plain loads.
+struct Window {
+    int64_t at;       // first byte of the window
+    uint32_t bytes;   // multiple of 16
+    int shift;        // elements from there to the row's first
+    int tail;         // the row's elements from this one on are not in the window
+};
+template <typename T>
+__device__ __forceinline__ Window window_of(int64_t t, int64_t rows, int cols) {
+    constexpr int SZ = sizeof(T);
+    Window w;
+    const int64_t o = t * cols * SZ, end = o + static_cast<int64_t>(cols) * SZ;
+    w.at = o & ~int64_t{15};
+    w.shift = static_cast<int>((o - w.at) / SZ);
+    int64_t stop = (end + 15) & ~int64_t{15};
+    w.tail = cols;
+    if (t == rows - 1 && stop != end) {
+        stop = end & ~int64_t{15};
+        w.tail = static_cast<int>((stop - o) / SZ);
+    }
+    w.bytes = static_cast<uint32_t>(stop - w.at);
+    return w;
+}
+// bytes a slot needs for one stream
+inline size_t window_max(int cols, size_t sz) { return (static_cast<size_t>(cols) * sz + 15 + 15) & ~static_cast<size_t>(15); }
+
+template <typename T, int EPT, int NT>
+__global__ void __launch_bounds__(NT, 1) block_norm_fwd_odd(FwdP p, int nst, uint32_t wmax, int* err) {
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ float red[2][NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(nst) * 2 * wmax);
+    const T *z = static_cast<const T*>(p.z), *r = static_cast<const T*>(p.r);
+    const T *wp = static_cast<const T*>(p.w_post), *wn = static_cast<const T*>(p.w_pre), *gate = static_cast<const T*>(p.gate);
+    T *h = static_cast<T*>(p.h), *y = static_cast<T*>(p.y);
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    const int64_t step = gridDim.x;
+    int64_t t = blockIdx.x;
+    auto issue = [&](int64_t row, int s) {
+        const Window w = window_of<T>(row, p.rows, p.cols);
+        const uint32_t bar = bars + 8u * s, dst = smem_u32(sm + static_cast<size_t>(s) * 2 * wmax);
+        mbar_expect_tx(bar, 2 * w.bytes);
+        bulk_g2s(dst, static_cast<const uint8_t*>(p.z) + w.at, w.bytes, bar);
+        bulk_g2s(dst + wmax, static_cast<const uint8_t*>(p.r) + w.at, w.bytes, bar);
+    };
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    mbar_init_fence();
+    __syncthreads();
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t + s * step < p.rows) issue(t + s * step, s);
+    float wq[EPT], wy[EPT];
+    auto gate_in = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            wq[j] = 0.f;
+            if (c < p.cols) {
+                wq[j] = p.b;
+                if (wp != nullptr) wq[j] *= ldf(wp + c);
+                if (gate != nullptr) wq[j] *= ldf(gate + row * p.cols + c);
+            }
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) wy[j] = wn != nullptr && j * NT + tid < p.cols ? ldf(wn + j * NT + tid) : 0.f;
+    int64_t gate_row = -1;
+    int turn = 0, s = 0, prev = 0;
+    uint32_t ph = 0;
+    bool ok = true, first = true;
+    auto total = [&]() {
+        float a = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) a += red[turn][w];
+        turn ^= 1;   // written again only after the next barrier
+        return a;
+    };
+    for (; t < p.rows; t += step) {
+        if (gate_row < 0 || (gate != nullptr && t / p.per_gate != gate_row)) {
+            gate_row = t / p.per_gate;
+            gate_in(gate_row);
+        }
+        const Window win = window_of<T>(t, p.rows, p.cols);
+        ok = mbar_wait(bars + 8u * s, ph);
+        const T* zs = reinterpret_cast<const T*>(sm + static_cast<size_t>(s) * 2 * wmax) + win.shift;
+        const T* rs = reinterpret_cast<const T*>(sm + static_cast<size_t>(s) * 2 * wmax + wmax) + win.shift;
+        const int64_t o = t * p.cols;
+        float fz[EPT];
+        float sz = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            fz[j] = 0.f;
+            if (c < p.cols && ok) fz[j] = c < win.tail ? ldf(zs + c) : ldf(z + o + c);
+            sz = fmaf(fz[j], fz[j], sz);
+        }
+        sz = warp_sum(sz);
+        if (lane == 0) red[turn][wid] = sz;
+        ok = __syncthreads_and(ok ? 1 : 0) != 0;
+        if (!ok) break;
+        // every thread is past the row before: its slot's next copy
+        if (tid == 0 && !first && t + (nst - 1) * step < p.rows) {
+            fence_proxy_async_smem();
+            issue(t + (nst - 1) * step, prev);
+        }
+        first = false;
+        const float tz = total();
+        float rz = 1.f;
+        if (wp != nullptr) {
+            rz = inv_sqrt(fmaf(tz, inv, p.eps));
+            if (p.rstd_z != nullptr && tid == 0) p.rstd_z[t] = rz;
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            if (c < p.cols) {
+                const float fr = c < win.tail ? ldf(rs + c) : ldf(r + o + c);
+                fz[j] = fmaf(fz[j] * wq[j], rz, p.a * fr);
+                ss = fmaf(fz[j], fz[j], ss);
+                stf(h + o + c, fz[j]);
+            }
+        }
+        prev = s;
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+        if (wn == nullptr) continue;
+        ss = warp_sum(ss);
+        if (lane == 0) red[turn][wid] = ss;
+        __syncthreads();
+        const float rh = inv_sqrt(fmaf(total(), inv, p.eps));
+        if (p.rstd_h != nullptr && tid == 0) p.rstd_h[t] = rh;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            if (c < p.cols) stf(y + o + c, fz[j] * rh * wy[j]);
+        }
+    }
+    if (ok) return;
+    if (tid == 0) {
+        atomicExch(err, 1);
+        int64_t row = t;   // rows t, t + step, ... are in flight; the slot of the row before t was not filled again
+        for (int i = 0; i + (first ? 0 : 1) < nst && row < p.rows; ++i, row += step) {
+            mbar_wait(bars + 8u * s, ph);
+            if (++s == nst) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    const float nan = __int_as_float(0x7FC00000);
+    for (; t < p.rows; t += step) {
+        for (int c = tid; c < p.cols; c += NT) {
+            stf(h + t * p.cols + c, nan);
+            if (wn != nullptr) stf(y + t * p.cols + c, nan);
+        }
+        if (tid == 0 && wp != nullptr && p.rstd_z != nullptr) p.rstd_z[t] = nan;
+        if (tid == 0 && wn != nullptr && p.rstd_h != nullptr) p.rstd_h[t] = nan;
+    }
+}
+
+template <typename T, int EPT, int WHOLE, int NT>
+__global__ void __launch_bounds__(NT, 1) block_norm_bwd_odd(BwdP p, int nst, uint32_t wmax, int* err) {
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ float red[2][3][NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const T *dh = static_cast<const T*>(p.dh), *dy = static_cast<const T*>(p.dy), *z = static_cast<const T*>(p.z),
+            *h = static_cast<const T*>(p.h);
+    const T *wp = static_cast<const T*>(p.w_post), *wn = static_cast<const T*>(p.w_pre), *gate = static_cast<const T*>(p.gate);
+    const bool post = wp != nullptr, pre = wn != nullptr, need_z = post || gate != nullptr, has_dh = dh != nullptr;
+    uint32_t off = 0;
+    const uint32_t o_dh = off; off += has_dh ? wmax : 0;
+    const uint32_t o_dy = off; off += pre ? wmax : 0;
+    const uint32_t o_h = off; off += pre ? wmax : 0;
+    const uint32_t o_z = off; off += need_z ? wmax : 0;
+    const uint32_t slot_bytes = off;
+    const uint32_t streams = slot_bytes / wmax;
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(nst) * slot_bytes);
+    int64_t t0, t1, unit = 1, gate_row;
+    if (WHOLE) {
+        t0 = blockIdx.x * p.gates_per_block * p.per_gate;
+        t1 = min(p.rows, t0 + p.gates_per_block * p.per_gate);
+        gate_row = blockIdx.x * p.gates_per_block;
+    } else {
+        gate_row = blockIdx.x / p.splits;
+        t0 = gate_row * p.per_gate + (blockIdx.x - gate_row * p.splits);
+        t1 = (gate_row + 1) * p.per_gate;
+        unit = p.splits;
+    }
+    auto issue = [&](int64_t t, int s) {
+        const Window w = window_of<T>(t, p.rows, p.cols);
+        const uint32_t bar = bars + 8u * s, dst = smem_u32(sm + static_cast<size_t>(s) * slot_bytes);
+        mbar_expect_tx(bar, streams * w.bytes);
+        auto copy = [&](uint32_t o, const void* src) { bulk_g2s(dst + o, static_cast<const uint8_t*>(src) + w.at, w.bytes, bar); };
+        if (has_dh) copy(o_dh, p.dh);
+        if (pre) copy(o_dy, p.dy);
+        if (pre) copy(o_h, p.h);
+        if (need_z) copy(o_z, p.z);
+    };
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    mbar_init_fence();
+    __syncthreads();
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t0 + s * unit < t1) issue(t0 + s * unit, s);
+    float q[EPT], wf[EPT], S[EPT], Sn[EPT], Sp[WHOLE ? EPT : 1];
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        S[j] = Sn[j] = 0.f;
+        if (WHOLE) Sp[j] = 0.f;
+        wf[j] = pre && j * NT + tid < p.cols ? ldf(wn + j * NT + tid) : 0.f;
+    }
+    auto gate_in = [&]() {
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            q[j] = 0.f;
+            if (c < p.cols) {
+                q[j] = p.b;
+                if (post) q[j] *= ldf(wp + c);
+                if (gate != nullptr) q[j] *= ldf(gate + gate_row * p.cols + c);
+            }
+        }
+    };
+    gate_in();
+    int64_t gate_end = WHOLE ? (gate_row + 1) * p.per_gate : 0;
+    auto flush = [&]() {   // a gate row ends: its gradient, and its share of dw_post
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            if (c >= p.cols) continue;
+            const float bs = p.b * S[j];
+            Sp[WHOLE ? j : 0] = fmaf(ldf(gate + gate_row * p.cols + c), bs, Sp[WHOLE ? j : 0]);
+            stf(static_cast<T*>(p.dgate) + gate_row * p.cols + c, post ? bs * ldf(wp + c) : bs);
+            S[j] = 0.f;
+        }
+    };
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    int s = 0, prev = 0, turn = 0;
+    uint32_t ph = 0;
+    bool ok = true, first = true;
+    int64_t t = t0;
+    float rzn = post && t < t1 ? p.rstd_z[t] : 1.f, rhn = pre && t < t1 ? p.rstd_h[t] : 0.f;
+    for (; t < t1; t += unit) {
+        const float rz = rzn, rh = rhn;
+        const bool more = t + unit < t1;
+        rzn = post && more ? p.rstd_z[t + unit] : 1.f;
+        rhn = pre && more ? p.rstd_h[t + unit] : 0.f;
+        if (WHOLE && t >= gate_end) {
+            flush();
+            ++gate_row;
+            gate_end += p.per_gate;
+            gate_in();
+        }
+        const Window win = window_of<T>(t, p.rows, p.cols);
+        ok = mbar_wait(bars + 8u * s, ph);
+        const uint8_t* slot = sm + static_cast<size_t>(s) * slot_bytes;
+        const int64_t o = t * p.cols;
+        auto get = [&](uint32_t so, const T* g, int c) {
+            return c < win.tail ? ldf(reinterpret_cast<const T*>(slot + so) + win.shift + c) : ldf(g + o + c);
+        };
+        float a[3] = {0.f, 0.f, 0.f};
+        float v[EPT];   // dh + rh u
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            v[j] = 0.f;
+            if (c >= p.cols || !ok) continue;
+            float fh = 0.f;
+            if (has_dh) v[j] = get(o_dh, dh, c);
+            if (pre) {
+                const float fy = get(o_dy, dy, c);
+                fh = get(o_h, h, c);
+                a[0] = fmaf(wf[j], fy * fh, a[0]);
+                Sn[j] = fmaf(fy * fh, rh, Sn[j]);
+                v[j] = fmaf(rh, fy * wf[j], v[j]);
+            }
+            if (post) {
+                const float qz = q[j] * get(o_z, z, c);
+                a[1] = fmaf(v[j], qz, a[1]);
+                a[2] = fmaf(fh, qz, a[2]);
+            }
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) a[k] += __shfl_xor_sync(0xffffffffu, a[k], i);
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) red[turn][k][wid] = a[k];
+        ok = __syncthreads_and(ok ? 1 : 0) != 0;
+        if (!ok) break;
+        if (tid == 0 && !first && t + (nst - 1) * unit < t1) {   // every thread is past the row before
+            fence_proxy_async_smem();
+            issue(t + (nst - 1) * unit, prev);
+        }
+        first = false;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            a[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < NT / 32; ++w) a[k] += red[turn][k][w];
+        }
+        turn ^= 1;
+        const float c1 = rh * rh * rh * inv * a[0];
+        const float c2 = post ? rz * rz * rz * inv * (a[1] - c1 * a[2]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            if (c >= p.cols) continue;
+            float D = v[j];
+            if (pre) D = fmaf(-c1, get(o_h, h, c), D);
+            // dr may be dh: this thread has read its dh already
+            const float fz = need_z ? get(o_z, z, c) : 0.f;
+            const float Dr = D * rz;
+            stf(static_cast<T*>(p.dr) + o + c, p.a * D);
+            stf(static_cast<T*>(p.dz) + o + c, fmaf(-c2, fz, q[j] * Dr));
+            S[j] = fmaf(Dr, fz, S[j]);
+        }
+        prev = s;
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+    float* ps = p.part_s != nullptr ? p.part_s + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    float* pp = p.part_pre != nullptr ? p.part_pre + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    const float nan = __int_as_float(0x7FC00000);
+    if (!ok) {
+        if (tid == 0) {
+            atomicExch(err, 1);
+            int64_t row = t;
+            for (int i = 0; i + (first ? 0 : 1) < nst && row < t1; ++i, row += unit) {
+                mbar_wait(bars + 8u * s, ph);
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        for (int64_t row = t; row < t1; row += unit)
+            for (int c = tid; c < p.cols; c += NT) {
+                stf(static_cast<T*>(p.dr) + row * p.cols + c, nan);
+                stf(static_cast<T*>(p.dz) + row * p.cols + c, nan);
+            }
+        if (WHOLE)
+            for (int64_t gi = gate_row; gi * p.per_gate < t1; ++gi)
+                for (int c = tid; c < p.cols; c += NT) stf(static_cast<T*>(p.dgate) + gi * p.cols + c, nan);
+    } else if (WHOLE) {
+        flush();
+    }
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        const int c = j * NT + tid;
+        if (c >= p.cols) continue;
+        if (ps != nullptr) ps[c] = ok ? (WHOLE ? Sp[WHOLE ? j : 0] : S[j]) : nan;
+        if (pp != nullptr) pp[c] = ok ? Sn[j] : nan;
+    }
+}
+
 // ---------------------------------------------------- sums over the partial rows
 struct SumP {
     const float *part_s, *part_pre;
@@ -1041,6 +1411,23 @@ int launch_fwd_ring(const FwdP& p, int nvec, cudaStream_t st) {
     return launch_fwd_ring<T, VPT, NT, MB, 1>(p, tw, st);
 }
 
+template <typename T, int EPT, int NT>
+int launch_fwd_odd(const FwdP& p, cudaStream_t st) {
+    constexpr auto k = block_norm_fwd_odd<T, EPT, NT>;
+    if (int rc = allow_smem<k>()) return rc;
+    const size_t wmax = window_max(p.cols, sizeof(T));
+    int nst = 4;   // one row in use, three in flight
+    while (nst > 2 && nst * (2 * wmax + 8) > 200u * 1024u) --nst;
+    const size_t smem = nst * (2 * wmax + 8);
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, NT, smem);
+    const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm));
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    k<<<static_cast<unsigned>(grid), NT, smem, st>>>(p, nst, static_cast<uint32_t>(wmax), err);
+    return check_launch("block_norm_fwd_odd");
+}
+
 // Which kernel: by the row's 16-byte vectors, and whether there are rows enough that a team takes
 // several.  Fractions of the measured copy rate with many rows, bf16 unless said:
 //   ring, 1 vector a thread  256 columns 0.92, 512 0.94, 1024 0.94, 2048 0.91 (2 vectors: 0.87 and less)
@@ -1049,6 +1436,7 @@ int launch_fwd_ring(const FwdP& p, int nvec, cudaStream_t st) {
 //         2, 384 threads     5120 0.90, 6144 0.93
 //         4 vectors          7168 1.00, 8192 0.96 (2 vectors, 512 threads: 0.96, 0.94), 16384 0.76
 //   registers               0.67 to 0.87 over the same widths; first to finish when a team has one row
+//   odd widths              fp32 1001 0.73, bf16 4095 0.35 (registers, element loads: 0.59, 0.22)
 template <typename T>
 int launch_fwd(const FwdP& p, cudaStream_t st) {
     constexpr int EPV = Vec<T>::N;
@@ -1071,8 +1459,13 @@ int launch_fwd(const FwdP& p, cudaStream_t st) {
         if (nvec <= 2048) return launch_fwd_team<T, EPV, 4>(p, (nvec + 127) / 128, st);
     } else {
         if (p.cols <= 128) return launch_fwd_team<T, 1, 4>(p, 1, st);
-        if (p.cols <= 2048) return launch_fwd_team<T, 1, 4>(p, (p.cols + 127) / 128, st);
-        if (p.cols <= 4096) return launch_fwd_team<T, 1, 8>(p, (p.cols + 255) / 256, st);
+        if (p.rows <= sm_count() && p.cols <= 2048) return launch_fwd_team<T, 1, 4>(p, (p.cols + 127) / 128, st);
+        if (p.cols <= 256) return launch_fwd_odd<T, 4, 64>(p, st);
+        if (p.cols <= 512) return launch_fwd_odd<T, 4, 128>(p, st);
+        if (p.cols <= 1024) return launch_fwd_odd<T, 4, 256>(p, st);
+        if (p.cols <= 2048) return launch_fwd_odd<T, 8, 256>(p, st);
+        if (p.cols <= 4096) return launch_fwd_odd<T, 8, 512>(p, st);
+        if (p.cols <= 8192) return launch_fwd_odd<T, 16, 512>(p, st);
     }
     const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(sm_count()) * 8);
     block_norm_fwd_generic<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
@@ -1135,6 +1528,25 @@ int launch_bwd_ring(BwdP& p, int nvec, size_t slot, int64_t& grid, cudaStream_t 
     return launch_bwd_ring<T, VPT, 0, NT, 0>(p, nvec, slot, grid, teams, per_sm, st);
 }
 
+template <typename T, int EPT, int NT>
+int launch_bwd_odd(BwdP& p, int streams, int64_t& grid, cudaStream_t st) {
+    constexpr auto k = block_norm_bwd_odd<T, EPT, 0, NT>;
+    constexpr auto kw = block_norm_bwd_odd<T, EPT, 1, NT>;
+    if (int rc = allow_smem<k>()) return rc;
+    if (int rc = allow_smem<kw>()) return rc;
+    const size_t wmax = window_max(p.cols, sizeof(T)), slot = streams * wmax + 8;
+    int nst = 4;   // one row in use, three in flight
+    while (nst > 2 && nst * slot > 200u * 1024u) --nst;
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kw, NT, nst * slot);
+    grid = split_rows(p, static_cast<int64_t>(sm_count()) * std::max(1, per_sm));
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    if (p.splits == 0) kw<<<static_cast<unsigned>(grid), NT, nst * slot, st>>>(p, nst, static_cast<uint32_t>(wmax), err);
+    else k<<<static_cast<unsigned>(grid), NT, nst * slot, st>>>(p, nst, static_cast<uint32_t>(wmax), err);
+    return check_launch("block_norm_bwd_odd");
+}
+
 template <typename T>
 int launch_bwd(BwdP p, void* dw_post, void* dw_pre, float* ws, cudaStream_t st) {
     constexpr int EPV = Vec<T>::N;
@@ -1151,8 +1563,16 @@ int launch_bwd(BwdP p, void* dw_post, void* dw_pre, float* ws, cudaStream_t st) 
     // By the row's 16-byte vectors; fractions of the measured copy rate with many rows, bf16 unless said:
     // 1 a thread 2048 columns 0.93 (2: 0.87), 1024 0.89, 512 0.90, 256 0.86; 2 a thread 4096 0.97
     // (1, 512 threads: 0.90 to 0.93), 5120 0.95, fp32 4096 0.94, fp32 1024 0.90 (1: 0.84); 4 a thread 8192
-    // 0.96, fp32 8192 0.94, 16384 0.42 (its sums spill).
-    if (nvec == 0 || nvec > 2048 || slot > 200u * 1024u) {
+    // 0.96, fp32 8192 0.86, 16384 0.44 (its sums spill).  Odd widths: fp32 1001 0.64, bf16 4095 0.33 (the
+    // generic kernel: 0.23, 0.10).
+    if (nvec == 0 && p.cols >= 64 && p.cols <= 8192 && 2 * (streams * window_max(p.cols, sizeof(T)) + 8) <= 220u * 1024u) {
+        if (p.cols <= 256) rc = launch_bwd_odd<T, 4, 64>(p, streams, grid, st);
+        else if (p.cols <= 512) rc = launch_bwd_odd<T, 4, 128>(p, streams, grid, st);
+        else if (p.cols <= 1024) rc = launch_bwd_odd<T, 4, 256>(p, streams, grid, st);
+        else if (p.cols <= 2048) rc = launch_bwd_odd<T, 8, 256>(p, streams, grid, st);
+        else if (p.cols <= 4096) rc = launch_bwd_odd<T, 8, 512>(p, streams, grid, st);
+        else rc = launch_bwd_odd<T, 16, 512>(p, streams, grid, st);
+    } else if (nvec == 0 || nvec > 2048 || slot > 200u * 1024u) {
         grid = split_rows(p, static_cast<int64_t>(sm_count()) * 4);
         block_norm_bwd_generic<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
         rc = check_launch("block_norm_bwd");
