@@ -33,6 +33,7 @@
 
 #include <atomic>
 
+#include "head_simt.cuh"
 #include "liger_train.h"
 #include "tc_gemm.cuh"
 
@@ -687,31 +688,42 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_f32(const int64_t* __
     for (int v = threadIdx.x; v < V; v += kRowThreads) z[v] = sc * (expf(z[v] - l) - (v == y ? 1.0f : 0.0f));
 }
 
-// loss and stats: fixed-order fp64 sums of the tokens' terms; NaN if a kernel recorded an error or the
-// scan found a bad label or bad sequences
-__global__ void __launch_bounds__(1024) policy_final(const float* __restrict__ term, const float* __restrict__ kl,
-                                                     const float* __restrict__ clip, int64_t T, const Hdr* hdr,
-                                                     float* loss, float* stats) {
-    __shared__ double red[3][32];
-    double s[3] = {0.0, 0.0, 0.0};
-    for (int64_t t = threadIdx.x; t < T; t += 1024) {
-        s[0] += static_cast<double>(term[t]);
-        s[1] += static_cast<double>(kl[t]);
-        s[2] += static_cast<double>(clip[t]);
+// loss and stats: the tokens' terms added in a fixed order; NaN if a kernel recorded an error or the
+// scan found a bad label or bad sequences.  A thread adds its tokens in fp32 with the rounding errors
+// carried along (fp64 adds run at a small fraction of the fp32 rate: 16 us for 4096 tokens in fp64), the
+// threads' sums are joined in fp64.
+__device__ __forceinline__ void add_with_error(float v, float& sum, float& err) {
+    const float t = sum + v, b = t - sum;
+    err += (sum - (t - b)) + (v - b);
+    sum = t;
+}
+constexpr int kFinalThreads = 256;
+__global__ void __launch_bounds__(kFinalThreads) policy_final(const float* __restrict__ term, const float* __restrict__ kl,
+                                                              const float* __restrict__ clip, int64_t T, const Hdr* hdr,
+                                                              float* loss, float* stats) {
+    constexpr int NW = kFinalThreads / 32;
+    __shared__ double red[3][NW];
+    float s[3] = {0.f, 0.f, 0.f}, e[3] = {0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < T; t += kFinalThreads) {
+        add_with_error(term[t], s[0], e[0]);
+        add_with_error(kl[t], s[1], e[1]);
+        add_with_error(clip[t], s[2], e[2]);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
+        // an infinity's error term is NaN: the plain sum stands for it
+        double d = isfinite(s[i]) ? static_cast<double>(s[i]) + static_cast<double>(e[i]) : static_cast<double>(s[i]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-        if ((threadIdx.x & 31) == 0) red[i][threadIdx.x >> 5] = s[i];
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if ((threadIdx.x & 31) == 0) red[i][threadIdx.x >> 5] = d;
     }
     __syncthreads();
-    if (threadIdx.x < 96) {   // one warp for each sum (fp64 adds are slow: five in a row, not 32)
-        const int i = threadIdx.x >> 5;
-        double tot = red[i][threadIdx.x & 31];
+    if (threadIdx.x < 3) {
+        const int i = threadIdx.x;
+        double tot = 0.0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-        if ((threadIdx.x & 31) != 0) return;
+        for (int w = 0; w < NW; ++w) tot += red[i][w];
         const double n = static_cast<double>(hdr->n_valid);
         float r = static_cast<float>(i == 0 ? tot : n > 0.0 ? tot / n : 0.0);
         if (hdr->err != 0 || hdr->bad != 0) r = __int_as_float(0x7fc00000);
@@ -862,11 +874,8 @@ int run_simt(const Args& a, const Layout& L, float scale) {
         const bool first = c == 0, last = c == L.nchunks - 1;
         if ((rc = simt<TI, TI, TI, 0>(cl, V, H, X + t0 * H, H, 1, W, 1, H, Z, (TI*)nullptr, V, nullptr, 0, a.st)))
             return rc;
-        if (a.pol != nullptr)
-            policy_rows_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, 1, *a.pol, nullptr, t0);
-        else
-            dlogits_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, scale, a.scale_dev, lse + t0,
-                                                      lossrow + t0);
+        dlogits_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, scale, a.scale_dev, lse + t0,
+                                                  lossrow + t0);
         if ((rc = check_launch("dlogits_f32"))) return rc;
         if (dX && (rc = simt<float, TI, TI, 1>(cl, H, V, Z, V, 1, W, H, 1, nullptr, dX + t0 * H, H, a.labels + t0,
                                                a.ignore, a.st)))
@@ -1535,7 +1544,7 @@ namespace {
 // Workspace of the policy loss: the cross-entropy's, then its own per-token arrays.
 struct PolicyLayout {
     Layout L;
-    size_t seq, n_seq, coef, term, kl, clip, total;
+    size_t seq, n_seq, coef, term, kl, clip, split, total;
 };
 
 // Tokens per chunk of the policy loss on the tensor-core path when the caller leaves it open: up to
@@ -1557,6 +1566,7 @@ PolicyLayout policy_layout(int64_t T, int64_t H, int64_t V, int64_t B, int64_t c
     P.kl = o; o += per_token;
     P.clip = o; o += per_token;
     P.n_seq = o; o = up256(o + sizeof(int) * static_cast<size_t>(B));
+    P.split = o; o += P.L.tc ? 0 : sizeof(float) * static_cast<size_t>(kSplitFloats);
     P.total = o;
     return P;
 }
@@ -1569,7 +1579,7 @@ constexpr int64_t kPadRows = 16;          // rows of X that a GEMM over fewer is
 struct LogpLayout {
     bool tc;
     int64_t C, nvt;
-    size_t hdr, labs, zlab, part, scr, total;
+    size_t hdr, labs, zlab, part, scr, split, total;
     CompactLayout comp;
 };
 
@@ -1587,6 +1597,7 @@ LogpLayout logp_layout(int64_t T, int64_t H, int64_t V, int dtype) {
     // (few tokens: 4 tokens times at most 2048 blocks)
     P.part = o; o = up256(o + (P.tc ? sizeof(float2) * static_cast<size_t>(std::max<int64_t>(P.C * P.nvt, kFewParts)) : 0));
     P.scr = o; o = up256(o + (P.tc ? 0 : sizeof(float) * static_cast<size_t>(P.C * V)));
+    P.split = o; o += P.tc ? 0 : sizeof(float) * static_cast<size_t>(kSplitFloats);
     P.comp = compact_regions(o, 0, std::max(T, kPadRows), H, 2);
     P.total = P.tc ? P.comp.total : o;
     return P;
@@ -1710,6 +1721,75 @@ int read_hdr(const char* who, const Hdr* hdr, Hdr* out, cudaStream_t st) {
 
 unsigned scan_grid(int64_t T) { return static_cast<unsigned>(std::min<int64_t>(ceil_div(T, 256), 4 * sm_count())); }
 
+// Z = X_c W^T of cl rows off the tensor cores
+template <typename TI>
+int simt_logits(const TI* Xc, const TI* W, float* Z, int cl, int H, int V, float* split, cudaStream_t st) {
+    HeadGemm g{};
+    g.M = cl;
+    g.N = V;
+    g.K = H;
+    g.sam = H;
+    g.sak = 1;
+    g.sbk = 1;
+    g.sbn = H;
+    g.ldo = V;
+    return launch_head_gemm(Xc, W, Z, g, split, st);
+}
+
+// The policy loss off the tensor cores, in token chunks of L.C rows.
+template <typename TI>
+int run_policy_simt(const Args& a, const Layout& L, float* split) {
+    const TI *X = static_cast<const TI*>(a.X), *W = static_cast<const TI*>(a.W);
+    TI *dX = static_cast<TI*>(a.dX), *dW = static_cast<TI*>(a.dW);
+    float* Z = reinterpret_cast<float*>(a.ws + L.scr);
+    float* acc = reinterpret_cast<float*>(a.ws + L.acc);
+    const int H = static_cast<int>(a.H), V = static_cast<int>(a.V);
+    int rc;
+    for (int64_t c = 0; c < L.nchunks; ++c) {
+        const int64_t t0 = c * L.C;
+        const int cl = static_cast<int>(std::min(L.C, a.T - t0));
+        const bool first = c == 0, last = c == L.nchunks - 1;
+        if ((rc = simt_logits(X + t0 * H, W, Z, cl, H, V, split, a.st))) return rc;
+        policy_rows_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, 1, *a.pol, nullptr, t0);
+        if ((rc = check_launch("linear_policy rows"))) return rc;
+        if (dX) {   // dX_c = D W
+            HeadGemm g{};
+            g.M = cl;
+            g.N = H;
+            g.K = V;
+            g.sam = V;
+            g.sak = 1;
+            g.sbk = H;
+            g.sbn = 1;
+            g.ldo = H;
+            g.labels = a.labels + t0;
+            g.ignore = a.ignore;
+            if ((rc = launch_head_gemm(Z, W, dX + t0 * H, g, split, a.st))) return rc;
+        }
+        if (dW) {   // dW (+)= D^T X_c; bf16 with several chunks: the sum in fp32, rounded with the last
+            HeadGemm g{};
+            g.M = V;
+            g.N = H;
+            g.K = cl;
+            g.sam = 1;
+            g.sak = V;
+            g.sbk = H;
+            g.sbn = 1;
+            g.ldo = H;
+            const bool f32 = a.dtype == LIGER_F32;
+            g.add = !first && (f32 || !last) ? 1 : 0;
+            if (f32 || last) {
+                if (!f32 && !first) g.base = acc;
+                rc = launch_head_gemm(Z, X + t0 * H, dW, g, split, a.st);
+            } else {
+                rc = launch_head_gemm(Z, X + t0 * H, acc, g, split, a.st);
+            }
+            if (rc) return rc;
+        }
+    }
+    return LIGER_OK;
+}
+
 // The log-probabilities of n rows at X with labels labs; idx: original token of a row (null: the row)
 int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* labs, const int64_t* idx, int64_t n, int H,
                 int V, int64_t ignore, float* logp, uint8_t* w8, const LogpLayout& L, cudaStream_t st) {
@@ -1777,8 +1857,8 @@ int run_logp_simt(const void* X, const void* W, const int64_t* labs, int64_t T, 
     pol.logp = logp;
     for (int64_t t0 = 0; t0 < T; t0 += L.C) {
         const int cl = static_cast<int>(std::min(L.C, T - t0));
-        if (int rc = simt<TI, TI, TI, 0>(cl, V, H, static_cast<const TI*>(X) + t0 * H, H, 1, static_cast<const TI*>(W), 1,
-                                         H, Z, static_cast<TI*>(nullptr), V, nullptr, 0, st))
+        if (int rc = simt_logits(static_cast<const TI*>(X) + t0 * H, static_cast<const TI*>(W), Z, cl, H, V,
+                                 reinterpret_cast<float*>(w8 + L.split), st))
             return rc;
         policy_rows_f32<<<cl, kRowThreads, 0, st>>>(labs + t0, ignore, Z, V, V, 0, pol, nullptr, t0);
         if (int rc = check_launch("linear_logp rows")) return rc;
@@ -1915,9 +1995,9 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
     const Args a{X, W, labs, T, H, V, ignore, reduction, grad_scale, loss, dX, dW, w8, dtype, st, nullptr, &pol, nullptr};
     int rc;
     if (PL.L.tc) rc = n < T ? run_tc_compact(a, n, chunk, 0.f) : run_tc(a, PL.L, 0.f);
-    else rc = dtype == LIGER_F32 ? run_simt<float>(a, PL.L, 0.f) : run_simt<__nv_bfloat16>(a, PL.L, 0.f);
+    else rc = dtype == LIGER_F32 ? run_policy_simt<float>(a, PL.L, f32(PL.split)) : run_policy_simt<__nv_bfloat16>(a, PL.L, f32(PL.split));
     if (rc) return rc;
-    policy_final<<<1, 1024, 0, st>>>(f32(PL.term), f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
+    policy_final<<<1, kFinalThreads, 0, st>>>(f32(PL.term), f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
     return check_launch("linear_policy");
 }
 
