@@ -61,7 +61,8 @@ def parse_args(argv=None):
     p.add_argument("--op", default="chain",
                    choices=["chain", "linear_ce", "linear_ce_two_pass", "rmsnorm_qkv_rope", "fused_linear_swiglu",
                             "fused_linear_swiglu_fwd_save", "fused_linear_swiglu_bwd_saved", "rmsnorm", "rope",
-                            "swiglu"],
+                            "swiglu", "block_norm", "swiglu_ckpt8", "fused_linear_swiglu_ckpt8", "linear_logp",
+                            "linear_policy"],
                    help="chain: the benchmark step (default); otherwise time that one operator alone at --seq "
                         "tokens (single-kernel profiling cases; prints a JSON line with ms per call)")
     p.add_argument("--chunk", type=int, default=0, help="--op linear_ce: token chunk (0 = automatic)")
@@ -1084,6 +1085,26 @@ def single_op(args):
             ws = torch.empty(L.liger_linear_ce_two_pass_workspace(S, HIDDEN, VOCAB), dtype=torch.uint8, device=dev)
             fn = lambda: L.liger_linear_ce_two_pass_fwd_bwd(X, W, lab, loss, dX, dW, ws)
             flops = 8.0 * S * HIDDEN * VOCAB
+    elif op in ("linear_logp", "linear_policy"):
+        X = to_torch(normal(7, "op.X", (S, HIDDEN), "bf16"), dev)
+        W = to_torch(normal(7, "op.W", (VOCAB, HIDDEN), "bf16", 0.0, 0.02), dev)
+        lab = torch.from_numpy(labels(7, "op.labels", S, VOCAB, args.ignore_frac)).to(dev)
+        n = int((lab != -100).sum())
+        logp = torch.empty(S, device=dev)
+        if op == "linear_logp":
+            ws = torch.empty(L.liger_linear_logp_workspace(S, HIDDEN, VOCAB), dtype=torch.uint8, device=dev)
+            fn = lambda: L.liger_linear_logp_fwd(X, W, lab, logp, ws)
+            flops = 2.0 * n * HIDDEN * VOCAB
+        else:
+            B = 8
+            cu = torch.linspace(0, S, B + 1, device=dev).to(torch.int32)
+            old, ref = torch.full((S,), -12.0, device=dev), torch.full((S,), -12.1, device=dev)
+            adv = torch.linspace(-1, 1, B, device=dev)
+            loss, dX, dW = torch.empty(1, device=dev), torch.empty_like(X), torch.empty_like(W)
+            ws = torch.empty(L.liger_linear_policy_workspace(S, HIDDEN, VOCAB, B, args.chunk), dtype=torch.uint8, device=dev)
+            fn = lambda: L.liger_linear_policy_fwd_bwd(X, W, lab, old, adv, loss, dX, dW, ws, ref_logp=ref, cu_seqlens=cu,
+                                                       logp=logp, reduction="seq_mean", beta=0.04, chunk=args.chunk)
+            flops = 6.0 * n * HIDDEN * VOCAB
     elif op == "rmsnorm_qkv_rope":
         N = 3 * HEADS * HEAD_DIM
         x = to_torch(normal(7, "op.x", (S, HIDDEN), "bf16"), dev)
@@ -1097,7 +1118,7 @@ def single_op(args):
         fn = lambda: L.liger_rmsnorm_qkv_rope_fwd(x, wn, Wq, Wk, Wv, q, k, v, ws, 1, S, HEADS, HEADS, HEAD_DIM,
                                                   eps=EPS, theta=THETA)
         flops = 2.0 * S * HIDDEN * N
-    elif op in ("rmsnorm", "rope", "swiglu"):
+    elif op in ("rmsnorm", "rope", "swiglu", "block_norm", "swiglu_ckpt8"):
         # forward then backward, HBM-bound: report GB/s of the algorithmic bytes
         e = 2
         if op == "rmsnorm":
@@ -1120,6 +1141,27 @@ def single_op(args):
                 L.liger_rope_fwd(q, k, None, THETA)
                 L.liger_rope_bwd(q, k, None, THETA)
             nbytes = 2 * (2 * 2 * S * HEADS * HEAD_DIM * e)
+        elif op == "block_norm":
+            z, r, dh, dy = (to_torch(normal(7, f"op.b{c}", (S, HIDDEN), "bf16"), dev) for c in "zrhy")
+            w = to_torch(normal(7, "op.bw", (HIDDEN,), "bf16", 1.0, 0.1), dev)
+            h, y, dr, dz = (torch.empty_like(z) for _ in range(4))
+            rz, rh = torch.empty(S, device=dev), torch.empty(S, device=dev)
+            dwp, dg, dwn = (torch.empty_like(w) for _ in range(3))
+            wsb = torch.empty(L.liger_block_norm_bwd_workspace(S, HIDDEN, 1), dtype=torch.uint8, device=dev)
+
+            def fn():
+                L.liger_block_norm_fwd(z, r, h, y, w, w, w, rz, rh, eps=EPS)
+                L.liger_block_norm_bwd(dh, dy, z, h, dr, dz, wsb, w, w, w, rz, rh, dwp, dg, dwn)
+            nbytes = (4 + 6) * S * HIDDEN * e + 16 * S
+        elif op == "swiglu_ckpt8":
+            g, u, dy = (to_torch(normal(7, f"op.c{c}", (S, INTER), "bf16"), dev) for c in "gud")
+            y, dg, du = torch.empty_like(g), torch.empty_like(g), torch.empty_like(g)
+            kept = (*L.liger_ckpt8_empty(S, INTER), *L.liger_ckpt8_empty(S, INTER))
+
+            def fn():
+                L.liger_swiglu_fwd_ckpt8(g, u, y, *kept)
+                L.liger_swiglu_bwd_ckpt8(dy, *kept, dg, du)
+            nbytes = 6 * S * INTER * e + 4 * (S * INTER + S * (INTER // 32))
         else:
             g = to_torch(normal(7, "op.g", (S, INTER), "bf16"), dev)
             u = to_torch(normal(7, "op.u", (S, INTER), "bf16"), dev)
@@ -1139,6 +1181,16 @@ def single_op(args):
         if op == "fused_linear_swiglu":
             fn = lambda: L.liger_fused_linear_swiglu_fwd(X, Wg, Wu, out)
             flops = 4.0 * S * HIDDEN * INTER
+        elif op == "fused_linear_swiglu_ckpt8":     # forward and backward
+            kept = (*L.liger_ckpt8_empty(S, INTER), *L.liger_ckpt8_empty(S, INTER))
+            dH = to_torch(normal(7, "op.mdH", (S, INTER), "bf16"), dev)
+            dX, dWg, dWu = torch.empty_like(X), torch.empty_like(Wg), torch.empty_like(Wu)
+            ws = torch.empty(L.liger_fused_linear_swiglu_workspace(S, INTER), dtype=torch.uint8, device=dev)
+
+            def fn():
+                L.liger_fused_linear_swiglu_fwd_ckpt8(X, Wg, Wu, out, *kept)
+                L.liger_fused_linear_swiglu_bwd_ckpt8(X, Wg, Wu, dH, *kept, dX, dWg, dWu, ws)
+            flops = 12.0 * S * HIDDEN * INTER
         elif op == "fused_linear_swiglu_fwd_save":
             g, u = torch.empty_like(out), torch.empty_like(out)
             fn = lambda: L.liger_fused_linear_swiglu_fwd_save(X, Wg, Wu, out, g, u)

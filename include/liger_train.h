@@ -131,7 +131,8 @@ int liger_fused_linear_swiglu_bwd_ckpt8(const void* X, const void* Wg, const voi
  * loss needs of the old and of the reference policy.  Forward only; the logits
  * never reach device memory on the bf16 tensor-core path (H >= 64 and a
  * multiple of 8, V >= 256); other cases run in fp32 with a [chunk x V] buffer.
- *   X [T, H], W [V, H] in dtype, labels int64 [T], logp float [T].
+ *   X [T, H], W [V, H] in dtype, labels int64 [T], logp float [T].  Off the
+ *   tensor cores V is at most 4194240, and so are the rows of a chunk.
  *   ws: at least liger_linear_logp_workspace bytes, 256-byte aligned.
  * liger_linear_logp_fwd waits for a scan of the labels: a label outside [0, V)
  * that is not ignore_index returns LIGER_ERR_LABEL with nothing else queued,

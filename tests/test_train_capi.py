@@ -114,6 +114,7 @@ def _policy(fn, **kw):
 def test_logp_checks(lib):
     for fn in (lib.liger_linear_logp_fwd, lib.liger_linear_logp_fwd_async):
         assert _logp(fn, dtype=3) == -3 and _logp(fn, T=-1) == -2 and _logp(fn, V=0) == -2 and _logp(fn, H=0) == -2
+        assert _logp(fn, V=5000000, dtype=0) == -2 and _logp(fn, T=1 << 23, V=2, dtype=0) == -2
         assert _logp(fn, T=1 << 31) == -2 and _logp(fn, T=0, X=None) == 0
         for k in ("X", "W", "labels", "logp"):
             assert _logp(fn, **{k: None}) == -1, k
@@ -131,7 +132,7 @@ def test_policy_checks(lib):
         assert _policy(fn, dtype=3) == -3
         for kw in (dict(T=-1), dict(H=0), dict(V=0), dict(B=0), dict(chunk=-1), dict(reduction=3), dict(reduction=-1),
                    dict(flags=2), dict(lo=-0.1), dict(lo=1.1), dict(hi=-0.1), dict(lo=nan), dict(hi=nan), dict(beta=nan),
-                   dict(gs=nan), dict(T=1 << 31)):
+                   dict(gs=nan), dict(T=1 << 31), dict(V=5000000, dtype=0), dict(T=1 << 23, V=2, dtype=0)):
             assert _policy(fn, **kw) == -2, kw
         for k in ("X", "W", "labels", "cu", "old", "ref", "adv", "loss"):
             assert _policy(fn, **{k: None}) == -1, k

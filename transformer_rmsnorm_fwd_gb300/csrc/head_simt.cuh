@@ -15,6 +15,7 @@ namespace liger {
 namespace {
 
 constexpr int kHT = 64, kHK = 16;
+constexpr int64_t kHeadRows = 65535 * kHT;           // most rows of a product (grid limit)
 constexpr int64_t kSplitFloats = int64_t{1} << 22;   // workspace of the partial tiles
 
 struct HeadGemm {
@@ -119,7 +120,6 @@ template <typename TA, typename TB, typename TO>
 int launch_head_gemm(const TA* A, const TB* B, TO* out, HeadGemm g, float* part, cudaStream_t st) {
     if (g.M == 0 || g.N == 0) return LIGER_OK;
     const int64_t tm = ceil_div(g.M, kHT), tn = ceil_div(g.N, kHT);
-    if (tm > 65535) return fail(LIGER_ERR_SHAPE, "head: SIMT grid too large");
     const int64_t fit = kSplitFloats / (static_cast<int64_t>(g.M) * g.N);
     int64_t splits = std::min<int64_t>({ceil_div(2 * sm_count(), tm * tn), ceil_div(g.K, 2 * kHK), fit, 32});
     if (splits < 2) splits = 1;

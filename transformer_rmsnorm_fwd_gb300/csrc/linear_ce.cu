@@ -1587,7 +1587,7 @@ LogpLayout logp_layout(int64_t T, int64_t H, int64_t V, int dtype) {
     LogpLayout P{};
     P.tc = use_tc(H, V, dtype);
     P.nvt = ceil_div(V, kVT);
-    P.C = P.tc ? kAutoChunkTC : std::max<int64_t>(128, (int64_t{1} << 26) / V);
+    P.C = P.tc ? kAutoChunkTC : std::max<int64_t>(128, (int64_t{1} << 26) / V);   // as layout()
     P.C = std::max<int64_t>(1, std::min(P.C, T));
     const size_t t = static_cast<size_t>(std::max<int64_t>(T, 1));
     size_t o = 0;
@@ -1866,15 +1866,17 @@ int run_logp_simt(const void* X, const void* W, const int64_t* labs, int64_t T, 
     return LIGER_OK;
 }
 
-bool head_shape_ok(int64_t T, int64_t H, int64_t V) {
-    return T >= 0 && H > 0 && V > 0 && H <= (1 << 30) && V <= (1 << 30) && T <= (int64_t{1} << 31) - 1;
+// Off the tensor cores the products' tiles limit the rows of a chunk and the vocabulary.
+bool head_shape_ok(int64_t T, int64_t H, int64_t V, int dtype, int64_t chunk = 0) {
+    if (!(T >= 0 && H > 0 && V > 0 && H <= (1 << 30) && V <= (1 << 30) && T <= (int64_t{1} << 31) - 1)) return false;
+    return use_tc(H, V, dtype) || (V <= kHeadRows && std::min(T, layout(T, H, V, chunk, dtype).C) <= kHeadRows);
 }
 
 int logp_impl(const char* who, const void* X, const void* W, const int64_t* labels, int64_t T, int64_t H, int64_t V,
               int64_t ignore, float* logp, void* ws, size_t ws_bytes, int dtype, void* stream, bool sync) {
     clear_error();
     if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
-    if (!head_shape_ok(T, H, V))
+    if (!head_shape_ok(T, H, V, dtype))
         return fail(LIGER_ERR_SHAPE, "%s: T=%lld H=%lld V=%lld", who, (long long)T, (long long)H, (long long)V);
     if (T == 0) return LIGER_OK;
     if (!X || !W || !labels || !logp) return fail(LIGER_ERR_NULL, "%s: X, W, labels, logp required", who);
@@ -1938,7 +1940,7 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
                 int dtype, void* stream, bool sync) {
     clear_error();
     if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
-    if (!head_shape_ok(T, H, V) || chunk < 0 || B < 1 || B > (1 << 30) || reduction < 0 || reduction > 2 ||
+    if (chunk < 0 || !head_shape_ok(T, H, V, dtype, chunk) || B < 1 || B > (1 << 30) || reduction < 0 || reduction > 2 ||
         (flags & ~LIGER_POLICY_ADV_PER_TOKEN))
         return fail(LIGER_ERR_SHAPE, "%s: T=%lld H=%lld V=%lld B=%lld chunk=%lld reduction=%d flags=%d", who, (long long)T,
                     (long long)H, (long long)V, (long long)B, (long long)chunk, reduction, flags);
@@ -2005,7 +2007,7 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
 }  // namespace liger
 
 extern "C" size_t liger_linear_logp_workspace(int64_t T, int64_t H, int64_t V, int dtype) {
-    if (!head_shape_ok(T, H, V) || (dtype != LIGER_F32 && dtype != LIGER_BF16)) return 0;
+    if ((dtype != LIGER_F32 && dtype != LIGER_BF16) || !head_shape_ok(T, H, V, dtype)) return 0;
     return logp_layout(T, H, V, dtype).total;
 }
 
@@ -2022,7 +2024,7 @@ extern "C" int liger_linear_logp_fwd_async(const void* X, const void* W, const i
 }
 
 extern "C" size_t liger_linear_policy_workspace(int64_t T, int64_t H, int64_t V, int64_t B, int64_t chunk, int dtype) {
-    if (!head_shape_ok(T, H, V) || B < 1 || chunk < 0 || (dtype != LIGER_F32 && dtype != LIGER_BF16)) return 0;
+    if ((dtype != LIGER_F32 && dtype != LIGER_BF16) || B < 1 || chunk < 0 || !head_shape_ok(T, H, V, dtype, chunk)) return 0;
     return policy_layout(T, H, V, B, chunk, dtype).total;
 }
 
