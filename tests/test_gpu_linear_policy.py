@@ -154,6 +154,22 @@ def test_policy(L, T, H, V, dt, starts, chunk, wait):
         _compare(o, r, i, dt, tc)
 
 
+@pytest.mark.parametrize("T,H,V", [
+    (2600, 2048, 66536),    # 88 dX tiles: a full round and 12 split tiles, over two slabs of the vocabulary
+    (2600, 2048, 3000),     # the same in one launch
+    (20, 4096, 70000),      # 16 tiles split over all pairs
+    (130, 520, 2100),       # 3 tiles; k ranges that do not divide the k-blocks
+])
+def test_policy_split_dx(L, T, H, V):
+    i = _inputs(T, H, V, "bf16", [0, T // 2, T], seed=T, masked=0.0)
+    r = _ref(i, "seq_mean", 0.2, 0.2, 0.05, 1.0)
+    o = _call(L, i, "bf16", "seq_mean", 0.2, 0.2, 0.05, 1.0)
+    _compare(o, r, i, "bf16", True)
+    again = _call(L, i, "bf16", "seq_mean", 0.2, 0.2, 0.05, 1.0, wait=False)
+    for k in o:
+        assert torch.equal(o[k], again[k]), k
+
+
 def test_forms_agree_and_repeat(L):
     """No masked token: both forms are the same bits; a second run is the same bits; one output alone equals both."""
     i = _inputs(500, 128, 1000, "bf16", [0, 200, 500], masked=0.0)

@@ -489,6 +489,7 @@ struct Policy {
     float* coef;                              // [tokens run] the scale c_t, in the order the GEMMs run them
     float *term, *kl, *clip;                  // [T] w l, kl and 1 where clipped, by original token
     float* logp;                              // [T] by original token, or NULL
+    float* kpart;                             // dX: the split tiles' sums
 };
 
 // exp(d) - d - 1 without the cancellation of small d: its Taylor series (terms d^2 / 2! to d^9 / 9!,
@@ -940,6 +941,133 @@ int launch_logits(const __nv_bfloat16* Xc, int cl, int H, int V, const CUtensorM
     return LIGER_OK;
 }
 
+// ---- dX of the policy loss
+// K is the whole vocabulary and the tiles are few (256 tokens at hidden 4096: 16 tiles for 76 CTA
+// pairs, 2000 k-blocks each), so the last, partly filled round of tiles, which may be the only one, is
+// split along K over the idle pairs, each item leaving fp32 sums that dx_join adds up.  Above
+// kDxSlabRows vocabulary rows in several rounds the launches go over slabs as for the cross-entropy.
+// Times at hidden 4096, vocabulary 128256 with and without the split: DXTIMES.
+constexpr int kPairs = 80;               // most CTA pairs planned for
+constexpr int kDxMinBlocks = 16;         // fewest k-blocks of an item
+constexpr int64_t kDxMaxSlabs = 4;       // slabs whose split sums the workspace holds
+constexpr int64_t kTileFloats = 256 * 256;
+
+struct DxPlan {
+    int64_t slab;     // vocabulary rows per launch
+    int slabs, full, rem, splits;   // rem tiles from `full` on are split into `splits` (0: none)
+};
+
+DxPlan dx_plan(int64_t rows, int64_t H, int64_t V) {
+    DxPlan p{};
+    const int64_t pairs = std::min<int64_t>(std::max(1, sm_count() / 2), kPairs);
+    const int64_t tiles = ceil_div(rows, int64_t{256}) * ceil_div(H, int64_t{256});
+    p.slab = tiles <= pairs ? V : dx_slab(V);
+    p.slabs = static_cast<int>(ceil_div(V, p.slab));
+    p.rem = static_cast<int>(tiles % pairs);
+    p.full = static_cast<int>(tiles) - p.rem;
+    if (p.rem > 0 && p.slabs <= kDxMaxSlabs)
+        p.splits = static_cast<int>(std::min<int64_t>(pairs / p.rem, ceil_div(p.slab, int64_t{tc::BK}) / kDxMinBlocks));
+    if (p.splits < 2) p.splits = 0;
+    return p;
+}
+
+// out = the sum of a split tile's items (slabs x splits of them, in that order) minus the one-hot part
+__global__ void __launch_bounds__(256) dx_join(const float* __restrict__ part, int items, int rem, int slabs, int full,
+                                               int num_n, int num_m, const int64_t* __restrict__ labels,
+                                               int64_t ignore, const float* __restrict__ tok_scale,
+                                               const __nv_bfloat16* __restrict__ W, __nv_bfloat16* out, int rows, int H) {
+    // the tile's row and column block, as the kernel's raster over groups of 8 column blocks gives them
+    const int t = full + static_cast<int>(blockIdx.x);
+    int mi, ni;
+    const int gfull = num_n / tc::GROUP_N, in_full = gfull * num_m * tc::GROUP_N;
+    if (t < in_full) {
+        const int g = t / (num_m * tc::GROUP_N), w = t - g * num_m * tc::GROUP_N;
+        mi = w / tc::GROUP_N;
+        ni = g * tc::GROUP_N + (w - mi * tc::GROUP_N);
+    } else {
+        const int width = num_n - gfull * tc::GROUP_N, w = t - in_full;
+        mi = w / width;
+        ni = gfull * tc::GROUP_N + (w - mi * width);
+    }
+    const int splits = items / rem;
+    // a block takes 8 rows of the tile: 32 threads a row, 8 columns each
+    const int lr = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5), lc = (threadIdx.x & 31) * 8;
+    const int row = mi * 256 + lr, col = ni * 256 + lc;
+    if (row >= rows || col >= H) return;
+    float v[8] = {};
+    for (int sl = 0; sl < slabs; ++sl)
+        for (int s = 0; s < splits; ++s) {
+            const float* src = part + ((static_cast<int64_t>(sl) * items + s * rem + blockIdx.x) * 256 + lr) * 256 + lc;
+            float f[4], g[4];
+            unpack(ldg16_cs(src), f);
+            unpack(ldg16_cs(src + 4), g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += f[e];
+                v[4 + e] += g[e];
+            }
+        }
+    const int64_t y = labels[row];
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (y != ignore) {
+        const float c = tok_scale[row];
+        float w[8];
+        unpack(ldg16(W + y * H + col), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(-c, w[e], v[e]);
+        o = pack(v);
+    }
+    stg16(out + static_cast<int64_t>(row) * H + col, o);
+}
+
+// dX of the cl rows of the chunk at t0: D = P [cl, V], e as set up for the chunk
+int policy_dx(const Args& a, const Layout& L, const __nv_bfloat16* P, const tc::EpiParams& e, int64_t t0, int cl) {
+    using namespace tc;
+    const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.W);
+    const int H = static_cast<int>(a.H);
+    const int64_t V = a.V;
+    const DxPlan p = dx_plan(cl, H, V);
+    float* dxacc = reinterpret_cast<float*>(a.ws + L.dxacc);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dX) + t0 * H;
+    const int items = p.rem * p.splits;
+    int rc;
+    for (int64_t v0 = 0; v0 < V; v0 += p.slab) {
+        const int vl = static_cast<int>(std::min<int64_t>(p.slab, V - v0));
+        const bool first = v0 == 0, last = v0 + vl >= V;
+        CUtensorMap mD, mW;
+        if ((rc = make_map(&mD, P + v0, vl, cl, L.ldp, BK, BM))) return rc;        // A: D[:, slab] (K-major)
+        if ((rc = make_map(&mW, W + v0 * H, H, vl, H, MN_BOX, BK))) return rc;     // B: W[slab, :] (MN-major)
+        EpiParams d = e;
+        d.p_out = nullptr;
+        d.M = cl;
+        d.N = H;
+        d.raster = RASTER_N_GROUPS;
+        d.hint_a = HINT_NORMAL;
+        d.hint_b = HINT_NORMAL;
+        d.acc = dxacc;
+        d.lda = H;
+        d.acc_read = first ? 0 : 1;
+        d.acc_write = last ? 0 : 1;
+        d.out_write = last ? 1 : 0;
+        d.out = out;
+        d.ldo = H;
+        d.keys = nullptr;
+        d.corr_src = last ? W : nullptr;
+        d.ld_corr = H;
+        if (p.splits > 0) {
+            d.full_tiles = p.full;
+            d.ksplits = p.splits;
+            d.kpart = a.pol->kpart + (v0 / p.slab) * items * kTileFloats;
+        }
+        if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1, 1>(mD, mW, cl, H, vl, d, a.st))) return rc;
+    }
+    if (p.splits == 0) return LIGER_OK;
+    dx_join<<<dim3(static_cast<unsigned>(p.rem), 32), 256, 0, a.st>>>(
+        a.pol->kpart, items, p.rem, p.slabs, p.full, static_cast<int>(ceil_div(H, 256)), static_cast<int>(ceil_div(cl, 256)),
+        a.labels + t0, a.ignore, e.tok_scale, W, out, cl, H);
+    return check_launch("dx_join");
+}
+
 int run_tc(const Args& a, const Layout& L, float scale) {
     using namespace tc;
     if (int rc = ensure_sort_attr()) return rc;
@@ -1003,7 +1131,9 @@ int run_tc(const Args& a, const Layout& L, float scale) {
         if ((rc = check_launch("dlogits_bf16"))) return rc;
         if (a.pol != nullptr) e.tok_scale = a.pol->coef + t0;
         // 3. dX_c = D W, minus scale * W[label] in fp32
-        if (a.dX && dx_slab(V) < V) {
+        if (a.dX && a.pol != nullptr) {
+            if ((rc = policy_dx(a, L, P, e, t0, cl))) return rc;
+        } else if (a.dX && dx_slab(V) < V) {
             // over vocabulary slabs, summed in fp32; the last slab subtracts scale * W[label]
             // and writes dX in bf16
             float* dxacc = reinterpret_cast<float*>(a.ws + L.dxacc);
@@ -1033,9 +1163,7 @@ int run_tc(const Args& a, const Layout& L, float scale) {
                 d.ld_corr = H;
                 d.corr_scale = scale;
                 d.scale_ptr = a.scale_dev;
-                rc = a.pol != nullptr ? launch_gemm<0, 1, EPI_ACCUM, 1, 1>(mDs_k, mWs_mn, cl, H, vl, d, a.st)
-                                      : launch_gemm<0, 1, EPI_ACCUM, 1>(mDs_k, mWs_mn, cl, H, vl, d, a.st);
-                if (rc) return rc;
+                if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1>(mDs_k, mWs_mn, cl, H, vl, d, a.st))) return rc;
             }
         } else if (a.dX) {
             EpiParams d = e;
@@ -1050,9 +1178,7 @@ int run_tc(const Args& a, const Layout& L, float scale) {
             d.ld_corr = H;
             d.corr_scale = scale;
             d.scale_ptr = a.scale_dev;
-            rc = a.pol != nullptr ? launch_gemm<0, 1, EPI_STORE, 1, 1>(mD_k, mW_mn, cl, H, V, d, a.st)
-                                  : launch_gemm<0, 1, EPI_STORE, 1>(mD_k, mW_mn, cl, H, V, d, a.st);
-            if (rc) return rc;
+            if ((rc = launch_gemm<0, 1, EPI_STORE, 1>(mD_k, mW_mn, cl, H, V, d, a.st))) return rc;
         }
         // 4. dW (+)= D^T X_c, minus scale * X_t in fp32 for each token t labelled with the row
         if (a.dW) {
@@ -1544,7 +1670,7 @@ namespace {
 // Workspace of the policy loss: the cross-entropy's, then its own per-token arrays.
 struct PolicyLayout {
     Layout L;
-    size_t seq, n_seq, coef, term, kl, clip, split, total;
+    size_t seq, n_seq, coef, term, kl, clip, split, kpart, total;
 };
 
 // Tokens per chunk of the policy loss on the tensor-core path when the caller leaves it open: up to
@@ -1567,6 +1693,8 @@ PolicyLayout policy_layout(int64_t T, int64_t H, int64_t V, int64_t B, int64_t c
     P.clip = o; o += per_token;
     P.n_seq = o; o = up256(o + sizeof(int) * static_cast<size_t>(B));
     P.split = o; o += P.L.tc ? 0 : sizeof(float) * static_cast<size_t>(kSplitFloats);
+    // items of one launch: at most as many as CTA pairs
+    P.kpart = o; o += P.L.tc ? sizeof(float) * static_cast<size_t>(kPairs * kTileFloats * std::min(kDxMaxSlabs, ceil_div(V, dx_slab(V)))) : 0;
     P.total = o;
     return P;
 }
@@ -1993,7 +2121,7 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
         return ok ? LIGER_OK : check_launch("linear_policy memset");
     }
     const Policy pol{old_logp, ref_logp, adv, flags & LIGER_POLICY_ADV_PER_TOKEN, reduction, 1.f - eps_low, 1.f + eps_high,
-                     beta, grad_scale, seq, n_seq, hdr, B, f32(PL.coef), f32(PL.term), f32(PL.kl), f32(PL.clip), logp};
+                     beta, grad_scale, seq, n_seq, hdr, B, f32(PL.coef), f32(PL.term), f32(PL.kl), f32(PL.clip), logp, f32(PL.kpart)};
     const Args a{X, W, labs, T, H, V, ignore, reduction, grad_scale, loss, dX, dW, w8, dtype, st, nullptr, &pol, nullptr};
     int rc;
     if (PL.L.tc) rc = n < T ? run_tc_compact(a, n, chunk, 0.f) : run_tc(a, PL.L, 0.f);

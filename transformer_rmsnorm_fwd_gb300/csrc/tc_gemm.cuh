@@ -135,6 +135,12 @@ struct EpiParams {
     const int* lstart;
     int nseg;
     int64_t lstride;
+    // Work of a TOKSCALE EPI_ACCUM kernel with K-major A whose tiles leave SMs idle: the tiles from
+    // full_tiles on are split along K into ksplits items each (ksplits 0: none are).  An item leaves its
+    // fp32 sums, TM rows of BN, in kpart[item] and nothing else: the caller adds them up and applies what
+    // the epilogue does to whole tiles.  Items of one k range follow each other.
+    int full_tiles, ksplits;
+    float* kpart;
     // EPI_SOFTMAX: out[row, col] = corr_scale * exp(z - lse[row]) (bf16; +0 on rows
     // labelled ignore_index), the softmax part of the logit gradient
     const float* lse;
@@ -491,6 +497,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int num_m = (M + Cfg::TM - 1) / Cfg::TM, num_n = (N + BN - 1) / BN;
     const int ntiles = num_m * num_n;
     const int nkb = (K + BK - 1) / BK;
+    // work items: the tiles, or whole tiles and then (k range, tile) for the split ones
+    constexpr bool KSPLIT = TOKSCALE && EPI == EPI_ACCUM && !A_MN;
+    const int split_tiles = KSPLIT && ep.ksplits > 0 ? ntiles - ep.full_tiles : 0;
+    const int items = ntiles + split_tiles * (ep.ksplits - 1);
+    const int kb_per = KSPLIT && ep.ksplits > 0 ? (nkb + ep.ksplits - 1) / ep.ksplits : nkb;
+    // tile and k-blocks [kb0, kb1) of item w; returns its place in kpart, or -1 for a whole tile
+    auto item = [&](int w, int& tile, int& kb0, int& kb1) {
+        tile = w;
+        kb0 = 0;
+        kb1 = nkb;
+        if (!KSPLIT || split_tiles == 0 || w < ep.full_tiles) return -1;
+        const int q = w - ep.full_tiles, s = q / split_tiles;
+        tile = ep.full_tiles + (q - s * split_tiles);
+        kb0 = s * kb_per;
+        kb1 = kb0 + kb_per < nkb ? kb0 + kb_per : nkb;
+        if (kb1 <= kb0) kb1 = kb0 + 1;   // a range past K: one k-block of fill values, sums of 0
+        return q;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::ST; ++s) {
@@ -563,10 +587,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int s = 0; s < Cfg::ST; ++s) issued[s] = false, issued_phase[s] = 0;
             bool ok = true;
             const int a_row0 = static_cast<int>(crank) * BM;   // this CTA's rows within the tile
-            for (int t = unit; t < ntiles && ok; t += nunits) {
-                int mi, ni;
-                tile_mn(t, mi, ni);
-                for (int kb = 0; kb < nkb; ++kb) {
+            for (int t = unit; t < items && ok; t += nunits) {
+                int mi, ni, tile, kb0, kb1;
+                item(t, tile, kb0, kb1);
+                tile_mn(tile, mi, ni);
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(empty_bar(stage), phase ^ 1u)) {
                         atomicExch(ep.err, ERR_TMA_EMPTY);
                         ok = false;
@@ -652,7 +677,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (PAIR) mma_commit_pair(bar);
                 else mma_commit(bar);
             };
-            for (int t = unit; t < ntiles && ok; t += nunits, ++it) {
+            for (int t = unit; t < items && ok; t += nunits, ++it) {
+                int tile, kb0, kb1;
+                item(t, tile, kb0, kb1);
                 const int as = it & 1;
                 const uint32_t aphase = (it >> 1) & 1;
                 if (!mbar_wait(tempty_bar(as), aphase ^ 1u)) {
@@ -662,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(as * BN);
-                for (int kb = 0; kb < nkb; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(full_bar(stage), phase)) {
                         atomicExch(ep.err, ERR_MMA_FULL);
                         ok = false;
@@ -675,8 +702,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int k = 0; k < BK / UMMA_K; ++k) {
                         const uint64_t da = smem_desc(sa + k * a_kstep, a_lbo, 1024u);
                         const uint64_t db = smem_desc(sb + k * b_kstep, b_lbo, 1024u);
-                        if (PAIR) mma_bf16_pair(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
-                        else mma_bf16(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
+                        if (PAIR) mma_bf16_pair(d, da, db, idesc, ((kb - kb0) | k) != 0 ? 1u : 0u);
+                        else mma_bf16(d, da, db, idesc, ((kb - kb0) | k) != 0 ? 1u : 0u);
                     }
                     any = true;
                     commit(empty_bar(stage));
@@ -706,9 +733,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             else mbar_arrive(tempty_bar(a));
         };
         int it = 0;
-        for (int t = unit; t < ntiles; t += nunits, ++it) {
-            int mi, ni;
-            tile_mn(t, mi, ni);
+        for (int t = unit; t < items; t += nunits, ++it) {
+            int mi, ni, tile, kb0, kb1;
+            const int kpart = item(t, tile, kb0, kb1);   // >= 0: an item of a split tile
+            tile_mn(tile, mi, ni);
             const int as = it & 1;
             const uint32_t aphase = (it >> 1) & 1;
             const bool mhi = ep.msplit_mt > 0 && mi >= ep.msplit_mt;   // a row block of the second product
@@ -723,14 +751,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint4 pre[8], pre2[8];   // EPI_ACCUM: fp32 sum blocks c and c + 1, in flight
             const uint32_t rows = __ballot_sync(0xffffffffu, row_ok);   // bit r: row - lane + r is in range
             uint8_t* ablk = nullptr;
+            const bool part = KSPLIT && kpart >= 0;   // its sums alone, in rows of BN
+            const int acc_read = part ? 0 : ep.acc_read, acc_write = part ? 1 : ep.acc_write;
+            const int out_write = part ? 0 : ep.out_write;
+            const int64_t lda = part ? BN : ep.lda;
             if (EPI == EPI_ACCUM) {
-                ablk = reinterpret_cast<uint8_t*>(ep.acc + static_cast<int64_t>(row - lane) * ep.lda + n0);
+                ablk = reinterpret_cast<uint8_t*>(
+                    part ? ep.kpart + (static_cast<int64_t>(kpart) * Cfg::TM + static_cast<int>(crank) * BM + q * 32) * BN
+                         : ep.acc + static_cast<int64_t>(row - lane) * ep.lda + n0);
                 if (row_ok && ep.lstart != nullptr) {
                     k_lo = ep.lstart[row];
                     k_hi = ep.lstart[row + 1];
                 }
-                load_block<8, true>(lane, ablk, ep.lda * 4, ep.acc_read ? rows : 0u, chunks_below(n0, ep.N, 4, 8), pre);
-                load_block<8, true>(lane, ablk + 128, ep.lda * 4, ep.acc_read ? rows : 0u, chunks_below(n0 + 32, ep.N, 4, 8),
+                load_block<8, true>(lane, ablk, lda * 4, acc_read ? rows : 0u, chunks_below(n0, ep.N, 4, 8), pre);
+                load_block<8, true>(lane, ablk + 128, lda * 4, acc_read ? rows : 0u, chunks_below(n0 + 32, ep.N, 4, 8),
                                     pre2);
             }
             const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(as), aphase));
@@ -1123,9 +1157,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                                     ? reinterpret_cast<uint8_t*>(obase + static_cast<int64_t>(row - lane) * ep.ldo + n0)
                                     : nullptr;
                 const int64_t ylab = (row_ok && ep.labels != nullptr) ? ep.labels[row] : ep.ignore_index;
-                const bool zero_row = ep.labels != nullptr && ylab == ep.ignore_index;
+                const bool zero_row = !part && ep.labels != nullptr && ylab == ep.ignore_index;
                 const __nv_bfloat16* lrow = (ep.labels != nullptr && ep.corr_src != nullptr && ep.keys == nullptr &&
-                                             row_ok && !zero_row)
+                                             row_ok && !zero_row && !part)
                                                 ? ep.corr_src + ylab * ep.ld_corr + n0
                                                 : nullptr;
                 const int nseg = ep.nseg > 1 ? ep.nseg : 1;
@@ -1134,11 +1168,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) {
                     __syncwarp();   // the previous block's row runs have been read
-                    if (ep.acc_read) {
+                    if (acc_read) {
                         uint4(&cur)[8] = (c & 1) ? pre2 : pre;
                         stage_block<8>(s_acc, lane, cur);   // block c, fetched two blocks ahead
                         if (c + 2 < BN / 32)
-                            load_block<8, true>(lane, ablk + (c + 2) * 128, ep.lda * 4, rows,
+                            load_block<8, true>(lane, ablk + (c + 2) * 128, lda * 4, rows,
                                                 chunks_below(n0 + (c + 2) * 32, ep.N, 4, 8), cur);
                     }
                     float v[32];
@@ -1160,7 +1194,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.f;
                     }
-                    if (ep.acc_read) {
+                    if (acc_read) {
                         __syncwarp();
                         uint4 o[8];
                         unstage_row<8>(s_acc, lane, o);
@@ -1172,7 +1206,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             for (int e = 0; e < 4; ++e) v[g * 4 + e] += f[e];
                         }
                     }
-                    if (ep.acc_write) {   // this lane's row only: no other lane reads it before the next barrier
+                    if (acc_write) {   // this lane's row only: no other lane reads it before the next barrier
                         uint4 w[8];
 #pragma unroll
                         for (int g = 0; g < 8; ++g) {
@@ -1181,15 +1215,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         stage_row<8>(s_acc, lane, w);
                     }
-                    if (ep.out_write) {
+                    if (out_write) {
                         const uint4 u[4] = {pack_bf8(v), pack_bf8(v + 8), pack_bf8(v + 16), pack_bf8(v + 24)};
                         stage_row<4>(s_out, lane, u);
                     }
                     __syncwarp();
-                    if (ep.acc_write)
-                        store_block<8, true>(s_acc, lane, ablk + c * 128, ep.lda * 4, rows,
+                    if (acc_write)
+                        store_block<8, true>(s_acc, lane, ablk + c * 128, lda * 4, rows,
                                              chunks_below(n0 + c * 32, ep.N, 4, 8));
-                    if (ep.out_write)
+                    if (out_write)
                         store_block<4, true>(s_out, lane, oblk + c * 64, ep.ldo * 2, rows,
                                              chunks_below(n0 + c * 32, ep.N, 8, 4));
                 }
@@ -1284,7 +1318,8 @@ int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int 
         }
         units_of[dev].store(max_units, std::memory_order_release);
     }
-    const int tiles = ((M + Cfg::TM - 1) / Cfg::TM) * ((N + BN - 1) / BN);
+    int tiles = ((M + Cfg::TM - 1) / Cfg::TM) * ((N + BN - 1) / BN);
+    if (ep.ksplits > 0) tiles += (tiles - ep.full_tiles) * (ep.ksplits - 1);   // work items
     int units = max_units;
     if (grid_limit > 0) units = std::min(units, PAIR ? std::max(1, grid_limit / 2) : grid_limit);
     units = std::max(1, std::min(units, tiles));
