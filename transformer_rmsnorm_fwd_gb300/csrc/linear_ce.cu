@@ -946,7 +946,8 @@ int launch_logits(const __nv_bfloat16* Xc, int cl, int H, int V, const CUtensorM
 // pairs, 2000 k-blocks each), so the last, partly filled round of tiles, which may be the only one, is
 // split along K over the idle pairs, each item leaving fp32 sums that dx_join adds up.  Above
 // kDxSlabRows vocabulary rows in several rounds the launches go over slabs as for the cross-entropy.
-// Times at hidden 4096, vocabulary 128256 with and without the split: DXTIMES.
+// At hidden 4096, vocabulary 128256, with the split and without: 256 tokens 211 and 619 us, 2741 tokens
+// 1618 and 1881 us.
 constexpr int kPairs = 80;               // most CTA pairs planned for
 constexpr int kDxMinBlocks = 16;         // fewest k-blocks of an item
 constexpr int64_t kDxMaxSlabs = 4;       // slabs whose split sums the workspace holds
