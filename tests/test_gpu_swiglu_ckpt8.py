@@ -175,7 +175,10 @@ def _linear_inputs(T, H, I, seed):
 
 
 @pytest.mark.parametrize("T,H,I", [(1, 64, 8), (3, 72, 40), (130, 128, 136), (257, 520, 696), (300, 1024, 256), (64, 64, 1376),
-                                   (5000, 256, 320)])
+                                   (5000, 256, 320),
+                                   # dX split along K over idle CTA pairs: one row, part of a row tile, several
+                                   # column tiles, k ranges that do not divide the k-blocks
+                                   (1, 112, 9016), (7, 520, 2056), (200, 264, 8200), (300, 72, 6000)])
 def test_linear_step(L, T, H, I):
     X, Wg, Wu, dH = _linear_inputs(T, H, I, T)
     g8, gs = L.liger_ckpt8_empty(T, I)

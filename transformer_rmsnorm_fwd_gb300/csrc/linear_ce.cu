@@ -944,7 +944,7 @@ int launch_logits(const __nv_bfloat16* Xc, int cl, int H, int V, const CUtensorM
 // ---- dX of the policy loss
 // K is the whole vocabulary and the tiles are few (256 tokens at hidden 4096: 16 tiles for 76 CTA
 // pairs, 2000 k-blocks each), so the last, partly filled round of tiles, which may be the only one, is
-// split along K over the idle pairs, each item leaving fp32 sums that dx_join adds up.  Above
+// split along K over the idle pairs, each item leaving fp32 sums that split_join adds up.  Above
 // kDxSlabRows vocabulary rows in several rounds the launches go over slabs as for the cross-entropy.
 // At hidden 4096, vocabulary 128256, with the split and without: 256 tokens 211 and 619 us, 2741 tokens
 // 1618 and 1881 us.
@@ -970,55 +970,6 @@ DxPlan dx_plan(int64_t rows, int64_t H, int64_t V) {
         p.splits = static_cast<int>(std::min<int64_t>(pairs / p.rem, ceil_div(p.slab, int64_t{tc::BK}) / kDxMinBlocks));
     if (p.splits < 2) p.splits = 0;
     return p;
-}
-
-// out = the sum of a split tile's items (slabs x splits of them, in that order) minus the one-hot part
-__global__ void __launch_bounds__(256) dx_join(const float* __restrict__ part, int items, int rem, int slabs, int full,
-                                               int num_n, int num_m, const int64_t* __restrict__ labels,
-                                               int64_t ignore, const float* __restrict__ tok_scale,
-                                               const __nv_bfloat16* __restrict__ W, __nv_bfloat16* out, int rows, int H) {
-    // the tile's row and column block, as the kernel's raster over groups of 8 column blocks gives them
-    const int t = full + static_cast<int>(blockIdx.x);
-    int mi, ni;
-    const int gfull = num_n / tc::GROUP_N, in_full = gfull * num_m * tc::GROUP_N;
-    if (t < in_full) {
-        const int g = t / (num_m * tc::GROUP_N), w = t - g * num_m * tc::GROUP_N;
-        mi = w / tc::GROUP_N;
-        ni = g * tc::GROUP_N + (w - mi * tc::GROUP_N);
-    } else {
-        const int width = num_n - gfull * tc::GROUP_N, w = t - in_full;
-        mi = w / width;
-        ni = gfull * tc::GROUP_N + (w - mi * width);
-    }
-    const int splits = items / rem;
-    // a block takes 8 rows of the tile: 32 threads a row, 8 columns each
-    const int lr = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5), lc = (threadIdx.x & 31) * 8;
-    const int row = mi * 256 + lr, col = ni * 256 + lc;
-    if (row >= rows || col >= H) return;
-    float v[8] = {};
-    for (int sl = 0; sl < slabs; ++sl)
-        for (int s = 0; s < splits; ++s) {
-            const float* src = part + ((static_cast<int64_t>(sl) * items + s * rem + blockIdx.x) * 256 + lr) * 256 + lc;
-            float f[4], g[4];
-            unpack(ldg16_cs(src), f);
-            unpack(ldg16_cs(src + 4), g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[e] += f[e];
-                v[4 + e] += g[e];
-            }
-        }
-    const int64_t y = labels[row];
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (y != ignore) {
-        const float c = tok_scale[row];
-        float w[8];
-        unpack(ldg16(W + y * H + col), w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(-c, w[e], v[e]);
-        o = pack(v);
-    }
-    stg16(out + static_cast<int64_t>(row) * H + col, o);
 }
 
 // dX of the cl rows of the chunk at t0: D = P [cl, V], e as set up for the chunk
@@ -1058,15 +1009,16 @@ int policy_dx(const Args& a, const Layout& L, const __nv_bfloat16* P, const tc::
         if (p.splits > 0) {
             d.full_tiles = p.full;
             d.ksplits = p.splits;
+            d.kpart_rows = TileCfg<1>::TM;
             d.kpart = a.pol->kpart + (v0 / p.slab) * items * kTileFloats;
         }
-        if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1, 1>(mD, mW, cl, H, vl, d, a.st))) return rc;
+        if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1, MODE_TOKENS>(mD, mW, cl, H, vl, d, a.st))) return rc;
     }
     if (p.splits == 0) return LIGER_OK;
-    dx_join<<<dim3(static_cast<unsigned>(p.rem), 32), 256, 0, a.st>>>(
-        a.pol->kpart, items, p.rem, p.slabs, p.full, static_cast<int>(ceil_div(H, 256)), static_cast<int>(ceil_div(cl, 256)),
-        a.labels + t0, a.ignore, e.tok_scale, W, out, cl, H);
-    return check_launch("dx_join");
+    const SplitJoin j{a.pol->kpart, p.rem, p.splits, p.slabs, p.full, TileCfg<1>::TM, static_cast<int>(ceil_div(cl, 256)),
+                      static_cast<int>(ceil_div(H, 256)), a.labels + t0, a.ignore, e.tok_scale, W, out, cl, H};
+    split_join<<<dim3(static_cast<unsigned>(p.rem), TileCfg<1>::TM / 8), 256, 0, a.st>>>(j);
+    return check_launch("linear_policy dX");
 }
 
 int run_tc(const Args& a, const Layout& L, float scale) {
@@ -1216,7 +1168,7 @@ int run_tc(const Args& a, const Layout& L, float scale) {
             d.acc_read = first ? 0 : 1;
             d.acc_write = last ? 0 : 1;
             d.out_write = last ? 1 : 0;
-            rc = a.pol != nullptr ? launch_gemm<1, 1, EPI_ACCUM, 1, 1>(mD_mn, mX_mn, V, H, cl, d, a.st)
+            rc = a.pol != nullptr ? launch_gemm<1, 1, EPI_ACCUM, 1, MODE_TOKENS>(mD_mn, mX_mn, V, H, cl, d, a.st)
                                   : launch_gemm<1, 1, EPI_ACCUM, 1>(mD_mn, mX_mn, V, H, cl, d, a.st);
             if (rc) return rc;
         }

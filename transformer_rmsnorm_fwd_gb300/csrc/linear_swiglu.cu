@@ -130,9 +130,12 @@ int fwd_impl(const void* X, const void* Wg, const void* Wu, void* out, void* g_s
 
 // dX = dG W_g + dU W_u (one GEMM over K = 2I) and dW_g = dG^T X, dW_u = dU^T X,
 // from dG and dU [T, I] bf16.
+// split_dx: with few tiles of dX, K is split over the idle CTA pairs, the items' fp32 sums standing in
+// dW_g's memory, which is not written before dX is done (backward of one token at hidden 112, intermediate 9016:
+// 35 us, 97 without; of 256 tokens at 4096, 11008: 150 and 202).
 int grads_from_dgdu(const void* X, const void* Wg, const void* Wu, const __nv_bfloat16* dG,
                     const __nv_bfloat16* dU, void* dX, void* dWg, void* dWu, int64_t T, int64_t H, int64_t I,
-                    int* d_err, cudaStream_t st) {
+                    int* d_err, cudaStream_t st, bool split_dx = false) {
     using namespace tc;
     int rc;
     CUtensorMap mdG_k, mdU_k, mG_mn, mU_mn;
@@ -149,9 +152,29 @@ int grads_from_dgdu(const void* X, const void* Wg, const void* Wu, const __nv_bf
     d.ldo = H;
     d.ksplit_nkb = nkb1;
     d.raster = RASTER_N_GROUPS;
-    if ((rc = launch_gemm<0, 1, EPI_STORE, 1>(mdG_k, mG_mn, static_cast<int>(T), static_cast<int>(H), 2 * nkb1 * BK,
-                                              d, st, 0, &mdU_k, &mU_mn)))
+    // items of at least 16 k-blocks, as many as there are CTA pairs and dW_g's bytes hold
+    const int64_t tm = ceil_div(T, static_cast<int64_t>(TileCfg<1>::TM)), tn = ceil_div(H, static_cast<int64_t>(BN));
+    const int64_t rows = std::min<int64_t>(T, TileCfg<1>::TM);
+    const int64_t splits = !split_dx ? 0 : std::min<int64_t>({sm_count() / 2 / (tm * tn), 2 * nkb1 / 16,
+                                                              I * H * 2 / (tm * tn * rows * BN * 4)});
+    if (splits >= 2) {
+        d.acc_write = 0;
+        d.out_write = 1;
+        d.full_tiles = 0;
+        d.ksplits = static_cast<int>(splits);
+        d.kpart_rows = static_cast<int>(rows);
+        d.kpart = static_cast<float*>(dWg);
+        if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1, MODE_SPLIT>(mdG_k, mG_mn, static_cast<int>(T), static_cast<int>(H),
+                                                              2 * nkb1 * BK, d, st, 0, &mdU_k, &mU_mn)))
+            return rc;
+        const SplitJoin j{d.kpart, static_cast<int>(tm * tn), d.ksplits, 1, 0, d.kpart_rows, static_cast<int>(tm),
+                          static_cast<int>(tn), nullptr, 0, nullptr, nullptr, d.out, d.M, d.N};
+        split_join<<<dim3(static_cast<unsigned>(tm * tn), static_cast<unsigned>(ceil_div(rows, int64_t{8}))), 256, 0, st>>>(j);
+        if ((rc = check_launch("fused_linear_swiglu dX"))) return rc;
+    } else if ((rc = launch_gemm<0, 1, EPI_STORE, 1>(mdG_k, mG_mn, static_cast<int>(T), static_cast<int>(H),
+                                                     2 * nkb1 * BK, d, st, 0, &mdU_k, &mU_mn))) {
         return rc;
+    }
     CUtensorMap mdG_mn, mdU_mn, mX_mn;
     if ((rc = make_map(&mdG_mn, dG, I, T, I, MN_BOX, BK))) return rc;
     if ((rc = make_map(&mdU_mn, dU, I, T, I, MN_BOX, BK))) return rc;
@@ -283,7 +306,7 @@ namespace {
 template <typename DgDu>
 int bwd_kept(const char* who, const void* X, const void* Wg, const void* Wu, const void* dH, const void* g, const void* u,
              void* dX, void* dWg, void* dWu, void* ws, size_t ws_bytes, int64_t T, int64_t H, int64_t I, int dtype,
-             cudaStream_t st, DgDu dgdu) {
+             cudaStream_t st, DgDu dgdu, bool split_dx = false) {
     if (int rc = check_shapes(T, H, I, dtype, who)) return rc;
     if (!Wg || !Wu || !dWg || !dWu || (T > 0 && (!X || !dH || !g || !u || !dX)))
         return fail(LIGER_ERR_NULL, "%s: null tensor pointer", who);
@@ -307,7 +330,7 @@ int bwd_kept(const char* who, const void* X, const void* Wg, const void* Wu, con
     // 1. dG, dU from dh and the saved g, u (the elementwise SwiGLU backward)
     if (int rc = dgdu(dG, dU)) return rc;
     // 2-3. as in the backward with recompute
-    return grads_from_dgdu(X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st);
+    return grads_from_dgdu(X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st, split_dx);
 }
 
 }  // namespace
@@ -336,5 +359,6 @@ extern "C" int liger_fused_linear_swiglu_bwd_ckpt8(const void* X, const void* Wg
                     [&](__nv_bfloat16* dG, __nv_bfloat16* dU) {
                         return liger_swiglu_bwd_ckpt8(dH, gate8, gate_scale, up8, up_scale, dG, dU, T, I, LIGER_BF16,
                                                       stream);
-                    });
+                    },
+                    true);
 }

@@ -93,6 +93,9 @@ enum Epi : int {
 enum Raster : int { RASTER_M_FASTEST = 0, RASTER_N_FASTEST = 1, RASTER_N_GROUPS = 2 };
 constexpr int GROUP_N = 8;
 
+// Variants of a kernel (template parameter MODE)
+enum Mode : int { MODE_PLAIN = 0, MODE_TOKENS = 1, MODE_SPLIT = 2 };
+
 enum Err : int { ERR_TMA_EMPTY = 1, ERR_MMA_FULL = 2, ERR_MMA_TMEM = 3, ERR_EPI_TMEM = 4 };
 
 struct EpiParams {
@@ -125,7 +128,7 @@ struct EpiParams {
     int64_t ld_corr;
     float corr_scale;
     const float* scale_ptr;             // non-null: corr_scale is read from here (set on the device)
-    // TOKSCALE kernels: a scale for each token in place of corr_scale (the token is the row, or
+    // MODE_TOKENS kernels: a scale for each token in place of corr_scale (the token is the row, or
     // the key's t)
     const float* tok_scale;
     // The keys may come in nseg sorted segments with one start table each,
@@ -135,11 +138,12 @@ struct EpiParams {
     const int* lstart;
     int nseg;
     int64_t lstride;
-    // Work of a TOKSCALE EPI_ACCUM kernel with K-major A whose tiles leave SMs idle: the tiles from
-    // full_tiles on are split along K into ksplits items each (ksplits 0: none are).  An item leaves its
-    // fp32 sums, TM rows of BN, in kpart[item] and nothing else: the caller adds them up and applies what
-    // the epilogue does to whole tiles.  Items of one k range follow each other.
-    int full_tiles, ksplits;
+    // Work of a MODE_TOKENS or MODE_SPLIT EPI_ACCUM kernel with K-major A whose tiles leave SMs idle:
+    // the tiles from full_tiles on are split along K into ksplits items each (ksplits 0: none are).  An
+    // item leaves its fp32 sums, kpart_rows (TM, or M if that is less) rows of BN, in kpart[item] and
+    // nothing else: split_join adds them up and applies what the epilogue does to whole tiles.  Items of
+    // one k range follow each other.
+    int full_tiles, ksplits, kpart_rows;
     float* kpart;
     // EPI_SOFTMAX: out[row, col] = corr_scale * exp(z - lse[row]) (bf16; +0 on rows
     // labelled ignore_index), the softmax part of the logit gradient
@@ -470,7 +474,7 @@ __device__ __forceinline__ uint4 pack_bf8(const float* f) {
 // one-time attribute set in one unit never stands in for another's.
 namespace {
 
-template <int A_MN, int B_MN, int EPI, int PAIR = 0, int TOKSCALE = 0>
+template <int A_MN, int B_MN, int EPI, int PAIR = 0, int MODE = MODE_PLAIN>
 __global__ void __launch_bounds__(THREADS, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2, int M, int N,
@@ -498,7 +502,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int ntiles = num_m * num_n;
     const int nkb = (K + BK - 1) / BK;
     // work items: the tiles, or whole tiles and then (k range, tile) for the split ones
-    constexpr bool KSPLIT = TOKSCALE && EPI == EPI_ACCUM && !A_MN;
+    constexpr bool TOKSCALE = MODE == MODE_TOKENS;
+    constexpr bool KSPLIT = MODE != MODE_PLAIN && EPI == EPI_ACCUM && !A_MN;
     const int split_tiles = KSPLIT && ep.ksplits > 0 ? ntiles - ep.full_tiles : 0;
     const int items = ntiles + split_tiles * (ep.ksplits - 1);
     const int kb_per = KSPLIT && ep.ksplits > 0 ? (nkb + ep.ksplits - 1) / ep.ksplits : nkb;
@@ -757,7 +762,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t lda = part ? BN : ep.lda;
             if (EPI == EPI_ACCUM) {
                 ablk = reinterpret_cast<uint8_t*>(
-                    part ? ep.kpart + (static_cast<int64_t>(kpart) * Cfg::TM + static_cast<int>(crank) * BM + q * 32) * BN
+                    part ? ep.kpart + (static_cast<int64_t>(kpart) * ep.kpart_rows + static_cast<int>(crank) * BM + q * 32) * BN
                          : ep.acc + static_cast<int64_t>(row - lane) * ep.lda + n0);
                 if (row_ok && ep.lstart != nullptr) {
                     k_lo = ep.lstart[row];
@@ -1286,12 +1291,12 @@ int make_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, i
 // 256 x 256 tiles.  grid_limit = 0: one block per SM (pairs: as many as fit).
 namespace {
 
-template <int A_MN, int B_MN, int EPI, int PAIR = 0, int TOKSCALE = 0>
+template <int A_MN, int B_MN, int EPI, int PAIR = 0, int MODE = MODE_PLAIN>
 int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int K, const EpiParams& ep,
                 cudaStream_t st, int grid_limit = 0, const CUtensorMap* ma2 = nullptr,
                 const CUtensorMap* mb2 = nullptr) {
     using Cfg = TileCfg<PAIR>;
-    auto kern = tc_gemm_kernel<A_MN, B_MN, EPI, PAIR, TOKSCALE>;
+    auto kern = tc_gemm_kernel<A_MN, B_MN, EPI, PAIR, MODE>;
     // per instantiation and device: function attributes belong to each device's context.
     // units_of[dev] = 0 until the attribute is set; threads that race here all set the
     // same attribute and store the same count (published with release / acquire).
@@ -1348,6 +1353,68 @@ int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int 
     }
     kern<<<units, THREADS, Cfg::SMEM, st>>>(ma, mb, ma2 ? *ma2 : ma, mb2 ? *mb2 : mb, M, N, K, ep);
     return check_launch("tc_gemm");
+}
+
+// bf16 out of the split tiles of a RASTER_N_GROUPS launch over CTA pairs: the sum of a tile's items, in
+// the order of the k ranges and, when the launches went over `slabs` runs of K (items apart), of
+// those.  With labels, minus tok_scale[row] corr[labels[row], :], and +0 on rows labelled `ignore`.
+struct SplitJoin {
+    const float* part;
+    int rem, splits, slabs, full, part_rows;   // rem tiles from `full` on
+    int num_m, num_n;
+    const int64_t* labels;
+    int64_t ignore;
+    const float* tok_scale;
+    const __nv_bfloat16* corr;
+    __nv_bfloat16* out;
+    int M, N;
+};
+__global__ void __launch_bounds__(256) split_join(SplitJoin p) {
+    constexpr int TM = TileCfg<1>::TM;
+    // the tile's row and column block, as the kernel's raster gives them
+    const int t = p.full + static_cast<int>(blockIdx.x);
+    const int gfull = p.num_n / GROUP_N, in_full = gfull * p.num_m * GROUP_N;
+    int mi, ni;
+    if (t < in_full) {
+        const int g = t / (p.num_m * GROUP_N), w = t - g * p.num_m * GROUP_N;
+        mi = w / GROUP_N;
+        ni = g * GROUP_N + (w - mi * GROUP_N);
+    } else {
+        const int width = p.num_n - gfull * GROUP_N, w = t - in_full;
+        mi = w / width;
+        ni = gfull * GROUP_N + (w - mi * width);
+    }
+    // a block takes 8 rows of the tile: 32 threads a row, 8 columns each
+    const int lr = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5), lc = (threadIdx.x & 31) * 8;
+    const int row = mi * TM + lr, col = ni * BN + lc;
+    if (row >= p.M || col >= p.N) return;
+    float v[8] = {};
+    const int items = p.slabs * p.splits;   // item i of this tile: slab i / splits, k range i % splits
+#pragma unroll 4
+    for (int i = 0; i < items; ++i) {
+        const float* src =
+            p.part + ((static_cast<int64_t>(i) * p.rem + blockIdx.x) * p.part_rows + lr) * BN + lc;
+        float f[4], g[4];
+        unpack(ldg16_cs(src), f);
+        unpack(ldg16_cs(src + 4), g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] += f[e];
+            v[4 + e] += g[e];
+        }
+    }
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (p.labels == nullptr) {
+        o = pack(v);
+    } else if (const int64_t y = p.labels[row]; y != p.ignore) {
+        const float c = p.tok_scale[row];
+        float w[8];
+        unpack(ldg16(p.corr + y * p.N + col), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(-c, w[e], v[e]);
+        o = pack(v);
+    }
+    stg16(p.out + static_cast<int64_t>(row) * p.N + col, o);
 }
 
 }  // namespace
