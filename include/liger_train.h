@@ -13,7 +13,11 @@
  *
  * Every call here except liger_linear_logp_fwd and liger_linear_policy_fwd_bwd
  * (which wait for their label scan) queues work only and can be captured in a
- * CUDA graph after a first call on the device.
+ * CUDA graph after a first call on the device.  A bounded wait that expires in a
+ * kernel (see liger.h) leaves NaN in the block norms' unfinished rows and sums,
+ * in logp and in the policy's loss and stats; liger_device_status names the
+ * block norms' as RMSNorm's and the 8-bit FusedLinearSwiGLU's as
+ * FusedLinearSwiGLU's.
  */
 #ifndef LIGER_TRAIN_H
 #define LIGER_TRAIN_H
@@ -116,7 +120,8 @@ int liger_swiglu_bwd_ckpt8(const void* dy, const int8_t* gate8, const uint8_t* g
  * backward reads them instead of recomputing g and u (8 T H I flops).
  * Arguments, shapes (bf16; H >= 64, H and I multiples of 8), workspace
  * (liger_fused_linear_swiglu_workspace) and errors otherwise as
- * liger_fused_linear_swiglu_fwd_save / _bwd_saved; codes 16-byte aligned. */
+ * liger_fused_linear_swiglu_fwd_save / _bwd_saved; codes 16-byte aligned.  dWg
+ * is written twice: sums of dX stand in it until dX is done. */
 int liger_fused_linear_swiglu_fwd_ckpt8(const void* X, const void* Wg, const void* Wu, void* out, int8_t* gate8,
                                         uint8_t* gate_scale, int8_t* up8, uint8_t* up_scale, int64_t T, int64_t H,
                                         int64_t I, int dtype, void* stream);

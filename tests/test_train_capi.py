@@ -45,6 +45,7 @@ def test_block_norm_fwd_checks(lib):
     assert _norm_fwd(lib, dtype=2) == -3
     assert _norm_fwd(lib, rows=-1) == -2 and _norm_fwd(lib, cols=0) == -2 and _norm_fwd(lib, gates=-1) == -2
     assert _norm_fwd(lib, gates=4) == -2                    # 6 rows
+    assert _norm_fwd(lib, rows=1 << 46, cols=1 << 20) == -2
     assert _norm_fwd(lib, gates=0) == -1 and _norm_fwd(lib, gate=None) == -1
     assert _norm_fwd(lib, eps=-1.0) == -2 and _norm_fwd(lib, eps=float("nan")) == -2
     for k in ("z", "r", "h", "y"):
@@ -70,6 +71,7 @@ def test_swiglu_ckpt8_checks(lib):
     for fn in (lib.liger_swiglu_fwd_ckpt8, lib.liger_swiglu_bwd_ckpt8):
         good = [OK] * 7
         assert fn(*good, 4, 64, 5, None) == -3
+        assert fn(*good, 1 << 40, 1 << 20, 1, None) == -2
         assert fn(*good, -1, 64, 1, None) == -2 and fn(*good, 4, -64, 1, None) == -2
         assert fn(*([None] * 7), 0, 64, 1, None) == 0
         for k in range(7):

@@ -95,7 +95,7 @@ int resident(K kern, int threads, size_t smem, std::atomic<int> (&cache)[64]) {
 
 inline int check_common(const char* who, int64_t rows, int64_t cols, int64_t gates, const void* gate, int dtype) {
     if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
-    if (rows < 0 || cols <= 0 || cols > (1 << 24) || gates < 0 || rows > (int64_t{1} << 40))
+    if (rows < 0 || cols <= 0 || cols > (1 << 24) || gates < 0 || rows > (int64_t{1} << 48) / cols)
         return fail(LIGER_ERR_SHAPE, "%s: rows=%lld cols=%lld gates=%lld", who, (long long)rows, (long long)cols,
                     (long long)gates);
     if (gates > 0 && rows % gates)

@@ -375,7 +375,7 @@ int launch_bwd(const void* dy, const int8_t* gate8, const uint8_t* gs, const int
 int check(const char* who, int64_t rows, int64_t cols, int dtype, std::initializer_list<const void*> wide,
           std::initializer_list<const void*> bytes) {
     if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
-    if (rows < 0 || cols < 0 || cols > (1 << 30) || rows > (int64_t{1} << 40))
+    if (rows < 0 || cols < 0 || cols > (1 << 30) || rows > (int64_t{1} << 48) / std::max<int64_t>(cols, 1))
         return fail(LIGER_ERR_SHAPE, "%s: rows=%lld cols=%lld", who, (long long)rows, (long long)cols);
     if (rows == 0 || cols == 0) return LIGER_OK;
     for (const void* p : wide)
