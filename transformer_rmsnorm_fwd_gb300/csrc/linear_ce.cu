@@ -490,6 +490,7 @@ struct Policy {
     float *term, *kl, *clip;                  // [T] w l, kl and 1 where clipped, by original token
     float* logp;                              // [T] by original token, or NULL
     float* kpart;                             // dX: the split tiles' sums
+    __nv_bfloat16* xpad;                      // [kPadRows][H]
 };
 
 // exp(d) - d - 1 without the cancellation of small d: its Taylor series (terms d^2 / 2! to d^9 / 9!,
@@ -916,6 +917,18 @@ int ensure_sort_attr() {
     return LIGER_OK;
 }
 
+// A GEMM over fewer rows of X than this is given them among rows of zeros: every CTA reads the same few
+// lines of X at the same time, and over one to fifteen rows they sit in so few L2 slices that this bounds
+// it (logits at 4096 x 128256: 1 token 305 us, 9 206, 10 264, 16 181).
+constexpr int64_t kPadRows = 16;
+int pad_rows(const __nv_bfloat16* X, int64_t n, int64_t H, __nv_bfloat16* pad, cudaStream_t st) {
+    const size_t row = static_cast<size_t>(H) * 2;
+    if (cudaMemsetAsync(pad + n * H, 0, (kPadRows - n) * row, st) != cudaSuccess ||
+        cudaMemcpyAsync(pad, X, n * row, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
+        return check_launch("rows of X");
+    return LIGER_OK;
+}
+
 // Z = X_c W^T for the cl rows at Xc with the logits epilogue e (its labels, zlab,
 // part and p_out set for row 0 of the chunk), in launches over rows_in_l2 rows: each
 // launch sweeps the whole vocabulary over its rows of X (an 8192-row chunk at hidden
@@ -1070,7 +1083,13 @@ int run_tc(const Args& a, const Layout& L, float scale) {
         e.part = part;
         e.nvt = static_cast<int>(L.nvt);
         e.zlab = zlab + t0;
-        if ((rc = launch_logits(Xc, cl, H, V, mW_k, e, L.ldp, L.nvt, a.st))) return rc;
+        if (a.pol != nullptr && cl < kPadRows) {
+            if ((rc = pad_rows(Xc, cl, H, a.pol->xpad, a.st))) return rc;
+            rc = launch_logits(a.pol->xpad, cl, H, V, mW_k, e, L.ldp, L.nvt, a.st, kPadRows);
+        } else {
+            rc = launch_logits(Xc, cl, H, V, mW_k, e, L.ldp, L.nvt, a.st);
+        }
+        if (rc) return rc;
         // 2. lse, loss terms, P -> D in place
         if (a.pol != nullptr)
             policy_rows_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
@@ -1623,7 +1642,7 @@ namespace {
 // Workspace of the policy loss: the cross-entropy's, then its own per-token arrays.
 struct PolicyLayout {
     Layout L;
-    size_t seq, n_seq, coef, term, kl, clip, split, kpart, total;
+    size_t seq, n_seq, coef, term, kl, clip, split, kpart, xpad, total;
 };
 
 // Tokens per chunk of the policy loss on the tensor-core path when the caller leaves it open: up to
@@ -1648,12 +1667,12 @@ PolicyLayout policy_layout(int64_t T, int64_t H, int64_t V, int64_t B, int64_t c
     P.split = o; o += P.L.tc ? 0 : sizeof(float) * static_cast<size_t>(kSplitFloats);
     // items of one launch: at most as many as CTA pairs
     P.kpart = o; o += P.L.tc ? sizeof(float) * static_cast<size_t>(kPairs * kTileFloats * std::min(kDxMaxSlabs, ceil_div(V, dx_slab(V)))) : 0;
+    P.xpad = o; o += P.L.tc ? up256(2 * static_cast<size_t>(kPadRows * H)) : 0;
     P.total = o;
     return P;
 }
 
 constexpr int64_t kFewParts = 4 * 2048;   // partials of the few-token path
-constexpr int64_t kPadRows = 16;          // rows of X that a GEMM over fewer is given (see run_logp_tc)
 
 // Workspace of the log-probabilities.  Tensor-core path: header, labels, z at the label, the row
 // partials of a chunk; then, for the form that drops ignored tokens, their X rows and index maps.
@@ -1800,6 +1819,10 @@ int read_hdr(const char* who, const Hdr* hdr, Hdr* out, cudaStream_t st) {
     return LIGER_OK;
 }
 
+// Whether dropping the tokens that are not valid saves a row tile of the GEMMs; if it does not, the
+// tokens run as they are (seven launches fewer).
+bool worth_compacting(int64_t n, int64_t T) { return ceil_div(n, int64_t{256}) < ceil_div(T, int64_t{256}); }
+
 unsigned scan_grid(int64_t T) { return static_cast<unsigned>(std::min<int64_t>(ceil_div(T, 256), 4 * sm_count())); }
 
 // Z = X_c W^T of cl rows off the tensor cores
@@ -1896,14 +1919,8 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
     }
     int64_t x_rows = 0;
     if (n < kPadRows) {
-        // Every CTA reads the same few lines of X at the same time; over one to fifteen rows they sit
-        // in so few L2 slices that this bounds the GEMM (9 tokens 206 us, 10 264 us, 16 181 us at 4096 x
-        // 128256), so X is read among rows of zeros.
         __nv_bfloat16* pad = reinterpret_cast<__nv_bfloat16*>(w8 + L.comp.dxc);
-        const size_t row = static_cast<size_t>(H) * 2;
-        if (cudaMemsetAsync(pad, 0, kPadRows * row, st) != cudaSuccess ||
-            cudaMemcpyAsync(pad, X, n * row, cudaMemcpyDeviceToDevice, st) != cudaSuccess)
-            return check_launch("linear_logp rows of X");
+        if ((rc = pad_rows(X, n, H, pad, st))) return rc;
         X = pad;
         x_rows = kPadRows;
     }
@@ -1994,6 +2011,7 @@ int logp_impl(const char* who, const void* X, const void* W, const int64_t* labe
                    : run_logp_simt<__nv_bfloat16>(X, W, labs, T, (int)H, (int)V, ignore, logp, w8, L, st);
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16*>(X), *w = static_cast<const __nv_bfloat16*>(W);
     const int64_t* idx = nullptr;
+    if (n < T && !worth_compacting(n, T)) n = T;
     if (n < T) {   // only the tokens that are not ignored, in order
         int* cnt = reinterpret_cast<int*>(w8 + L.comp.cnt);
         int64_t* at = reinterpret_cast<int64_t*>(w8 + L.comp.idx);
@@ -2074,10 +2092,11 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
         return ok ? LIGER_OK : check_launch("linear_policy memset");
     }
     const Policy pol{old_logp, ref_logp, adv, flags & LIGER_POLICY_ADV_PER_TOKEN, reduction, 1.f - eps_low, 1.f + eps_high,
-                     beta, grad_scale, seq, n_seq, hdr, B, f32(PL.coef), f32(PL.term), f32(PL.kl), f32(PL.clip), logp, f32(PL.kpart)};
+                     beta, grad_scale, seq, n_seq, hdr, B, f32(PL.coef), f32(PL.term), f32(PL.kl), f32(PL.clip), logp, f32(PL.kpart),
+                     reinterpret_cast<__nv_bfloat16*>(w8 + PL.xpad)};
     const Args a{X, W, labs, T, H, V, ignore, reduction, grad_scale, loss, dX, dW, w8, dtype, st, nullptr, &pol, nullptr};
     int rc;
-    if (PL.L.tc) rc = n < T ? run_tc_compact(a, n, chunk, 0.f) : run_tc(a, PL.L, 0.f);
+    if (PL.L.tc) rc = n < T && worth_compacting(n, T) ? run_tc_compact(a, n, chunk, 0.f) : run_tc(a, PL.L, 0.f);
     else rc = dtype == LIGER_F32 ? run_policy_simt<float>(a, PL.L, f32(PL.split)) : run_policy_simt<__nv_bfloat16>(a, PL.L, f32(PL.split));
     if (rc) return rc;
     policy_final<<<1, kFinalThreads, 0, st>>>(f32(PL.term), f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
