@@ -57,7 +57,9 @@ def _forward(L, d, a, b, rows, in_place=False):
 
 
 SHAPES = [(1, 1), (1, 4096), (3, 64), (5, 33), (257, 1001), (64, 8192), (7, 520), (300, 4096), (2, 16384), (4, 20000),
-          (1000, 256), (33, 2050), (1, 65), (700, 129), (400, 1023), (301, 3001), (330, 4095), (200, 5003), (160, 8191), (400, 2047)]
+          (1000, 256), (33, 2050), (1, 65), (700, 129), (400, 1023), (301, 3001), (330, 4095), (200, 5003), (160, 8191), (400, 2047),
+          # rows enough for every form of the staged kernels: several teams a block, one, wide rows
+          (5000, 256), (3000, 512), (2500, 640), (320, 1536), (330, 5120), (400, 8192), (170, 12288), (170, 16384)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -84,6 +86,20 @@ def test_forward(L, rows, cols, dtype):
                 check(y, y64, (mag * rh64[:, None] + h64.abs() * (rh64 * scale)[:, None]) * w, 2 * chain, "y")
             else:
                 assert bool((rh == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,gates", [(3000, 1024, 6), (3000, 1024, 750), (6000, 256, 1500), (6000, 512, 2000),
+                                             (400, 4096, 8), (400, 4096, 200), (336, 6144, 7), (1200, 1001, 300), (900, 77, 90)])
+def test_forward_gate_rows(L, rows, cols, gates, dtype):
+    """Gate rows shared by some rows, that teams of warps meet in every order."""
+    d = _make(rows, cols, dtype, True, gates, True, seed=4)
+    h, y, rz, rh = _forward(L, d, 1.0, 0.8, rows)
+    h64, y64, rz64, rh64, mag = _fwd64(d, 1.0, 0.8, rows, gates)
+    chain = cols / 32 + 40
+    check(h, h64, mag, chain, "h")
+    scale = (mag.square().mean(1) + EPS).sqrt() * rh64
+    check(y, y64, (mag * rh64[:, None] + h64.abs() * (rh64 * scale)[:, None]) * d["w_pre"].double().abs(), 2 * chain, "y")
 
 
 def _bwd64(d, h, a, b, rows, gates):

@@ -130,7 +130,8 @@ template <typename T, int VPT, int WHOLE, int NT, int ONE>
 __global__ void __launch_bounds__(NT, 1) block_norm_bwd_ring(BwdP p, int tw, int nst, int* err) {
     constexpr int VEC = Vec<T>::N, NP = VEC / 2;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ __align__(16) float red[2][3][(NT / 32 + 3) / 4 * 4 + 4];
+    // per team its warps' sums, from a multiple of 4: at most 4 entries for every 2 warps
+    __shared__ __align__(16) float red[2][3][NT / 32 * 2];
     __shared__ int failed;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (ONE) tw = blockDim.x >> 5;
