@@ -171,15 +171,15 @@ int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* lab
  *   adv: float [B], or [T] with LIGER_POLICY_ADV_PER_TOKEN in flags.
  *   old_logp float [T]; ref_logp float [T], may be NULL when beta is 0 (then no
  *   kl).  Nothing of old_logp, ref_logp or a per-token adv is read at tokens that are
- *   not valid.  0 <= eps_low <= 1, eps_high >= 0.
+ *   not valid, and X may hold anything there.  0 <= eps_low <= 1, eps_high >= 0.
  *   loss: one float; stats: two floats or NULL, the mean kl and the share of
  *   clipped tokens over the valid tokens; logp: float [T] or NULL, 0 at tokens
  *   that are not valid; dX [T, H], dW [V, H] in dtype, each may be NULL.  Rows
  *   of dX of tokens that are not valid are written as +0.
  *   Token chunks and the GEMM path by dtype and shape are as in
  *   liger_linear_ce_fwd_bwd, but chunk 0 is min(T, 8192) on the tensor-core
- *   path: per chunk the logits exist only in a [chunk x V] workspace buffer.  ws: at least liger_linear_policy_workspace bytes,
- *   256-byte aligned.
+ *   path: per chunk the logits exist only in a [chunk x V] workspace buffer.
+ *   ws: at least liger_linear_policy_workspace bytes, 256-byte aligned.
  *   The call waits for a scan of the labels and sequences: a bad label returns
  *   LIGER_ERR_LABEL, bad cu_seqlens LIGER_ERR_SHAPE, with nothing else queued,
  *   and only valid tokens go through the GEMMs.  The _async form does not wait

@@ -266,6 +266,31 @@ def test_non_finite_inputs_reach_the_loss(L):
 
 
 @pytest.mark.parametrize("wait", [True, False])
+@pytest.mark.parametrize("T,H,V,dt,masked,chunk", [(200, 64, 300, "bf16", 0.3, 0), (900, 128, 600, "bf16", 0.7, 0),
+                                                   (900, 128, 600, "bf16", 0.05, 256), (9, 72, 1003, "bf16", 0.5, 0),
+                                                   (8300, 64, 300, "bf16", 0.01, 8300), (77, 40, 300, "bf16", 0.4, 32),
+                                                   (120, 33, 100, "f32", 0.4, 0), (120, 33, 100, "f32", 0.4, 50)])
+def test_hidden_states_of_tokens_that_are_not_valid(L, T, H, V, dt, masked, chunk, wait):
+    """Padding may hold anything: NaN and infinities in X at masked tokens and outside the sequences reach no output."""
+    i = _inputs(T, H, V, dt, [2, T // 2, T - 3], seed=T, masked=masked)
+    args = (dt, "seq_mean", 0.2, 0.2, 0.05, 1.0)
+    clean = _call(L, i, *args, wait=wait, chunk=chunk)
+    junk = i["X"].clone()
+    junk[~i["valid"]] = float("nan")
+    junk[0] = float("inf")
+    got = _call(L, dict(i, X=junk), *args, wait=wait, chunk=chunk)
+    for k, v in clean.items():
+        assert torch.equal(got[k], v) and bool(torch.isfinite(v).all()), k
+    out, ws = [], torch.empty(L.liger_linear_logp_workspace(T, H, V, _code(L, dt)), dtype=torch.uint8, device="cuda")
+    for X in (i["X"], junk):
+        logp = torch.full((T,), 7.0, device="cuda")
+        lab = torch.where(i["valid"], i["labels"], IGN)
+        L.liger_linear_logp_fwd(X, i["W"], lab, logp, ws, wait=wait)
+        out.append(logp)
+    assert torch.equal(*out) and bool(torch.isfinite(out[0]).all())
+
+
+@pytest.mark.parametrize("wait", [True, False])
 @pytest.mark.parametrize("T,H,V,dt", [(1, 64, 256, "bf16"), (1, 512, 5000, "bf16"), (300, 320, 2037, "bf16"), (77, 40, 300, "bf16"),
                                       (65, 33, 100, "f32"), (1, 3, 2, "f32"), (9000, 64, 300, "bf16"),
                                       (2, 128, 300, "bf16"), (3, 72, 1003, "bf16"), (4, 4096, 5001, "bf16"), (5, 256, 257, "bf16"),

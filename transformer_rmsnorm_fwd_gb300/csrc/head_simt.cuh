@@ -24,6 +24,7 @@ struct HeadGemm {
     int splits, k_per;        // K split into `splits` runs of k_per (a multiple of kHK)
     float* part;              // [splits][M][N] when splits > 1
     const int64_t* labels;    // rows labelled `ignore` are written +0 (NULL: none)
+    const int64_t* klabels;   // B's rows k labelled `ignore` count as zeros, whatever they hold (NULL: none)
     int64_t ignore;
     int add;                  // out += (fp32 outputs)
     const float* base;        // added before the store (the sum of earlier chunks), ldo apart, or NULL
@@ -54,7 +55,9 @@ __global__ void __launch_bounds__(256) head_gemm(const TA* __restrict__ A, const
             const int mm = ak ? e / kHK : e % kHT, ka = ak ? e % kHK : e / kHT;
             const int nn = bn ? e % kHT : e / kHK, kb = bn ? e / kHT : e % kHK;
             ra[i] = m0 + mm < g.M && k + ka < k1 ? ldf(A + (m0 + mm) * g.sam + (k + ka) * g.sak) : 0.f;
-            rb[i] = n0 + nn < g.N && k + kb < k1 ? ldf(B + (k + kb) * g.sbk + (n0 + nn) * g.sbn) : 0.f;
+            const bool in = n0 + nn < g.N && k + kb < k1;
+            rb[i] = in ? ldf(B + (k + kb) * g.sbk + (n0 + nn) * g.sbn) : 0.f;
+            if (g.klabels != nullptr && in && g.klabels[k + kb] == g.ignore) rb[i] = 0.f;
         }
     };
     auto put = [&](int buf) {
