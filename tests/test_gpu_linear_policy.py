@@ -306,6 +306,30 @@ def test_logp(L, T, H, V, dt, wait):
         assert bool((logp[~i["valid"]] == 0).all())
 
 
+@pytest.mark.parametrize("T,V", [(1, 300), (2, 5000), (3, 70001), (4, 300), (5, 300), (40, 5000)])
+def test_logp_of_non_finite_rows_of_the_head(L, T, V):
+    """A row of W whose logit is -inf has probability 0, wherever it stands; a NaN row makes every logp NaN."""
+    i = _inputs(T, 64, V, "bf16", [0, T], seed=V, masked=0.0)
+    i["X"][:, 5] = 1.0
+    i["labels"].fill_(V // 2)
+    ws = torch.empty(L.liger_linear_logp_workspace(T, 64, V), dtype=torch.uint8, device="cuda")
+    for row in (0, 1, 2, 17, V - 1):
+        W = i["W"].clone()
+        W[row, 5] = float("-inf")
+        keep = torch.arange(V, device="cuda") != row
+        i2 = dict(i, W=W[keep], labels=i["labels"] - int(row < V // 2))
+        i2["old"] = i2["ref"] = torch.zeros(T, device="cuda")
+        r = _ref(i2, "sum", 0.2, 0.2, 0.0, 1.0)
+        for value, wait in ((float("-inf"), True), (float("-inf"), False), (float("nan"), False)):
+            W[row, 5] = value
+            logp = torch.full((T,), 7.0, device="cuda")
+            L.liger_linear_logp_fwd(i["X"], W, i["labels"], logp, ws, wait=wait)
+            if value == value:
+                assert bool(((logp.double() - r["logp"]).abs() <= r["eps"]).all()), row
+            else:
+                assert bool(torch.isnan(logp).all()), row
+
+
 def test_logp_bad_label(L):
     i = _inputs(50, 64, 300, "bf16", [0, 50], masked=0.2)
     ws = torch.empty(L.liger_linear_logp_workspace(50, 64, 300), dtype=torch.uint8, device="cuda")

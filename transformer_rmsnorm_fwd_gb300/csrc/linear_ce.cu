@@ -1779,14 +1779,15 @@ __global__ void __launch_bounds__(256) logp_few(const __nv_bfloat16* __restrict_
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (v0 + r < V) top = fmaxf(top, z[r]);
+            const float base = top == -INFINITY ? 0.f : top;   // only -inf so far: exp(-inf) = 0, not NaN
             float add = 0.f;
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (v0 + r < V) {
-                    add += expf(z[r] - top);
+                    add += expf(z[r] - base);
                     if (v0 + r == y) zlab[lane] = z[r];
                 }
-            s = s * expf(m - top) + add;
+            s = s * expf(m - base) + add;
             m = top;
         }
     }
@@ -1797,7 +1798,7 @@ __global__ void __launch_bounds__(256) logp_few(const __nv_bfloat16* __restrict_
         for (int w = 0; w < 8; ++w) top = fmaxf(top, ms[w][threadIdx.x].x);
         for (int w = 0; w < 8; ++w) {
             const float2 p = ms[w][threadIdx.x];
-            if (p.y > 0.f) sum += p.y * expf(p.x - top);   // a warp without rows has s = 0
+            if (p.y != 0.f) sum += p.y * expf(p.x - top);   // a warp without rows has s = 0; NaN is passed on
         }
         part[static_cast<int64_t>(threadIdx.x) * nparts + blockIdx.x] = make_float2(top, sum);
     }
