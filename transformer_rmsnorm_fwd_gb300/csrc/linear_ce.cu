@@ -42,7 +42,7 @@ namespace liger {
 namespace {
 
 constexpr int kVT = tc::BN;   // vocab tile of the (m, s) partials
-constexpr int kMaxSortKeys = 8192;      // label keys sorted per block (shared memory)
+constexpr int kMaxSortKeys = 8192;      // label keys sorted together (shared memory)
 constexpr int64_t kAutoChunkTC = 8192;   // tensor-core path: most rows per chunk chosen automatically
 constexpr int64_t kMaxChunkTC = 65536;   // tensor-core path: most rows per chunk a caller may ask for
 // The dX GEMM's K is the whole vocabulary: over 150 k vocabulary rows the tiles of a
@@ -313,45 +313,50 @@ __device__ __forceinline__ float block_reduce(float v, bool is_max, float* sh) {
 }
 
 // Sort the (label << 32 | token) keys of each segment of seg tokens (ignored
-// tokens -> ~0), one block per segment (bitonic, in shared memory), for the
-// one-hot correction of the dW epilogue.  Segment b covers tokens
-// [b*seg, min(n, (b+1)*seg)) and its sorted keys go to out[b*seg ...]; the
+// tokens -> ~0) for the one-hot correction of the dW epilogue.  Segment b covers
+// tokens [b*seg, min(n, (b+1)*seg)) and its sorted keys go to out[b*seg ...]; the
 // token index in a key is absolute (b*seg + i) or relative to the segment (i).
-__global__ void __launch_bounds__(1024) sort_label_keys(const int64_t* __restrict__ labels, int64_t n, int seg,
-                                                        int64_t ignore, int absolute,
-                                                        unsigned long long* __restrict__ out) {
-    extern __shared__ unsigned long long sk[];
-    const int64_t b0 = static_cast<int64_t>(blockIdx.x) * seg;
+// By ranks: a block finds how many keys of the segment (blockIdx.y) stand before each
+// of 32 keys, one per lane, its warps counting over an eighth of the segment each,
+// four labels a load from shared memory (2741 keys: 6.6 us, 52 sorted by one block).
+constexpr int kRankThreads = 256;
+__global__ void __launch_bounds__(kRankThreads) sort_label_keys(const int64_t* __restrict__ labels, int64_t n, int seg,
+                                                                int64_t ignore, int absolute,
+                                                                unsigned long long* __restrict__ out) {
+    __shared__ __align__(16) uint32_t lab[kMaxSortKeys];
+    __shared__ int before[kRankThreads / 32][32];
+    const int64_t b0 = static_cast<int64_t>(blockIdx.y) * seg;
     const int cnt = static_cast<int>(n - b0 < seg ? n - b0 : seg);
-    int npow2 = 1;
-    while (npow2 < cnt) npow2 <<= 1;
-    const unsigned base = absolute ? static_cast<unsigned>(b0) : 0u;
-    for (int i = threadIdx.x; i < npow2; i += 1024) {
-        unsigned long long key = ~0ull;
-        if (i < cnt) {
-            const int64_t y = labels[b0 + i];
-            if (y != ignore) key = (static_cast<unsigned long long>(y) << 32) | (base + static_cast<unsigned>(i));
-        }
-        sk[i] = key;
+    const int i0 = blockIdx.x * 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (i0 >= cnt) return;
+    const int quads = (cnt + 3) / 4;
+    for (int i = threadIdx.x; i < quads * 4; i += kRankThreads) {
+        const int64_t y = i < cnt ? labels[b0 + i] : ignore;
+        lab[i] = y == ignore ? 0xFFFFFFFFu : static_cast<uint32_t>(y);   // labels are below 2^30
     }
     __syncthreads();
-    for (int k = 2; k <= npow2; k <<= 1) {
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int i = threadIdx.x; i < npow2; i += 1024) {
-                const int p = i ^ j;
-                if (p > i) {
-                    const bool up = (i & k) == 0;
-                    const unsigned long long a = sk[i], b = sk[p];
-                    if ((a > b) == up) {
-                        sk[i] = b;
-                        sk[p] = a;
-                    }
-                }
-            }
-            __syncthreads();
-        }
+    // in the order of label, then token: labels up to this key's ahead of the 32, below it behind them
+    const int i = i0 + lane;
+    const uint32_t y = i < cnt ? lab[i] : 0u;
+    const uint4* l4 = reinterpret_cast<const uint4*>(lab);
+    int k = 0;
+    for (int j = warp; j < i0 / 4; j += kRankThreads / 32) {
+        const uint4 v = l4[j];
+        k += (v.x <= y) + (v.y <= y) + (v.z <= y) + (v.w <= y);
     }
-    for (int i = threadIdx.x; i < cnt; i += 1024) out[b0 + i] = sk[i];
+    for (int j = (i0 + 32) / 4 + warp; j < quads; j += kRankThreads / 32) {   // its padding is below no label
+        const uint4 v = l4[j];
+        k += (v.x < y) + (v.y < y) + (v.z < y) + (v.w < y);
+    }
+    if (warp == 0)
+        for (int j = i0; j < min(cnt, i0 + 32); ++j) k += lab[j] < y || (lab[j] == y && j < i);
+    before[warp][lane] = k;
+    __syncthreads();
+    if (warp != 0 || i >= cnt) return;
+    int rank = 0;
+    for (int w = 0; w < kRankThreads / 32; ++w) rank += before[w][lane];
+    const unsigned token = (absolute ? static_cast<unsigned>(b0) : 0u) + static_cast<unsigned>(i);
+    out[b0 + rank] = y == 0xFFFFFFFFu ? ~0ull : (static_cast<unsigned long long>(y) << 32) | token;
 }
 
 // Start tables of every segment (blockIdx.y): lstart[s*(V+1) + v] = first index
@@ -382,10 +387,8 @@ int sort_labels(const int64_t* labels, int64_t n, int seg, int64_t ignore, int V
                 unsigned long long* keys, int* lstart, cudaStream_t st) {
     const int64_t nseg = ceil_div(n, static_cast<int64_t>(seg));
     if (nseg <= 0) return LIGER_OK;
-    int npow2 = 1;
-    while (npow2 < seg) npow2 <<= 1;
-    sort_label_keys<<<static_cast<unsigned>(nseg), 1024, sizeof(unsigned long long) * npow2, st>>>(
-        labels, n, seg, ignore, absolute ? 1 : 0, keys);
+    const dim3 ranks(static_cast<unsigned>(ceil_div(std::min<int64_t>(n, seg), int64_t{32})), static_cast<unsigned>(nseg));
+    sort_label_keys<<<ranks, kRankThreads, 0, st>>>(labels, n, seg, ignore, absolute ? 1 : 0, keys);
     if (int rc = check_launch("sort_label_keys")) return rc;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(V + 1, 256), 2 * sm_count())),
                     static_cast<unsigned>(nseg));
@@ -622,22 +625,27 @@ __global__ void __launch_bounds__(256) policy_scan(const int64_t* __restrict__ l
 // The row pass of the bf16 path: lse from the (m, s) partials, the token's terms and scale, and P
 // rewritten in place into the softmax part of D, c_t P exp(m_tile - lse).  P null: lse and logp only.
 // idx: original token of a row (null: t0 + row).
+// HBM-bound, P read and written once.  blockIdx.y takes a run of `piece` 16-byte vectors of the row, each
+// repeating the lse from the row's few KB of partials, four vectors a thread in flight: 2741 rows of
+// 128256 218 us in runs of 8192, 0.95 of the copy rate (4096: 222, 2048: 253, 237 a whole row at a time with one
+// vector in flight); 8 rows 6 us in runs of 2048 (8192: 10).
 __global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* __restrict__ labels, int64_t ignore,
                                                                 const float2* __restrict__ part, int nvt,
                                                                 const float* __restrict__ zlab, __nv_bfloat16* P,
                                                                 int64_t ldp, int V, const Policy pol,
                                                                 const int64_t* __restrict__ idx, int64_t t0,
-                                                                float* __restrict__ coef) {
+                                                                float* __restrict__ coef, int piece) {
     extern __shared__ float fac[];   // [nvt]
     __shared__ float red[32];
     const int64_t row = blockIdx.x;
     __nv_bfloat16* prow = P + row * ldp;
-    const int nv8 = (V + 7) / 8;
+    const int k0 = blockIdx.y * piece, k1 = min((V + 7) / 8, k0 + piece);
+    const bool write = threadIdx.x == 0 && blockIdx.y == 0;   // the token's values
     if (labels[row] == ignore) {
         if (P != nullptr) {
-            for (int k = threadIdx.x; k < nv8; k += kRowThreads)
+            for (int k = k0 + threadIdx.x; k < k1; k += kRowThreads)
                 stg16(prow + static_cast<int64_t>(k) * 8, make_uint4(0, 0, 0, 0));
-            if (threadIdx.x == 0) coef[row] = 0.f;
+            if (write) coef[row] = 0.f;
         }
         return;
     }
@@ -655,20 +663,30 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* _
     float lp = zlab[row] - l;
     if (pol.hdr->err != 0) lp = __int_as_float(0x7FC00000);   // a GEMM gave up on a bounded wait
     const int64_t t = idx != nullptr ? idx[row] : t0 + row;
-    if (pol.logp != nullptr && threadIdx.x == 0) pol.logp[t] = lp;
+    if (pol.logp != nullptr && write) pol.logp[t] = lp;
     if (P == nullptr) return;
-    const float sc = policy_token(pol, t, lp, threadIdx.x == 0);
-    if (threadIdx.x == 0) coef[row] = sc;
-    for (int j = threadIdx.x; j < nvt; j += kRowThreads) fac[j] = sc * expf(pr[j].x - l);
+    const float sc = policy_token(pol, t, lp, write);
+    if (write) coef[row] = sc;
+    const int f0 = k0 * 8 / kVT, f1 = (k1 * 8 - 1) / kVT;   // the piece's vocabulary tiles
+    for (int j = f0 + threadIdx.x; j <= f1; j += kRowThreads) fac[j - f0] = sc * expf(pr[j].x - l);
     __syncthreads();
-    for (int k = threadIdx.x; k < nv8; k += kRowThreads) {
-        const int col = k * 8;
-        const float f = fac[col / kVT];
-        float v[8];
-        unpack(ldg16(prow + col), v);
+    constexpr int U = 4;
+    for (int kk = k0 + threadIdx.x; kk < k1; kk += U * kRowThreads) {
+        uint4 w[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= f;
-        stg16(prow + col, pack(v));
+        for (int u = 0; u < U; ++u)
+            if (kk + u * kRowThreads < k1) w[u] = ldg16_cs(prow + static_cast<int64_t>(kk + u * kRowThreads) * 8);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = kk + u * kRowThreads;
+            if (k >= k1) continue;
+            const float f = fac[k * 8 / kVT - f0];
+            float v[8];
+            unpack(w[u], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= f;
+            stg16(prow + static_cast<int64_t>(k) * 8, pack(v));
+        }
     }
 }
 
@@ -702,44 +720,49 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_f32(const int64_t* __
 }
 
 // loss and stats: the tokens' terms added in a fixed order; NaN if a kernel recorded an error or the
-// scan found a bad label or bad sequences.  A thread adds its tokens in fp32 with the rounding errors
+// scan found a bad label or bad sequences.  A warp adds its tokens in fp32 with the rounding errors
 // carried along (fp64 adds run at a small fraction of the fp32 rate: 16 us for 4096 tokens in fp64), the
-// threads' sums are joined in fp64.
+// warps' sums are joined in fp64.
 __device__ __forceinline__ void add_with_error(float v, float& sum, float& err) {
     const float t = sum + v, b = t - sum;
     err += (sum - (t - b)) + (v - b);
     sum = t;
 }
-constexpr int kFinalThreads = 256;
+constexpr int kFinalThreads = 1024;   // 256 are launched for few tokens
 __global__ void __launch_bounds__(kFinalThreads) policy_final(const float* __restrict__ term, const float* __restrict__ kl,
                                                               const float* __restrict__ clip, int64_t T, const Hdr* hdr,
                                                               float* loss, float* stats) {
-    constexpr int NW = kFinalThreads / 32;
-    __shared__ double red[3][NW];
+    __shared__ double red[3][32];
+    const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float s[3] = {0.f, 0.f, 0.f}, e[3] = {0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int64_t t = threadIdx.x; t < T; t += kFinalThreads) {
+    for (int64_t t = threadIdx.x; t < T; t += nt) {
         add_with_error(term[t], s[0], e[0]);
         add_with_error(kl[t], s[1], e[1]);
         add_with_error(clip[t], s[2], e[2]);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        // an infinity's error term is NaN: the plain sum stands for it
-        double d = isfinite(s[i]) ? static_cast<double>(s[i]) + static_cast<double>(e[i]) : static_cast<double>(s[i]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        if ((threadIdx.x & 31) == 0) red[i][threadIdx.x >> 5] = d;
+        for (int o = 16; o > 0; o >>= 1) {
+            const float e2 = __shfl_xor_sync(0xffffffffu, e[i], o);
+            add_with_error(__shfl_xor_sync(0xffffffffu, s[i], o), s[i], e[i]);
+            e[i] += e2;
+        }
+        // an infinity's error term is NaN: the plain sum stands for it
+        if (lane == 0)
+            red[i][warp] = isfinite(s[i]) ? static_cast<double>(s[i]) + static_cast<double>(e[i]) : static_cast<double>(s[i]);
     }
     __syncthreads();
-    if (threadIdx.x < 3) {
-        const int i = threadIdx.x;
-        double tot = 0.0;
+    if (warp < 3) {
+        const int i = warp;
+        double tot = lane < nt / 32 ? red[i][lane] : 0.0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) tot += red[i][w];
+        for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
         const double n = static_cast<double>(hdr->n_valid);
         float r = static_cast<float>(i == 0 ? tot : n > 0.0 ? tot / n : 0.0);
         if (hdr->err != 0 || hdr->bad != 0) r = __int_as_float(0x7fc00000);
+        if (lane != 0) return;
         if (i == 0) *loss = r;
         else if (stats != nullptr) stats[i - 1] = r;
     }
@@ -914,20 +937,6 @@ int run_simt(const Args& a, const Layout& L, float scale) {
     return LIGER_OK;
 }
 
-int ensure_sort_attr() {
-    // per device: function attributes belong to each device's context (racing threads set the same value)
-    static std::atomic<bool> done[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("sort_label_keys device");
-    if (!done[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(sort_label_keys, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(sizeof(unsigned long long) * kMaxSortKeys)) != cudaSuccess)
-            return check_launch("sort_label_keys attribute");
-        done[dev].store(true, std::memory_order_release);
-    }
-    return LIGER_OK;
-}
-
 // A GEMM over fewer rows of X than this is given them among rows of zeros: every CTA reads the same few
 // lines of X at the same time, and over one to fifteen rows they sit in so few L2 slices that this bounds
 // it (logits at 4096 x 128256: 1 token 305 us, 9 206, 10 264, 16 181).
@@ -1047,7 +1056,6 @@ int policy_dx(const Args& a, const Layout& L, const __nv_bfloat16* P, const tc::
 
 int run_tc(const Args& a, const Layout& L, float scale) {
     using namespace tc;
-    if (int rc = ensure_sort_attr()) return rc;
     const __nv_bfloat16* X = static_cast<const __nv_bfloat16*>(a.X);
     const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.W);
     float* lse = reinterpret_cast<float*>(a.ws + L.lse);
@@ -1109,12 +1117,12 @@ int run_tc(const Args& a, const Layout& L, float scale) {
             rc = launch_logits(Xc, cl, H, V, mW_k, e, L.ldp, L.nvt, a.st);
         }
         if (rc) return rc;
-        // 2. lse, loss terms, P -> D in place
+        // 2. lse, loss terms, P -> D in place (policy loss: long runs of a row where they fill the GPU)
+        const int piece = cl * ceil_div(V, 8 * 8192) >= 8 * sm_count() ? 8192 : 2048;
         if (a.pol != nullptr)
-            policy_rows_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
-                                                                  zlab + t0, P, L.ldp, V, *a.pol,
-                                                                  a.idx != nullptr ? a.idx + t0 : nullptr, t0,
-                                                                  a.pol->coef + t0);
+            policy_rows_bf16<<<dim3(cl, static_cast<unsigned>(ceil_div(ceil_div(V, 8), piece))), kRowThreads, fac_smem,
+                               a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt), zlab + t0, P, L.ldp, V, *a.pol,
+                                       a.idx != nullptr ? a.idx + t0 : nullptr, t0, a.pol->coef + t0, piece);
         else
             dlogits_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
                                                               zlab + t0, P, L.ldp, V, scale, a.scale_dev, lse + t0,
@@ -1322,7 +1330,6 @@ Layout2 layout2(int64_t T, int64_t H, int64_t V, int64_t vchunk) {
 
 int run_two_pass(const Args& a, const Layout2& L, float scale) {
     using namespace tc;
-    if (int rc = ensure_sort_attr()) return rc;
     const __nv_bfloat16* X = static_cast<const __nv_bfloat16*>(a.X);
     const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.W);
     float* lse = reinterpret_cast<float*>(a.ws + L.lse);
@@ -1936,7 +1943,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
              : nn == 2 ? launch_logp_few<2, 1>(X, W, labs, nn, H, V, part, zlab, most, np, st)
                        : launch_logp_few<4, 2>(X, W, labs, nn, H, V, part, zlab, most, np, st);
         if (rc) return rc;
-        policy_rows_bf16<<<nn, kRowThreads, 0, st>>>(labs, ignore, part, np, zlab, nullptr, 0, V, pol, idx, 0, nullptr);
+        policy_rows_bf16<<<nn, kRowThreads, 0, st>>>(labs, ignore, part, np, zlab, nullptr, 0, V, pol, idx, 0, nullptr, 0);
         return check_launch("linear_logp rows");
     }
     int64_t x_rows = 0;
@@ -1963,7 +1970,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
         e.zlab = zlab + t0;
         if ((rc = launch_logits(X + t0 * H, cl, H, V, mW_k, e, 0, L.nvt, st, x_rows))) return rc;
         policy_rows_bf16<<<cl, kRowThreads, 0, st>>>(labs + t0, ignore, part, static_cast<int>(L.nvt), zlab + t0, nullptr,
-                                                     0, V, pol, idx != nullptr ? idx + t0 : nullptr, t0, nullptr);
+                                                     0, V, pol, idx != nullptr ? idx + t0 : nullptr, t0, nullptr, 0);
         if ((rc = check_launch("linear_logp rows"))) return rc;
     }
     return LIGER_OK;
@@ -2123,7 +2130,7 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
     if (PL.L.tc) rc = n < T && worth_compacting(n, T) ? run_tc_compact(a, n, chunk, 0.f) : run_tc(a, PL.L, 0.f);
     else rc = dtype == LIGER_F32 ? run_policy_simt<float>(a, PL.L, f32(PL.split)) : run_policy_simt<__nv_bfloat16>(a, PL.L, f32(PL.split));
     if (rc) return rc;
-    policy_final<<<1, kFinalThreads, 0, st>>>(f32(PL.term), f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
+    policy_final<<<1, T <= 1024 ? 256 : kFinalThreads, 0, st>>>(f32(PL.term), f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
     return check_launch("linear_policy");
 }
 
