@@ -121,7 +121,7 @@ int liger_swiglu_bwd_ckpt8(const void* dy, const int8_t* gate8, const uint8_t* g
  * Arguments, shapes (bf16; H >= 64, H and I multiples of 8), workspace
  * (liger_fused_linear_swiglu_workspace) and errors otherwise as
  * liger_fused_linear_swiglu_fwd_save / _bwd_saved; codes 16-byte aligned.  dWg
- * is written twice: sums of dX stand in it until dX is done. */
+ * or dX is written twice: sums of the other gradients may stand in it first. */
 int liger_fused_linear_swiglu_fwd_ckpt8(const void* X, const void* Wg, const void* Wu, void* out, int8_t* gate8,
                                         uint8_t* gate_scale, int8_t* up8, uint8_t* up_scale, int64_t T, int64_t H,
                                         int64_t I, int dtype, void* stream);

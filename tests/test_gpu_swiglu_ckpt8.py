@@ -216,6 +216,13 @@ def test_linear_step(L, T, H, I):
     check(dWu, du64.T @ x64, du64.abs().T @ x64.abs(), bf + 2 * T + 100, "dWu")
 
 
+@pytest.mark.parametrize("T,H,I", [(4100, 1032, 2040), (4096, 264, 5000), (8200, 2056, 1104), (4351, 328, 5000)])
+def test_linear_step_of_many_tokens(L, T, H, I):
+    """The last round of dW's tiles split over the tokens (several column blocks, ragged row blocks of both weights, both tile
+    orders), and a forward whose rows are swept in two groups (8200 x 2056)."""
+    test_linear_step(L, T, H, I)
+
+
 def test_linear_gradient_against_differences(L):
     """The backward of the checkpointed values is the slope of the plain MLP within what 8 bits allow: the directional
     derivative of sum(dH * out) along a change of Wu, whose gradient uses g read back (error <= 1/128 of a group's top)."""

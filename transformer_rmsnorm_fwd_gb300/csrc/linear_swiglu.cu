@@ -101,6 +101,18 @@ int fwd_impl(const void* X, const void* Wg, const void* Wu, void* out, void* g_s
     const int ntile_n = static_cast<int>(ceil_div(I, BN / 2));
     // launches over rows_in_l2 rows of X, each sweeping all of W_g, W_u over rows that stay in L2
     const int64_t sub = rows_in_l2(H, T);
+    if (q.g8 != nullptr) {   // the same sweeps in one launch: CTA pairs idle at the end of the last only (8192 tokens: 897 us, 914 in two)
+        CUtensorMap mX;
+        if ((rc = make_map(&mX, X, H, T, H, BK, BM))) return rc;
+        e.m_group = static_cast<int>(ceil_div(sub, static_cast<int64_t>(TileCfg<1>::TM)));
+        e.ldq = ceil_div(I, kCkptGroup);
+        e.g8 = q.g8;
+        e.u8 = q.u8;
+        e.g8s = q.g8s;
+        e.u8s = q.u8s;
+        return launch_gemm<0, 0, EPI_SWIGLU_CKPT8, 1>(mX, mG, static_cast<int>(T), ntile_n * BN, static_cast<int>(H), e,
+                                                      as_stream(stream), 0, &mX, &mU);
+    }
     for (int64_t m0 = 0; m0 < T; m0 += sub) {
         const int ml = static_cast<int>(std::min<int64_t>(sub, T - m0));
         CUtensorMap mX;
@@ -110,17 +122,6 @@ int fwd_impl(const void* X, const void* Wg, const void* Wu, void* out, void* g_s
         f.out = e.out + m0 * I;
         if (e.out2 != nullptr) f.out2 = e.out2 + m0 * I;
         if (e.out3 != nullptr) f.out3 = e.out3 + m0 * I;
-        if (q.g8 != nullptr) {
-            f.ldq = ceil_div(I, kCkptGroup);
-            f.g8 = q.g8 + m0 * I;
-            f.u8 = q.u8 + m0 * I;
-            f.g8s = q.g8s + m0 * f.ldq;
-            f.u8s = q.u8s + m0 * f.ldq;
-            if ((rc = launch_gemm<0, 0, EPI_SWIGLU_CKPT8, 1>(mX, mG, ml, ntile_n * BN, static_cast<int>(H), f,
-                                                             as_stream(stream), 0, &mX, &mU)))
-                return rc;
-            continue;
-        }
         if ((rc = launch_gemm<0, 0, EPI_SWIGLU, 1>(mX, mG, ml, ntile_n * BN, static_cast<int>(H), f, as_stream(stream),
                                                    0, &mX, &mU)))
             return rc;
@@ -130,76 +131,136 @@ int fwd_impl(const void* X, const void* Wg, const void* Wu, void* out, void* g_s
 
 // dX = dG W_g + dU W_u (one GEMM over K = 2I) and dW_g = dG^T X, dW_u = dU^T X,
 // from dG and dU [T, I] bf16.
-// split_dx: with few tiles of dX, K is split over the idle CTA pairs, the items' fp32 sums standing in
-// dW_g's memory, which is not written before dX is done (backward of one token at hidden 112, intermediate 9016:
-// 35 us, 97 without; of 256 tokens at 4096, 11008: 150 and 202).
-int grads_from_dgdu(const void* X, const void* Wg, const void* Wu, const __nv_bfloat16* dG,
-                    const __nv_bfloat16* dU, void* dX, void* dWg, void* dWu, int64_t T, int64_t H, int64_t I,
-                    int* d_err, cudaStream_t st, bool split_dx = false) {
+// split: the K of tiles that would leave CTA pairs idle is split over them, the items' fp32 sums
+// standing in the memory of the output that is formed last.
+//  * few tiles of dX: all of them, the sums in dW_g (backward of one token at hidden 112, intermediate
+//    9016: 35 us, 97 without; of 256 tokens at 4096, 11008: 150 and 202).
+//  * else the last, partly filled round of dW's tiles, the sums in dX (8192 tokens at 4096, 11008:
+//    18.1 rounds, 849 us, 878 without), where a tile takes long enough to pay for it.
+struct GradArgs {
+    const void *X, *Wg, *Wu;
+    const __nv_bfloat16 *dG, *dU;
+    void *dX, *dWg, *dWu;
+    int64_t T, H, I;
+    int* d_err;
+    cudaStream_t st;
+};
+
+int dx_from_dgdu(const GradArgs& a, int64_t splits) {
     using namespace tc;
     int rc;
     CUtensorMap mdG_k, mdU_k, mG_mn, mU_mn;
-    if ((rc = make_map(&mdG_k, dG, I, T, I, BK, BM))) return rc;
-    if ((rc = make_map(&mdU_k, dU, I, T, I, BK, BM))) return rc;
-    if ((rc = make_map(&mG_mn, Wg, H, I, H, MN_BOX, BK))) return rc;
-    if ((rc = make_map(&mU_mn, Wu, H, I, H, MN_BOX, BK))) return rc;
-    const int nkb1 = static_cast<int>(ceil_div(I, BK));
+    if ((rc = make_map(&mdG_k, a.dG, a.I, a.T, a.I, BK, BM))) return rc;
+    if ((rc = make_map(&mdU_k, a.dU, a.I, a.T, a.I, BK, BM))) return rc;
+    if ((rc = make_map(&mG_mn, a.Wg, a.H, a.I, a.H, MN_BOX, BK))) return rc;
+    if ((rc = make_map(&mU_mn, a.Wu, a.H, a.I, a.H, MN_BOX, BK))) return rc;
+    const int nkb1 = static_cast<int>(ceil_div(a.I, BK));
     EpiParams d{};
-    d.err = d_err;
-    d.M = static_cast<int>(T);
-    d.N = static_cast<int>(H);
-    d.out = static_cast<__nv_bfloat16*>(dX);
-    d.ldo = H;
+    d.err = a.d_err;
+    d.M = static_cast<int>(a.T);
+    d.N = static_cast<int>(a.H);
+    d.out = static_cast<__nv_bfloat16*>(a.dX);
+    d.ldo = a.H;
     d.ksplit_nkb = nkb1;
     d.raster = RASTER_N_GROUPS;
-    // items of at least 16 k-blocks, as many as there are CTA pairs and dW_g's bytes hold
-    const int64_t tm = ceil_div(T, static_cast<int64_t>(TileCfg<1>::TM)), tn = ceil_div(H, static_cast<int64_t>(BN));
-    const int64_t rows = std::min<int64_t>(T, TileCfg<1>::TM);
-    const int64_t splits = !split_dx ? 0 : std::min<int64_t>({sm_count() / 2 / (tm * tn), 2 * nkb1 / 16,
-                                                              I * H * 2 / (tm * tn * rows * BN * 4)});
-    if (splits >= 2) {
-        d.acc_write = 0;
-        d.out_write = 1;
-        d.full_tiles = 0;
-        d.ksplits = static_cast<int>(splits);
-        d.kpart_rows = static_cast<int>(rows);
-        d.kpart = static_cast<float*>(dWg);
-        if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1, MODE_SPLIT>(mdG_k, mG_mn, static_cast<int>(T), static_cast<int>(H),
-                                                              2 * nkb1 * BK, d, st, 0, &mdU_k, &mU_mn)))
-            return rc;
-        const SplitJoin j{d.kpart, static_cast<int>(tm * tn), d.ksplits, 1, 0, d.kpart_rows, static_cast<int>(tm),
-                          static_cast<int>(tn), nullptr, 0, nullptr, nullptr, d.out, d.M, d.N};
-        split_join<<<dim3(static_cast<unsigned>(tm * tn), static_cast<unsigned>(ceil_div(rows, int64_t{8}))), 256, 0, st>>>(j);
-        if ((rc = check_launch("fused_linear_swiglu dX"))) return rc;
-    } else if ((rc = launch_gemm<0, 1, EPI_STORE, 1>(mdG_k, mG_mn, static_cast<int>(T), static_cast<int>(H),
-                                                     2 * nkb1 * BK, d, st, 0, &mdU_k, &mU_mn))) {
+    if (splits < 2)
+        return launch_gemm<0, 1, EPI_STORE, 1>(mdG_k, mG_mn, d.M, d.N, 2 * nkb1 * BK, d, a.st, 0, &mdU_k, &mU_mn);
+    const int tm = (d.M + TileCfg<1>::TM - 1) / TileCfg<1>::TM, tn = (d.N + BN - 1) / BN;
+    d.out_write = 1;
+    d.ksplits = static_cast<int>(splits);
+    d.kpart_rows = std::min<int>(d.M, TileCfg<1>::TM);
+    d.kpart = static_cast<float*>(a.dWg);
+    if ((rc = launch_gemm<0, 1, EPI_ACCUM, 1, MODE_SPLIT>(mdG_k, mG_mn, d.M, d.N, 2 * nkb1 * BK, d, a.st, 0, &mdU_k,
+                                                          &mU_mn)))
         return rc;
-    }
+    SplitJoin j{};
+    j.part = d.kpart;
+    j.rem = tm * tn;
+    j.splits = d.ksplits;
+    j.slabs = 1;
+    j.part_rows = d.kpart_rows;
+    j.num_m = tm;
+    j.num_n = tn;
+    j.out = d.out;
+    j.M = d.M;
+    j.N = d.N;
+    split_join<<<dim3(static_cast<unsigned>(j.rem), static_cast<unsigned>(ceil_div(j.part_rows, 8))), 256, 0, a.st>>>(j);
+    return check_launch("fused_linear_swiglu dX");
+}
+
+int dw_from_dgdu(const GradArgs& a, bool split) {
+    using namespace tc;
+    int rc;
     CUtensorMap mdG_mn, mdU_mn, mX_mn;
-    if ((rc = make_map(&mdG_mn, dG, I, T, I, MN_BOX, BK))) return rc;
-    if ((rc = make_map(&mdU_mn, dU, I, T, I, MN_BOX, BK))) return rc;
-    if ((rc = make_map(&mX_mn, X, H, T, H, MN_BOX, BK))) return rc;
+    if ((rc = make_map(&mdG_mn, a.dG, a.I, a.T, a.I, MN_BOX, BK))) return rc;
+    if ((rc = make_map(&mdU_mn, a.dU, a.I, a.T, a.I, MN_BOX, BK))) return rc;
+    if ((rc = make_map(&mX_mn, a.X, a.H, a.T, a.H, MN_BOX, BK))) return rc;
     EpiParams w{};
-    w.err = d_err;
-    w.M = static_cast<int>(I);
-    w.N = static_cast<int>(H);
-    w.ldo = H;
+    w.err = a.d_err;
+    w.M = static_cast<int>(a.I);
+    w.N = static_cast<int>(a.H);
+    w.ldo = a.H;
     w.out_write = 1;
     // n fastest touches all of X in every wave: fine while X stays in L2 (up to 32 MiB), above
     // that groups of 8 column blocks of it do (each dG / dU block is then read once per group)
-    w.raster = T * H * 2 > (int64_t{32} << 20) ? RASTER_N_GROUPS : RASTER_N_FASTEST;
+    w.raster = a.T * a.H * 2 > (int64_t{32} << 20) ? RASTER_N_GROUPS : RASTER_N_FASTEST;
     w.hint_a = HINT_EVICT_FIRST;
     w.hint_b = HINT_EVICT_LAST;   // X: reused by every row block
     // dW_g and dW_u in one launch: the row blocks of dU^T follow those of dG^T (2 x 43
     // row blocks at intermediate 11008: 1376 tiles fill 18.1 waves of the 76 CTA pairs,
     // where two launches of 688 tiles fill 9.05 waves each)
-    const int mt = static_cast<int>(ceil_div(I, static_cast<int64_t>(TileCfg<1>::TM)));
-    w.out = static_cast<__nv_bfloat16*>(dWg);
-    w.out2 = static_cast<__nv_bfloat16*>(dWu);
+    const int mt = static_cast<int>(ceil_div(a.I, static_cast<int64_t>(TileCfg<1>::TM)));
+    w.out = static_cast<__nv_bfloat16*>(a.dWg);
+    w.out2 = static_cast<__nv_bfloat16*>(a.dWu);
     w.msplit_mt = mt;
-    w.M2 = static_cast<int>(I);
-    return launch_gemm<1, 1, EPI_ACCUM, 1>(mdG_mn, mX_mn, mt * TileCfg<1>::TM + static_cast<int>(I),
-                                           static_cast<int>(H), static_cast<int>(T), w, st, 0, &mdU_mn, &mX_mn);
+    w.M2 = static_cast<int>(a.I);
+    const int M = mt * TileCfg<1>::TM + static_cast<int>(a.I), N = static_cast<int>(a.H), K = static_cast<int>(a.T);
+    const int64_t tn = ceil_div(a.H, static_cast<int64_t>(BN)), tiles = 2 * mt * tn, pairs = sm_count() / 2;
+    const int64_t rem = tiles % pairs, tile_bytes = int64_t{TileCfg<1>::TM} * BN * 4;
+    const int64_t splits = !split || rem == 0 || a.T < 4096 ? 0
+                           : std::min<int64_t>({pairs / rem, a.T / (16 * BK), a.T * a.H * 2 / (rem * tile_bytes)});
+    if (splits < 2) return launch_gemm<1, 1, EPI_ACCUM, 1>(mdG_mn, mX_mn, M, N, K, w, a.st, 0, &mdU_mn, &mX_mn);
+    w.full_tiles = static_cast<int>(tiles - rem);
+    w.ksplits = static_cast<int>(splits);
+    w.kpart_rows = TileCfg<1>::TM;
+    w.kpart = static_cast<float*>(a.dX);
+    if ((rc = launch_gemm<1, 1, EPI_ACCUM, 1, MODE_SPLIT>(mdG_mn, mX_mn, M, N, K, w, a.st, 0, &mdU_mn, &mX_mn))) return rc;
+    SplitJoin j{};
+    j.part = w.kpart;
+    j.rem = static_cast<int>(rem);
+    j.splits = w.ksplits;
+    j.slabs = 1;
+    j.full = w.full_tiles;
+    j.part_rows = w.kpart_rows;
+    j.num_m = 2 * mt;
+    j.num_n = static_cast<int>(tn);
+    j.out = w.out;
+    j.M = w.M;
+    j.N = w.N;
+    j.n_fastest = w.raster == RASTER_N_FASTEST ? 1 : 0;
+    j.msplit_mt = mt;
+    j.M2 = w.M2;
+    j.out2 = w.out2;
+    split_join<<<dim3(static_cast<unsigned>(rem), static_cast<unsigned>(j.part_rows / 8)), 256, 0, a.st>>>(j);
+    return check_launch("fused_linear_swiglu dW");
+}
+
+int grads_from_dgdu(const void* X, const void* Wg, const void* Wu, const __nv_bfloat16* dG,
+                    const __nv_bfloat16* dU, void* dX, void* dWg, void* dWu, int64_t T, int64_t H, int64_t I,
+                    int* d_err, cudaStream_t st, bool split = false) {
+    using namespace tc;
+    const GradArgs a{X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st};
+    // dX: items of at least 16 k-blocks, as many as there are CTA pairs and dW_g's bytes hold
+    const int64_t tiles = ceil_div(T, static_cast<int64_t>(TileCfg<1>::TM)) * ceil_div(H, static_cast<int64_t>(BN));
+    const int64_t rows = std::min<int64_t>(T, TileCfg<1>::TM);
+    const int64_t splits = !split ? 0 : std::min<int64_t>({sm_count() / 2 / tiles, 2 * ceil_div(I, BK) / 16,
+                                                           I * H * 2 / (tiles * rows * BN * 4)});
+    if (split && splits < 2) {
+        if (int rc = dw_from_dgdu(a, true)) return rc;
+        return dx_from_dgdu(a, 0);
+    }
+    if (int rc = dx_from_dgdu(a, splits)) return rc;
+    return dw_from_dgdu(a, false);
 }
 
 }  // namespace
@@ -306,7 +367,7 @@ namespace {
 template <typename DgDu>
 int bwd_kept(const char* who, const void* X, const void* Wg, const void* Wu, const void* dH, const void* g, const void* u,
              void* dX, void* dWg, void* dWu, void* ws, size_t ws_bytes, int64_t T, int64_t H, int64_t I, int dtype,
-             cudaStream_t st, DgDu dgdu, bool split_dx = false) {
+             cudaStream_t st, DgDu dgdu, bool split = false) {
     if (int rc = check_shapes(T, H, I, dtype, who)) return rc;
     if (!Wg || !Wu || !dWg || !dWu || (T > 0 && (!X || !dH || !g || !u || !dX)))
         return fail(LIGER_ERR_NULL, "%s: null tensor pointer", who);
@@ -330,7 +391,7 @@ int bwd_kept(const char* who, const void* X, const void* Wg, const void* Wu, con
     // 1. dG, dU from dh and the saved g, u (the elementwise SwiGLU backward)
     if (int rc = dgdu(dG, dU)) return rc;
     // 2-3. as in the backward with recompute
-    return grads_from_dgdu(X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st, split_dx);
+    return grads_from_dgdu(X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st, split);
 }
 
 }  // namespace

@@ -138,7 +138,7 @@ struct EpiParams {
     const int* lstart;
     int nseg;
     int64_t lstride;
-    // Work of a MODE_TOKENS or MODE_SPLIT EPI_ACCUM kernel with K-major A whose tiles leave SMs idle:
+    // Work of a MODE_SPLIT EPI_ACCUM kernel, or MODE_TOKENS with K-major A, whose tiles leave SMs idle:
     // the tiles from full_tiles on are split along K into ksplits items each (ksplits 0: none are).  An
     // item leaves its fp32 sums, kpart_rows (TM, or M if that is less) rows of BN, in kpart[item] and
     // nothing else: split_join adds them up and applies what the epilogue does to whole tiles.  Items of
@@ -187,6 +187,7 @@ struct EpiParams {
     int8_t *g8, *u8;
     uint8_t *g8s, *u8s;
     int64_t ldq;
+    int m_group;   // row blocks that one sweep over all columns takes (they stay in L2)
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int nkb = (K + BK - 1) / BK;
     // work items: the tiles, or whole tiles and then (k range, tile) for the split ones
     constexpr bool TOKSCALE = MODE == MODE_TOKENS;
-    constexpr bool KSPLIT = MODE != MODE_PLAIN && EPI == EPI_ACCUM && !A_MN;
+    constexpr bool KSPLIT = EPI == EPI_ACCUM && (MODE == MODE_SPLIT || (MODE == MODE_TOKENS && !A_MN));
     const int split_tiles = KSPLIT && ep.ksplits > 0 ? ntiles - ep.full_tiles : 0;
     const int items = ntiles + split_tiles * (ep.ksplits - 1);
     const int kb_per = KSPLIT && ep.ksplits > 0 ? (nkb + ep.ksplits - 1) / ep.ksplits : nkb;
@@ -575,6 +576,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mi = w / width;
                 ni = full * GROUP_N + (w - mi * width);
             }
+        } else if (EPI == EPI_SWIGLU_CKPT8) {
+            // m fastest within groups of m_group row blocks, one group after the other
+            const int g = t / (ep.m_group * num_n), w = t - g * ep.m_group * num_n;
+            const int gm = min(ep.m_group, num_m - g * ep.m_group);
+            ni = w / gm;
+            mi = g * ep.m_group + (w - ni * gm);
         } else {
             ni = t / num_m;
             mi = t - ni * num_m;
@@ -1355,7 +1362,7 @@ int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int 
     return check_launch("tc_gemm");
 }
 
-// bf16 out of the split tiles of a RASTER_N_GROUPS launch over CTA pairs: the sum of a tile's items, in
+// bf16 out of the split tiles of a launch over CTA pairs (RASTER_N_GROUPS, or RASTER_N_FASTEST with n_fastest): the sum of a tile's items, in
 // the order of the k ranges and, when the launches went over `slabs` runs of K (items apart), of
 // those.  With labels, minus tok_scale[row] corr[labels[row], :], and +0 on rows labelled `ignore`.
 struct SplitJoin {
@@ -1368,6 +1375,9 @@ struct SplitJoin {
     const __nv_bfloat16* corr;
     __nv_bfloat16* out;
     int M, N;
+    int n_fastest;
+    int msplit_mt, M2;        // row blocks from msplit_mt (> 0) on are a second product's, M2 rows to out2
+    __nv_bfloat16* out2;
 };
 __global__ void __launch_bounds__(256) split_join(SplitJoin p) {
     constexpr int TM = TileCfg<1>::TM;
@@ -1375,7 +1385,10 @@ __global__ void __launch_bounds__(256) split_join(SplitJoin p) {
     const int t = p.full + static_cast<int>(blockIdx.x);
     const int gfull = p.num_n / GROUP_N, in_full = gfull * p.num_m * GROUP_N;
     int mi, ni;
-    if (t < in_full) {
+    if (p.n_fastest) {
+        mi = t / p.num_n;
+        ni = t - mi * p.num_n;
+    } else if (t < in_full) {
         const int g = t / (p.num_m * GROUP_N), w = t - g * p.num_m * GROUP_N;
         mi = w / GROUP_N;
         ni = g * GROUP_N + (w - mi * GROUP_N);
@@ -1386,8 +1399,9 @@ __global__ void __launch_bounds__(256) split_join(SplitJoin p) {
     }
     // a block takes 8 rows of the tile: 32 threads a row, 8 columns each
     const int lr = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 5), lc = (threadIdx.x & 31) * 8;
-    const int row = mi * TM + lr, col = ni * BN + lc;
-    if (row >= p.M || col >= p.N) return;
+    const bool second = p.msplit_mt > 0 && mi >= p.msplit_mt;
+    const int row = (second ? mi - p.msplit_mt : mi) * TM + lr, col = ni * BN + lc;
+    if (row >= (second ? p.M2 : p.M) || col >= p.N) return;
     float v[8] = {};
     const int items = p.slabs * p.splits;   // item i of this tile: slab i / splits, k range i % splits
 #pragma unroll 4
@@ -1414,7 +1428,7 @@ __global__ void __launch_bounds__(256) split_join(SplitJoin p) {
         for (int e = 0; e < 8; ++e) v[e] = fmaf(-c, w[e], v[e]);
         o = pack(v);
     }
-    stg16(p.out + static_cast<int64_t>(row) * p.N + col, o);
+    stg16((second ? p.out2 : p.out) + static_cast<int64_t>(row) * p.N + col, o);
 }
 
 }  // namespace
