@@ -1179,7 +1179,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t s_acc = sbuf, s_out = sbuf + 4096u;
                 // two blocks of 32 columns per round (one for each fetch buffer), not all eight
                 // unrolled: the code of a round stays in the instruction cache, where eight copies of
-                // it were fetched anew for every tile (dW of 64 tokens at 128256 x 4096: 440 us, 660 with eight)
+                // it were fetched anew for every tile (dW of 64 tokens at 128256 x 4096 by this loop alone: 460 us, 660 with eight)
                 auto accum_block = [&](int c, uint4(&cur)[8]) {
                     __syncwarp();   // the previous block's row runs have been read
                     if (acc_read) {
@@ -1240,10 +1240,43 @@ __global__ void __launch_bounds__(THREADS, 1)
                         store_block<4, true>(s_out, lane, oblk + c * 64, ep.ldo * 2, rows,
                                              chunks_below(n0 + c * 32, ep.N, 8, 4));
                 };
+                // MN-major A with token scales (dW of the policy loss): where a warp's rows have nothing but
+                // their product (no sum to read or write, no label), 64 columns a round, whole 128-byte lines
+                // of a row, the next columns' TMEM load in flight.  One warp per scheduler takes all of a
+                // tile's rows, whose latency bounds the kernel when K is short (dW of 64 tokens at 128256 x
+                // 4096: 307 us, 460 without)
+                constexpr bool QUICK = MODE == MODE_TOKENS && A_MN;
+                if (QUICK && !acc_read && !acc_write && nseg == 1 && ep.labels == nullptr &&
+                    __all_sync(0xffffffffu, k_lo == k_hi)) {
+                    uint32_t ra[32], rb[32];
+                    auto put = [&](const uint32_t(&r)[32], int j0) {   // 32 columns of this lane's row, from chunk j0
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(r[g * 8 + e]);
+                            sts16(s_acc + stage_slot<8>(lane, j0 + g), pack_bf8(f));
+                        }
+                    };
+                    tmem_ld32_issue(taddr, ra);
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; c += 2) {
-                    accum_block(c, pre);
-                    accum_block(c + 1, pre2);
+                    for (int c = 0; c < BN / 32; c += 2) {
+                        tmem_ld_wait(ra);
+                        tmem_ld32_issue(taddr + (c + 1) * 32, rb);
+                        __syncwarp();   // the previous round's row runs have been read
+                        put(ra, 0);
+                        tmem_ld_wait(rb);
+                        if (c + 2 < BN / 32) tmem_ld32_issue(taddr + (c + 2) * 32, ra);
+                        put(rb, 4);
+                        __syncwarp();
+                        store_block<8, true>(s_acc, lane, oblk + c * 64, ep.ldo * 2, rows, chunks_below(n0 + c * 32, ep.N, 8, 8));
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < BN / 32; c += 2) {
+                        accum_block(c, pre);
+                        accum_block(c + 1, pre2);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
