@@ -656,29 +656,31 @@ __global__ void __launch_bounds__(1024) block_norm_sums(SumP p) {
     const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V;
     const int task = blockIdx.y;
+    wait_for_stream();
     if (task == 0 && p.dw_pre == nullptr) return;
     if (task == 1 && p.dw_post == nullptr && !(p.dgate != nullptr && p.gates == 1 && p.splits > 0)) return;
     const float* part = task == 0 ? p.part_pre : p.part_s;
     const bool weighted = task == 1 && p.splits > 0 && p.gates > 1;   // by the unit's gate row
-    int64_t b0 = 0, b1 = p.nparts;
+    const int splits = static_cast<int>(p.splits);   // as the number of partial rows at most kMaxParts
+    int b0 = 0, b1 = static_cast<int>(p.nparts);
     if (task >= 2) {
-        b0 = (task - 2) * p.splits;
-        b1 = b0 + p.splits;
+        b0 = (task - 2) * splits;
+        b1 = b0 + splits;
     }
     const T* gate = static_cast<const T*>(p.gate);
     float s[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) s[e] = 0.f;
     if (c < p.cols) {
-#pragma unroll 4
-        for (int64_t b = b0 + sl; b < b1; b += 32) {
+#pragma unroll 8
+        for (int b = b0 + sl; b < b1; b += 32) {
             float v[V];
-            const float* src = part + b * p.cols + c;
+            const float* src = part + static_cast<int64_t>(b) * p.cols + c;
             if constexpr (V == 4) unpack(ldg16(src), v);
             else v[0] = *src;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                if (weighted) v[e] *= ldf(gate + b / p.splits * p.cols + c + e);
+                if (weighted) v[e] *= ldf(gate + static_cast<int64_t>(b / splits) * p.cols + c + e);
                 s[e] += v[e];
             }
         }
@@ -716,10 +718,10 @@ int launch_sums(const SumP& s, cudaStream_t st) {
     if (s.dw_pre == nullptr && s.dw_post == nullptr && s.dgate == nullptr) return LIGER_OK;
     const unsigned tasks = 2u + (s.dgate != nullptr && s.gates > 1 && s.splits > 0 ? static_cast<unsigned>(s.gates) : 0u);
     if (s.cols % 4 == 0)
-        block_norm_sums<T, 4><<<dim3(static_cast<unsigned>(ceil_div(s.cols, 128)), tasks), 1024, 0, st>>>(s);
-    else
-        block_norm_sums<T, 1><<<dim3(static_cast<unsigned>(ceil_div(s.cols, 32)), tasks), 1024, 0, st>>>(s);
-    return check_launch("block_norm_sums");
+        return launch_early("block_norm_sums", block_norm_sums<T, 4>, dim3(static_cast<unsigned>(ceil_div(s.cols, 128)), tasks),
+                            1024, 0, st, s);
+    return launch_early("block_norm_sums", block_norm_sums<T, 1>, dim3(static_cast<unsigned>(ceil_div(s.cols, 32)), tasks),
+                        1024, 0, st, s);
 }
 
 // ------------------------------------------------------------------ launches

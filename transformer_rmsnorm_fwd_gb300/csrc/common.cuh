@@ -164,6 +164,26 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// A kernel launched with launch_early may be set up while the kernel before it on the stream still
+// runs; it calls wait_for_stream before it touches memory, which returns when that kernel is
+// done and its writes can be read.  Saves part of the gap between two short kernels.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+int launch_early(const char* what, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(static_cast<unsigned>(threads));
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+    return check_launch(what);
+}
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace liger

@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(256) head_gemm(const TA* __restrict__ A, const
     const int m0 = blockIdx.y * kHT, n0 = blockIdx.x * kHT;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int k0 = blockIdx.z * g.k_per, k1 = min(g.K, k0 + g.k_per);
+    wait_for_stream();
     // consecutive threads take consecutive elements of each operand's contiguous dimension
     const bool ak = g.sak == 1, bn = g.sbn == 1;
     float ra[4], rb[4];
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(256) head_gemm(const TA* __restrict__ A, const
 template <typename TO>
 __global__ void __launch_bounds__(256) head_join(TO* out, HeadGemm g) {
     const int64_t mn = static_cast<int64_t>(g.M) * g.N;
+    wait_for_stream();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < mn; i += static_cast<int64_t>(gridDim.x) * 256) {
         float v = 0.f;
 #pragma unroll 4
@@ -129,13 +131,12 @@ int launch_head_gemm(const TA* A, const TB* B, TO* out, HeadGemm g, float* part,
     g.k_per = static_cast<int>(ceil_div(ceil_div(g.K, splits), kHK) * kHK);
     g.splits = static_cast<int>(std::max<int64_t>(1, ceil_div(g.K, g.k_per)));
     g.part = part;
-    head_gemm<TA, TB, TO><<<dim3(static_cast<unsigned>(tn), static_cast<unsigned>(tm), static_cast<unsigned>(g.splits)), 256, 0, st>>>(
-        A, B, out, g);
-    if (int rc = check_launch("head_gemm")) return rc;
+    const dim3 grid(static_cast<unsigned>(tn), static_cast<unsigned>(tm), static_cast<unsigned>(g.splits));
+    if (int rc = launch_early("head_gemm", head_gemm<TA, TB, TO>, grid, 256, 0, st, A, B, out, g)) return rc;
     if (g.splits > 1) {
         const int64_t mn = static_cast<int64_t>(g.M) * g.N;
-        head_join<TO><<<static_cast<unsigned>(std::min<int64_t>(ceil_div(mn, 256), 8 * sm_count())), 256, 0, st>>>(out, g);
-        return check_launch("head_join");
+        const dim3 blocks(static_cast<unsigned>(std::min<int64_t>(ceil_div(mn, 256), 8 * sm_count())));
+        return launch_early("head_join", head_join<TO>, blocks, 256, 0, st, out, g);
     }
     return LIGER_OK;
 }

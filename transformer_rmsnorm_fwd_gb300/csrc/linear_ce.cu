@@ -696,6 +696,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_f32(const int64_t* __
                                                                const int64_t* __restrict__ idx, int64_t t0) {
     __shared__ float red[32];
     const int64_t row = blockIdx.x;
+    wait_for_stream();
     const int64_t y = labels[row];
     float* z = Z + row * ldz;
     if (y == ignore) {
@@ -735,6 +736,7 @@ __global__ void __launch_bounds__(kFinalThreads) policy_final(const float* __res
     __shared__ double red[3][32];
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float s[3] = {0.f, 0.f, 0.f}, e[3] = {0.f, 0.f, 0.f};
+    wait_for_stream();
 #pragma unroll 4
     for (int64_t t = threadIdx.x; t < T; t += nt) {
         add_with_error(term[t], s[0], e[0]);
@@ -1881,8 +1883,9 @@ int run_policy_simt(const Args& a, const Layout& L, float* split) {
         const int cl = static_cast<int>(std::min(L.C, a.T - t0));
         const bool first = c == 0, last = c == L.nchunks - 1;
         if ((rc = simt_logits(X + t0 * H, W, Z, cl, H, V, split, a.st))) return rc;
-        policy_rows_f32<<<cl, kRowThreads, 0, a.st>>>(a.labels + t0, a.ignore, Z, V, V, 1, *a.pol, nullptr, t0);
-        if ((rc = check_launch("linear_policy rows"))) return rc;
+        if ((rc = launch_early("linear_policy rows", policy_rows_f32, dim3(cl), kRowThreads, 0, a.st, a.labels + t0, a.ignore,
+                               Z, V, V, 1, *a.pol, nullptr, t0)))
+            return rc;
         if (dX) {   // dX_c = D W
             HeadGemm g{};
             g.M = cl;
@@ -1987,8 +1990,9 @@ int run_logp_simt(const void* X, const void* W, const int64_t* labs, int64_t T, 
         if (int rc = simt_logits(static_cast<const TI*>(X) + t0 * H, static_cast<const TI*>(W), Z, cl, H, V,
                                  reinterpret_cast<float*>(w8 + L.split), st))
             return rc;
-        policy_rows_f32<<<cl, kRowThreads, 0, st>>>(labs + t0, ignore, Z, V, V, 0, pol, nullptr, t0);
-        if (int rc = check_launch("linear_logp rows")) return rc;
+        if (int rc = launch_early("linear_logp rows", policy_rows_f32, dim3(cl), kRowThreads, 0, st, labs + t0, ignore, Z, V, V,
+                                  0, pol, nullptr, t0))
+            return rc;
     }
     return LIGER_OK;
 }
@@ -2130,8 +2134,8 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
     if (PL.L.tc) rc = n < T && worth_compacting(n, T) ? run_tc_compact(a, n, chunk, 0.f) : run_tc(a, PL.L, 0.f);
     else rc = dtype == LIGER_F32 ? run_policy_simt<float>(a, PL.L, f32(PL.split)) : run_policy_simt<__nv_bfloat16>(a, PL.L, f32(PL.split));
     if (rc) return rc;
-    policy_final<<<1, T <= 1024 ? 256 : kFinalThreads, 0, st>>>(f32(PL.term), f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
-    return check_launch("linear_policy");
+    return launch_early("linear_policy", policy_final, dim3(1), T <= 1024 ? 256 : kFinalThreads, 0, st, f32(PL.term),
+                        f32(PL.kl), f32(PL.clip), T, hdr, loss, stats);
 }
 
 }  // namespace
