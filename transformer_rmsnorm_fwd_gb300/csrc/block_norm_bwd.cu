@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(256) block_norm_bwd_generic(BwdP p) {
     float* pp = p.part_pre != nullptr ? p.part_pre + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
     const bool need_s = wp != nullptr || p.gate != nullptr;
     const float inv = 1.0f / static_cast<float>(p.cols);
+    wait_for_stream();
     for (int j = threadIdx.x; j < p.cols; j += blockDim.x) {
         if (ps != nullptr) ps[j] = 0.f;
         if (pp != nullptr) pp[j] = 0.f;
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_ring(BwdP p, int tw, int
     for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     mbar_init_fence();
     __syncthreads();
+    wait_for_stream();
     if (tt == 0)
         for (int s = 0; s < nst; ++s)
             if (t0 + s * step < t1) issue(t0 + s * step, s);
@@ -478,6 +480,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_odd(BwdP p, int nst, uin
         for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
     mbar_init_fence();
     __syncthreads();
+    wait_for_stream();
     if (tid == 0)
         for (int s = 0; s < nst; ++s)
             if (t0 + s * unit < t1) issue(t0 + s * unit, s);
@@ -758,8 +761,8 @@ int launch_bwd_ring(const BwdP& p, int nvec, size_t slot, int64_t grid, int team
     if (int rc = allow_smem<k>()) return rc;
     int* err = nullptr;
     if (int rc = rmsnorm_err_word(&err)) return rc;
-    k<<<static_cast<unsigned>(grid), teams * tw * 32, smem, st>>>(p, tw, static_cast<int>(nst), err);
-    return check_launch("block_norm_bwd_ring");
+    return launch_early("block_norm_bwd_ring", k, dim3(static_cast<unsigned>(grid)), teams * tw * 32, smem, st, p, tw,
+                        static_cast<int>(nst), err);
 }
 
 // Splits the rows and launches: 256 threads' worth of teams where a row takes less (TEAMS: whether it can).
@@ -797,9 +800,8 @@ int launch_bwd_odd(BwdP& p, int streams, int64_t& grid, cudaStream_t st) {
     grid = split_rows(p, static_cast<int64_t>(sm_count()) * std::max(1, per_sm));
     int* err = nullptr;
     if (int rc = rmsnorm_err_word(&err)) return rc;
-    if (p.splits == 0) kw<<<static_cast<unsigned>(grid), NT, nst * slot, st>>>(p, nst, static_cast<uint32_t>(wmax), err);
-    else k<<<static_cast<unsigned>(grid), NT, nst * slot, st>>>(p, nst, static_cast<uint32_t>(wmax), err);
-    return check_launch("block_norm_bwd_odd");
+    return launch_early("block_norm_bwd_odd", p.splits == 0 ? kw : k, dim3(static_cast<unsigned>(grid)), NT, nst * slot, st, p,
+                        nst, static_cast<uint32_t>(wmax), err);
 }
 
 template <typename T>
@@ -829,8 +831,7 @@ int launch_bwd(BwdP p, void* dw_post, void* dw_pre, float* ws, cudaStream_t st) 
         else rc = launch_bwd_odd<T, 16, 512>(p, streams, grid, st);
     } else if (nvec == 0 || nvec > 2048 || slot > 200u * 1024u) {
         grid = split_rows(p, static_cast<int64_t>(sm_count()) * 4);
-        block_norm_bwd_generic<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
-        rc = check_launch("block_norm_bwd");
+        rc = launch_early("block_norm_bwd", block_norm_bwd_generic<T>, dim3(static_cast<unsigned>(grid)), 256, 0, st, p);
     } else if (!F32 && nvec <= 256) rc = launch_bwd_ring<T, 1, 256, 1>(p, nvec, slot, grid, st);
     else if (nvec <= 512) rc = launch_bwd_ring<T, 2, 256, 1>(p, nvec, slot, grid, st);
     else if (nvec <= 768) rc = launch_bwd_ring<T, 2, 384, 0>(p, nvec, slot, grid, st);

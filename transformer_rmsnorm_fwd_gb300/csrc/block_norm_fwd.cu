@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(256) block_norm_fwd_generic(FwdP p) {
     const T *wp = static_cast<const T*>(p.w_post), *wn = static_cast<const T*>(p.w_pre);
     T *h = static_cast<T*>(p.h), *y = static_cast<T*>(p.y);
     const float inv = 1.0f / static_cast<float>(p.cols);
+    wait_for_stream();
     for (int64_t t = blockIdx.x; t < p.rows; t += gridDim.x) {
         const int64_t o = t * p.cols;
         const T* g = p.gate != nullptr ? static_cast<const T*>(p.gate) + t / p.per_gate * p.cols : nullptr;
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(512) block_norm_fwd_team(FwdP p, int tw) {
     const float inv = 1.0f / static_cast<float>(p.cols);
     Frag<T, VEC> fp[VPT], fn[VPT], fg[VPT];
     bool live[VPT];
+    wait_for_stream();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int c = j * nt + tt;
@@ -248,6 +250,7 @@ __global__ void __launch_bounds__(NT, MB) block_norm_fwd_ring(FwdP p, int tw, in
         for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
     mbar_init_fence();
     __syncthreads();
+    wait_for_stream();
     if (tt == 0)
         for (int s = 0; s < nst; ++s)
             if (t + s * step < p.rows) issue(t + s * step, s);
@@ -450,6 +453,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_fwd_odd(FwdP p, int nst, uin
         for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
     mbar_init_fence();
     __syncthreads();
+    wait_for_stream();
     if (tid == 0)
         for (int s = 0; s < nst; ++s)
             if (t + s * step < p.rows) issue(t + s * step, s);
@@ -572,8 +576,7 @@ int launch_fwd_team(const FwdP& p, int tw, cudaStream_t st) {
     const int teams = std::max(1, 8 / tw), threads = teams * tw * 32;
     auto k = block_norm_fwd_team<T, VEC, VPT>;
     const int64_t grid = std::min<int64_t>(ceil_div(p.rows, teams), static_cast<int64_t>(sm_count()) * resident(k, threads, 0, cache[tw]));
-    k<<<static_cast<unsigned>(grid), threads, 0, st>>>(p, tw);
-    return check_launch("block_norm_fwd_team");
+    return launch_early("block_norm_fwd_team", k, dim3(static_cast<unsigned>(grid)), threads, 0, st, p, tw);
 }
 
 template <typename T, int VPT, int GATES, int NT, int MB, int ONE>
@@ -596,8 +599,7 @@ int launch_fwd_ring(const FwdP& p, int tw, cudaStream_t st) {
     const int64_t grid = std::min<int64_t>(ceil_div(p.rows, teams), static_cast<int64_t>(sm_count()) * per_sm);
     int* err = nullptr;
     if (int rc = rmsnorm_err_word(&err)) return rc;
-    k<<<static_cast<unsigned>(grid), threads, nst * slot, st>>>(p, tw, nst, err);
-    return check_launch("block_norm_fwd_ring");
+    return launch_early("block_norm_fwd_ring", k, dim3(static_cast<unsigned>(grid)), threads, nst * slot, st, p, tw, nst, err);
 }
 
 template <typename T, int VPT, int NT, int MB, int ONE>
@@ -628,8 +630,8 @@ int launch_fwd_odd(const FwdP& p, cudaStream_t st) {
     const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm));
     int* err = nullptr;
     if (int rc = rmsnorm_err_word(&err)) return rc;
-    k<<<static_cast<unsigned>(grid), NT, smem, st>>>(p, nst, static_cast<uint32_t>(wmax), err);
-    return check_launch("block_norm_fwd_odd");
+    return launch_early("block_norm_fwd_odd", k, dim3(static_cast<unsigned>(grid)), NT, smem, st, p, nst,
+                        static_cast<uint32_t>(wmax), err);
 }
 
 // Which kernel: by the row's 16-byte vectors, and whether there are rows enough that a team takes
@@ -673,8 +675,7 @@ int launch_fwd(const FwdP& p, cudaStream_t st) {
         if (p.cols <= 8192) return launch_fwd_odd<T, 16, 512>(p, st);
     }
     const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(sm_count()) * 8);
-    block_norm_fwd_generic<T><<<static_cast<unsigned>(grid), 256, 0, st>>>(p);
-    return check_launch("block_norm_fwd");
+    return launch_early("block_norm_fwd", block_norm_fwd_generic<T>, dim3(static_cast<unsigned>(grid)), 256, 0, st, p);
 }
 
 }  // namespace

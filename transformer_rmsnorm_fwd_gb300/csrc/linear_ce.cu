@@ -222,6 +222,7 @@ __global__ void gather_rows(const uint4* __restrict__ src, const int64_t* __rest
 // dst = the rows of src, those of ignored tokens as zeros
 __global__ void masked_rows(const uint4* __restrict__ src, const int64_t* __restrict__ labels, int64_t ignore, int64_t T,
                             int64_t hv, uint4* __restrict__ dst) {
+    wait_for_stream();
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         const bool keep = labels[t] != ignore;
         for (int64_t v = threadIdx.x; v < hv; v += blockDim.x)
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(kRankThreads) sort_label_keys(const int64_t* _
     const int64_t b0 = static_cast<int64_t>(blockIdx.y) * seg;
     const int cnt = static_cast<int>(n - b0 < seg ? n - b0 : seg);
     const int i0 = blockIdx.x * 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_stream();
     if (i0 >= cnt) return;
     const int quads = (cnt + 3) / 4;
     for (int i = threadIdx.x; i < quads * 4; i += kRankThreads) {
@@ -370,6 +372,7 @@ __global__ void label_starts(const unsigned long long* __restrict__ keys, int64_
     const unsigned long long* k = keys + b0;
     int* ls = lstart + static_cast<int64_t>(blockIdx.y) * (V + 1);
     const int base = absolute ? static_cast<int>(b0) : 0;
+    wait_for_stream();
     for (int v = blockIdx.x * blockDim.x + threadIdx.x; v <= V; v += gridDim.x * blockDim.x) {
         const unsigned long long key = static_cast<unsigned long long>(v) << 32;
         int lo = 0, hi = cnt;
@@ -388,12 +391,12 @@ int sort_labels(const int64_t* labels, int64_t n, int seg, int64_t ignore, int V
     const int64_t nseg = ceil_div(n, static_cast<int64_t>(seg));
     if (nseg <= 0) return LIGER_OK;
     const dim3 ranks(static_cast<unsigned>(ceil_div(std::min<int64_t>(n, seg), int64_t{32})), static_cast<unsigned>(nseg));
-    sort_label_keys<<<ranks, kRankThreads, 0, st>>>(labels, n, seg, ignore, absolute ? 1 : 0, keys);
-    if (int rc = check_launch("sort_label_keys")) return rc;
+    if (int rc = launch_early("sort_label_keys", sort_label_keys, ranks, kRankThreads, 0, st, labels, n, seg, ignore,
+                              absolute ? 1 : 0, keys))
+        return rc;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(V + 1, 256), 2 * sm_count())),
                     static_cast<unsigned>(nseg));
-    label_starts<<<grid, 256, 0, st>>>(keys, n, seg, V, absolute ? 1 : 0, lstart);
-    return check_launch("label_starts");
+    return launch_early("label_starts", label_starts, grid, 256, 0, st, keys, n, seg, V, absolute ? 1 : 0, lstart);
 }
 
 // Merge the per-tile (m, s) of one chunk row into lse and rewrite P in place
@@ -641,6 +644,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* _
     __nv_bfloat16* prow = P + row * ldp;
     const int k0 = blockIdx.y * piece, k1 = min((V + 7) / 8, k0 + piece);
     const bool write = threadIdx.x == 0 && blockIdx.y == 0;   // the token's values
+    wait_for_stream();
     if (labels[row] == ignore) {
         if (P != nullptr) {
             for (int k = k0 + threadIdx.x; k < k1; k += kRowThreads)
@@ -1052,8 +1056,7 @@ int policy_dx(const Args& a, const Layout& L, const __nv_bfloat16* P, const tc::
     if (p.splits == 0) return LIGER_OK;
     const SplitJoin j{a.pol->kpart, p.rem, p.splits, p.slabs, p.full, TileCfg<1>::TM, static_cast<int>(ceil_div(cl, 256)),
                       static_cast<int>(ceil_div(H, 256)), a.labels + t0, a.ignore, e.tok_scale, W, out, cl, H};
-    split_join<<<dim3(static_cast<unsigned>(p.rem), TileCfg<1>::TM / 8), 256, 0, a.st>>>(j);
-    return check_launch("linear_policy dX");
+    return launch_early("linear_policy dX", split_join, dim3(static_cast<unsigned>(p.rem), TileCfg<1>::TM / 8), 256, 0, a.st, j);
 }
 
 int run_tc(const Args& a, const Layout& L, float scale) {
@@ -1074,9 +1077,10 @@ int run_tc(const Args& a, const Layout& L, float scale) {
     if (a.pol != nullptr && a.idx == nullptr && a.dW != nullptr && a.pol->xclean != nullptr) {
         // dW = D^T X sums over all tokens: a zero of D times whatever stands in X at a token that is
         // not valid is NaN if that is no finite number (4096 tokens of 4096: 10 us)
-        masked_rows<<<static_cast<int>(std::min<int64_t>(a.T, 8 * sm_count())), 256, 0, a.st>>>(
-            reinterpret_cast<const uint4*>(X), a.labels, a.ignore, a.T, a.H * 2 / 16, reinterpret_cast<uint4*>(a.pol->xclean));
-        if ((rc = check_launch("masked_rows"))) return rc;
+        if ((rc = launch_early("masked_rows", masked_rows, dim3(static_cast<unsigned>(std::min<int64_t>(a.T, 8 * sm_count()))),
+                               256, 0, a.st, reinterpret_cast<const uint4*>(X), a.labels, a.ignore, a.T, a.H * 2 / 16,
+                               reinterpret_cast<uint4*>(a.pol->xclean))))
+            return rc;
         X = a.pol->xclean;
     }
     CUtensorMap mW_k, mW_mn;
@@ -1099,6 +1103,7 @@ int run_tc(const Args& a, const Layout& L, float scale) {
 
         EpiParams e{};
         e.err = &hdr->err;
+        e.early = a.pol != nullptr ? 1 : 0;
         e.ignore_index = a.ignore;
         e.labels = a.labels + t0;
         // 1. logits -> P, (m, s) partials, z at label
@@ -1121,15 +1126,18 @@ int run_tc(const Args& a, const Layout& L, float scale) {
         if (rc) return rc;
         // 2. lse, loss terms, P -> D in place (policy loss: long runs of a row where they fill the GPU)
         const int piece = cl * ceil_div(V, 8 * 8192) >= 8 * sm_count() ? 8192 : 2048;
-        if (a.pol != nullptr)
-            policy_rows_bf16<<<dim3(cl, static_cast<unsigned>(ceil_div(ceil_div(V, 8), piece))), kRowThreads, fac_smem,
-                               a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt), zlab + t0, P, L.ldp, V, *a.pol,
-                                       a.idx != nullptr ? a.idx + t0 : nullptr, t0, a.pol->coef + t0, piece);
-        else
+        if (a.pol != nullptr) {
+            const dim3 grid(cl, static_cast<unsigned>(ceil_div(ceil_div(V, 8), piece)));
+            rc = launch_early("linear_policy rows", policy_rows_bf16, grid, kRowThreads, fac_smem, a.st, a.labels + t0, a.ignore,
+                              part, static_cast<int>(L.nvt), zlab + t0, P, L.ldp, V, *a.pol,
+                              a.idx != nullptr ? a.idx + t0 : nullptr, t0, a.pol->coef + t0, piece);
+        } else {
             dlogits_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
                                                               zlab + t0, P, L.ldp, V, scale, a.scale_dev, lse + t0,
                                                               lossrow + t0);
-        if ((rc = check_launch("dlogits_bf16"))) return rc;
+            rc = check_launch("dlogits_bf16");
+        }
+        if (rc) return rc;
         if (a.pol != nullptr) e.tok_scale = a.pol->coef + t0;
         // 3. dX_c = D W, minus scale * W[label] in fp32
         if (a.dX && a.pol != nullptr) {
@@ -1746,6 +1754,7 @@ __global__ void __launch_bounds__(256) logp_few(const __nv_bfloat16* __restrict_
     extern __shared__ uint4 xs[];   // [NT][H / 8]
     __shared__ float2 ms[8][NT];
     const int nv = H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_stream();
     for (int i = threadIdx.x; i < NT * nv; i += 256)
         xs[i] = i < n * nv ? ldg16(X + static_cast<int64_t>(i) * 8) : make_uint4(0, 0, 0, 0);
     const int64_t y = lane < n ? labels[lane] : -1;
@@ -1833,8 +1842,7 @@ int launch_logp_few(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, logp_few<NT, R>, 256, smem);
     // every block has rows, and no more blocks than the workspace holds partials for
     nparts = static_cast<int>(std::min<int64_t>({ceil_div(V, 8 * R), static_cast<int64_t>(sm_count()) * std::max(1, per_sm), most_parts}));
-    logp_few<NT, R><<<nparts, 256, smem, st>>>(X, W, labs, n, H, V, part, nparts, zlab);
-    return check_launch("logp_few");
+    return launch_early("logp_few", logp_few<NT, R>, dim3(nparts), 256, smem, st, X, W, labs, n, H, V, part, nparts, zlab);
 }
 
 // Reads the header of the scan back and waits for it.
@@ -1946,8 +1954,8 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
              : nn == 2 ? launch_logp_few<2, 1>(X, W, labs, nn, H, V, part, zlab, most, np, st)
                        : launch_logp_few<4, 2>(X, W, labs, nn, H, V, part, zlab, most, np, st);
         if (rc) return rc;
-        policy_rows_bf16<<<nn, kRowThreads, 0, st>>>(labs, ignore, part, np, zlab, nullptr, 0, V, pol, idx, 0, nullptr, 0);
-        return check_launch("linear_logp rows");
+        return launch_early("linear_logp rows", policy_rows_bf16, dim3(nn), kRowThreads, 0, st, labs, ignore, part, np, zlab,
+                            nullptr, 0, V, pol, idx, 0, nullptr, 0);
     }
     int64_t x_rows = 0;
     if (n < kPadRows) {
@@ -1960,6 +1968,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
         const int cl = static_cast<int>(std::min(L.C, n - t0));
         EpiParams e{};
         e.err = &reinterpret_cast<Hdr*>(w8 + L.hdr)->err;
+        e.early = 1;
         e.ignore_index = ignore;
         e.labels = labs + t0;
         e.M = cl;
@@ -1972,9 +1981,10 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
         e.nvt = static_cast<int>(L.nvt);
         e.zlab = zlab + t0;
         if ((rc = launch_logits(X + t0 * H, cl, H, V, mW_k, e, 0, L.nvt, st, x_rows))) return rc;
-        policy_rows_bf16<<<cl, kRowThreads, 0, st>>>(labs + t0, ignore, part, static_cast<int>(L.nvt), zlab + t0, nullptr,
-                                                     0, V, pol, idx != nullptr ? idx + t0 : nullptr, t0, nullptr, 0);
-        if ((rc = check_launch("linear_logp rows"))) return rc;
+        if ((rc = launch_early("linear_logp rows", policy_rows_bf16, dim3(cl), kRowThreads, 0, st, labs + t0, ignore, part,
+                               static_cast<int>(L.nvt), zlab + t0, nullptr, 0, V, pol, idx != nullptr ? idx + t0 : nullptr, t0,
+                               nullptr, 0)))
+            return rc;
     }
     return LIGER_OK;
 }

@@ -108,6 +108,7 @@ int fwd_impl(const void* X, const void* Wg, const void* Wu, void* out, void* g_s
         if ((rc = make_map(&mX, X, H, T, H, BK, BM))) return rc;
         e.m_group = static_cast<int>(ceil_div(sub, static_cast<int64_t>(TileCfg<1>::TM)));
         e.ldq = ceil_div(I, kCkptGroup);
+        e.early = 1;
         e.g8 = q.g8;
         e.u8 = q.u8;
         e.g8s = q.g8s;
@@ -146,6 +147,7 @@ struct GradArgs {
     int64_t T, H, I;
     int* d_err;
     cudaStream_t st;
+    int early;
 };
 
 int dx_from_dgdu(const GradArgs& a, int64_t splits) {
@@ -165,6 +167,7 @@ int dx_from_dgdu(const GradArgs& a, int64_t splits) {
     d.ldo = a.H;
     d.ksplit_nkb = nkb1;
     d.raster = RASTER_N_GROUPS;
+    d.early = a.early;
     if (splits < 2)
         return launch_gemm<0, 1, EPI_STORE, 1>(mdG_k, mG_mn, d.M, d.N, 2 * nkb1 * BK, d, a.st, 0, &mdU_k, &mU_mn);
     const int tm = (d.M + TileCfg<1>::TM - 1) / TileCfg<1>::TM, tn = (d.N + BN - 1) / BN;
@@ -186,8 +189,8 @@ int dx_from_dgdu(const GradArgs& a, int64_t splits) {
     j.out = d.out;
     j.M = d.M;
     j.N = d.N;
-    split_join<<<dim3(static_cast<unsigned>(j.rem), static_cast<unsigned>(ceil_div(j.part_rows, 8))), 256, 0, a.st>>>(j);
-    return check_launch("fused_linear_swiglu dX");
+    return launch_early("fused_linear_swiglu dX", split_join,
+                        dim3(static_cast<unsigned>(j.rem), static_cast<unsigned>(ceil_div(j.part_rows, 8))), 256, 0, a.st, j);
 }
 
 int dw_from_dgdu(const GradArgs& a, bool split) {
@@ -216,6 +219,7 @@ int dw_from_dgdu(const GradArgs& a, bool split) {
     w.out2 = static_cast<__nv_bfloat16*>(a.dWu);
     w.msplit_mt = mt;
     w.M2 = static_cast<int>(a.I);
+    w.early = a.early;
     const int M = mt * TileCfg<1>::TM + static_cast<int>(a.I), N = static_cast<int>(a.H), K = static_cast<int>(a.T);
     const int64_t tn = ceil_div(a.H, static_cast<int64_t>(BN)), tiles = 2 * mt * tn, pairs = sm_count() / 2;
     const int64_t rem = tiles % pairs, tile_bytes = int64_t{TileCfg<1>::TM} * BN * 4;
@@ -243,15 +247,15 @@ int dw_from_dgdu(const GradArgs& a, bool split) {
     j.msplit_mt = mt;
     j.M2 = w.M2;
     j.out2 = w.out2;
-    split_join<<<dim3(static_cast<unsigned>(rem), static_cast<unsigned>(j.part_rows / 8)), 256, 0, a.st>>>(j);
-    return check_launch("fused_linear_swiglu dW");
+    return launch_early("fused_linear_swiglu dW", split_join,
+                        dim3(static_cast<unsigned>(rem), static_cast<unsigned>(j.part_rows / 8)), 256, 0, a.st, j);
 }
 
 int grads_from_dgdu(const void* X, const void* Wg, const void* Wu, const __nv_bfloat16* dG,
                     const __nv_bfloat16* dU, void* dX, void* dWg, void* dWu, int64_t T, int64_t H, int64_t I,
                     int* d_err, cudaStream_t st, bool split = false) {
     using namespace tc;
-    const GradArgs a{X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st};
+    const GradArgs a{X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st, split ? 1 : 0};
     // dX: items of at least 16 k-blocks, as many as there are CTA pairs and dW_g's bytes hold
     const int64_t tiles = ceil_div(T, static_cast<int64_t>(TileCfg<1>::TM)) * ceil_div(H, static_cast<int64_t>(BN));
     const int64_t rows = std::min<int64_t>(T, TileCfg<1>::TM);

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_fwd_ckpt8_vec(const T* gate, 
                                                                  uint8_t* __restrict__ gs, int8_t* __restrict__ up8,
                                                                  uint8_t* __restrict__ us, int64_t n, int cols, int groups) {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+    wait_for_stream();
     // whole warps run the loop: base is the warp's first piece
     const int lane = threadIdx.x & 31;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; base < n; base += kUnroll * stride) {
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_fwd_ckpt8_wide(const T* gate,
                                                                   uint8_t* __restrict__ gs, int8_t* __restrict__ up8,
                                                                   uint8_t* __restrict__ us, int64_t n) {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+    wait_for_stream();
     const int lane = threadIdx.x & 31;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; base < n; base += U * stride) {
         Raw8<T> rg[U][2] = {}, ru[U][2] = {};
@@ -212,6 +214,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_ckpt8_vec(const T* dy, co
                                                                  const uint8_t* __restrict__ us, T* dgate, T* dup,
                                                                  int64_t n, int cols, int groups) {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+    wait_for_stream();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += kUnroll * stride) {
         Raw8<T> rd[kUnroll] = {};
         uint2 cg[kUnroll], cu[kUnroll];
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_fwd_ckpt8_any(const T* gate, 
                                                                  int groups) {
     const int lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kGroupsAny;
+    wait_for_stream();
     for (int64_t w = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kGroupsAny; w < ngroups; w += step) {
         Element el[kGroupsAny];
         float g[kGroupsAny], u[kGroupsAny];
@@ -301,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_ckpt8_any(const T* dy, co
                                                                  int64_t ngroups, int cols, int groups) {
     const int lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kGroupsAny;
+    wait_for_stream();
     for (int64_t w = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kGroupsAny; w < ngroups; w += step) {
         Element el[kGroupsAny];
         float d[kGroupsAny];
@@ -340,18 +345,17 @@ int launch_fwd(const void* gate, const void* up, void* y, int8_t* gate8, uint8_t
     T* o = static_cast<T*>(y);
     const int groups = static_cast<int>(ceil_div(cols, kCkptGroup));
     const int64_t ngroups = rows * groups;
+    const char* who = "swiglu_fwd_ckpt8";
     if (cols % kCkptGroup == 0) {
         constexpr int U = sizeof(T) == 2 ? 2 : 1;   // fp32: one piece is four vectors of each input already
-        swiglu_fwd_ckpt8_wide<T, U><<<grid_for(ceil_div(ngroups * 2, U)), kThreads, 0, st>>>(g, u, o, gate8, gs, up8, us,
-                                                                                            ngroups * 2);
-    } else if (cols % 8 == 0) {
-        swiglu_fwd_ckpt8_vec<T><<<grid_for(ceil_div(ngroups * 4, kUnroll)), kThreads, 0, st>>>(g, u, o, gate8, gs, up8, us,
-                                                                                              ngroups * 4, cols, groups);
-    } else {
-        swiglu_fwd_ckpt8_any<T><<<grid_for(ceil_div(ngroups, kGroupsAny) * 32), kThreads, 0, st>>>(g, u, o, gate8, gs, up8, us,
-                                                                                                 ngroups, cols, groups);
+        return launch_early(who, swiglu_fwd_ckpt8_wide<T, U>, grid_for(ceil_div(ngroups * 2, U)), kThreads, 0, st, g, u, o,
+                            gate8, gs, up8, us, ngroups * 2);
     }
-    return check_launch("swiglu_fwd_ckpt8");
+    if (cols % 8 == 0)
+        return launch_early(who, swiglu_fwd_ckpt8_vec<T>, grid_for(ceil_div(ngroups * 4, kUnroll)), kThreads, 0, st, g, u, o,
+                            gate8, gs, up8, us, ngroups * 4, cols, groups);
+    return launch_early(who, swiglu_fwd_ckpt8_any<T>, grid_for(ceil_div(ngroups, kGroupsAny) * 32), kThreads, 0, st, g, u, o,
+                        gate8, gs, up8, us, ngroups, cols, groups);
 }
 
 template <typename T>
@@ -361,15 +365,13 @@ int launch_bwd(const void* dy, const int8_t* gate8, const uint8_t* gs, const int
     T *og = static_cast<T*>(dgate), *ou = static_cast<T*>(dup);
     const int groups = static_cast<int>(ceil_div(cols, kCkptGroup));
     const int64_t ngroups = rows * groups;
-    const unsigned grid = grid_for(ceil_div(ngroups * 4, kUnroll));
-    if (cols % kCkptGroup == 0)
-        swiglu_bwd_ckpt8_vec<T, true><<<grid, kThreads, 0, st>>>(d, gate8, gs, up8, us, og, ou, ngroups * 4, cols, groups);
-    else if (cols % 8 == 0)
-        swiglu_bwd_ckpt8_vec<T, false><<<grid, kThreads, 0, st>>>(d, gate8, gs, up8, us, og, ou, ngroups * 4, cols, groups);
-    else
-        swiglu_bwd_ckpt8_any<T><<<grid_for(ceil_div(ngroups, kGroupsAny) * 32), kThreads, 0, st>>>(d, gate8, gs, up8, us, og,
-                                                                                                 ou, ngroups, cols, groups);
-    return check_launch("swiglu_bwd_ckpt8");
+    const char* who = "swiglu_bwd_ckpt8";
+    if (cols % 8 == 0)
+        return launch_early(who, cols % kCkptGroup == 0 ? swiglu_bwd_ckpt8_vec<T, true> : swiglu_bwd_ckpt8_vec<T, false>,
+                            grid_for(ceil_div(ngroups * 4, kUnroll)), kThreads, 0, st, d, gate8, gs, up8, us, og, ou,
+                            ngroups * 4, cols, groups);
+    return launch_early(who, swiglu_bwd_ckpt8_any<T>, grid_for(ceil_div(ngroups, kGroupsAny) * 32), kThreads, 0, st, d, gate8,
+                        gs, up8, us, og, ou, ngroups, cols, groups);
 }
 
 int check(const char* who, int64_t rows, int64_t cols, int dtype, std::initializer_list<const void*> wide,

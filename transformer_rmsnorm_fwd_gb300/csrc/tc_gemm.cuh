@@ -188,6 +188,7 @@ struct EpiParams {
     uint8_t *g8s, *u8s;
     int64_t ldq;
     int m_group;   // row blocks that one sweep over all columns takes (they stay in L2)
+    int early;     // set up while the kernel before still runs (barriers, TMEM), as launch_early; CTA pairs only
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -557,6 +558,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (PAIR) cluster_sync_all();   // both CTAs' barriers initialised before any cross-CTA arrive
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(slot_ptr);
+    wait_for_stream();   // launched early: nothing above reads or writes global memory
 
     auto tile_mn = [&](int t, int& mi, int& ni) {
         if (ep.raster == RASTER_N_FASTEST) {
@@ -1376,7 +1378,7 @@ int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int 
     units = std::max(1, std::min(units, tiles));
     if (PAIR) {
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute at[1];
+        cudaLaunchAttribute at[2] = {};
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = 2;
         at[0].val.clusterDim.y = 1;
@@ -1385,8 +1387,10 @@ int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int 
         cfg.blockDim = dim3(THREADS);
         cfg.dynamicSmemBytes = Cfg::SMEM;
         cfg.stream = st;
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = ep.early ? 2 : 1;
         if (cudaLaunchKernelEx(&cfg, kern, ma, mb, ma2 ? *ma2 : ma, mb2 ? *mb2 : mb, M, N, K, ep) != cudaSuccess)
             return check_launch("tc_gemm pair launch");
         return check_launch("tc_gemm");
@@ -1395,9 +1399,9 @@ int launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, int M, int N, int 
     return check_launch("tc_gemm");
 }
 
-// bf16 out of the split tiles of a launch over CTA pairs (RASTER_N_GROUPS, or RASTER_N_FASTEST with n_fastest): the sum of a tile's items, in
-// the order of the k ranges and, when the launches went over `slabs` runs of K (items apart), of
-// those.  With labels, minus tok_scale[row] corr[labels[row], :], and +0 on rows labelled `ignore`.
+// bf16 out of the split tiles of a launch over CTA pairs (RASTER_N_GROUPS, or RASTER_N_FASTEST with
+// n_fastest): the sum of a tile's items, in the order of the k ranges and, when the launches went over
+// `slabs` runs of K (items apart), of those.  With labels, minus tok_scale[row] corr[labels[row], :], and +0 on rows labelled `ignore`.
 struct SplitJoin {
     const float* part;
     int rem, splits, slabs, full, part_rows;   // rem tiles from `full` on
@@ -1414,6 +1418,7 @@ struct SplitJoin {
 };
 __global__ void __launch_bounds__(256) split_join(SplitJoin p) {
     constexpr int TM = TileCfg<1>::TM;
+    wait_for_stream();
     // the tile's row and column block, as the kernel's raster gives them
     const int t = p.full + static_cast<int>(blockIdx.x);
     const int gfull = p.num_n / GROUP_N, in_full = gfull * p.num_m * GROUP_N;
