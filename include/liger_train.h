@@ -12,7 +12,8 @@
  *     loss with a KL term from the hidden states, with its gradients.
  *
  * Every call here except liger_linear_logp_fwd and liger_linear_policy_fwd_bwd
- * (which wait for their label scan) queues work only and can be captured in a
+ * (which wait for their label scan; work on the workspace may be queued by then)
+ * queues work only and can be captured in a
  * CUDA graph after a first call on the device.  A bounded wait that expires in a
  * kernel (see liger.h) leaves NaN in the block norms' unfinished rows and sums,
  * in logp and in the policy's loss and stats; liger_device_status names the
@@ -140,7 +141,7 @@ int liger_fused_linear_swiglu_bwd_ckpt8(const void* X, const void* Wg, const voi
  *   tensor cores V is at most 4194240, and so are the rows of a chunk.
  *   ws: at least liger_linear_logp_workspace bytes, 256-byte aligned.
  * liger_linear_logp_fwd waits for a scan of the labels: a label outside [0, V)
- * that is not ignore_index returns LIGER_ERR_LABEL with nothing else queued,
+ * that is not ignore_index returns LIGER_ERR_LABEL with logp left as it was,
  * and only tokens that are not ignored go through the GEMM.  The _async form
  * does not wait (it can be captured): it runs all tokens, and a bad label's
  * logp is NaN. */
@@ -181,7 +182,7 @@ int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* lab
  *   path: per chunk the logits exist only in a [chunk x V] workspace buffer.
  *   ws: at least liger_linear_policy_workspace bytes, 256-byte aligned.
  *   The call waits for a scan of the labels and sequences: a bad label returns
- *   LIGER_ERR_LABEL, bad cu_seqlens LIGER_ERR_SHAPE, with nothing else queued,
+ *   LIGER_ERR_LABEL, bad cu_seqlens LIGER_ERR_SHAPE, with no output written,
  *   and only valid tokens go through the GEMMs.  The _async form does not wait
  *   (it can be captured in a CUDA graph): all tokens go through the GEMMs, a bad
  *   label counts as ignored and bad cu_seqlens leave no valid token; either

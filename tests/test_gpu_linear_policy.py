@@ -253,6 +253,28 @@ def test_bad_labels_and_sequences(L):
         assert math.isnan(float(o["loss"])) and bool((o["dX"] == 0).all()) and bool((o["dW"] == 0).all())
 
 
+@pytest.mark.parametrize("T,H,V,dt,chunk", [(50, 64, 300, "bf16", 0), (50, 64, 300, "bf16", 16), (600, 64, 300, "bf16", 0),
+                                            (50, 33, 100, "f32", 0), (600, 33, 100, "f32", 128)])
+def test_a_bad_label_leaves_the_outputs(L, T, H, V, dt, chunk):
+    """The waiting forms write no output when the scan finds a bad label, and the next call on the workspace is not disturbed."""
+    i = _inputs(T, H, V, dt, [0, T], seed=T, masked=0.2)
+    ws = torch.empty(L.liger_linear_policy_workspace(T, H, V, 1, chunk, _code(L, dt)), dtype=torch.uint8, device="cuda")
+    good = _call(L, i, dt, "sum", 0.2, 0.2, 0.1, 1.0, chunk=chunk, ws=ws)
+    lab = i["labels"].clone()
+    lab[T - 1] = V
+    out = dict(loss=torch.full((1,), 7.0, device="cuda"), stats=torch.full((2,), 7.0, device="cuda"),
+               logp=torch.full((T,), 7.0, device="cuda"), dX=torch.full_like(i["X"], 7.0), dW=torch.full_like(i["W"], 7.0))
+    for _ in range(3):
+        with pytest.raises(L.LigerError) as e:
+            L.liger_linear_policy_fwd_bwd(i["X"], i["W"], lab, i["old"], i["adv"], out["loss"], out["dX"], out["dW"], ws,
+                                          ref_logp=i["ref"], cu_seqlens=i["cu"], logp=out["logp"], stats=out["stats"],
+                                          reduction="sum", beta=0.1, chunk=chunk)
+        assert e.value.status == -5
+        assert all(bool((v == 7).all()) for v in out.values())
+    again = _call(L, i, dt, "sum", 0.2, 0.2, 0.1, 1.0, chunk=chunk, ws=ws)
+    assert all(torch.equal(again[k], good[k]) for k in good)
+
+
 def test_non_finite_inputs_reach_the_loss(L):
     """NaN at a valid token is not hidden; a ratio of infinity is held by the clip when A > 0."""
     i = _inputs(60, 64, 300, "f32", [0, 60], masked=0.0)

@@ -168,7 +168,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // runs; it calls wait_for_stream before it touches memory, which returns when that kernel is
 // done and its writes can be read.  Saves part of the gap between two kernels: SwiGLU with checkpoints,
 // forward and backward, fp32 515 x 2739 19.7 us, 15.7 to 18 early; bf16 8192 x 11008 217 us, 212 early; the
-// policy loss, fp32, of 256 tokens at 256 x 1024, twelve kernels, 72 us, 58 early.
+// policy loss, fp32, of 256 tokens at 256 x 1024, nine kernels, 72 us, 58 early.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
 int launch_early(const char* what, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {

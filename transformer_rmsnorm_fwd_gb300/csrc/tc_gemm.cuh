@@ -1442,7 +1442,7 @@ __global__ void __launch_bounds__(256) split_join(SplitJoin p) {
     if (row >= (second ? p.M2 : p.M) || col >= p.N) return;
     float v[8] = {};
     const int items = p.slabs * p.splits;   // item i of this tile: slab i / splits, k range i % splits
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < items; ++i) {
         const float* src =
             p.part + ((static_cast<int64_t>(i) * p.rem + blockIdx.x) * p.part_rows + lr) * BN + lc;
