@@ -142,7 +142,8 @@ int liger_fused_linear_swiglu_bwd_ckpt8(const void* X, const void* Wg, const voi
  *   ws: at least liger_linear_logp_workspace bytes, 256-byte aligned.
  * liger_linear_logp_fwd waits for a scan of the labels: a label outside [0, V)
  * that is not ignore_index returns LIGER_ERR_LABEL with logp left as it was,
- * and only tokens that are not ignored go through the GEMM.  The _async form
+ * and tokens that are ignored do not go through the GEMM where leaving them out
+ * saves a tile of 256.  The _async form
  * does not wait (it can be captured): it runs all tokens, and a bad label's
  * logp is NaN. */
 size_t liger_linear_logp_workspace(int64_t T, int64_t H, int64_t V, int dtype);
@@ -183,7 +184,8 @@ int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* lab
  *   ws: at least liger_linear_policy_workspace bytes, 256-byte aligned.
  *   The call waits for a scan of the labels and sequences: a bad label returns
  *   LIGER_ERR_LABEL, bad cu_seqlens LIGER_ERR_SHAPE, with no output written,
- *   and only valid tokens go through the GEMMs.  The _async form does not wait
+ *   and tokens that are not valid do not go through the tensor-core GEMMs where
+ *   leaving them out saves a tile of 256.  The _async form does not wait
  *   (it can be captured in a CUDA graph): all tokens go through the GEMMs, a bad
  *   label counts as ignored and bad cu_seqlens leave no valid token; either
  *   makes the loss and stats NaN.
