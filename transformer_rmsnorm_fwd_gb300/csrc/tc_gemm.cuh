@@ -1242,23 +1242,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                         store_block<4, true>(s_out, lane, oblk + c * 64, ep.ldo * 2, rows,
                                              chunks_below(n0 + c * 32, ep.N, 8, 4));
                 };
-                // MN-major A with token scales (dW of the policy loss): where a warp's rows have nothing but
-                // their product (no sum to read or write, no label), 64 columns a round, whole 128-byte lines
-                // of a row, the next columns' TMEM load in flight.  One warp per scheduler takes all of a
+                // MN-major A with token scales (dW of the policy loss) and no sum to read or write: 64 columns a
+                // round, whole 128-byte lines of a row, the next columns' TMEM load in flight.  One warp per scheduler takes all of a
                 // tile's rows, whose latency bounds the kernel when K is short (dW of 64 tokens at 128256 x
-                // 4096: 307 us, 460 without)
+                // 4096: 303 us, 460 without; of 700: 483, 519)
                 constexpr bool QUICK = MODE == MODE_TOKENS && A_MN;
-                if (QUICK && !acc_read && !acc_write && nseg == 1 && ep.labels == nullptr &&
-                    __all_sync(0xffffffffu, k_lo == k_hi)) {
+                if (QUICK && !acc_read && !acc_write && nseg == 1 && ep.labels == nullptr) {
                     uint32_t ra[32], rb[32];
-                    auto put = [&](const uint32_t(&r)[32], int j0) {   // 32 columns of this lane's row, from chunk j0
+                    auto put = [&](const uint32_t(&r)[32], int c, int j0) {   // block c of this lane's row, from chunk j0
+                        float f[32];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            float f[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(r[g * 8 + e]);
-                            sts16(s_acc + stage_slot<8>(lane, j0 + g), pack_bf8(f));
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
+                        for (int kk = k_lo; kk < k_hi; ++kk) {
+                            const int64_t t = static_cast<int64_t>(ep.keys[kk] & 0xFFFFFFFFull);
+                            sub_scaled32(f, ep.corr_src + t * ep.ld_corr + n0 + c * 32, ep.tok_scale[t], ep.N - (n0 + c * 32));
                         }
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) sts16(s_acc + stage_slot<8>(lane, j0 + g), pack_bf8(f + g * 8));
                     };
                     tmem_ld32_issue(taddr, ra);
 #pragma unroll 1
@@ -1266,10 +1266,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld_wait(ra);
                         tmem_ld32_issue(taddr + (c + 1) * 32, rb);
                         __syncwarp();   // the previous round's row runs have been read
-                        put(ra, 0);
+                        put(ra, c, 0);
                         tmem_ld_wait(rb);
                         if (c + 2 < BN / 32) tmem_ld32_issue(taddr + (c + 2) * 32, ra);
-                        put(rb, 4);
+                        put(rb, c + 1, 4);
                         __syncwarp();
                         store_block<8, true>(s_acc, lane, oblk + c * 64, ep.ldo * 2, rows, chunks_below(n0 + c * 32, ep.N, 8, 8));
                     }
