@@ -188,6 +188,66 @@ def test_other_stream_and_graphs(L):
     _same(_snapshot(two), want[1])
 
 
+def test_kernels_wait_for_what_they_read(L):
+    """Each call right behind the kernel that writes its inputs, behind work of another stream that was joined in, and behind
+    a long kernel: eager, and replayed from a graph with such forks, where every kernel is set up ahead of its predecessor's end."""
+    T, H, V = 512, 1024, 2000
+    src = [torch.randn(T, H, device="cuda").to(BF) for _ in range(4)]
+    W = (torch.randn(V, H, device="cuda") * H ** -0.5).to(BF)
+    w = torch.ones(H, device="cuda", dtype=BF)
+    lab = torch.randint(0, V, (T,), device="cuda")
+    old, adv = torch.full((T,), -8.0, device="cuda"), torch.ones(1, device="cuda")
+    big = torch.empty(1 << 27, device="cuda")
+    side = torch.cuda.Stream()
+    ws_p = torch.empty(L.liger_linear_policy_workspace(T, H, V), dtype=torch.uint8, device="cuda")
+    ws_l = torch.empty(L.liger_linear_logp_workspace(T, H, V), dtype=torch.uint8, device="cuda")
+    ws_n = torch.empty(L.liger_block_norm_bwd_workspace(T, H, 0), dtype=torch.uint8, device="cuda")
+    t = {k: torch.empty(T, H, device="cuda", dtype=BF) for k in ("z", "r", "h", "y", "s", "dg", "du", "dr", "dz", "dX")}
+    t.update(dW=torch.empty_like(W), dwn=torch.empty_like(w), rh=torch.empty(T, device="cuda"), loss=torch.empty(1, device="cuda"),
+             logp=torch.empty(T, device="cuda"))
+    kept = (*L.liger_ckpt8_empty(T, H), *L.liger_ckpt8_empty(T, H))
+
+    def run():
+        for k in t:
+            t[k].fill_(float("nan"))
+        big.fill_(1.0)                                       # a long kernel, then short ones
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            big[:1 << 26].mul_(0.5)
+            t["r"].copy_(src[1])
+        t["z"].copy_(src[0])
+        main.wait_stream(side)                               # joined: r comes from the other stream
+        L.liger_block_norm_fwd(t["z"], t["r"], t["h"], t["y"], w_pre=w, rstd_h=t["rh"])
+        L.liger_swiglu_fwd_ckpt8(t["h"], t["y"], t["s"], *kept)
+        L.liger_swiglu_bwd_ckpt8(t["s"], *kept, t["dg"], t["du"])
+        L.liger_linear_logp_fwd(t["s"], W, lab, t["logp"], ws_l, wait=False)
+        L.liger_linear_policy_fwd_bwd(t["s"], W, lab, old, adv, t["loss"], t["dX"], t["dW"], ws_p, wait=False)
+        L.liger_block_norm_bwd(t["dg"], t["dX"], None, t["h"], t["dr"], t["dz"], ws_n, w_pre=w, rstd_h=t["rh"], dw_pre=t["dwn"])
+        big.fill_(2.0)
+
+    def result():
+        torch.cuda.synchronize()
+        return {k: v.clone() for k, v in t.items()}
+    run()
+    first = result()
+    assert all(bool(torch.isfinite(v).all()) for v in first.values())
+    h = (src[0].double() + src[1].double())
+    assert bool(((first["h"].double() - h).abs() <= 2.0 ** -8 * h.abs()).all())   # the joined stream's r was read
+    for _ in range(20):
+        run()
+    _same(result(), first)
+    own = torch.cuda.Stream()
+    own.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(own):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=own):
+            run()
+    for _ in range(20):
+        g.replay()
+    _same(result(), first)
+
+
 def test_threads(L):
     """Steps of four threads at once, each on its own stream and buffers."""
     steps = [Step(L, seed=10 + i) for i in range(4)]
