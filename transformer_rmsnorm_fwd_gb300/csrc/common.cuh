@@ -167,7 +167,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // A kernel launched with launch_early may be set up while the kernel before it on the stream still
 // runs; it calls wait_for_stream before it touches memory, which returns when that kernel is
 // done and its writes can be read.  Saves part of the gap between two kernels: SwiGLU with checkpoints,
-// forward and backward, fp32 515 x 2739 19.7 us, 15.7 to 18 early; bf16 8192 x 11008 217 us, 212 early; the
+// forward and backward, fp32 515 x 2739 19.7 us, 16 to 20 early; bf16 8192 x 11008 217 us, 212 early; the
 // policy loss, fp32, of 256 tokens at 256 x 1024, nine kernels, 72 us, 58 early.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
