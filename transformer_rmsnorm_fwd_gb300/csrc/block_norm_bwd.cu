@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_ring(BwdP p, int tw, int
                 D = __ffma2_rn(nc1, fh[e], D);
                 od[e] = __fmul2_rn(ra, D);
                 const float2 Dr = __fmul2_rn(D, rz2);
-                oz[e] = __ffma2_rn(nc2, fz[e], __fmul2_rn(q[j][e], Dr));
+                oz[e] = __fmul2_rn(q[j][e], Dr);
+                if (post) oz[e] = __ffma2_rn(nc2, fz[e], oz[e]);   // without it z has no part in dz: 0 z is NaN at an infinity
                 S[j][e] = __ffma2_rn(Dr, fz[e], S[j][e]);
             }
             const int64_t at = t * p.cols + static_cast<int64_t>(j * nt + tt) * VEC;
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_odd(BwdP p, int nst, uin
             const float fz = need_z ? get(o_z, z, c) : 0.f;
             const float Dr = D * rz;
             stf(static_cast<T*>(p.dr) + o + c, p.a * D);
-            stf(static_cast<T*>(p.dz) + o + c, fmaf(-c2, fz, q[j] * Dr));
+            stf(static_cast<T*>(p.dz) + o + c, post ? fmaf(-c2, fz, q[j] * Dr) : q[j] * Dr);
             S[j] = fmaf(Dr, fz, S[j]);
         }
         prev = s;
