@@ -1,8 +1,9 @@
-"""Block norms at the ends of the range: infinities in z where the formulas do not let them reach a gradient, on every kernel
-(staged rows, odd widths, the generic kernel), against the definition in 64 bits."""
+"""Block norms at the ends of the range: infinities in z where the formulas do not let them reach a gradient, and rows far from 1
+in size, on every kernel (staged rows, odd widths, the generic kernel), against the definition in 64 bits."""
 import pytest
 import torch
 
+import test_gpu_block_norm
 from test_gpu_block_norm import L, _backward, _bwd64, _make   # noqa: F401
 from train_util import check
 
@@ -38,3 +39,21 @@ def test_dz_without_post_norm_does_not_depend_on_z(L, rows, cols, gates, dtype, 
         at = (k * 2 + 1) % rows // rows_of
         col = torch.isfinite(got["dgate"][:, c].double())
         assert not bool(col[at]) and int(col.sum()) == gates - 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(40, 4096), (300, 256), (40, 1001), (12, 37), (6, 20000)])
+@pytest.mark.parametrize("h_size,z_size", [(1e15, 1.0), (1e17, 1.0), (1e-15, 1.0), (1.0, 1e15), (1.0, 1e17), (1.0, 1e-15)])
+def test_rows_far_from_one(L, monkeypatch, rows, cols, dtype, h_size, z_size):  # noqa: F811
+    """The scale of a row of size s is 1 / s, and its third power leaves fp32's range long before the gradients do."""
+    monkeypatch.setattr(test_gpu_block_norm, "EPS", 0.0)
+    d = _make(rows, cols, dtype, True, 1, True, seed=12)
+    d["dh"] = None
+    d["z"] = (d["z"].double() * z_size).to(d["z"].dtype)
+    h = (d["r"].double() * h_size).to(d["r"].dtype)
+    rz, rh = (x.double().square().mean(1).rsqrt().float() for x in (d["z"], h))
+    ref, mag = _bwd64(d, h, 1.0, 0.7, rows, 1)
+    got = _backward(L, d, h, rz, rh, 1.0, 0.7, rows, 1)
+    for k, v in got.items():
+        chain = cols / 32 + 60
+        check(v, ref[k], mag[k], chain if k in ("dr", "dz") else chain + rows + 64, k)

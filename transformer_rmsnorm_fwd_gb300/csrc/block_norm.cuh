@@ -31,6 +31,10 @@ __device__ __forceinline__ float inv_sqrt(float x) {
     return isfinite(n) ? n : r;   // x = 0, infinity or NaN: what rsqrt says
 }
 
+// r^3 s for a row's scale r and a sum s over the row: s is of the size of 1 / r, so it is taken up factor by factor
+// (r^3 alone leaves the range of fp32 for rows below 1e-12 or above 1e12 in size)
+__device__ __forceinline__ float cube_times(float r, float s) { return r * (r * (r * s)); }
+
 // ------------------------------------------- rows that are no whole 16-byte vectors
 // Rings for rows whose width is no multiple of a vector: rows then start anywhere, so a slot
 // takes the 16-byte aligned window around a row (the bytes of its neighbours in it are not looked at),

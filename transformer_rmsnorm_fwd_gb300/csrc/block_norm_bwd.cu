@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(256) block_norm_bwd_generic(BwdP p) {
             float s1 = 0.f;
             for (int j = threadIdx.x; j < p.cols; j += blockDim.x)
                 s1 = fmaf(ldf(dy + o + j) * ldf(wn + j), ldf(h + o + j), s1);
-            c1 = rh * rh * rh * inv * block_sum(s1, sh);
+            c1 = cube_times(rh, inv * block_sum(s1, sh));
         }
         auto dval = [&](int j) {
             float d = dh != nullptr ? ldf(dh + o + j) : 0.f;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(256) block_norm_bwd_generic(BwdP p) {
             float s2 = 0.f;
             for (int j = threadIdx.x; j < p.cols; j += blockDim.x)
                 s2 = fmaf(qval(j) * dval(j), ldf(z + o + j), s2);
-            c2 = rz * rz * rz * inv * block_sum(s2, sh);
+            c2 = cube_times(rz, inv * block_sum(s2, sh));
         }
         const bool last_of_gate = p.splits == 0 && (t + 1) % p.per_gate == 0;
         const bool first_of_gate = p.splits == 0 && t % p.per_gate == 0;
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_ring(BwdP p, int tw, int
             s = 0;
             ph ^= 1u;
         }
-        const float c1 = rh * rh * rh * inv * sums[0];
-        const float c2 = post ? rz * rz * rz * inv * (sums[1] - c1 * sums[2]) : 0.f;
+        const float c1 = cube_times(rh, inv * sums[0]);
+        const float c2 = post ? cube_times(rz, inv * (sums[1] - c1 * sums[2])) : 0.f;
         const float2 nc1 = make_float2(-c1, -c1), nc2 = make_float2(-c2, -c2), ra = make_float2(p.a, p.a);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -584,8 +584,8 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_odd(BwdP p, int nst, uin
             for (int w = 0; w < NT / 32; ++w) a[k] += red[turn][k][w];
         }
         turn ^= 1;
-        const float c1 = rh * rh * rh * inv * a[0];
-        const float c2 = post ? rz * rz * rz * inv * (a[1] - c1 * a[2]) : 0.f;
+        const float c1 = cube_times(rh, inv * a[0]);
+        const float c2 = post ? cube_times(rz, inv * (a[1] - c1 * a[2])) : 0.f;
 #pragma unroll
         for (int j = 0; j < EPT; ++j) {
             const int c = j * NT + tid;
