@@ -629,7 +629,8 @@ __global__ void __launch_bounds__(256) policy_scan(const int64_t* __restrict__ l
 
 // The row pass of the bf16 path: lse from the (m, s) partials, the token's terms and scale, and P
 // rewritten in place into the softmax part of D, c_t P exp(m_tile - lse).  P null: lse and logp only.
-// idx: original token of a row (null: t0 + row).
+// idx: original token of a row (null: t0 + row).  run_err: the error word of the GEMMs of this run (with compacted
+// tokens a header of its own, which the entry point's takes over at the end).
 // HBM-bound, P read and written once.  blockIdx.y takes a run of `piece` 16-byte vectors of the row, each
 // repeating the lse from the row's few KB of partials, four vectors a thread in flight: 2741 rows of
 // 128256 218 us in runs of 8192, 0.95 of the copy rate (4096: 222, 2048: 253, 237 a whole row at a time with one
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* _
                                                                 const float* __restrict__ zlab, __nv_bfloat16* P,
                                                                 int64_t ldp, int V, const Policy pol,
                                                                 const int64_t* __restrict__ idx, int64_t t0,
-                                                                float* __restrict__ coef, int piece) {
+                                                                float* __restrict__ coef, int piece, const int* run_err) {
     extern __shared__ float fac[];   // [nvt]
     __shared__ float red[32];
     const int64_t row = blockIdx.x;
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* _
     s = block_reduce<kRowThreads>(s, false, red);
     const float l = m + logf(s);
     float lp = zlab[row] - l;
-    if (pol.hdr->err != 0) lp = __int_as_float(0x7FC00000);   // a GEMM gave up on a bounded wait
+    if (*run_err != 0) lp = __int_as_float(0x7FC00000);   // the GEMM that made the partials gave up on a bounded wait
     const int64_t t = idx != nullptr ? idx[row] : t0 + row;
     if (pol.logp != nullptr && write) pol.logp[t] = lp;
     if (P == nullptr) return;
@@ -1140,7 +1141,7 @@ int run_tc(const Args& a, const Layout& L, float scale) {
             const dim3 grid(cl, static_cast<unsigned>(ceil_div(ceil_div(V, 8), piece)));
             rc = launch_early("linear_policy rows", policy_rows_bf16, grid, kRowThreads, fac_smem, a.st, a.labels + t0, a.ignore,
                               part, static_cast<int>(L.nvt), zlab + t0, P, L.ldp, V, *a.pol,
-                              a.idx != nullptr ? a.idx + t0 : nullptr, t0, a.pol->coef + t0, piece);
+                              a.idx != nullptr ? a.idx + t0 : nullptr, t0, a.pol->coef + t0, piece, &hdr->err);
         } else {
             dlogits_bf16<<<cl, kRowThreads, fac_smem, a.st>>>(a.labels + t0, a.ignore, part, static_cast<int>(L.nvt),
                                                               zlab + t0, P, L.ldp, V, scale, a.scale_dev, lse + t0,
@@ -1984,7 +1985,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
     Policy pol{};
     pol.logp = logp;
     pol.zero_logp = check != nullptr ? 1 : 0;
-    pol.hdr = reinterpret_cast<Hdr*>(w8 + L.hdr);
+    int* err = &reinterpret_cast<Hdr*>(w8 + L.hdr)->err;
     float2* part = reinterpret_cast<float2*>(w8 + L.part);
     float* zlab = reinterpret_cast<float*>(w8 + L.zlab);
     if (n <= kFewTokens && kFewTokens * static_cast<size_t>(H) * 2 <= kFewSmem) {
@@ -1996,7 +1997,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
                        : launch_logp_few<4, 2>(X, W, labs, nn, H, V, part, zlab, most, np, st);
         if (rc || (check != nullptr && (rc = (*check)()))) return rc;
         return launch_early("linear_logp rows", policy_rows_bf16, dim3(nn), kRowThreads, 0, st, labs, ignore, part, np, zlab,
-                            nullptr, 0, V, pol, idx, 0, nullptr, 0);
+                            nullptr, 0, V, pol, idx, 0, nullptr, 0, err);
     }
     int64_t x_rows = 0;
     if (n < kPadRows) {
@@ -2008,7 +2009,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
     for (int64_t t0 = 0; t0 < n; t0 += L.C) {
         const int cl = static_cast<int>(std::min(L.C, n - t0));
         EpiParams e{};
-        e.err = &reinterpret_cast<Hdr*>(w8 + L.hdr)->err;
+        e.err = err;
         e.early = 1;
         e.ignore_index = ignore;
         e.labels = labs + t0;
@@ -2025,7 +2026,7 @@ int run_logp_tc(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* l
         if (check != nullptr && t0 == 0 && (rc = (*check)())) return rc;
         if ((rc = launch_early("linear_logp rows", policy_rows_bf16, dim3(cl), kRowThreads, 0, st, labs + t0, ignore, part,
                                static_cast<int>(L.nvt), zlab + t0, nullptr, 0, V, pol, idx != nullptr ? idx + t0 : nullptr, t0,
-                               nullptr, 0)))
+                               nullptr, 0, err)))
             return rc;
     }
     return LIGER_OK;
