@@ -826,7 +826,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 // Pass 2: P = exp(z - m) (bf16 row runs for labelled rows) and its sum,
                 // kept as 8 partial sums so the adds do not form one serial chain.
-                const float ml = m * 1.4426950408889634f;
+                // (a tile of -inf, or of logits below -2.3e38: ml stays finite and the exponentials are 0,
+                // where -inf + inf would be NaN)
+                const float ml = fmaxf(m * 1.4426950408889634f, -3.402823466e38f);
                 float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                 const uint32_t prows = __ballot_sync(0xffffffffu, live);
                 uint8_t* pblk = ep.p_out != nullptr
