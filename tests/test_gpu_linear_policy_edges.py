@@ -106,3 +106,16 @@ def test_cross_entropy_with_a_tile_without_a_finite_logit(L):  # noqa: F811
         xw = float((i["X"].abs().double() @ i["W"][:512].abs().double().T).max())
         assert abs(float(loss) + float(lp.mean())) <= (2 * 64 + 64) * 2.0 ** -23 * xw
         assert bool((dW[512] == 0).all()) and bool(torch.isfinite(dX).all())
+
+
+def test_a_vocabulary_of_millions(L):  # noqa: F811
+    """A row's tiles number more than shared memory would hold factors for; every piece of the row keeps its own only."""
+    T, H, V = 2, 64, 3_200_003
+    i = _inputs(T, H, V, "bf16", [0, T], seed=6, masked=0.0)
+    r = _ref(i, "token_mean", 0.2, 0.2, 0.1, 1.0)
+    o = _call(L, i, "bf16", "token_mean", 0.2, 0.2, 0.1, 1.0)
+    assert bool(((o["logp"].double() - r["logp"]).abs() <= r["eps"]).all())
+    assert abs(float(o["loss"]) - r["loss"]) <= r["loss_off"] + 2 ** -22 * abs(r["loss"])
+    for k in ("dX", "dW"):      # sums over V / 16 steps of the tensor cores in 76 runs
+        bound = 2.0 ** -8 * r[k].abs() + (2 * 2.0 ** -8 + 3 * r["e"] + 2.0 ** -10) * r["m" + k[1]]
+        assert bool(((o[k].double() - r[k]).abs() <= bound).all()), k

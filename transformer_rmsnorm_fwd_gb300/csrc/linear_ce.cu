@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* _
                                                                 int64_t ldp, int V, const Policy pol,
                                                                 const int64_t* __restrict__ idx, int64_t t0,
                                                                 float* __restrict__ coef, int piece, const int* run_err) {
-    extern __shared__ float fac[];   // [nvt]
+    extern __shared__ float fac[];   // a factor for each vocabulary tile of the piece
     __shared__ float red[32];
     const int64_t row = blockIdx.x;
     __nv_bfloat16* prow = P + row * ldp;
@@ -1139,7 +1139,8 @@ int run_tc(const Args& a, const Layout& L, float scale) {
         const int piece = cl * ceil_div(V, 8 * 8192) >= 8 * sm_count() ? 8192 : 2048;
         if (a.pol != nullptr) {
             const dim3 grid(cl, static_cast<unsigned>(ceil_div(ceil_div(V, 8), piece)));
-            rc = launch_early("linear_policy rows", policy_rows_bf16, grid, kRowThreads, fac_smem, a.st, a.labels + t0, a.ignore,
+            const size_t piece_smem = sizeof(float) * static_cast<size_t>(piece * 8 / kVT + 1);
+            rc = launch_early("linear_policy rows", policy_rows_bf16, grid, kRowThreads, piece_smem, a.st, a.labels + t0, a.ignore,
                               part, static_cast<int>(L.nvt), zlab + t0, P, L.ldp, V, *a.pol,
                               a.idx != nullptr ? a.idx + t0 : nullptr, t0, a.pol->coef + t0, piece, &hdr->err);
         } else {
