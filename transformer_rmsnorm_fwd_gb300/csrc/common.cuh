@@ -114,8 +114,8 @@ __device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat16
 __device__ __forceinline__ void stf(float* p, float v) { *p = v; }
 __device__ __forceinline__ void stf(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// 16-byte loads / stores.  ldg_nc: read-only path, only for buffers no
-// thread of the same kernel writes.
+// 16-byte loads / stores.  ldg16_nc: read-only path, only for buffers that nothing writes while the
+// kernel lives (not in kernels that wait_for_stream).
 __device__ __forceinline__ uint4 ldg16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 // 16-byte load asking L2 to fetch the whole 256-byte block around it from DRAM
 // (for a thread whose next load falls in the same 256 bytes)
@@ -166,7 +166,10 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // A kernel launched with launch_early may be set up while the kernel before it on the stream still
 // runs; it calls wait_for_stream before it touches memory, which returns when that kernel is
-// done and its writes can be read.  Saves part of the gap between two kernels: SwiGLU with checkpoints,
+// done and its writes can be read.  Such a kernel reads by ordinary loads: no ldg16_nc, and no
+// `const T* __restrict__` among its parameters, which allows the compiler the same read-only loads
+// and to move them ahead of the wait, since it may take the data to be unchanged while the kernel
+// lives.  Here it is not: the kernel before may still be writing it.  Saves part of the gap between two kernels: SwiGLU with checkpoints,
 // forward and backward, fp32 515 x 2739 19.7 us, 16 to 20 early; bf16 8192 x 11008 217 us, 212 early; the
 // policy loss, fp32, of 256 tokens at 256 x 1024, nine kernels, 72 us, 58 early.
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

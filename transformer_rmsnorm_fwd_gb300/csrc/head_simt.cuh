@@ -40,7 +40,7 @@ __device__ __forceinline__ void head_store(const HeadGemm& g, TO* out, int m, in
 }
 
 template <typename TA, typename TB, typename TO>
-__global__ void __launch_bounds__(256) head_gemm(const TA* __restrict__ A, const TB* __restrict__ B, TO* out, HeadGemm g) {
+__global__ void __launch_bounds__(256) head_gemm(const TA* A, const TB* B, TO* out, HeadGemm g) {
     __shared__ __align__(16) float As[2][kHK][kHT + 4], Bs[2][kHK][kHT + 4];
     const int m0 = blockIdx.y * kHT, n0 = blockIdx.x * kHT;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;

@@ -221,13 +221,13 @@ __global__ void gather_rows(const uint4* __restrict__ src, const int64_t* __rest
 }
 
 // dst = the rows of src, those of ignored tokens as zeros
-__global__ void masked_rows(const uint4* __restrict__ src, const int64_t* __restrict__ labels, int64_t ignore, int64_t T,
-                            int64_t hv, uint4* __restrict__ dst) {
+__global__ void masked_rows(const uint4* src, const int64_t* labels, int64_t ignore, int64_t T, int64_t hv,
+                            uint4* __restrict__ dst) {
     wait_for_stream();
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         const bool keep = labels[t] != ignore;
         for (int64_t v = threadIdx.x; v < hv; v += blockDim.x)
-            dst[t * hv + v] = keep ? ldg16_nc(src + t * hv + v) : make_uint4(0, 0, 0, 0);
+            dst[t * hv + v] = keep ? ldg16(src + t * hv + v) : make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -322,7 +322,7 @@ __device__ __forceinline__ float block_reduce(float v, bool is_max, float* sh) {
 // of 32 keys, one per lane, its warps counting over an eighth of the segment each,
 // four labels a load from shared memory (2741 keys: 6.6 us, 52 sorted by one block).
 constexpr int kRankThreads = 256;
-__global__ void __launch_bounds__(kRankThreads) sort_label_keys(const int64_t* __restrict__ labels, int64_t n, int seg,
+__global__ void __launch_bounds__(kRankThreads) sort_label_keys(const int64_t* labels, int64_t n, int seg,
                                                                 int64_t ignore, int absolute,
                                                                 unsigned long long* __restrict__ out) {
     __shared__ __align__(16) uint32_t lab[kMaxSortKeys];
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kRankThreads) sort_label_keys(const int64_t* _
 // of label v among segment s's sorted keys, v in [0, V], plus s*seg when the
 // indices are absolute -- so the tokens of segment s labelled v are
 // keys[lstart[v] .. lstart[v+1]) of the array the table's indices refer to.
-__global__ void label_starts(const unsigned long long* __restrict__ keys, int64_t n, int seg, int V, int absolute,
+__global__ void label_starts(const unsigned long long* keys, int64_t n, int seg, int V, int absolute,
                              int* __restrict__ lstart) {
     const int64_t b0 = static_cast<int64_t>(blockIdx.y) * seg;
     const int cnt = static_cast<int>(n - b0 < seg ? n - b0 : seg);
@@ -635,11 +635,9 @@ __global__ void __launch_bounds__(256) policy_scan(const int64_t* __restrict__ l
 // repeating the lse from the row's few KB of partials, four vectors a thread in flight: 2741 rows of
 // 128256 218 us in runs of 8192, 0.95 of the copy rate (4096: 222, 2048: 253, 237 a whole row at a time with one
 // vector in flight); 8 rows 6 us in runs of 2048 (8192: 10).
-__global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* __restrict__ labels, int64_t ignore,
-                                                                const float2* __restrict__ part, int nvt,
-                                                                const float* __restrict__ zlab, __nv_bfloat16* P,
-                                                                int64_t ldp, int V, const Policy pol,
-                                                                const int64_t* __restrict__ idx, int64_t t0,
+__global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* labels, int64_t ignore, const float2* part,
+                                                                int nvt, const float* zlab, __nv_bfloat16* P, int64_t ldp,
+                                                                int V, const Policy pol, const int64_t* idx, int64_t t0,
                                                                 float* __restrict__ coef, int piece, const int* run_err) {
     extern __shared__ float fac[];   // a factor for each vocabulary tile of the piece
     __shared__ float red[32];
@@ -699,9 +697,9 @@ __global__ void __launch_bounds__(kRowThreads) policy_rows_bf16(const int64_t* _
 }
 
 // fp32 path: z row -> lse, the token's terms and scale, D in place (log-probability only: z is left)
-__global__ void __launch_bounds__(kRowThreads) policy_rows_f32(const int64_t* __restrict__ labels, int64_t ignore,
-                                                               float* Z, int64_t ldz, int V, int with_d, const Policy pol,
-                                                               const int64_t* __restrict__ idx, int64_t t0) {
+__global__ void __launch_bounds__(kRowThreads) policy_rows_f32(const int64_t* labels, int64_t ignore, float* Z, int64_t ldz,
+                                                               int V, int with_d, const Policy pol, const int64_t* idx,
+                                                               int64_t t0) {
     __shared__ float red[32];
     const int64_t row = blockIdx.x;
     wait_for_stream();
@@ -739,9 +737,8 @@ __device__ __forceinline__ void add_with_error(float v, float& sum, float& err) 
     sum = t;
 }
 constexpr int kFinalThreads = 1024;   // 256 are launched for few tokens
-__global__ void __launch_bounds__(kFinalThreads) policy_final(const float* __restrict__ term, const float* __restrict__ kl,
-                                                              const float* __restrict__ clip, int64_t T, const Hdr* hdr,
-                                                              float* loss, float* stats) {
+__global__ void __launch_bounds__(kFinalThreads) policy_final(const float* term, const float* kl, const float* clip, int64_t T,
+                                                              const Hdr* hdr, float* loss, float* stats) {
     __shared__ double red[3][32];
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float s[3] = {0.f, 0.f, 0.f}, e[3] = {0.f, 0.f, 0.f};
@@ -1760,9 +1757,9 @@ LogpLayout logp_layout(int64_t T, int64_t H, int64_t V, int dtype) {
 // writes one (m, s) per token, as the GEMM's epilogue does per tile, and the logit at the label.
 // HBM-bound up to 4 tokens (167 us); 8 are bound by the multiply-adds (322 us).
 template <int NT, int R>
-__global__ void __launch_bounds__(256) logp_few(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W,
-                                                const int64_t* __restrict__ labels, int n, int H, int V,
-                                                float2* __restrict__ part, int nparts, float* __restrict__ zlab) {
+__global__ void __launch_bounds__(256) logp_few(const __nv_bfloat16* X, const __nv_bfloat16* W, const int64_t* labels, int n,
+                                                int H, int V, float2* __restrict__ part, int nparts,
+                                                float* __restrict__ zlab) {
     extern __shared__ uint4 xs[];   // [NT][H / 8]
     __shared__ float2 ms[8][NT];
     const int nv = H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

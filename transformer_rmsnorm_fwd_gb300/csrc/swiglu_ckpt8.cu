@@ -208,10 +208,8 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg
 }
 
 template <typename T, bool FLAT>
-__global__ void __launch_bounds__(kThreads) swiglu_bwd_ckpt8_vec(const T* dy, const int8_t* __restrict__ gate8,
-                                                                 const uint8_t* __restrict__ gs,
-                                                                 const int8_t* __restrict__ up8,
-                                                                 const uint8_t* __restrict__ us, T* dgate, T* dup,
+__global__ void __launch_bounds__(kThreads) swiglu_bwd_ckpt8_vec(const T* dy, const int8_t* gate8, const uint8_t* gs,
+                                                                 const int8_t* up8, const uint8_t* us, T* dgate, T* dup,
                                                                  int64_t n, int cols, int groups) {
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
     wait_for_stream();
@@ -298,10 +296,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_fwd_ckpt8_any(const T* gate, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) swiglu_bwd_ckpt8_any(const T* dy, const int8_t* __restrict__ gate8,
-                                                                 const uint8_t* __restrict__ gs,
-                                                                 const int8_t* __restrict__ up8,
-                                                                 const uint8_t* __restrict__ us, T* dgate, T* dup,
+__global__ void __launch_bounds__(kThreads) swiglu_bwd_ckpt8_any(const T* dy, const int8_t* gate8, const uint8_t* gs,
+                                                                 const int8_t* up8, const uint8_t* us, T* dgate, T* dup,
                                                                  int64_t ngroups, int cols, int groups) {
     const int lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kGroupsAny;
