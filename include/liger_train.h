@@ -176,7 +176,8 @@ int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* lab
  *   not valid, and X may hold anything there.  0 <= eps_low <= 1, eps_high >= 0.
  *   loss: one float; stats: two floats or NULL, the mean kl and the share of
  *   clipped tokens over the valid tokens; logp: float [T] or NULL, 0 at tokens
- *   that are not valid; dX [T, H], dW [V, H] in dtype, each may be NULL.  Rows
+ *   that are not valid (it must not overlap old_logp, ref_logp or adv:
+ *   LIGER_ERR_SHAPE); dX [T, H], dW [V, H] in dtype, each may be NULL.  Rows
  *   of dX of tokens that are not valid are written as +0.
  *   Token chunks and the GEMM path by dtype and shape are as in
  *   liger_linear_ce_fwd_bwd, but chunk 0 is min(T, 8192) on the tensor-core

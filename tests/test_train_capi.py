@@ -145,3 +145,12 @@ def test_policy_checks(lib):
         need = lib.liger_linear_policy_workspace(4, 64, 300, 2, 0, 1)
         assert need > 0 and _policy(fn, n=need - 1) == -6 and _policy(fn, ws=None) == -6 and _policy(fn, ws=ODD) == -6
     assert lib.liger_linear_policy_workspace(4, 64, 300, 0, 0, 1) == 0
+
+
+def test_policy_logp_is_no_input(lib):
+    """logp over old_logp, ref_logp or adv would be read back as the policy's own: refused."""
+    at = lambda n: ctypes.c_void_p(0x100000 + n)
+    for fn in (lib.liger_linear_policy_fwd_bwd, lib.liger_linear_policy_fwd_bwd_async):
+        for kw in (dict(old=at(0)), dict(ref=at(0)), dict(adv=at(0)), dict(old=at(12)), dict(ref=at(-12)), dict(adv=at(-4)),
+                   dict(adv=at(-12), flags=1)):
+            assert _policy(fn, logp=at(0), **kw) == -2, kw

@@ -280,7 +280,8 @@ def liger_linear_policy_fwd_bwd(X, W, labels, old_logp, adv, loss, dX, dW, ws, r
 
     labels int64 [T]; old_logp, ref_logp float32 [T]; adv float32, one per sequence ([B]) or, with adv_per_token, one per
     token ([T]); cu_seqlens int32 [B + 1] or None (one sequence); reduction "token_mean", "seq_mean" or "sum"; stats
-    float32 [2] or None (mean KL, share of clipped tokens).  wait=False calls the _async form."""
+    float32 [2] or None (mean KL, share of clipped tokens); logp float32 [T] or None, no tensor of the inputs.  wait=False calls
+    the _async form."""
     lib = _loaded or _lib()
     dev, f32 = torch.cuda.current_device(), torch.float32
     T, H, V = _head(dev, X, W, labels)

@@ -2158,6 +2158,14 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
     if (!ws || ws_bytes < PL.total || (reinterpret_cast<uintptr_t>(ws) & 255))
         return fail(LIGER_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, PL.total,
                     ws_bytes);
+    // logp is written while other blocks still read the old and the reference policy's
+    const auto overlaps = [&](const float* p, int64_t n) {
+        const auto a = reinterpret_cast<uintptr_t>(logp), b = reinterpret_cast<uintptr_t>(p);
+        return a < b + static_cast<size_t>(n) * sizeof(float) && b < a + static_cast<size_t>(T) * sizeof(float);
+    };
+    if (logp && T > 0 && (overlaps(old_logp, T) || (ref_logp && overlaps(ref_logp, T)) ||
+                          overlaps(adv, flags & LIGER_POLICY_ADV_PER_TOKEN ? T : B)))
+        return fail(LIGER_ERR_SHAPE, "%s: logp overlaps old_logp, ref_logp or adv", who);
     cudaStream_t st = as_stream(stream);
     uint8_t* w8 = static_cast<uint8_t*>(ws);
     Hdr* hdr = reinterpret_cast<Hdr*>(w8 + PL.L.hdr);
