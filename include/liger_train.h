@@ -122,7 +122,9 @@ int liger_swiglu_bwd_ckpt8(const void* dy, const int8_t* gate8, const uint8_t* g
  * Arguments, shapes (bf16; H >= 64, H and I multiples of 8), workspace
  * (liger_fused_linear_swiglu_workspace) and errors otherwise as
  * liger_fused_linear_swiglu_fwd_save / _bwd_saved; codes 16-byte aligned.  dWg
- * or dX is written twice: sums of the other gradients may stand in it first. */
+ * or dX is written twice: sums of the other gradients may stand in it first.
+ * As there, the backward's dG and dU are rounded to bf16 once, as operands of
+ * the three products, whose sums are fp32. */
 int liger_fused_linear_swiglu_fwd_ckpt8(const void* X, const void* Wg, const void* Wu, void* out, int8_t* gate8,
                                         uint8_t* gate_scale, int8_t* up8, uint8_t* up_scale, int64_t T, int64_t H,
                                         int64_t I, int dtype, void* stream);
@@ -181,7 +183,8 @@ int liger_linear_logp_fwd_async(const void* X, const void* W, const int64_t* lab
  *   of dX of tokens that are not valid are written as +0.
  *   Token chunks and the GEMM path by dtype and shape are as in
  *   liger_linear_ce_fwd_bwd, but chunk 0 is min(T, 8192) on the tensor-core
- *   path: per chunk the logits exist only in a [chunk x V] workspace buffer.
+ *   path: per chunk the logits exist only in a [chunk x V] workspace buffer
+ *   (up to 8192 tokens that is all of them, and dW needs no fp32 [V x H] sum).
  *   ws: at least liger_linear_policy_workspace bytes, 256-byte aligned.
  *   The call waits for a scan of the labels and sequences: a bad label returns
  *   LIGER_ERR_LABEL, bad cu_seqlens LIGER_ERR_SHAPE, with no output written,

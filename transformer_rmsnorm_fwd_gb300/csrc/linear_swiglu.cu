@@ -394,7 +394,8 @@ int bwd_kept(const char* who, const void* X, const void* Wg, const void* Wu, con
     if (int rc0 = lsw_err_word(&d_err)) return rc0;
     __nv_bfloat16* dG = static_cast<__nv_bfloat16*>(ws);
     __nv_bfloat16* dU = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + need / 2);
-    // 1. dG, dU from dh and the saved g, u (the elementwise SwiGLU backward)
+    // 1. dG, dU from dh and the saved g, u (the elementwise SwiGLU backward), rounded to bf16: the
+    // tensor cores take no wider operands at this rate (gradients 2.4e-3 off in norm; fp32 products 1.7e-3)
     if (int rc = dgdu(dG, dU)) return rc;
     // 2-3. as in the backward with recompute
     return grads_from_dgdu(X, Wg, Wu, dG, dU, dX, dWg, dWu, T, H, I, d_err, st, split);
