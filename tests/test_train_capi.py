@@ -154,3 +154,15 @@ def test_policy_logp_is_no_input(lib):
         for kw in (dict(old=at(0)), dict(ref=at(0)), dict(adv=at(0)), dict(old=at(12)), dict(ref=at(-12)), dict(adv=at(-4)),
                    dict(adv=at(-12), flags=1)):
             assert _policy(fn, logp=at(0), **kw) == -2, kw
+
+
+def test_nothing_is_allocated_or_thrown():
+    """The library allocates nothing, and no exception can leave a C entry: no owning std types, new or throw in its sources."""
+    import glob
+    import re
+    src = os.path.join(_native.PKG, "csrc")
+    for f in glob.glob(os.path.join(src, "*.cu")) + glob.glob(os.path.join(src, "*.cuh")):
+        with open(f) as h:
+            text = re.sub(r"//[^\n]*", "", h.read())
+        found = re.findall(r"std::(?:function|vector|string|map|unordered_map|deque|unique_ptr|shared_ptr)\b|\bnew\s+\w|\bthrow\b", text)
+        assert not found, (os.path.basename(f), found)

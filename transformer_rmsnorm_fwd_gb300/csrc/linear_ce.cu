@@ -32,7 +32,6 @@
 #include <math.h>
 
 #include <atomic>
-#include <functional>
 
 #include "head_simt.cuh"
 #include "liger_train.h"
@@ -882,7 +881,16 @@ int simt(int M, int N, int K, const TA* A, int64_t sam, int64_t sak, const TB* B
 
 // ----------------------------------------------------------- orchestration
 // Waits for the label scan and says whether the call goes on (LIGER_OK), ends without work (kNothing) or fails.
-using Check = std::function<int()>;
+// A reference to the caller's lambda: nothing is allocated, and nothing can throw across the C entry.
+struct Check {
+    int (*call)(void*);
+    void* self;
+    int operator()() const { return call(self); }
+};
+template <typename F>
+Check check_of(F& f) {
+    return Check{[](void* p) { return (*static_cast<F*>(p))(); }, &f};
+}
 constexpr int kNothing = 1;
 
 struct Args {
@@ -2084,7 +2092,7 @@ int logp_impl(const char* who, const void* X, const void* W, const int64_t* labe
     int64_t n = T;
     HdrRead scan;
     const Check* before_rows = nullptr;
-    const Check check = [&]() -> int {
+    auto settle = [&]() -> int {
         Hdr h{};
         if (int rc = scan.wait("linear_logp scan", &h)) return rc;
         if (h.bad) return fail(LIGER_ERR_LABEL, "%s: a label is outside [0, %lld) and is not %lld", who, (long long)V,
@@ -2095,6 +2103,7 @@ int logp_impl(const char* who, const void* X, const void* W, const int64_t* labe
             return check_launch("linear_logp memset");
         return n == 0 ? kNothing : LIGER_OK;
     };
+    const Check check = check_of(settle);
     if (sync) {
         if (int rc = scan.post("linear_logp scan", hdr, st)) return rc;
         if (never_compacted(L.tc, T)) before_rows = &check;
@@ -2186,7 +2195,7 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
     }
     HdrRead scan;
     const Check* before_rows = nullptr;
-    const Check check = [&]() -> int {
+    auto settle = [&]() -> int {
         Hdr h{};
         if (int rc = scan.wait("linear_policy scan", &h)) return rc;
         if (h.bad & 2) return fail(LIGER_ERR_SHAPE, "%s: cu_seqlens descends or leaves [0, %lld]", who, (long long)T);
@@ -2198,6 +2207,7 @@ int policy_impl(const char* who, const void* X, const void* W, const int64_t* la
             return check_launch("linear_policy memset");
         return n == 0 ? kNothing : LIGER_OK;
     };
+    const Check check = check_of(settle);
     int rc = T == 0 ? kNothing : LIGER_OK;
     if (sync && T > 0) {
         if ((rc = scan.post("linear_policy scan", hdr, st))) return rc;
