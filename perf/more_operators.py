@@ -156,7 +156,10 @@ def prepare(case, seed):
         s["bias"] = randn(N, std=0.3) if case["bias"] else None
         s["residual"] = randn(T, N, std=1.5) if case["residual"] else None
         s["Y"] = torch.empty(T, N, dtype=dt, device="cuda")
-        s["pre"] = torch.empty_like(s["Y"]) if case["grads"] and case["act"] != "none" else None
+        # what the forward keeps for the activation's gradient: the sums before it, 16 bits an element (fp32: 32)
+        s["pre"] = None
+        if case["grads"] and case["act"] != "none":
+            s["pre"] = torch.empty(T, N, dtype=torch.float16 if case["dtype"] == BF16 else dt, device="cuda")
         if case["grads"]:
             s["dY"] = randn(T, N)
             s["dX"], s["dW"] = torch.empty_like(s["X"]), torch.empty_like(s["W"])
