@@ -189,7 +189,7 @@ def prepare(case, seed):
             noise = torch.rand(part.shape, device="cuda", generator=gen).clamp_(1e-20, 1 - 1e-7)
             s["tokens"][t:t + 1024] = (part.float() / case["temperature"] - noise.log_().neg_().log_()).argmax(1)
         s["logits"] = z
-        s["logp"], s["lse"] = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        s["logp"], s["row_max"], s["log_sum"] = (torch.empty(T, device="cuda") for _ in range(3))
         s["entropy"] = torch.empty(T, device="cuda") if case["entropy"] else None
         k = min(case["top"], V)
         s["top_logp"] = torch.empty(T, k, device="cuda") if k else None
@@ -255,12 +255,14 @@ def _own_rope(s):
 def _own_score(s):
     import transformer_rmsnorm_fwd_gb300 as L
     c = s["case"]
-    L.liger_token_logp_fwd(s["logits"], s["tokens"], s["logp"], lse=s["lse"], entropy=s["entropy"], top_logp=s["top_logp"],
-                           top_ids=s["top_ids"], temperature=c["temperature"], ignore_index=IGNORE)
-    out = {k: s[k] for k in ("logp", "lse", "entropy", "top_logp", "top_ids")}
+    L.liger_token_logp_fwd(s["logits"], s["tokens"], s["logp"], row_max=s["row_max"], log_sum=s["log_sum"],
+                           entropy=s["entropy"], top_logp=s["top_logp"], top_ids=s["top_ids"],
+                           temperature=c["temperature"], ignore_index=IGNORE)
+    out = {k: s[k] for k in ("logp", "row_max", "log_sum", "entropy", "top_logp", "top_ids")}
     if c["grads"]:
-        L.liger_token_logp_bwd(s["logits"], s["tokens"], s["lse"], s["g_logp"], s["dlogits"], entropy=s["entropy"],
-                               g_entropy=s["g_entropy"], temperature=c["temperature"], ignore_index=IGNORE)
+        L.liger_token_logp_bwd(s["logits"], s["tokens"], s["row_max"], s["log_sum"], s["g_logp"], s["dlogits"],
+                               entropy=s["entropy"], g_entropy=s["g_entropy"], temperature=c["temperature"],
+                               ignore_index=IGNORE)
         out["dlogits"] = s["dlogits"]
     return out
 
@@ -370,7 +372,7 @@ def _plain_score(s):
     c, tokens = s["case"], s["tokens"]
     T, V = c["tokens"], c["vocab"]
     k = min(c["top"], V)
-    logp, lse, ent = (torch.empty(T, device="cuda") for _ in range(3))
+    logp, top, log_sum, ent = (torch.empty(T, device="cuda") for _ in range(4))
     top_logp = torch.empty(T, k, device="cuda")
     top_ids = torch.empty(T, k, dtype=torch.int64, device="cuda")
     dz = torch.empty_like(s["logits"]) if c["grads"] else None
@@ -381,12 +383,13 @@ def _plain_score(s):
             best, ids = torch.sort(z, dim=1, descending=True, stable=True)
             best, top_ids[at] = best[:, :k] / c["temperature"], ids[:, :k]
             del ids
+        top[at] = z.amax(1)
         z = z / c["temperature"]
         m = z.amax(1, keepdim=True)
         e = torch.exp(z - m)
         total = e.sum(1, keepdim=True)
         p = e / total
-        lse[at] = (m + total.log())[:, 0]
+        log_sum[at] = total.log()[:, 0]
         lp = z - m - total.log()
         y = tokens[at]
         live = y != IGNORE
@@ -403,8 +406,8 @@ def _plain_score(s):
                 d = d - s["g_entropy"][at][:, None] * p * (lp + h)
             d.scatter_add_(1, y.clamp(min=0)[:, None], g)
             dz[at] = (d / c["temperature"]).to(dz.dtype)
-    out = {"logp": logp, "lse": lse, "entropy": ent if c["entropy"] else None, "top_logp": top_logp if k else None,
-           "top_ids": top_ids if k else None}
+    out = {"logp": logp, "row_max": top, "log_sum": log_sum, "entropy": ent if c["entropy"] else None,
+           "top_logp": top_logp if k else None, "top_ids": top_ids if k else None}
     if c["grads"]:
         out["dlogits"] = dz
     return out
@@ -439,9 +442,9 @@ def work(case):
         return {"bytes": passes * (2 * e * n * case["head"] + 4 * case["batch"] * case["seq"] * case["far"]),
                 "flops": passes * 3.0 * n * case["rotary"]}
     T, V, k = case["tokens"], case["vocab"], case["top"]
-    w = {"bytes": e * T * V + T * (16 + 4 * case["entropy"] + 12 * k), "flops": 6.0 * T * V}
+    w = {"bytes": e * T * V + T * (20 + 4 * case["entropy"] + 12 * k), "flops": 6.0 * T * V}
     if case["grads"]:
-        w["bytes"] += 2 * e * T * V + T * (16 + 8 * case["entropy"])
+        w["bytes"] += 2 * e * T * V + T * (20 + 8 * case["entropy"])
         w["flops"] += 8.0 * T * V
     return w
 
@@ -535,7 +538,7 @@ def _exact_rope(c, d):
 
 def _exact_score(c, d):
     T, k = c["tokens"], min(c["top"], c["vocab"])
-    parts = {"logp": [], "lse": [], "entropy": [], "top_logp": [], "top_ids": [], "dlogits": []}
+    parts = {"logp": [], "row_max": [], "log_sum": [], "entropy": [], "top_logp": [], "top_ids": [], "dlogits": []}
     for t in range(0, T, 256):
         at = slice(t, t + 256)
         z = d["logits"][at].double() / c["temperature"]
@@ -545,7 +548,8 @@ def _exact_score(c, d):
         y, rows = d["tokens"][at], torch.arange(z.shape[0], device=z.device)
         live = y >= 0
         parts["logp"].append(torch.where(live, z[rows, y.clamp(min=0)] - lse, 0.0))
-        parts["lse"].append(lse)
+        parts["row_max"].append(d["logits"][at].double().max(1).values)
+        parts["log_sum"].append(torch.logsumexp(z - z.max(1, keepdim=True).values, 1))
         parts["entropy"].append(ent)
         if k:
             ids = torch.argsort(z, dim=1, descending=True, stable=True)[:, :k]
