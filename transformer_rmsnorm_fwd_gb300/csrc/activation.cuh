@@ -1,0 +1,58 @@
+// Activations of the biased projections and their derivatives (liger_layer.h).
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "liger_layer.h"
+
+namespace liger {
+namespace {
+
+// Phi(p), the normal distribution function, as erfc(-p / sqrt 2) / 2: no cancellation for p < 0.
+__device__ __forceinline__ float normal_cdf(float p) { return 0.5f * erfcf(p * -0.70710678118654752f); }
+
+// 2 sqrt(2/pi) (p + 0.044715 p^3): gelu with tanh is p sigmoid of this, (1 + tanh a) / 2 = sigmoid(2 a)
+__device__ __forceinline__ float tanh_arg(float p) {
+    return p * fmaf(2.f * 0.79788456080286536f * 0.044715f, p * p, 2.f * 0.79788456080286536f);
+}
+// FAST: the hardware exponential and reciprocal (for results that are rounded to bf16 next)
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float x) {
+    return FAST ? __fdividef(1.0f, 1.0f + __expf(-x)) : 1.0f / (1.0f + expf(-x));
+}
+
+template <bool FAST>
+__device__ __forceinline__ float act_value(int act, float p) {
+    switch (act) {
+        case LIGER_ACT_RELU: return p > 0.f ? p : (p != p ? p : 0.f);
+        case LIGER_ACT_GELU: return p * normal_cdf(p);
+        case LIGER_ACT_GELU_TANH: return p * sigmoid<FAST>(tanh_arg(p));
+        case LIGER_ACT_SILU: return p * sigmoid<FAST>(p);
+        default: return p;
+    }
+}
+
+// d act / dp
+template <bool FAST>
+__device__ __forceinline__ float act_slope(int act, float p) {
+    switch (act) {
+        case LIGER_ACT_RELU: return p > 0.f ? 1.f : (p != p ? p : 0.f);
+        case LIGER_ACT_GELU: return fmaf(p * 0.39894228040143268f, expf(-0.5f * p * p), normal_cdf(p));
+        case LIGER_ACT_GELU_TANH: {
+            // s + p s (1 - s) d(arg)/dp; past 64 s is 0 or 1 (and p^2 may be infinite)
+            const float q = p > 64.f ? 64.f : p < -64.f ? -64.f : p;
+            const float s = sigmoid<FAST>(tanh_arg(q));
+            const float d = fmaf(6.f * 0.79788456080286536f * 0.044715f, q * q, 2.f * 0.79788456080286536f);
+            return fmaf(q * s * (1.f - s), d, s);
+        }
+        case LIGER_ACT_SILU: {
+            const float s = sigmoid<FAST>(p);
+            return s * fmaf(p, 1.f - s, 1.f);
+        }
+        default: return 1.f;
+    }
+}
+
+}  // namespace
+}  // namespace liger

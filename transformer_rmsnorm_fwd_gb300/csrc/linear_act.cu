@@ -1,0 +1,195 @@
+// The projection with bias, activation and residual sum in its epilogue, and its
+// backward (formulas in liger_layer.h).
+#include "activation.cuh"
+#include "linear_fma.cuh"
+
+namespace liger {
+namespace {
+
+constexpr int kSumRows = 64;    // fewest rows per partial row of db
+constexpr int kMaxSums = 256;   // most partial rows of db
+
+int64_t rows_per_sum(int64_t T) { return std::max<int64_t>(kSumRows, ceil_div(T, kMaxSums)); }
+
+// dP = dY act'(P) and the partial sums of db: a block takes 32 columns and a run of rows, 8 threads a column.
+// TP: type dP is kept in; dp NULL: not kept (dP is dY).
+template <typename T, typename TPRE, typename TP>
+__global__ void __launch_bounds__(256) linear_dp(const T* dy, const TPRE* pre, TP* dp, float* part, int64_t rows, int cols,
+                                                 int64_t run, int act) {
+    __shared__ float red[8][33];
+    wait_for_stream();
+    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * run, r1 = min(rows, r0 + run);
+    float s = 0.f;
+    if (col < cols)
+        for (int64_t r = r0 + sl; r < r1; r += 8) {
+            float d = ldf(dy + r * cols + col);
+            if (dp != nullptr) {
+                d *= act_slope<sizeof(T) == 2>(act, static_cast<float>(pre[r * cols + col]));
+                stf(dp + r * cols + col, d);
+            }
+            s += d;
+        }
+    red[sl][lane] = s;
+    __syncthreads();
+    if (part != nullptr && sl == 0 && col < cols) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += red[i][lane];
+        part[static_cast<int64_t>(blockIdx.y) * cols + col] = t;
+    }
+}
+
+// db: the partial rows added in ascending order
+template <typename T>
+__global__ void __launch_bounds__(256) linear_db(const float* part, T* db, int parts, int cols) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    wait_for_stream();
+    if (col >= cols) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) s += part[static_cast<int64_t>(i) * cols + col];
+    stf(db + col, s);
+}
+
+bool on_tensor_cores(int64_t H, int64_t N, int dtype) {
+    return dtype == LIGER_BF16 && H % 8 == 0 && N % 8 == 0 && H >= 64 && N >= 64;
+}
+
+int check_sizes(const char* who, int64_t T, int64_t H, int64_t N, int act, int dtype) {
+    if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
+    const int64_t most = int64_t{1} << 30, area = int64_t{1} << 40;
+    if (T < 0 || H <= 0 || N <= 0 || T > most || H > most || N > most || T * std::max(H, N) > area || H * N > area)
+        return fail(LIGER_ERR_SHAPE, "%s: T=%lld H=%lld N=%lld", who, (long long)T, (long long)H, (long long)N);
+    if (act < LIGER_ACT_NONE || act > LIGER_ACT_SILU) return fail(LIGER_ERR_SHAPE, "%s: act %d", who, act);
+    return LIGER_OK;
+}
+bool off16(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (!aligned16(p)) return true;
+    return false;
+}
+
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+// bytes of dP in the workspace, and all of it
+size_t dp_bytes(int64_t T, int64_t H, int64_t N, int act, int dtype) {
+    if (act == LIGER_ACT_NONE) return 0;
+    return round256(static_cast<size_t>(T) * static_cast<size_t>(N) * (on_tensor_cores(H, N, dtype) ? 2 : 4));
+}
+size_t sum_bytes(int64_t T, int64_t N) {
+    return round256(static_cast<size_t>(ceil_div(T, rows_per_sum(T))) * static_cast<size_t>(N) * 4);
+}
+
+template <typename T, typename TPRE>
+int fwd_fma(const void* X, const void* W, FmaEpi<T, TPRE> e, int64_t Tn, int64_t H, int64_t N, cudaStream_t st) {
+    FmaGemm g{static_cast<int>(Tn), static_cast<int>(N), static_cast<int>(H), H, 1, 1, H};
+    return launch_fma_gemm("linear_act_fwd", static_cast<const T*>(X), static_cast<const T*>(W), g, e, st);
+}
+
+// dX = dP W and dW = dP^T X from dP [T, N] in TP
+template <typename T, typename TP>
+int grads_fma(const TP* dP, const void* X, const void* W, void* dX, void* dW, int64_t Tn, int64_t H, int64_t N,
+              cudaStream_t st) {
+    if (dX != nullptr) {
+        FmaEpi<T, float> e{};
+        e.out = static_cast<T*>(dX);
+        FmaGemm g{static_cast<int>(Tn), static_cast<int>(H), static_cast<int>(N), N, 1, H, 1};
+        if (int rc = launch_fma_gemm("linear_act_bwd dX", dP, static_cast<const T*>(W), g, e, st)) return rc;
+    }
+    if (dW != nullptr) {
+        FmaEpi<T, float> e{};
+        e.out = static_cast<T*>(dW);
+        FmaGemm g{static_cast<int>(N), static_cast<int>(H), static_cast<int>(Tn), 1, N, H, 1};
+        if (int rc = launch_fma_gemm("linear_act_bwd dW", dP, static_cast<const T*>(X), g, e, st)) return rc;
+    }
+    return LIGER_OK;
+}
+
+struct LinearBwd {
+    const void *dY, *X, *W, *pre;
+    void *dX, *dW, *db, *dP;
+    float* part;
+    int64_t T, H, N;
+    int act;
+    cudaStream_t st;
+};
+
+template <typename T, typename TPRE, typename TP>
+int bwd_typed(const LinearBwd& a) {
+    const bool keep = a.act != LIGER_ACT_NONE;
+    if (keep || a.db != nullptr) {
+        const int64_t run = rows_per_sum(a.T);
+        const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 32)), static_cast<unsigned>(ceil_div(a.T, run)));
+        if (int rc = launch_early("linear_act_bwd dP", linear_dp<T, TPRE, TP>, grid, 256, 0, a.st, static_cast<const T*>(a.dY),
+                                  static_cast<const TPRE*>(a.pre), static_cast<TP*>(keep ? a.dP : nullptr),
+                                  a.db != nullptr ? a.part : nullptr, a.T, static_cast<int>(a.N), run, a.act))
+            return rc;
+        if (a.db != nullptr)
+            if (int rc = launch_early("linear_act_bwd db", linear_db<T>, dim3(static_cast<unsigned>(ceil_div(a.N, 256))), 256, 0,
+                                      a.st, static_cast<const float*>(a.part), static_cast<T*>(a.db), static_cast<int>(grid.y),
+                                      static_cast<int>(a.N)))
+                return rc;
+    }
+    if (keep) return grads_fma<T, TP>(static_cast<const TP*>(a.dP), a.X, a.W, a.dX, a.dW, a.T, a.H, a.N, a.st);
+    return grads_fma<T, T>(static_cast<const T*>(a.dY), a.X, a.W, a.dX, a.dW, a.T, a.H, a.N, a.st);
+}
+
+}  // namespace
+}  // namespace liger
+
+using namespace liger;
+
+extern "C" int liger_linear_act_fwd(const void* X, const void* W, const void* bias, const void* residual, void* Y, void* pre,
+                                    int64_t T, int64_t H, int64_t N, int act, int dtype, void* stream) {
+    clear_error();
+    const char* who = "linear_act_fwd";
+    if (int rc = check_sizes(who, T, H, N, act, dtype)) return rc;
+    if (T == 0) return LIGER_OK;
+    if (!X || !W || !Y) return fail(LIGER_ERR_NULL, "%s: X, W and Y are required", who);
+    if (off16({X, W, bias, residual, Y, pre})) return fail(LIGER_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
+    cudaStream_t st = as_stream(stream);
+    if (dtype == LIGER_F32) {
+        FmaEpi<float, float> e{static_cast<const float*>(bias), static_cast<const float*>(residual), static_cast<float*>(Y),
+                               static_cast<float*>(pre), act};
+        return fwd_fma(X, W, e, T, H, N, st);
+    }
+    using Bf = __nv_bfloat16;
+    FmaEpi<Bf, __half> e{static_cast<const Bf*>(bias), static_cast<const Bf*>(residual), static_cast<Bf*>(Y),
+                         static_cast<__half*>(pre), act};
+    return fwd_fma(X, W, e, T, H, N, st);
+}
+
+extern "C" size_t liger_linear_act_bwd_workspace(int64_t T, int64_t H, int64_t N, int act, int dtype) {
+    const bool good = check_sizes("linear_act_bwd_workspace", T, H, N, act, dtype) == LIGER_OK;
+    clear_error();
+    if (!good || T == 0) return 0;
+    return dp_bytes(T, H, N, act, dtype) + sum_bytes(T, N);
+}
+
+extern "C" int liger_linear_act_bwd(const void* dY, const void* X, const void* W, const void* pre, void* dX, void* dW, void* db,
+                                    void* ws, size_t ws_bytes, int64_t T, int64_t H, int64_t N, int act, int dtype,
+                                    void* stream) {
+    clear_error();
+    const char* who = "linear_act_bwd";
+    if (int rc = check_sizes(who, T, H, N, act, dtype)) return rc;
+    if (off16({dY, X, W, pre, dX, dW, db})) return fail(LIGER_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
+    cudaStream_t st = as_stream(stream);
+    const size_t esz = dtype == LIGER_F32 ? 4 : 2;
+    if (T == 0) {
+        if (dW != nullptr && cudaMemsetAsync(dW, 0, static_cast<size_t>(N) * static_cast<size_t>(H) * esz, st) != cudaSuccess)
+            return check_launch(who);
+        if (db != nullptr && cudaMemsetAsync(db, 0, static_cast<size_t>(N) * esz, st) != cudaSuccess) return check_launch(who);
+        return LIGER_OK;
+    }
+    if (!dY || (dX && !W) || (dW && !X) || (act != LIGER_ACT_NONE && !pre))
+        return fail(LIGER_ERR_NULL, "%s: dY is required, W for dX, X for dW, pre for an activation", who);
+    const size_t need = liger_linear_act_bwd_workspace(T, H, N, act, dtype);
+    if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+        return fail(LIGER_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, need, ws_bytes);
+    LinearBwd a{dY, X, W, pre, dX, dW, db, ws, nullptr, T, H, N, act, st};
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dp_bytes(T, H, N, act, dtype));
+    if (dtype == LIGER_F32) return bwd_typed<float, float, float>(a);
+    if (on_tensor_cores(H, N, dtype)) return bwd_typed<__nv_bfloat16, __half, __nv_bfloat16>(a);
+    return bwd_typed<__nv_bfloat16, __half, float>(a);
+}
