@@ -67,23 +67,6 @@ __device__ __forceinline__ Window window_of(int64_t t, int64_t rows, int cols) {
 // bytes a slot needs for one stream
 inline size_t window_max(int cols, size_t sz) { return (static_cast<size_t>(cols) * sz + 15 + 15) & ~static_cast<size_t>(15); }
 
-// Lets a kernel have as much dynamic shared memory as the device gives, once per device (racing
-// threads set the same value).
-template <auto KERN>
-int allow_smem() {
-    static std::atomic<bool> done[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("block_norm device");
-    if (done[dev].load(std::memory_order_acquire)) return LIGER_OK;
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, KERN) != cudaSuccess ||
-        cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             max_smem_optin() - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess)
-        return check_launch("block_norm attribute");
-    done[dev].store(true, std::memory_order_release);
-    return LIGER_OK;
-}
-
 // Resident blocks per SM of a kernel, asked once per device.
 template <typename K>
 int resident(K kern, int threads, size_t smem, std::atomic<int> (&cache)[64]) {

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "liger.h"
@@ -188,6 +189,25 @@ int launch_early(const char* what, void (*kernel)(P...), dim3 grid, int threads,
     cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
     return check_launch(what);
 }
+
+namespace {
+// Lets a kernel have as much dynamic shared memory as the device gives, once per device (racing
+// threads set the same value).
+template <auto KERN>
+int allow_smem() {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("kernel device");
+    if (done[dev].load(std::memory_order_acquire)) return LIGER_OK;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, KERN) != cudaSuccess ||
+        cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             max_smem_optin() - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess)
+        return check_launch("kernel attribute");
+    done[dev].store(true, std::memory_order_release);
+    return LIGER_OK;
+}
+}  // namespace
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

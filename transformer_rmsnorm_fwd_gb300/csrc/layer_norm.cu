@@ -6,6 +6,7 @@ namespace liger {
 namespace {
 
 constexpr int kMaxPartRows = 1024;   // most partial rows of dw and of db
+constexpr size_t kFwdFlight = 64u * 1024u, kBwdFlight = 128u * 1024u;   // bytes of rows in flight on an SM that the rings aim at
 
 // ------------------------------------------------------------- any width
 // A block per row, elements strided over its threads; the row is read again from the caches for
@@ -36,6 +37,399 @@ __global__ void __launch_bounds__(256) layer_norm_fwd_rows(const T* x, const T* 
             if (mean != nullptr) mean[r] = m;
             if (rstd != nullptr) rstd[r] = rs;
         }
+    }
+}
+
+// ------------------------------------------------------------- rows in registers
+// VEC consecutive elements as one thread holds them: a 16-byte vector, or one element where the rows
+// are no whole vectors.
+template <typename T, int VEC> struct Piece {
+    static_assert(VEC == Vec<T>::N, "whole vectors or single elements");
+    uint4 u;
+    __device__ __forceinline__ void load(const T* p) { u = ldg16(p); }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const { unpack(u, f); }
+    static __device__ __forceinline__ void put(T* p, const float (&f)[VEC]) { stg16(p, pack(f)); }
+};
+template <typename T> struct Piece<T, 1> {
+    float v;
+    __device__ __forceinline__ void load(const T* p) { v = ldf(p); }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = v; }
+    static __device__ __forceinline__ void put(T* p, const float (&f)[1]) { stf(p, f[0]); }
+};
+
+struct LnFwd {
+    const void *x, *w, *b;
+    void* y;
+    float *mean, *rstd;
+    int64_t rows;
+    int cols;
+    float eps;
+};
+
+// Few rows: a team of `tw` warps holds a row in registers, VPT pieces a thread; its mean and the
+// mean of the squared differences go over the team by shuffles and one named barrier each.
+template <typename T, int VEC, int VPT>
+__global__ void __launch_bounds__(512) layer_norm_fwd_team(LnFwd p, int tw) {
+    __shared__ float red[2][16];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int team = warp / tw, wt = warp - team * tw, teams = (blockDim.x >> 5) / tw;
+    const int tt = wt * 32 + lane, nt = tw * 32;   // thread of the team, threads of the team
+    const int npiece = p.cols / VEC;
+    const T *x = static_cast<const T*>(p.x), *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
+    T* y = static_cast<T*>(p.y);
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    int turn = 0;
+    auto team_sum = [&](float v) {
+        v = warp_sum(v);
+        if (tw == 1) return v;
+        float* sh = red[turn & 1] + team * tw;   // written again only after a barrier that follows every read of it
+        ++turn;
+        if (lane == 0) sh[wt] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(nt) : "memory");
+        float s = 0.f;
+        for (int i = 0; i < tw; ++i) s += sh[i];
+        return s;
+    };
+    wait_for_stream();
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * teams + team; t < p.rows; t += static_cast<int64_t>(gridDim.x) * teams) {
+        const int64_t o = t * p.cols;
+        Piece<T, VEC> cx[VPT], cw[VPT], cb[VPT];
+        bool live[VPT];
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = j * nt + tt;
+            live[j] = c < npiece;
+            if (live[j]) {
+                cx[j].load(x + o + static_cast<int64_t>(c) * VEC);
+                if (w != nullptr) cw[j].load(w + static_cast<int64_t>(c) * VEC);
+                if (b != nullptr) cb[j].load(b + static_cast<int64_t>(c) * VEC);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (live[j]) {
+                float f[VEC];
+                cx[j].get(f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s += f[e];
+            }
+        const float m = team_sum(s) * inv;
+        s = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (live[j]) {
+                float f[VEC];
+                cx[j].get(f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) s = fmaf(f[e] - m, f[e] - m, s);
+            }
+        const float rs = inv_sqrt(fmaf(team_sum(s), inv, p.eps));
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (live[j]) {
+                float f[VEC], g[VEC];
+                cx[j].get(f);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[e] = (f[e] - m) * rs;
+                if (w != nullptr) {
+                    cw[j].get(g);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) f[e] *= g[e];
+                }
+                if (b != nullptr) {
+                    cb[j].get(g);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) f[e] += g[e];
+                }
+                Piece<T, VEC>::put(y + o + static_cast<int64_t>(j * nt + tt) * VEC, f);
+            }
+        if (tt == 0) {
+            if (p.mean != nullptr) p.mean[t] = m;
+            if (p.rstd != nullptr) p.rstd[t] = rs;
+        }
+    }
+}
+
+// ------------------------------------------------------------- rows staged by bulk copies
+// Whether every thread of the team says so, with one team barrier.
+__device__ __forceinline__ bool team_all(int team, int threads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %3, 0;\n\t"
+        "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all)
+        : "r"(team + 1), "r"(threads), "r"(ok ? 1u : 0u)
+        : "memory");
+    return all != 0;
+}
+
+// Many rows: the same team per row, its rows brought into a ring of `nst` slots by bulk copies, so that
+// several rows per team are in flight without registers; a slot is read into registers at once and is
+// free again after the next team barrier.  The weights stay in registers over the rows.  Every wait is
+// bounded; on expiry the team records it, waits (bounded) for its copies and writes NaN into the rows it
+// did not finish.  ONE: a single team, known at compile time.
+template <typename T, int VPT, int NT, int MB, int ONE>
+__global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, int nst, int* err) {
+    constexpr int VEC = Vec<T>::N, NP = VEC / 2;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ __align__(16) float red[2][NT / 32 + 4][4];   // rows of 4: a team starts on a multiple of 4 warps or is a warp alone
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (ONE) tw = blockDim.x >> 5;
+    const int team = ONE ? 0 : warp / tw, wt = warp - team * tw, teams = ONE ? 1 : (blockDim.x >> 5) / tw;
+    const int tt = wt * 32 + lane, nt = tw * 32;
+    const int nvec = p.cols / VEC;
+    const uint32_t rb = static_cast<uint32_t>(p.cols) * sizeof(T);
+    const uint8_t* ring = sm + static_cast<size_t>(team) * nst * rb;
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(teams) * nst * rb) + 8u * team * nst;
+    const T *x = static_cast<const T*>(p.x), *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
+    T* y = static_cast<T*>(p.y);
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+    int64_t t = static_cast<int64_t>(blockIdx.x) * teams + team;
+    auto issue = [&](int64_t row, int s) {
+        mbar_expect_tx(bars + 8u * s, rb);
+        bulk_g2s(smem_u32(ring + static_cast<size_t>(s) * rb), x + row * p.cols, rb, bars + 8u * s);
+    };
+    for (int i = threadIdx.x; i < 2 * (NT / 32 + 4) * 4; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    mbar_init_fence();
+    __syncthreads();
+    wait_for_stream();
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t + s * step < p.rows) issue(t + s * step, s);
+    uint4 cw[VPT], cb[VPT];
+    bool live[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int64_t c = static_cast<int64_t>(j * nt + tt) * VEC;
+        live[j] = j * nt + tt < nvec;
+        cw[j] = cb[j] = make_uint4(0, 0, 0, 0);
+        if (live[j] && w != nullptr) cw[j] = ldg16(w + c);
+        if (live[j] && b != nullptr) cb[j] = ldg16(b + c);
+    }
+    int turn = 0;
+    const int at0 = ONE ? 0 : team * ((tw + 3) & ~3);
+    // Team-wide sum in two halves: gather() brings the warps' sums together and says whether every thread
+    // of the team got its row (one team barrier), total() adds them up.
+    auto gather = [&](float& v, bool& ok) {
+        v = warp_sum(v);
+        if (!ONE && tw == 1) {
+            ok = __all_sync(0xffffffffu, ok);
+            return;
+        }
+        if (lane == 0) (&red[turn][0][0])[at0 + wt] = v;
+        ok = ONE ? __syncthreads_and(ok ? 1 : 0) != 0 : team_all(team, nt, ok);
+    };
+    auto total = [&](float v) {
+        if (!ONE && tw == 1) return v;
+        const float4* q = reinterpret_cast<const float4*>(&red[turn][0][0] + at0);   // slots past the team's warps hold 0
+        turn ^= 1;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < (NT / 32 + 3) / 4; ++i)
+            if (i * 4 < tw) {
+                const float4 a = q[i];
+                s += (a.x + a.y) + (a.z + a.w);
+            }
+        return s;
+    };
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (; t < p.rows; t += step) {
+        ok = mbar_wait(bars + 8u * s, ph);
+        const uint8_t* slot = ring + static_cast<size_t>(s) * rb;
+        uint4 cx[VPT];
+        float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            cx[j] = make_uint4(0, 0, 0, 0);
+            if (live[j] && ok) cx[j] = *reinterpret_cast<const uint4*>(slot + static_cast<size_t>(j * nt + tt) * 16);
+            float2 f[NP];
+            unpack2(cx[j], f);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) a = __fadd2_rn(a, f[e]);
+        }
+        float sum = a.x + a.y;
+        gather(sum, ok);
+        if (!ok) break;
+        const float m = total(sum) * inv;
+        if (tt == 0 && t + nst * step < p.rows) {   // every thread of the team has read the slot
+            fence_proxy_async_smem();
+            issue(t + nst * step, s);
+        }
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+        const float2 nm = make_float2(-m, -m);
+        a = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (live[j]) {
+                float2 f[NP];
+                unpack2(cx[j], f);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    f[e] = __fadd2_rn(f[e], nm);
+                    a = __ffma2_rn(f[e], f[e], a);
+                }
+            }
+        sum = a.x + a.y;
+        bool same = true;
+        gather(sum, same);
+        const float rs = inv_sqrt(fmaf(total(sum), inv, p.eps));
+        const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (live[j]) {
+                float2 f[NP], g[NP], h[NP];
+                unpack2(cx[j], f);
+                unpack2(cw[j], g);
+                unpack2(cb[j], h);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    f[e] = __fmul2_rn(__fadd2_rn(f[e], nm), rs2);
+                    f[e] = w != nullptr ? __ffma2_rn(f[e], g[e], h[e]) : __fadd2_rn(f[e], h[e]);
+                }
+                stg16_cs(y + t * p.cols + static_cast<int64_t>(j * nt + tt) * VEC, pack2(f));
+            }
+        if (tt == 0) {
+            if (p.mean != nullptr) p.mean[t] = m;
+            if (p.rstd != nullptr) p.rstd[t] = rs;
+        }
+    }
+    if (ok) return;
+    if (tt == 0) {
+        atomicExch(err, 1);
+        int64_t row = t;
+        for (int i = 0; i < nst && row < p.rows; ++i, row += step) {   // the copies in flight
+            mbar_wait(bars + 8u * s, ph);
+            if (++s == nst) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    const float nan = __int_as_float(0x7FC00000);
+    for (; t < p.rows; t += step) {
+        for (int v = tt; v < nvec; v += nt) stg16(y + t * p.cols + static_cast<int64_t>(v) * VEC, nan16<T>());
+        if (tt == 0 && p.mean != nullptr) p.mean[t] = nan;
+        if (tt == 0 && p.rstd != nullptr) p.rstd[t] = nan;
+    }
+}
+
+// Rows that are no whole vectors: aligned windows around them (block_norm.cuh), EPT fixed columns a thread.
+template <typename T, int EPT, int NT>
+__global__ void __launch_bounds__(NT, 1) layer_norm_fwd_odd(LnFwd p, int nst, uint32_t wmax, int* err) {
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ float red[2][NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(nst) * wmax);
+    const T *x = static_cast<const T*>(p.x), *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
+    T* y = static_cast<T*>(p.y);
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    const int64_t step = gridDim.x;
+    int64_t t = blockIdx.x;
+    auto issue = [&](int64_t row, int s) {
+        const Window win = window_of<T>(row, p.rows, p.cols);
+        mbar_expect_tx(bars + 8u * s, win.bytes);
+        if (win.bytes > 0)
+            bulk_g2s(smem_u32(sm + static_cast<size_t>(s) * wmax), static_cast<const uint8_t*>(p.x) + win.at, win.bytes, bars + 8u * s);
+    };
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    mbar_init_fence();
+    __syncthreads();
+    wait_for_stream();
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t + s * step < p.rows) issue(t + s * step, s);
+    float wf[EPT], bf[EPT];
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        const int c = j * NT + tid;
+        wf[j] = w != nullptr && c < p.cols ? ldf(w + c) : 1.f;
+        bf[j] = b != nullptr && c < p.cols ? ldf(b + c) : 0.f;
+    }
+    int turn = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto total = [&]() {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) a += red[turn][i];
+        turn ^= 1;   // written again only after the next barrier
+        return a;
+    };
+    for (; t < p.rows; t += step) {
+        const Window win = window_of<T>(t, p.rows, p.cols);
+        ok = mbar_wait(bars + 8u * s, ph);
+        const T* xs = reinterpret_cast<const T*>(sm + static_cast<size_t>(s) * wmax) + win.shift;
+        const int64_t o = t * p.cols;
+        float f[EPT];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            f[j] = 0.f;
+            if (c < p.cols && ok) f[j] = c < win.tail ? ldf(xs + c) : ldf(x + o + c);
+            sum += f[j];
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) red[turn][wid] = sum;
+        ok = __syncthreads_and(ok ? 1 : 0) != 0;
+        if (!ok) break;
+        if (tid == 0 && t + nst * step < p.rows) {   // every thread has its elements of the row
+            fence_proxy_async_smem();
+            issue(t + nst * step, s);
+        }
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+        const float m = total() * inv;
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j)
+            if (j * NT + tid < p.cols) {
+                f[j] -= m;
+                sum = fmaf(f[j], f[j], sum);
+            }
+        sum = warp_sum(sum);
+        if (lane == 0) red[turn][wid] = sum;
+        __syncthreads();
+        const float rs = inv_sqrt(fmaf(total(), inv, p.eps));
+#pragma unroll
+        for (int j = 0; j < EPT; ++j)
+            if (j * NT + tid < p.cols) stf(y + o + j * NT + tid, fmaf(f[j] * rs, wf[j], bf[j]));
+        if (tid == 0) {
+            if (p.mean != nullptr) p.mean[t] = m;
+            if (p.rstd != nullptr) p.rstd[t] = rs;
+        }
+    }
+    if (ok) return;
+    if (tid == 0) {
+        atomicExch(err, 1);
+        int64_t row = t;
+        for (int i = 0; i < nst && row < p.rows; ++i, row += step) {   // the copies in flight
+            mbar_wait(bars + 8u * s, ph);
+            if (++s == nst) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    const float nan = __int_as_float(0x7FC00000);
+    for (; t < p.rows; t += step) {
+        for (int c = tid; c < p.cols; c += NT) stf(y + t * p.cols + c, nan);
+        if (tid == 0 && p.mean != nullptr) p.mean[t] = nan;
+        if (tid == 0 && p.rstd != nullptr) p.rstd[t] = nan;
     }
 }
 
@@ -86,29 +480,382 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_rows(LnBwd p) {
     }
 }
 
-// Column sums of the partial rows in ascending order: dw (blockIdx.y 0) and db (1).
-template <typename T>
-__global__ void __launch_bounds__(256) layer_norm_sums(const float* part_w, const float* part_b, T* dw, T* db, int parts,
-                                                       int cols) {
-    __shared__ float red[8][33];
+// ------------------------------------------------------------- backward, rows staged by bulk copies
+// A block takes every gridDim.x-th row; in it a team of `tw` warps takes every teams-th of those, the row's
+// dy, x (and dres) brought into the team's ring of `nst` slots.  Each thread owns VPT 16-byte column
+// vectors: the weight and its shares of dw and db stay in fp32 registers over the rows.  The two sums of a
+// row are reduced together (one team barrier a row), across which its values stay in registers, and the
+// slot is free at once for the next copies.  Arithmetic on column pairs with the packed fp32x2
+// instructions.  Every wait is bounded; on expiry the block records it, waits (bounded) for its copies and
+// writes NaN into the rows and sums it did not finish.
+template <typename T, int VPT, int NT, int ONE>
+__global__ void __launch_bounds__(NT, 1) layer_norm_bwd_ring(LnBwd p, int tw, int nst, int* err) {
+    constexpr int VEC = Vec<T>::N, NP = VEC / 2;
+    extern __shared__ __align__(128) uint8_t sm[];
+    // per team its warps' sums, from a multiple of 4: at most 4 entries for every warp
+    __shared__ __align__(16) float red[2][2][NT / 32 * 4];
+    __shared__ int failed;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (ONE) tw = blockDim.x >> 5;
+    const int team = ONE ? 0 : warp / tw, wt = warp - team * tw, teams = ONE ? 1 : (blockDim.x >> 5) / tw;
+    const int tt = wt * 32 + lane, nt = tw * 32;
+    const int nvec = p.cols / VEC;
+    const uint32_t rb = static_cast<uint32_t>(p.cols) * sizeof(T);
+    const T *dy = static_cast<const T*>(p.dy), *x = static_cast<const T*>(p.x), *dres = static_cast<const T*>(p.dres),
+            *w = static_cast<const T*>(p.w);
+    T* dx = static_cast<T*>(p.dx);
+    const bool res = dres != nullptr;
+    const uint32_t slot_bytes = rb * (res ? 3 : 2);
+    const uint8_t* ring = sm + static_cast<size_t>(team) * nst * slot_bytes;
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(teams) * nst * slot_bytes) + 8u * team * nst;
+    int64_t t = blockIdx.x + static_cast<int64_t>(team) * gridDim.x;
+    const int64_t step = static_cast<int64_t>(teams) * gridDim.x;
+    auto issue = [&](int64_t row, int s) {
+        const uint32_t bar = bars + 8u * s, dst = smem_u32(ring + static_cast<size_t>(s) * slot_bytes);
+        mbar_expect_tx(bar, slot_bytes);
+        bulk_g2s(dst, dy + row * p.cols, rb, bar);
+        bulk_g2s(dst + rb, x + row * p.cols, rb, bar);
+        if (res) bulk_g2s(dst + 2 * rb, dres + row * p.cols, rb, bar);
+    };
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    if (threadIdx.x == 0) failed = 0;
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    mbar_init_fence();
+    __syncthreads();
+    wait_for_stream();
+    if (tt == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t + s * step < p.rows) issue(t + s * step, s);
+    float2 wf[VPT][NP], Sw[VPT][NP], Sb[VPT][NP];
+    bool live[VPT];
+    const float2 zero2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        live[j] = j * nt + tt < nvec;
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            wf[j][e] = make_float2(1.f, 1.f);
+            Sw[j][e] = Sb[j][e] = zero2;
+        }
+        if (live[j] && w != nullptr) unpack2(ldg16(w + static_cast<int64_t>(j * nt + tt) * VEC), wf[j]);
+    }
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    const int at = ONE ? 0 : team * ((tw + 3) & ~3);
+    int s = 0, turn = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    // the next row's mean and rstd, fetched a row ahead
+    float mn = t < p.rows ? p.mean[t] : 0.f, rn = t < p.rows ? p.rstd[t] : 0.f;
+    for (; t < p.rows; t += step) {
+        const float m = mn, rs = rn;
+        if (t + step < p.rows) {
+            mn = p.mean[t + step];
+            rn = p.rstd[t + step];
+        }
+        ok = mbar_wait(bars + 8u * s, ph);
+        const uint8_t* slot = ring + static_cast<size_t>(s) * slot_bytes;
+        uint4 cy[VPT], cx[VPT], cr[VPT];
+        float2 a1 = zero2, a2 = zero2;
+        const float2 nm = make_float2(-m, -m), rs2 = make_float2(rs, rs);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const size_t o = static_cast<size_t>(j * nt + tt) * 16;
+            cy[j] = cx[j] = cr[j] = make_uint4(0, 0, 0, 0);
+            if (!(live[j] && ok)) continue;
+            cy[j] = *reinterpret_cast<const uint4*>(slot + o);
+            cx[j] = *reinterpret_cast<const uint4*>(slot + rb + o);
+            if (res) cr[j] = *reinterpret_cast<const uint4*>(slot + 2 * rb + o);
+            float2 fy[NP], fx[NP];
+            unpack2(cy[j], fy);
+            unpack2(cx[j], fx);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const float2 xh = __fmul2_rn(__fadd2_rn(fx[e], nm), rs2);
+                const float2 g = __fmul2_rn(fy[e], wf[j][e]);
+                a1 = __fadd2_rn(a1, g);
+                a2 = __ffma2_rn(g, xh, a2);
+                Sw[j][e] = __ffma2_rn(fy[e], xh, Sw[j][e]);
+                Sb[j][e] = __fadd2_rn(Sb[j][e], fy[e]);
+            }
+        }
+        float s1 = a1.x + a1.y, s2 = a2.x + a2.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+        }
+        if (!ONE && tw == 1) {
+            ok = __all_sync(0xffffffffu, ok);
+        } else {
+            if (lane == 0) {
+                red[turn][0][at + wt] = s1;
+                red[turn][1][at + wt] = s2;
+            }
+            ok = ONE ? __syncthreads_and(ok ? 1 : 0) != 0 : team_all(team, nt, ok);
+        }
+        if (!ok) break;
+        if (ONE || tw > 1) {
+            s1 = s2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < (NT / 32 + 3) / 4; ++i)   // entries past the team's warps hold 0
+                if (ONE || i * 4 < tw) {
+                    const float4 f = reinterpret_cast<const float4*>(red[turn][0] + at)[i];
+                    const float4 g = reinterpret_cast<const float4*>(red[turn][1] + at)[i];
+                    s1 += (f.x + f.y) + (f.z + f.w);
+                    s2 += (g.x + g.y) + (g.z + g.w);
+                }
+            turn ^= 1;   // this buffer is written again only after the next barrier
+        }
+        if (tt == 0 && t + nst * step < p.rows) {   // every thread of the team has the row's values
+            fence_proxy_async_smem();
+            issue(t + nst * step, s);
+        }
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+        const float2 nc1 = make_float2(-s1 * inv, -s1 * inv), nc2 = make_float2(-s2 * inv, -s2 * inv);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (!live[j]) continue;
+            float2 fy[NP], fx[NP], o[NP];
+            unpack2(cy[j], fy);
+            unpack2(cx[j], fx);
+            unpack2(cr[j], o);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const float2 xh = __fmul2_rn(__fadd2_rn(fx[e], nm), rs2);
+                float2 g = __ffma2_rn(fy[e], wf[j][e], nc1);
+                g = __ffma2_rn(nc2, xh, g);
+                o[e] = __ffma2_rn(rs2, g, o[e]);
+            }
+            stg16_cs(dx + t * p.cols + static_cast<int64_t>(j * nt + tt) * VEC, pack2(o));
+        }
+    }
+    if (!ok) {
+        if (tt == 0) {
+            failed = 1;
+            atomicExch(err, 1);
+            int64_t row = t;   // the team's copies in flight: rows t, t + step, ..., the first in slot s
+            for (int i = 0; i < nst && row < p.rows; ++i, row += step) {
+                mbar_wait(bars + 8u * s, ph);
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        for (int64_t row = t; row < p.rows; row += step)
+            for (int v = tt; v < nvec; v += nt) stg16(dx + row * p.cols + static_cast<int64_t>(v) * VEC, nan16<T>());
+    }
+    // the block's partial rows: the teams' sums in the order of the teams, through the ring's memory once no
+    // copy is in flight (every team has waited for all its rows, or for its copies above)
+    __syncthreads();
+    const bool bad = failed != 0;
+    float2* acc = reinterpret_cast<float2*>(sm);   // per column vector: NP of dw, NP of db
+    float* pw = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    float* pb = p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    for (int k = 0; k < teams; ++k) {
+        if (team == k) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (!live[j]) continue;
+                const int v = j * nt + tt;
+                float2 sw[NP], sb[NP];
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    sw[e] = Sw[j][e];
+                    sb[e] = Sb[j][e];
+                    if (k > 0) {
+                        sw[e] = __fadd2_rn(acc[v * 2 * NP + e], sw[e]);
+                        sb[e] = __fadd2_rn(acc[v * 2 * NP + NP + e], sb[e]);
+                    }
+                    if (k + 1 < teams) {
+                        acc[v * 2 * NP + e] = sw[e];
+                        acc[v * 2 * NP + NP + e] = sb[e];
+                    }
+                }
+                if (k + 1 == teams) {
+#pragma unroll
+                    for (int e = 0; e < NP; e += 2) {
+                        const int64_t c = static_cast<int64_t>(v) * VEC + 2 * e;
+                        const float2 ow[2] = {sw[e], sw[e + 1]}, ob[2] = {sb[e], sb[e + 1]};
+                        if (pw != nullptr) stg16(pw + c, bad ? nan16<float>() : pack2(ow));
+                        if (pb != nullptr) stg16(pb + c, bad ? nan16<float>() : pack2(ob));
+                    }
+                }
+            }
+        }
+        if (k + 1 < teams) __syncthreads();
+    }
+}
+
+// Rows that are no whole vectors: aligned windows around them (block_norm.cuh), EPT fixed columns a thread.
+template <typename T, int EPT, int NT>
+__global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, uint32_t wmax, int* err) {
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ float red[2][2][NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const T *dy = static_cast<const T*>(p.dy), *x = static_cast<const T*>(p.x), *dres = static_cast<const T*>(p.dres),
+            *w = static_cast<const T*>(p.w);
+    T* dx = static_cast<T*>(p.dx);
+    const bool res = dres != nullptr;
+    const uint32_t slot_bytes = wmax * (res ? 3 : 2);
+    const uint32_t bars = smem_u32(sm + static_cast<size_t>(nst) * slot_bytes);
+    int64_t t = blockIdx.x;
+    const int64_t step = gridDim.x;
+    auto issue = [&](int64_t row, int s) {
+        const Window win = window_of<T>(row, p.rows, p.cols);
+        const uint32_t bar = bars + 8u * s, dst = smem_u32(sm + static_cast<size_t>(s) * slot_bytes);
+        mbar_expect_tx(bar, (res ? 3 : 2) * win.bytes);
+        if (win.bytes == 0) return;
+        bulk_g2s(dst, static_cast<const uint8_t*>(p.dy) + win.at, win.bytes, bar);
+        bulk_g2s(dst + wmax, static_cast<const uint8_t*>(p.x) + win.at, win.bytes, bar);
+        if (res) bulk_g2s(dst + 2 * wmax, static_cast<const uint8_t*>(p.dres) + win.at, win.bytes, bar);
+    };
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
+    mbar_init_fence();
+    __syncthreads();
+    wait_for_stream();
+    if (tid == 0)
+        for (int s = 0; s < nst; ++s)
+            if (t + s * step < p.rows) issue(t + s * step, s);
+    float wf[EPT], Sw[EPT], Sb[EPT];
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        wf[j] = w != nullptr && j * NT + tid < p.cols ? ldf(w + j * NT + tid) : 1.f;
+        Sw[j] = Sb[j] = 0.f;
+    }
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    int s = 0, turn = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    float mn = t < p.rows ? p.mean[t] : 0.f, rn = t < p.rows ? p.rstd[t] : 0.f;
+    for (; t < p.rows; t += step) {
+        const float m = mn, rs = rn;
+        if (t + step < p.rows) {
+            mn = p.mean[t + step];
+            rn = p.rstd[t + step];
+        }
+        const Window win = window_of<T>(t, p.rows, p.cols);
+        ok = mbar_wait(bars + 8u * s, ph);
+        const uint8_t* slot = sm + static_cast<size_t>(s) * slot_bytes;
+        const int64_t o = t * p.cols;
+        auto get = [&](uint32_t so, const T* g, int c) {
+            return c < win.tail ? ldf(reinterpret_cast<const T*>(slot + so) + win.shift + c) : ldf(g + o + c);
+        };
+        float g[EPT], xh[EPT], r[EPT];
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const int c = j * NT + tid;
+            g[j] = xh[j] = r[j] = 0.f;
+            if (c >= p.cols || !ok) continue;
+            const float d = get(0, dy, c);
+            xh[j] = (get(wmax, x, c) - m) * rs;
+            if (res) r[j] = get(2 * wmax, dres, c);
+            g[j] = d * wf[j];
+            s1 += g[j];
+            s2 = fmaf(g[j], xh[j], s2);
+            Sw[j] = fmaf(d, xh[j], Sw[j]);
+            Sb[j] += d;
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) {
+            s1 += __shfl_xor_sync(0xffffffffu, s1, i);
+            s2 += __shfl_xor_sync(0xffffffffu, s2, i);
+        }
+        if (lane == 0) {
+            red[turn][0][wid] = s1;
+            red[turn][1][wid] = s2;
+        }
+        ok = __syncthreads_and(ok ? 1 : 0) != 0;
+        if (!ok) break;
+        if (tid == 0 && t + nst * step < p.rows) {   // every thread has its elements of the row
+            fence_proxy_async_smem();
+            issue(t + nst * step, s);
+        }
+        if (++s == nst) {
+            s = 0;
+            ph ^= 1u;
+        }
+        s1 = s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) {
+            s1 += red[turn][0][i];
+            s2 += red[turn][1][i];
+        }
+        turn ^= 1;
+        s1 *= inv;
+        s2 *= inv;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j)
+            if (j * NT + tid < p.cols) stf(dx + o + j * NT + tid, fmaf(rs, g[j] - s1 - xh[j] * s2, r[j]));
+    }
+    float* pw = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    float* pb = p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
+    const float nan = __int_as_float(0x7FC00000);
+    if (!ok) {
+        if (tid == 0) {
+            atomicExch(err, 1);
+            int64_t row = t;
+            for (int i = 0; i < nst && row < p.rows; ++i, row += step) {
+                mbar_wait(bars + 8u * s, ph);
+                if (++s == nst) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        for (int64_t row = t; row < p.rows; row += step)
+            for (int c = tid; c < p.cols; c += NT) stf(dx + row * p.cols + c, nan);
+    }
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+        const int c = j * NT + tid;
+        if (c >= p.cols) continue;
+        if (pw != nullptr) pw[c] = ok ? Sw[j] : nan;
+        if (pb != nullptr) pb[c] = ok ? Sb[j] : nan;
+    }
+}
+
+// dw (blockIdx.y 0) and db (1) from the partial rows: a block of 32 warps over 32 groups of V columns, warp w
+// adding the partial rows w, w + 32, ... in ascending order, the slices then added in their order.
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) layer_norm_sums(const float* part_w, const float* part_b, T* dw, T* db, int parts,
+                                                        int cols) {
+    __shared__ float red[32][32][V];
     wait_for_stream();
     const float* part = blockIdx.y == 0 ? part_w : part_b;
     T* out = blockIdx.y == 0 ? dw : db;
     if (out == nullptr) return;
     const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
-    float s = 0.f;
-    if (col < cols)
-#pragma unroll 4
-        for (int i = sl; i < parts; i += 8) s += part[static_cast<int64_t>(i) * cols + col];
-    red[sl][lane] = s;
-    __syncthreads();
-    if (sl == 0 && col < cols) {
-        float t = 0.f;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V;
+    float s[V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += red[i][lane];
-        stf(out + col, t);
+    for (int e = 0; e < V; ++e) s[e] = 0.f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int i = sl; i < parts; i += 32) {
+            float v[V];
+            const float* src = part + static_cast<int64_t>(i) * cols + c;
+            if constexpr (V == 4) unpack(ldg16(src), v);
+            else v[0] = *src;
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[e] += v[e];
+        }
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) red[sl][lane][e] = s[e];
+    __syncthreads();
+    if (sl != 0 || c >= cols) return;
+    for (int i = 1; i < 32; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[e] += red[i][lane][e];
+#pragma unroll
+    for (int e = 0; e < V; ++e) stf(out + c + e, s[e]);
 }
 
 int check_sizes(const char* who, int64_t rows, int64_t cols, int dtype) {
@@ -118,26 +865,158 @@ int check_sizes(const char* who, int64_t rows, int64_t cols, int dtype) {
     return LIGER_OK;
 }
 
+// ------------------------------------------------------------------ launches
+template <typename T, int VEC, int VPT>
+int fwd_team(const LnFwd& p, int tw, cudaStream_t st) {
+    const int teams = std::max(1, 8 / tw), threads = teams * tw * 32;
+    const int64_t grid = std::min<int64_t>(ceil_div(p.rows, teams), 8 * sm_count());
+    return launch_early("layernorm_fwd", layer_norm_fwd_team<T, VEC, VPT>, dim3(static_cast<unsigned>(grid)), threads, 0, st, p, tw);
+}
+
+template <typename T, int VPT, int NT, int MB, int ONE>
+int fwd_ring_teams(const LnFwd& p, int tw, cudaStream_t st) {
+    const int teams = std::max(1, NT / 32 / tw), threads = teams * tw * 32;
+    const size_t slot = static_cast<size_t>(teams) * (static_cast<size_t>(p.cols) * sizeof(T) + 8);
+    constexpr auto k = layer_norm_fwd_ring<T, VPT, NT, MB, ONE>;
+    if (int rc = allow_smem<k>()) return rc;
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, 2 * slot);
+    per_sm = std::max(1, per_sm);
+    const int nst = static_cast<int>(std::max<size_t>(2, std::min<size_t>(4, (kFwdFlight + per_sm * slot - 1) / (per_sm * slot))));
+    if (nst > 2) {
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, nst * slot);
+        per_sm = std::max(1, per_sm);
+    }
+    const int64_t grid = std::min<int64_t>(ceil_div(p.rows, teams), static_cast<int64_t>(sm_count()) * per_sm);
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    return launch_early("layernorm_fwd", k, dim3(static_cast<unsigned>(grid)), threads, nst * slot, st, p, tw, nst, err);
+}
+// TEAMS: whether rows can be short enough that a block holds several teams
+template <typename T, int VPT, int NT, int MB, int TEAMS>
+int fwd_ring(const LnFwd& p, int nvec, cudaStream_t st) {
+    const int tw = static_cast<int>(ceil_div(nvec, 32 * VPT));
+    if constexpr (TEAMS != 0)
+        if (NT / 32 / tw > 1) return fwd_ring_teams<T, VPT, NT, MB, 0>(p, tw, st);
+    return fwd_ring_teams<T, VPT, NT, MB, 1>(p, tw, st);
+}
+
+template <typename T, int EPT, int NT>
+int fwd_odd(const LnFwd& p, cudaStream_t st) {
+    constexpr auto k = layer_norm_fwd_odd<T, EPT, NT>;
+    if (int rc = allow_smem<k>()) return rc;
+    const size_t wmax = window_max(p.cols, sizeof(T)), smem = 3 * (wmax + 8);
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, NT, smem);
+    const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm));
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    return launch_early("layernorm_fwd", k, dim3(static_cast<unsigned>(grid)), NT, smem, st, p, 3, static_cast<uint32_t>(wmax), err);
+}
+
 template <typename T>
-int run_fwd(const void* x, const void* w, const void* b, void* y, float* mean, float* rstd, int64_t rows, int cols,
-            float eps, cudaStream_t st) {
-    const int64_t grid = std::min<int64_t>(rows, 8 * sm_count());
+int run_fwd(const LnFwd& p, cudaStream_t st) {
+    constexpr int EPV = Vec<T>::N;
+    if (p.cols % EPV == 0) {
+        const int nvec = p.cols / EPV;
+        const int64_t few = static_cast<int64_t>(sm_count()) * std::max(1, 512 / std::max(nvec, 32));
+        if (p.rows <= few && nvec <= 512) return fwd_team<T, EPV, 1>(p, (nvec + 31) / 32, st);
+        if (p.rows <= few && nvec <= 2048) return fwd_team<T, EPV, 4>(p, (nvec + 127) / 128, st);
+        if (nvec <= 32) return fwd_ring<T, 1, 256, 2, 1>(p, nvec, st);
+        if (nvec <= 512) return fwd_ring<T, 2, 256, 2, 1>(p, nvec, st);
+        if (nvec <= 1024) return fwd_ring<T, 4, 256, 2, 0>(p, nvec, st);
+        if (nvec <= 2048) return fwd_ring<T, 4, 512, 1, 0>(p, nvec, st);
+    } else {
+        if (p.cols <= 128) return fwd_team<T, 1, 4>(p, 1, st);
+        if (p.rows <= sm_count() && p.cols <= 2048) return fwd_team<T, 1, 4>(p, (p.cols + 127) / 128, st);
+        if (p.cols <= 512) return fwd_odd<T, 4, 128>(p, st);
+        if (p.cols <= 1024) return fwd_odd<T, 4, 256>(p, st);
+        if (p.cols <= 2048) return fwd_odd<T, 8, 256>(p, st);
+        if (p.cols <= 4096) return fwd_odd<T, 8, 512>(p, st);
+        if (p.cols <= 8192) return fwd_odd<T, 16, 512>(p, st);
+    }
+    const int64_t grid = std::min<int64_t>(p.rows, 8 * sm_count());
     return launch_early("layernorm_fwd", layer_norm_fwd_rows<T>, dim3(static_cast<unsigned>(grid)), 256, 0, st,
-                        static_cast<const T*>(x), static_cast<const T*>(w), static_cast<const T*>(b), static_cast<T*>(y),
-                        mean, rstd, rows, cols, eps);
+                        static_cast<const T*>(p.x), static_cast<const T*>(p.w), static_cast<const T*>(p.b), static_cast<T*>(p.y),
+                        p.mean, p.rstd, p.rows, p.cols, p.eps);
+}
+
+template <typename T, int VPT, int NT, int ONE>
+int bwd_ring_teams(const LnBwd& p, int nvec, int teams, int64_t& grid, cudaStream_t st) {
+    const int tw = static_cast<int>(ceil_div(nvec, 32 * VPT)), threads = teams * tw * 32;
+    const size_t slot = static_cast<size_t>(p.dres != nullptr ? 3 : 2) * p.cols * sizeof(T);
+    constexpr auto k = layer_norm_bwd_ring<T, VPT, NT, ONE>;
+    if (int rc = allow_smem<k>()) return rc;
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, teams * (slot + 8));
+    per_sm = std::max(1, per_sm);
+    size_t nst = std::max<size_t>(1, std::min<size_t>(8, kBwdFlight / (per_sm * teams * slot)));
+    if (nst == 1 && 2 * teams * (slot + 8) <= 220u * 1024u) nst = 2;
+    // the sums of the teams go through the ring's memory at the end: 16 bytes a vector and element pair
+    const size_t sums = teams > 1 ? static_cast<size_t>(nvec) * Vec<T>::N * 8 : 0;
+    const size_t smem = std::max(teams * nst * (slot + 8), sums);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem);
+    grid = std::min<int64_t>({ceil_div(p.rows, teams), kMaxPartRows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm)});
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    return launch_early("layernorm_bwd", k, dim3(static_cast<unsigned>(grid)), threads, smem, st, p, tw, static_cast<int>(nst), err);
+}
+template <typename T, int VPT, int NT, int TEAMS>
+int bwd_ring(const LnBwd& p, int nvec, int64_t& grid, cudaStream_t st) {
+    const int teams = std::max<int>(1, 8 / static_cast<int>(ceil_div(nvec, 32 * VPT)));
+    if constexpr (TEAMS != 0)
+        if (teams > 1) return bwd_ring_teams<T, VPT, NT, 0>(p, nvec, teams, grid, st);
+    return bwd_ring_teams<T, VPT, NT, 1>(p, nvec, 1, grid, st);
+}
+
+template <typename T, int EPT, int NT>
+int bwd_odd(const LnBwd& p, int64_t& grid, cudaStream_t st) {
+    constexpr auto k = layer_norm_bwd_odd<T, EPT, NT>;
+    if (int rc = allow_smem<k>()) return rc;
+    const size_t wmax = window_max(p.cols, sizeof(T)), slot = (p.dres != nullptr ? 3 : 2) * wmax + 8;
+    int nst = 4;   // one row in use, three in flight
+    while (nst > 2 && nst * slot > 200u * 1024u) --nst;
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, NT, nst * slot);
+    grid = std::min<int64_t>({p.rows, kMaxPartRows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm)});
+    int* err = nullptr;
+    if (int rc = rmsnorm_err_word(&err)) return rc;
+    return launch_early("layernorm_bwd", k, dim3(static_cast<unsigned>(grid)), NT, nst * slot, st, p, nst,
+                        static_cast<uint32_t>(wmax), err);
 }
 
 template <typename T>
 int run_bwd(LnBwd p, void* dw, void* db, cudaStream_t st) {
-    const int64_t most = std::min<int64_t>({p.rows, kMaxPartRows, 4 * sm_count()});
-    p.rows_per_block = ceil_div(p.rows, most);
-    const int64_t grid = ceil_div(p.rows, p.rows_per_block);
-    if (int rc = launch_early("layernorm_bwd", layer_norm_bwd_rows<T>, dim3(static_cast<unsigned>(grid)), 256, 0, st, p))
-        return rc;
+    constexpr int EPV = Vec<T>::N;
+    constexpr bool F32 = sizeof(T) == 4;
+    const int streams = p.dres != nullptr ? 3 : 2;
+    const int nvec = p.cols % EPV == 0 ? p.cols / EPV : 0;
+    int64_t grid = 0;
+    int rc;
+    if (nvec == 0 && p.cols >= 64 && p.cols <= 8192 && 2 * (streams * window_max(p.cols, sizeof(T)) + 8) <= 220u * 1024u) {
+        if (p.cols <= 256) rc = bwd_odd<T, 4, 64>(p, grid, st);
+        else if (p.cols <= 512) rc = bwd_odd<T, 4, 128>(p, grid, st);
+        else if (p.cols <= 1024) rc = bwd_odd<T, 4, 256>(p, grid, st);
+        else if (p.cols <= 2048) rc = bwd_odd<T, 8, 256>(p, grid, st);
+        else if (p.cols <= 4096) rc = bwd_odd<T, 8, 512>(p, grid, st);
+        else rc = bwd_odd<T, 16, 512>(p, grid, st);
+    } else if (nvec == 0 || nvec > 2048 || static_cast<size_t>(streams) * p.cols * sizeof(T) > 200u * 1024u) {
+        const int64_t most = std::min<int64_t>({p.rows, kMaxPartRows, 4 * sm_count()});
+        p.rows_per_block = ceil_div(p.rows, most);
+        grid = ceil_div(p.rows, p.rows_per_block);
+        rc = launch_early("layernorm_bwd", layer_norm_bwd_rows<T>, dim3(static_cast<unsigned>(grid)), 256, 0, st, p);
+    } else if (!F32 && nvec <= 256) rc = bwd_ring<T, 1, 256, 1>(p, nvec, grid, st);
+    else if (nvec <= 512) rc = bwd_ring<T, 2, 256, 1>(p, nvec, grid, st);
+    else if (nvec <= 1024) rc = bwd_ring<T, 2, 512, 0>(p, nvec, grid, st);
+    else rc = bwd_ring<T, 4, 512, 0>(p, nvec, grid, st);
+    if (rc) return rc;
     if (dw == nullptr && db == nullptr) return LIGER_OK;
-    return launch_early("layernorm_bwd sums", layer_norm_sums<T>, dim3(static_cast<unsigned>(ceil_div(p.cols, 32)), 2), 256, 0,
-                        st, static_cast<const float*>(p.part_w), static_cast<const float*>(p.part_b), static_cast<T*>(dw),
-                        static_cast<T*>(db), static_cast<int>(grid), p.cols);
+    const float *pw = p.part_w, *pb = p.part_b;
+    if (p.cols % 4 == 0)
+        return launch_early("layernorm_bwd sums", layer_norm_sums<T, 4>, dim3(static_cast<unsigned>(ceil_div(p.cols, 128)), 2), 1024,
+                            0, st, pw, pb, static_cast<T*>(dw), static_cast<T*>(db), static_cast<int>(grid), p.cols);
+    return launch_early("layernorm_bwd sums", layer_norm_sums<T, 1>, dim3(static_cast<unsigned>(ceil_div(p.cols, 32)), 2), 1024, 0,
+                        st, pw, pb, static_cast<T*>(dw), static_cast<T*>(db), static_cast<int>(grid), p.cols);
 }
 
 }  // namespace
@@ -156,8 +1035,8 @@ extern "C" int liger_layernorm_fwd(const void* x, const void* w, const void* b, 
     if (misaligned({x, w, b, y}, 16)) return fail(LIGER_ERR_ALIGN, "%s: tensors must be 16-byte aligned", who);
     if (misaligned({mean, rstd}, 4)) return fail(LIGER_ERR_ALIGN, "%s: mean and rstd must be 4-byte aligned", who);
     cudaStream_t st = as_stream(stream);
-    return dtype == LIGER_F32 ? run_fwd<float>(x, w, b, y, mean, rstd, rows, static_cast<int>(cols), eps, st)
-                              : run_fwd<__nv_bfloat16>(x, w, b, y, mean, rstd, rows, static_cast<int>(cols), eps, st);
+    const LnFwd p{x, w, b, y, mean, rstd, rows, static_cast<int>(cols), eps};
+    return dtype == LIGER_F32 ? run_fwd<float>(p, st) : run_fwd<__nv_bfloat16>(p, st);
 }
 
 extern "C" size_t liger_layernorm_bwd_workspace(int64_t rows, int64_t cols) {

@@ -57,6 +57,14 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
+// 1-D bulk copy shared -> global (the same alignments), and the wait until the copies that this thread has
+// started so have read their shared memory.
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_done() {
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
 // Orders this thread's earlier generic-proxy accesses to shared memory before
 // later async-proxy (bulk copy / TMA / tensor core) accesses.
 __device__ __forceinline__ void fence_proxy_async_smem() {
