@@ -1,7 +1,10 @@
 // Activations of the biased projections and their derivatives (liger_layer.h).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "liger_layer.h"
@@ -33,6 +36,29 @@ __device__ __forceinline__ float act_value(int act, float p) {
     }
 }
 
+// The same for 32 values, the choice made once.
+template <bool FAST>
+__device__ __forceinline__ void act_values(int act, float (&v)[32]) {
+    auto each = [&](auto a) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = act_value<FAST>(decltype(a)::value, v[j]);
+    };
+    switch (act) {
+        case LIGER_ACT_RELU: each(std::integral_constant<int, LIGER_ACT_RELU>()); break;
+        case LIGER_ACT_GELU: each(std::integral_constant<int, LIGER_ACT_GELU>()); break;
+        case LIGER_ACT_GELU_TANH: each(std::integral_constant<int, LIGER_ACT_GELU_TANH>()); break;
+        case LIGER_ACT_SILU: each(std::integral_constant<int, LIGER_ACT_SILU>()); break;
+        default: break;
+    }
+}
+
+// What the backward's slope is formed from (kept by the forward): half precision beside bf16 tensors, fp32 beside fp32.
+__device__ __forceinline__ void keep_pre(float* p, float v) { *p = v; }
+// half precision holds up to 65504: larger values (where every activation's slope has its limit) as that; NaN stays
+__device__ __forceinline__ void keep_pre(__half* p, float v) {
+    *p = __float2half_rn(v > 65504.f ? 65504.f : v < -65504.f ? -65504.f : v);
+}
+
 // d act / dp
 template <bool FAST>
 __device__ __forceinline__ float act_slope(int act, float p) {
@@ -51,6 +77,22 @@ __device__ __forceinline__ float act_slope(int act, float p) {
             return s * fmaf(p, 1.f - s, 1.f);
         }
         default: return 1.f;
+    }
+}
+
+// f[j] *= d act / dp (v[j]), the choice made once.
+template <bool FAST, int N>
+__device__ __forceinline__ void mul_slopes(int act, const float (&v)[N], float (&f)[N]) {
+    auto each = [&](auto a) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] *= act_slope<FAST>(decltype(a)::value, v[j]);
+    };
+    switch (act) {
+        case LIGER_ACT_RELU: each(std::integral_constant<int, LIGER_ACT_RELU>()); break;
+        case LIGER_ACT_GELU: each(std::integral_constant<int, LIGER_ACT_GELU>()); break;
+        case LIGER_ACT_GELU_TANH: each(std::integral_constant<int, LIGER_ACT_GELU_TANH>()); break;
+        case LIGER_ACT_SILU: each(std::integral_constant<int, LIGER_ACT_SILU>()); break;
+        default: break;
     }
 }
 

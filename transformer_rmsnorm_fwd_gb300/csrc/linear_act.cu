@@ -2,14 +2,70 @@
 // backward (formulas in liger_layer.h).
 #include "activation.cuh"
 #include "linear_fma.cuh"
+#include "linear_small.cuh"
 
 namespace liger {
 namespace {
 
 constexpr int kSumRows = 64;    // fewest rows per partial row of db
 constexpr int kMaxSums = 256;   // most partial rows of db
+constexpr int64_t kSmallTokens = 128;
 
 int64_t rows_per_sum(int64_t T) { return std::max<int64_t>(kSumRows, ceil_div(T, kMaxSums)); }
+
+// The same for bf16 in whole 16-byte vectors: a block takes 256 columns and a run of rows, 32 threads of 8
+// columns a row, 8 rows side by side.
+__global__ void __launch_bounds__(256) linear_dp_vec(const __nv_bfloat16* dy, const __half* pre, __nv_bfloat16* dp, float* part,
+                                                     int64_t rows, int cols, int64_t run, int act) {
+    __shared__ float red[8][256 + 4];
+    wait_for_stream();
+    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * 8;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * run, r1 = min(rows, r0 + run);
+    float s[8] = {};
+    if (col < cols) {
+        constexpr int U = 4;   // rows in flight
+        for (int64_t r = r0 + sl; r < r1; r += 8 * U) {
+            uint4 d[U], h[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (r + 8 * i < r1) {
+                    d[i] = ldg16_cs(dy + (r + 8 * i) * cols + col);
+                    if (dp != nullptr) h[i] = ldg16_cs(pre + (r + 8 * i) * cols + col);
+                }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (r + 8 * i < r1) {
+                    float f[8];
+                    unpack(d[i], f);
+                    if (dp != nullptr) {
+                        const __half2* q = reinterpret_cast<const __half2*>(&h[i]);
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 w = __half22float2(q[e]);
+                            v[2 * e] = w.x;
+                            v[2 * e + 1] = w.y;
+                        }
+                        mul_slopes<true>(act, v, f);
+                        stg16(dp + (r + 8 * i) * cols + col, pack(f));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] += f[e];
+                }
+        }
+    }
+    if (part == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[sl][lane + 32 * e] = s[e];
+    __syncthreads();
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (c >= cols) return;
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += red[i][(threadIdx.x >> 3) + 32 * (threadIdx.x & 7)];
+    part[static_cast<int64_t>(blockIdx.y) * cols + c] = t;
+}
 
 // dP = dY act'(P) and the partial sums of db: a block takes 32 columns and a run of rows, 8 threads a column.
 // TP: type dP is kept in; dp NULL: not kept (dP is dY).
@@ -115,24 +171,160 @@ struct LinearBwd {
     cudaStream_t st;
 };
 
+// ------------------------------------------------------------- tensor cores
+int64_t pair_tiles(int64_t M, int64_t N) {
+    return ceil_div(M, static_cast<int64_t>(tc::TileCfg<1>::TM)) * ceil_div(N, static_cast<int64_t>(tc::BN));
+}
+// Whether T tokens by F features go in 128-feature tiles (linear_small.cuh) and not in 256 x 256 tiles of CTA pairs.
+bool goes_small(int64_t T, int64_t F) { return T <= kSmallTokens || 2 * pair_tiles(T, F) <= sm_count() / 2; }
+int small_tokens(int64_t T) { return T <= 256 ? 256 : 128; }
+
+int fwd_tc(const void* X, const void* W, const void* bias, const void* residual, void* Y, void* pre, int64_t T, int64_t H,
+           int64_t N, int act, cudaStream_t st) {
+    using namespace tc;
+    int* err = nullptr;
+    int rc;
+    if ((rc = lsw_err_word(&err))) return rc;
+    if (goes_small(T, N)) {
+        SmallParams p{};
+        p.F = static_cast<int>(N);
+        p.T = static_cast<int>(T);
+        p.K = static_cast<int>(H);
+        p.bias = static_cast<const __nv_bfloat16*>(bias);
+        p.residual = static_cast<const __nv_bfloat16*>(residual);
+        p.out = static_cast<__nv_bfloat16*>(Y);
+        p.pre = static_cast<__half*>(pre);
+        p.act = act;
+        p.err = err;
+        return launch_small<0>("linear_act_fwd", W, X, p, small_tokens(T), st);
+    }
+    CUtensorMap mX, mW;
+    if ((rc = make_map(&mX, X, H, T, H, BK, BM))) return rc;
+    if ((rc = make_map(&mW, W, H, N, H, BK, B_BOX_ROWS))) return rc;
+    EpiParams e{};
+    e.err = err;
+    e.M = static_cast<int>(T);
+    e.N = static_cast<int>(N);
+    e.out = static_cast<__nv_bfloat16*>(Y);
+    e.ldo = N;
+    e.src = static_cast<const __nv_bfloat16*>(residual);
+    e.bias16 = static_cast<const __nv_bfloat16*>(bias);
+    e.pre16 = static_cast<__half*>(pre);
+    e.act = act;
+    e.hint_a = HINT_EVICT_LAST;    // X: reused by every column tile
+    e.hint_b = HINT_EVICT_FIRST;   // W: streamed once per group of rows
+    e.m_group = static_cast<int>(ceil_div(rows_in_l2(H, T), static_cast<int64_t>(TileCfg<1>::TM)));
+    e.early = 1;
+    return launch_gemm<0, 0, EPI_LINEAR, 1>(mX, mW, e.M, e.N, static_cast<int>(H), e, st);
+}
+
+// dX = dP W and dW = dP^T X from dP [T, N] bf16.  The last, partly filled round of dW's tiles is split along
+// the tokens, its fp32 sums standing in dX's memory, which is formed after it.
+int grads_tc(const LinearBwd& a, const void* dP) {
+    using namespace tc;
+    const int T = static_cast<int>(a.T), H = static_cast<int>(a.H), N = static_cast<int>(a.N);
+    int* err = nullptr;
+    int rc;
+    if ((rc = lsw_err_word(&err))) return rc;
+    if (a.dW != nullptr) {
+        CUtensorMap mP, mX;
+        if ((rc = make_map(&mP, dP, N, T, N, MN_BOX, BK))) return rc;
+        if ((rc = make_map(&mX, a.X, H, T, H, MN_BOX, BK))) return rc;
+        EpiParams w{};
+        w.err = err;
+        w.M = N;
+        w.N = H;
+        w.out = static_cast<__nv_bfloat16*>(a.dW);
+        w.ldo = H;
+        w.out_write = 1;
+        // n fastest touches all of X in every round: fine while X stays in L2 (up to 32 MiB), above that groups
+        // of 8 column blocks of it do
+        w.raster = a.T * a.H * 2 > (int64_t{32} << 20) ? RASTER_N_GROUPS : RASTER_N_FASTEST;
+        w.hint_a = HINT_EVICT_FIRST;
+        w.hint_b = HINT_EVICT_LAST;   // X: reused by every row block
+        w.early = 1;
+        const int64_t tiles = pair_tiles(N, H), pairs = sm_count() / 2, rem = tiles % pairs;
+        const int64_t tile_bytes = int64_t{TileCfg<1>::TM} * BN * 4;
+        const int64_t splits = a.dX == nullptr || rem == 0 ? 0
+                               : std::min<int64_t>({pairs / rem, a.T / (16 * BK), a.T * a.H * 2 / (rem * tile_bytes)});
+        if (splits < 2) {
+            if ((rc = launch_gemm<1, 1, EPI_ACCUM, 1>(mP, mX, N, H, T, w, a.st))) return rc;
+        } else {
+            w.full_tiles = static_cast<int>(tiles - rem);
+            w.ksplits = static_cast<int>(splits);
+            w.kpart_rows = TileCfg<1>::TM;
+            w.kpart = static_cast<float*>(a.dX);
+            if ((rc = launch_gemm<1, 1, EPI_ACCUM, 1, MODE_SPLIT>(mP, mX, N, H, T, w, a.st))) return rc;
+            SplitJoin j{};
+            j.part = w.kpart;
+            j.rem = static_cast<int>(rem);
+            j.splits = w.ksplits;
+            j.slabs = 1;
+            j.full = w.full_tiles;
+            j.part_rows = w.kpart_rows;
+            j.num_m = static_cast<int>(ceil_div(a.N, static_cast<int64_t>(TileCfg<1>::TM)));
+            j.num_n = static_cast<int>(ceil_div(a.H, static_cast<int64_t>(BN)));
+            j.out = w.out;
+            j.M = N;
+            j.N = H;
+            j.n_fastest = w.raster == RASTER_N_FASTEST ? 1 : 0;
+            if ((rc = launch_early("linear_act_bwd dW", split_join,
+                                   dim3(static_cast<unsigned>(rem), static_cast<unsigned>(j.part_rows / 8)), 256, 0, a.st, j)))
+                return rc;
+        }
+    }
+    if (a.dX == nullptr) return LIGER_OK;
+    if (goes_small(a.T, a.H)) {
+        SmallParams p{};
+        p.F = H;
+        p.T = T;
+        p.K = N;
+        p.out = static_cast<__nv_bfloat16*>(a.dX);
+        p.err = err;
+        return launch_small<1>("linear_act_bwd dX", a.W, dP, p, small_tokens(a.T), a.st);
+    }
+    CUtensorMap mP, mW;
+    if ((rc = make_map(&mP, dP, N, T, N, BK, BM))) return rc;
+    if ((rc = make_map(&mW, a.W, H, N, H, MN_BOX, BK))) return rc;
+    EpiParams d{};
+    d.err = err;
+    d.M = T;
+    d.N = H;
+    d.out = static_cast<__nv_bfloat16*>(a.dX);
+    d.ldo = H;
+    d.raster = RASTER_N_GROUPS;
+    d.early = 1;
+    return launch_gemm<0, 1, EPI_STORE, 1>(mP, mW, T, H, N, d, a.st);
+}
+
 template <typename T, typename TPRE, typename TP>
 int bwd_typed(const LinearBwd& a) {
     const bool keep = a.act != LIGER_ACT_NONE;
+    constexpr bool TC = sizeof(T) == 2 && sizeof(TP) == 2;   // bf16 in whole vectors, for the tensor cores
     if (keep || a.db != nullptr) {
         const int64_t run = rows_per_sum(a.T);
-        const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 32)), static_cast<unsigned>(ceil_div(a.T, run)));
-        if (int rc = launch_early("linear_act_bwd dP", linear_dp<T, TPRE, TP>, grid, 256, 0, a.st, static_cast<const T*>(a.dY),
-                                  static_cast<const TPRE*>(a.pre), static_cast<TP*>(keep ? a.dP : nullptr),
-                                  a.db != nullptr ? a.part : nullptr, a.T, static_cast<int>(a.N), run, a.act))
-            return rc;
+        const dim3 grid(static_cast<unsigned>(ceil_div(a.N, TC ? 256 : 32)), static_cast<unsigned>(ceil_div(a.T, run)));
+        float* part = a.db != nullptr ? a.part : nullptr;
+        const T* dy = static_cast<const T*>(a.dY);
+        const TPRE* pre = static_cast<const TPRE*>(a.pre);
+        TP* dp = static_cast<TP*>(keep ? a.dP : nullptr);
+        int rc;
+        if constexpr (TC)
+            rc = launch_early("linear_act_bwd dP", linear_dp_vec, grid, 256, 0, a.st, dy, pre, dp, part, a.T,
+                              static_cast<int>(a.N), run, a.act);
+        else
+            rc = launch_early("linear_act_bwd dP", linear_dp<T, TPRE, TP>, grid, 256, 0, a.st, dy, pre, dp, part, a.T,
+                              static_cast<int>(a.N), run, a.act);
+        if (rc) return rc;
         if (a.db != nullptr)
             if (int rc = launch_early("linear_act_bwd db", linear_db<T>, dim3(static_cast<unsigned>(ceil_div(a.N, 256))), 256, 0,
                                       a.st, static_cast<const float*>(a.part), static_cast<T*>(a.db), static_cast<int>(grid.y),
                                       static_cast<int>(a.N)))
                 return rc;
     }
-    if (keep) return grads_fma<T, TP>(static_cast<const TP*>(a.dP), a.X, a.W, a.dX, a.dW, a.T, a.H, a.N, a.st);
-    return grads_fma<T, T>(static_cast<const T*>(a.dY), a.X, a.W, a.dX, a.dW, a.T, a.H, a.N, a.st);
+    if constexpr (TC) return grads_tc(a, keep ? a.dP : a.dY);
+    else if (keep) return grads_fma<T, TP>(static_cast<const TP*>(a.dP), a.X, a.W, a.dX, a.dW, a.T, a.H, a.N, a.st);
+    else return grads_fma<T, T>(static_cast<const T*>(a.dY), a.X, a.W, a.dX, a.dW, a.T, a.H, a.N, a.st);
 }
 
 }  // namespace
@@ -154,6 +346,7 @@ extern "C" int liger_linear_act_fwd(const void* X, const void* W, const void* bi
                                static_cast<float*>(pre), act};
         return fwd_fma(X, W, e, T, H, N, st);
     }
+    if (on_tensor_cores(H, N, dtype)) return fwd_tc(X, W, bias, residual, Y, pre, T, H, N, act, st);
     using Bf = __nv_bfloat16;
     FmaEpi<Bf, __half> e{static_cast<const Bf*>(bias), static_cast<const Bf*>(residual), static_cast<Bf*>(Y),
                          static_cast<__half*>(pre), act};

@@ -2,8 +2,6 @@
 // C[m, n] = sum_k A(m, k) B(k, n), any strides, then the projection's epilogue.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include "activation.cuh"
 #include "common.cuh"
 
@@ -26,12 +24,6 @@ struct FmaEpi {
     TPRE* pre;
     int act;
 };
-
-__device__ __forceinline__ void keep_pre(float* p, float v) { *p = v; }
-// half precision holds up to 65504: larger values (where every activation's slope has its limit) as that; NaN stays
-__device__ __forceinline__ void keep_pre(__half* p, float v) {
-    *p = __float2half_rn(v > 65504.f ? 65504.f : v < -65504.f ? -65504.f : v);
-}
 
 template <typename TA, typename TB, typename TO, typename TPRE>
 __global__ void __launch_bounds__(256) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {

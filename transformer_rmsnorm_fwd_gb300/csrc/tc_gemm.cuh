@@ -39,6 +39,7 @@
 
 #include <atomic>
 
+#include "activation.cuh"
 #include "ckpt8.cuh"
 #include "common.cuh"
 #include "mbarrier.cuh"
@@ -83,7 +84,8 @@ enum Epi : int {
     EPI_SWIGLU_BWD = 4,
     EPI_QKV_ROPE = 5,
     EPI_SOFTMAX = 6,
-    EPI_SWIGLU_CKPT8 = 7
+    EPI_SWIGLU_CKPT8 = 7,
+    EPI_LINEAR = 8
 };
 
 // Tile order of the persistent loop: m fastest, n fastest, or groups of
@@ -187,6 +189,11 @@ struct EpiParams {
     int8_t *g8, *u8;
     uint8_t *g8s, *u8s;
     int64_t ldq;
+    // EPI_LINEAR: p = acc + bias16[col] (NULL: 0), kept in pre16 (IEEE half, NULL: not kept), then
+    // out = act(p) + src[row, col] (NULL: 0; src may be out); ldo for all three
+    const __nv_bfloat16* bias16;
+    __half* pre16;
+    int act;
     int m_group;   // row blocks that one sweep over all columns takes (they stay in L2)
     int early;     // set up while the kernel before still runs (barriers, TMEM), as launch_early; CTA pairs only
 };
@@ -578,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mi = w / width;
                 ni = full * GROUP_N + (w - mi * width);
             }
-        } else if (EPI == EPI_SWIGLU_CKPT8) {
+        } else if (EPI == EPI_SWIGLU_CKPT8 || EPI == EPI_LINEAR) {
             // m fastest within groups of m_group row blocks, one group after the other
             const int g = t / (ep.m_group * num_n), w = t - g * ep.m_group * num_n;
             const int gm = min(ep.m_group, num_m - g * ep.m_group);
@@ -890,6 +897,77 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     store_block<4, true>(sbuf, lane, oblk + c * 64, ep.ldo * 2, rows,
                                          chunks_below(n0 + c * 32, ep.N, 8, 4));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) release_acc(as);
+            } else if (EPI == EPI_LINEAR) {
+                const int64_t o0 = static_cast<int64_t>(row - lane) * ep.ldo + n0;
+                // staging: out at +0, the kept sums at +2 KB, the residual block at +4 KB
+                const uint32_t s_out = sbuf, s_pre = sbuf + 2048u, s_res = sbuf + 4096u;
+                // the next 32 TMEM columns load while the current ones are used
+                uint32_t ra[32], rb[32];
+                auto linear_chunk = [&](int c, uint32_t(&cur)[32], uint32_t(&nxt)[32]) {
+                    if (c + 1 < BN / 32) tmem_ld32_issue(taddr + (c + 1) * 32, nxt);
+                    const int left = ep.N - (n0 + c * 32);   // a multiple of 8
+                    if (left > 0) {
+                        const int nch = chunks_below(n0 + c * 32, ep.N, 8, 4);
+                        uint4 res[4];
+                        if (ep.src != nullptr)
+                            load_block<4, false>(lane, reinterpret_cast<const uint8_t*>(ep.src + o0 + c * 32), ep.ldo * 2, rows,
+                                                 nch, res);
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(cur[j]);
+                        if (ep.bias16 != nullptr) {
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                if (g * 8 < left) {
+                                    float f[8];
+                                    unpack(ldg16(ep.bias16 + n0 + c * 32 + g * 8), f);
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) v[g * 8 + e] += f[e];
+                                }
+                        }
+                        __syncwarp();   // the previous block's row runs have been read
+                        if (ep.src != nullptr) stage_block<4>(s_res, lane, res);
+                        if (ep.pre16 != nullptr) {
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                __half h[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) keep_pre(h + e, v[g * 8 + e]);
+                                sts16(s_pre + stage_slot<4>(lane, g), *reinterpret_cast<const uint4*>(h));
+                            }
+                        }
+                        act_values<true>(ep.act, v);
+                        if (ep.src != nullptr) {
+                            __syncwarp();
+                            unstage_row<4>(s_res, lane, res);   // now this lane's row
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                float f[8];
+                                unpack(res[g], f);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) v[g * 8 + e] += f[e];
+                            }
+                        }
+                        const uint4 u[4] = {pack_bf8(v), pack_bf8(v + 8), pack_bf8(v + 16), pack_bf8(v + 24)};
+                        stage_row<4>(s_out, lane, u);
+                        __syncwarp();
+                        store_block<4, false>(s_out, lane, reinterpret_cast<uint8_t*>(ep.out + o0 + c * 32), ep.ldo * 2, rows, nch);
+                        if (ep.pre16 != nullptr)
+                            store_block<4, true>(s_pre, lane, reinterpret_cast<uint8_t*>(ep.pre16 + o0 + c * 32), ep.ldo * 2, rows,
+                                                 nch);
+                    }
+                    if (c + 1 < BN / 32) tmem_ld_wait(nxt);
+                };
+                tmem_ld32_issue(taddr, ra);
+                tmem_ld_wait(ra);
+#pragma unroll 1
+                for (int c = 0; c < BN / 32; c += 2) {
+                    linear_chunk(c, ra, rb);
+                    linear_chunk(c + 1, rb, ra);
                 }
                 tc_fence_before();
                 __syncwarp();
