@@ -4,13 +4,14 @@
 
 #include "common.cuh"
 #include "liger_layer.h"
+#include "mbarrier.cuh"
 
 namespace liger {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kLowest = -3.402823466e38f;
-constexpr int kThreads = 256;
+constexpr int kRowThreads = 256;
 
 struct LogpFwd {
     const void* z;
@@ -34,98 +35,397 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// ---- a cluster of blocks on one row
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the same shared object in block `rank` of the cluster
+__device__ __forceinline__ uint32_t peer(const void* p, int rank) {
+    uint32_t o;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(o) : "r"(smem_u32(p)), "r"(rank) : "memory");
+    return o;
+}
+__device__ __forceinline__ float peer_float(const float* p, int rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long peer_key(const unsigned long long* p, int rank) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
+    return v;
+}
+
 // A number whose unsigned order is that of the floats: -0 as +0, NaN above all.
 __device__ __forceinline__ uint32_t order_of(float v) {
     if (v != v) return 0xFFFFFFFFu;
     const uint32_t b = __float_as_uint(v + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+// The float of an order (+0 for either zero, a NaN for all of them)
+__device__ __forceinline__ float value_of(uint32_t o) {
+    if (o == 0xFFFFFFFFu) return NAN;
+    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
 // ... and with the index behind it, the lowest first
 __device__ __forceinline__ unsigned long long rank_key(float v, uint32_t index) {
     return static_cast<unsigned long long>(order_of(v)) << 32 | (0xFFFFFFFFu - index);
 }
 
-// Sums over the block, in every thread; sh holds a float per warp.
-__device__ __forceinline__ float block_max_nan(float v, float* sh) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = sh[0];
-    for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i) t = max_nan(t, sh[i]);
-    return t;
-}
-__device__ __forceinline__ float block_add(float v, float* sh) {
-    v = warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.f;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) t += sh[i];
-    return t;
-}
-
+// ------------------------------------------------------------------ forward
 // With d = (z - m) / (temperature ln 2), m the largest logit, s = sum 2^d and u = sum d 2^d:
 //     log_sum = ln 2 log2 s,  logp = (z_y - m) / temperature - log_sum,  entropy = ln 2 (log2 s - u / s)
 // z - m is formed first: logits of the type's lowest value, or all far from 0, lose nothing.
-// A logit of -inf has d below any limit: held at -200, where 2^d is 0, so that d 2^d is not NaN.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logp_rows(LogpFwd p) {
-    __shared__ float sh[8];
-    __shared__ unsigned long long shk[8];
-    wait_for_stream();
-    const int64_t t = blockIdx.x;
-    const T* z = static_cast<const T*>(p.z) + t * p.ld;
-    const float c = p.inv_temp * kLog2e;
-    float m = -INFINITY;
-    for (int64_t v = threadIdx.x; v < p.V; v += kThreads) m = max_nan(m, ldf(z + v));
-    m = block_max_nan(m, sh);
-    const bool none = m == -INFINITY;
-    const float mf = m != m ? m : fmaxf(m, kLowest);
-    float s = 0.f, u = 0.f;
-    for (int64_t v = threadIdx.x; v < p.V; v += kThreads) {
-        const float d = max_nan((ldf(z + v) - mf) * c, -200.f);
-        const float e = ex2(d);
-        s += e;
-        u = fmaf(d, e, u);
-    }
-    s = block_add(s, sh);
-    u = block_add(u, sh);
-    const float ls = log2f(s);
-    if (threadIdx.x == 0) {
-        if (p.row_max != nullptr) p.row_max[t] = m;
-        if (p.log_sum != nullptr) p.log_sum[t] = none ? -INFINITY : ls * kLn2;
-        if (p.entropy != nullptr) p.entropy[t] = none ? 0.f : (ls - u / s) * kLn2;
-        if (p.logp != nullptr) {
-            const int64_t y = p.tokens[t];
-            float r = 0.f;
-            if (y != p.ignore) {
-                if (y < 0 || y >= p.V) r = NAN;
-                else r = none ? -INFINITY : fmaf(ldf(z + y) - mf, p.inv_temp, -ls * kLn2);
-            }
-            p.logp[t] = r;
-        }
-    }
-    unsigned long long last = ~0ull;
-    for (int i = 0; i < p.k; ++i) {
-        unsigned long long best = 0;
-        for (int64_t v = threadIdx.x; v < p.V; v += kThreads) {
-            const unsigned long long key = rank_key(ldf(z + v), static_cast<uint32_t>(v));
-            if (key < last && key > best) best = key;
-        }
+//
+// One pass over the row's 16-byte vectors: a thread keeps a running maximum with s and u relative to it (they
+// are rescaled when it grows, which is rare after the first vectors), and the largest logit it has seen with that
+// vector's index.  The block (a cluster of blocks where there are few rows, each with its share of the row)
+// joins the sums.
+// Alternatives: threads are taken together in kGroups groups; the k-th largest of the groups' best logits is a
+// lower bound on the row's k-th largest, since k groups have one that large, and with random logits hardly more than k
+// logits reach it.  So only threads whose best reaches the bound look at their vectors again (from L2), 32
+// vectors at a time by their whole warp, and put what reaches it on a list, which is then ranked.  Equal logits
+// go by index throughout, so a constant row leaves a short list too.  A list that overflows (largest logits
+// crowded in one group's vectors) is given up, and the k largest are found one after the other.
+
+// Largest 64-bit key or float (NaN above all) over the block, in every thread.
+template <int NT>
+__device__ __forceinline__ unsigned long long block_max_key(unsigned long long v, unsigned long long* sh) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) shk[threadIdx.x >> 5] = best;
-        __syncthreads();
-        for (int w = 0; w < 8; ++w) best = max(best, shk[w]);
-        last = best;
-        if (threadIdx.x == 0) {
-            const uint32_t v = 0xFFFFFFFFu - static_cast<uint32_t>(best);
-            p.top_ids[t * p.k + i] = v;
-            p.top_logp[t * p.k + i] = none ? -INFINITY : fmaf(ldf(z + v) - mf, p.inv_temp, -ls * kLn2);
+    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();   // the previous one has been read
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) v = max(v, sh[w]);
+    return v;
+}
+
+// Running maximum with the sums relative to it.
+struct Sums {
+    float m, s, u;
+};
+// The sums of `a` relative to a larger maximum m (c: log2 e / temperature).  The difference is held at -1e4,
+// where the factor is 0, so that 0 times it is not NaN.
+__device__ __forceinline__ void raise(Sums& a, float m, float c) {
+    const float d = max_nan((a.m - m) * c, -1e4f), f = ex2(d);
+    a.u = fmaf(a.s, d, a.u) * f;
+    a.s *= f;
+    a.m = m;
+}
+__device__ __forceinline__ void join(Sums& a, Sums b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    raise(a, m, c);
+    raise(b, m, c);
+    a.s += b.s;
+    a.u += b.u;
+}
+
+constexpr int kGroups = 64;         // groups of threads
+constexpr int kList = 2048;         // candidates of a block
+constexpr int kSecond = LIGER_TOP_MAX * kList / kGroups;   // ... that reach the second bound: k groups' shares at most
+constexpr int kUnroll = 4;          // vectors of a thread in flight
+constexpr int kShortRow = 256;      // rows of at most this many vectors: 64 threads
+
+// a row's vectors: vector v holds elements v EPV - shift + (0 .. EPV - 1); those in [first, last) are whole
+template <typename T>
+struct RowVecs {
+    const T* base;       // element 0 of vector 0 (aligned; up to EPV - 1 elements before the row)
+    int shift;
+    int64_t n, first, last, V;
+    __device__ RowVecs(const T* z, int64_t vocab) {
+        constexpr int EPV = Vec<T>::N;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(z);
+        shift = static_cast<int>((at & 15) / sizeof(T));
+        base = z - shift;
+        V = vocab;
+        n = (V + shift + EPV - 1) / EPV;
+        first = shift > 0 ? 1 : 0;
+        last = (V + shift) / EPV;
+    }
+    // the elements of vector v, -inf where it reaches past the row (nothing outside the row is read)
+    __device__ __forceinline__ void get(int64_t v, float (&f)[Vec<T>::N]) const {
+        constexpr int EPV = Vec<T>::N;
+        if (v >= first && v < last) {
+            unpack(ldg16(base + v * EPV), f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                const int64_t i = v * EPV + e - shift;
+                f[e] = i >= 0 && i < V ? ldf(base + v * EPV + e) : -INFINITY;
+            }
         }
+    }
+};
+
+// Finds the `k` largest of n keys (all different, none 0) by counting and leaves them in order in out[0 .. k).
+template <int NT>
+__device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n, int k, unsigned long long* out) {
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const unsigned long long x = keys[i];
+        int above = 0;
+        for (int j = 0; j < n; ++j) above += keys[j] > x ? 1 : 0;
+        if (above < k) out[above] = x;
+    }
+}
+
+struct RowShared {
+    unsigned long long best[LIGER_TOP_MAX];   // this block's k largest keys in order (0: no more)
+    unsigned long long groups[kGroups], red[kRowThreads / 32], bound;
+    Sums sums[kRowThreads / 32];
+    Sums total;
+    float row_max;
+    int count, count2;
+};
+
+template <typename T, int NT, bool ENT>
+__global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p) {
+    constexpr int EPV = Vec<T>::N, NP = EPV / 2;
+    __shared__ RowShared sh;
+    extern __shared__ __align__(16) unsigned long long list[];   // [kList + kSecond] with k > 0
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+    wait_for_stream();
+    const int64_t t = blockIdx.x / static_cast<unsigned>(ranks);
+    const T* z = static_cast<const T*>(p.z) + t * p.ld;
+    const RowVecs<T> row(z, p.V);
+    const int64_t v0 = row.n * rank / ranks, v1 = row.n * (rank + 1) / ranks;   // this block's vectors
+    const float c = p.inv_temp * kLog2e;
+    // the token's logit, asked for early
+    int64_t y = p.ignore;
+    float zy = 0.f;
+    if (rank == 0 && tid == 0 && p.tokens != nullptr) {
+        y = p.tokens[t];
+        if (y != p.ignore && y >= 0 && y < p.V) zy = ldf(z + y);
+    }
+    Sums a{kLowest, 0.f, 0.f};
+    float best = -INFINITY;   // the thread's largest logit (NaN above all), and its vector
+    int64_t best_v = -1;
+    const float2 c2 = make_float2(c, c);
+    auto take = [&](const float (&f)[kUnroll][EPV], int64_t v, int count) {
+        float gm = kLowest;
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            if (q >= count) break;
+            float m = f[q][0];
+#pragma unroll
+            for (int e = 1; e < EPV; ++e) m = max_nan(m, f[q][e]);
+            if (m > best || best_v < 0 || (m != m && best == best)) {
+                best = m;
+                best_v = v + q * NT;
+            }
+            gm = fmaxf(gm, m);
+        }
+        if (gm > a.m) raise(a, gm, c);
+        const float2 nm = make_float2(-a.m, -a.m);
+        float2 s2 = make_float2(0.f, 0.f), u2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            if (q >= count) break;
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                float2 d = __fmul2_rn(__fadd2_rn(make_float2(f[q][2 * e], f[q][2 * e + 1]), nm), c2);
+                if (ENT) {   // a logit of -inf has d below any limit: held where 2^d is 0, so that d 2^d is not NaN
+                    d.x = max_nan(d.x, -200.f);
+                    d.y = max_nan(d.y, -200.f);
+                }
+                const float2 x = make_float2(ex2(d.x), ex2(d.y));
+                s2 = __fadd2_rn(s2, x);
+                if (ENT) u2 = __ffma2_rn(d, x, u2);
+            }
+        }
+        a.s += s2.x + s2.y;
+        if (ENT) a.u += u2.x + u2.y;
+    };
+    int64_t v = v0 + tid;
+    for (; v + (kUnroll - 1) * NT < v1; v += kUnroll * NT) {
+        float f[kUnroll][EPV];
+        if (v >= row.first && v + (kUnroll - 1) * NT < row.last) {
+            uint4 x[kUnroll];
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) x[q] = ldg16(row.base + (v + q * NT) * EPV);
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) unpack(x[q], f[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) row.get(v + q * NT, f[q]);
+        }
+        take(f, v, kUnroll);
+    }
+    if (v < v1) {
+        float f[kUnroll][EPV];
+        int count = 0;
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q)
+            if (v + q * NT < v1) {
+                row.get(v + q * NT, f[q]);
+                count = q + 1;
+            }
+        take(f, v, count);
+    }
+    // the block's sums
+    Sums w = a;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Sums b{__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o), __shfl_xor_sync(0xffffffffu, w.u, o)};
+        join(w, b, c);
+    }
+    if (lane == 0) sh.sums[warp] = w;
+    // its largest logit, and the groups' best, as keys: the order of the value, then the vector's index
+    const unsigned long long mine =
+        best_v < 0 ? 0 : static_cast<unsigned long long>(order_of(best)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(best_v));
+    const unsigned long long top = block_max_key<NT>(mine, sh.red);   // (with two barriers)
+    if (tid == 0) {
+        w = sh.sums[0];
+        for (int i = 1; i < NT / 32; ++i) join(w, sh.sums[i], c);
+        sh.total = w;
+        sh.row_max = value_of(static_cast<uint32_t>(top >> 32));
+        sh.count = sh.count2 = 0;
+    }
+    if (p.k > 0) {
+        constexpr int PER = NT / kGroups;   // neighbouring threads of a group
+        unsigned long long g = mine;
+#pragma unroll
+        for (int o = PER / 2; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if (tid % PER == 0) sh.groups[tid / PER] = g;
+        if (tid < LIGER_TOP_MAX) sh.best[tid] = 0;
+        if (tid == 0) sh.bound = 0;
+        __syncthreads();
+        if (tid < kGroups) {   // the k-th largest of the groups' (those without an element: 0, and not distinct)
+            const unsigned long long x = sh.groups[tid];
+            int above = 0;
+#pragma unroll 8
+            for (int i = 0; i < kGroups; ++i) above += sh.groups[i] > x ? 1 : 0;
+            if (x != 0 && above == p.k - 1) sh.bound = x;
+        }
+        __syncthreads();
+        const unsigned long long bound = sh.bound;
+        const uint32_t bound_o = static_cast<uint32_t>(bound >> 32), bound_v = 0xFFFFFFFFu - static_cast<uint32_t>(bound);
+        uint32_t hot = __ballot_sync(0xffffffffu, mine != 0 && mine >= bound);
+        while (hot != 0) {   // the vectors of one thread at a time, over the warp
+            const int64_t vt = v0 + warp * 32 + (__ffs(hot) - 1);
+            hot &= hot - 1;
+            for (int64_t x = vt + static_cast<int64_t>(lane) * NT; x < v1; x += 32 * NT) {
+                float f[EPV];
+                row.get(x, f);
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    const int64_t i = x * EPV + e - row.shift;
+                    const uint32_t o = order_of(f[e]);
+                    if (i >= 0 && i < p.V && (o > bound_o || (o == bound_o && (bound == 0 || static_cast<uint32_t>(x) <= bound_v)))) {
+                        const int at = atomicAdd(&sh.count, 1);   // in any order: the keys are ranked
+                        if (at < kList) list[at] = rank_key(f[e], static_cast<uint32_t>(i));
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const int n = sh.count;
+        if (n > kList) {
+            // given up: the largest below the last one found, k times
+            unsigned long long last = ~0ull;
+            for (int i = 0; i < p.k; ++i) {
+                unsigned long long b = 0;
+                for (int64_t x = v0 + tid; x < v1; x += NT) {
+                    float f[EPV];
+                    row.get(x, f);
+#pragma unroll
+                    for (int e = 0; e < EPV; ++e) {
+                        const int64_t j = x * EPV + e - row.shift;
+                        const unsigned long long key = rank_key(f[e], static_cast<uint32_t>(j));
+                        if (j >= 0 && j < p.V && key < last && key > b) b = key;
+                    }
+                }
+                last = block_max_key<NT>(b, sh.red);
+                if (tid == 0) sh.best[i] = last;
+                if (last == 0) break;   // a share of fewer than k elements
+            }
+        } else if (n <= 2 * kGroups) {
+            rank_keys<NT>(list, n, p.k, sh.best);
+        } else {
+            // the same bound again, over the list: the k-th largest of kGroups groups' best
+            if (tid < kGroups) {
+                unsigned long long g2 = 0;
+                for (int i = tid; i < n; i += kGroups) g2 = max(g2, list[i]);
+                sh.groups[tid] = g2;
+            }
+            __syncthreads();
+            if (tid < kGroups) {
+                const unsigned long long x = sh.groups[tid];
+                int above = 0;
+#pragma unroll 8
+                for (int i = 0; i < kGroups; ++i) above += sh.groups[i] > x ? 1 : 0;
+                if (above == p.k - 1) sh.bound = x;
+            }
+            __syncthreads();
+            const unsigned long long b2 = sh.bound;
+            for (int i = tid; i < n; i += NT)
+                if (list[i] >= b2) list[kList + atomicAdd(&sh.count2, 1)] = list[i];
+            __syncthreads();
+            rank_keys<NT>(list + kList, sh.count2, p.k, sh.best);
+        }
+    }
+    __syncthreads();
+    if (ranks > 1) cluster_sync();
+    if (rank == 0) {
+        // the blocks' sums in their order, and their alternatives ranked again
+        Sums all = sh.total;
+        float m = sh.row_max;
+        for (int r = 1; r < ranks; ++r) {
+            const Sums b{peer_float(&sh.total.m, r), peer_float(&sh.total.s, r), peer_float(&sh.total.u, r)};
+            join(all, b, c);
+            m = max_nan(m, peer_float(&sh.row_max, r));
+        }
+        const bool none = m == -INFINITY;
+        const float l2 = log2f(all.s), ls = l2 * kLn2;   // relative to all.m, which is m but for NaN (all.s is NaN then)
+        if (tid == 0) {
+            if (p.row_max != nullptr) p.row_max[t] = m;
+            if (p.log_sum != nullptr) p.log_sum[t] = none ? -INFINITY : ls;
+            if (p.entropy != nullptr) p.entropy[t] = none ? 0.f : (l2 - all.u / all.s) * kLn2;
+            if (p.logp != nullptr) {
+                float r = 0.f;
+                if (y != p.ignore) {
+                    if (y < 0 || y >= p.V) r = NAN;
+                    else r = none ? -INFINITY : fmaf(zy - all.m, p.inv_temp, -ls);
+                }
+                p.logp[t] = r;
+            }
+        }
+        if (p.k > 0) {
+            const unsigned long long* keys = sh.best;
+            if (ranks > 1) {
+                for (int i = tid; i < ranks * p.k; i += NT) list[i] = peer_key(&sh.best[i % p.k], i / p.k);
+                __syncthreads();
+                unsigned long long* out = list + ranks * p.k;   // (0 marks a missing one: below all keys, of which there are k)
+                for (int i = tid; i < ranks * p.k; i += NT) {
+                    const unsigned long long x = list[i];
+                    int above = 0;
+                    for (int j = 0; j < ranks * p.k; ++j) above += list[j] > x ? 1 : 0;
+                    if (x != 0 && above < p.k) out[above] = x;
+                }
+                __syncthreads();
+                keys = out;
+            }
+            for (int i = tid; i < p.k; i += NT) {
+                const unsigned long long key = keys[i];
+                p.top_ids[t * p.k + i] = 0xFFFFFFFFu - static_cast<uint32_t>(key);
+                p.top_logp[t * p.k + i] = none ? -INFINITY : fmaf(value_of(static_cast<uint32_t>(key >> 32)) - all.m, p.inv_temp, -ls);
+            }
+        }
+    }
+    if (ranks > 1) {
+        __syncwarp();
+        cluster_sync();   // no block exits while another reads from it
     }
 }
 
@@ -140,9 +440,11 @@ struct LogpBwd {
     int64_t ldd;
 };
 
-// dz = (g 1[v = y] - p (g + h (a + H))) / temperature with a = log p, p = e^a
-template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logp_bwd_rows(LogpBwd p) {
+// dz = (g 1[v = y] - p (g + h (a + H))) / temperature with a = log p, p = e^a: every element read and written once.
+// A block takes a run of a row's vectors; VECS: logits and gradients have the same place within 16 bytes.
+template <typename T, bool VECS>
+__global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) {
+    constexpr int EPV = Vec<T>::N;
     wait_for_stream();
     const int64_t t = blockIdx.x;
     const T* z = static_cast<const T*>(p.z) + t * p.ld;
@@ -154,15 +456,89 @@ __global__ void __launch_bounds__(kThreads) token_logp_bwd_rows(LogpBwd p) {
     const float h = p.g_entropy != nullptr ? p.g_entropy[t] : 0.f, H = p.g_entropy != nullptr ? p.entropy[t] : 0.f;
     const float m = p.row_max[t], ls = p.log_sum[t];
     const bool zero = (g == 0.f && h == 0.f) || (m == -INFINITY && g == g && h == h);
-    for (int64_t v = threadIdx.x; v < p.V; v += kThreads) {
-        float d = 0.f;
-        if (!zero) {
-            const float a = max_nan(fmaf(ldf(z + v) - m, p.inv_temp, -ls), -1e4f);
-            const float pr = ex2(a * kLog2e);
-            d = (v == y ? g : 0.f) - pr * fmaf(h, a + H, g);
+    auto one = [&](float zv, int64_t i) {
+        const float a = max_nan(fmaf(zv - m, p.inv_temp, -ls), -1e4f);   // of -inf: held where e^a is 0
+        const float d = ex2(a * kLog2e) * fmaf(h, a + H, g);
+        return ((i == y ? g : 0.f) - d) * p.inv_temp;
+    };
+    if constexpr (!VECS) {
+        for (int64_t i = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; i < p.V; i += static_cast<int64_t>(gridDim.y) * kRowThreads)
+            stf(dz + i, zero ? 0.f : one(ldf(z + i), i));
+        return;
+    } else {
+        const RowVecs<T> row(z, p.V);
+        T* out = dz - row.shift;
+        const int64_t v0 = row.n * blockIdx.y / gridDim.y, v1 = row.n * (blockIdx.y + 1) / gridDim.y;
+        for (int64_t v = v0 + threadIdx.x; v < v1; v += kUnroll * kRowThreads) {
+            uint4 x[kUnroll];
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) {
+                const int64_t w = v + q * kRowThreads;
+                if (!zero && w < v1 && w >= row.first && w < row.last) x[q] = ldg16(row.base + w * EPV);
+            }
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) {
+                const int64_t w = v + q * kRowThreads, i0 = w * EPV - row.shift;
+                if (w >= v1) break;
+                if (w >= row.first && w < row.last) {
+                    float f[EPV] = {};
+                    if (!zero) {
+                        unpack(x[q], f);
+#pragma unroll
+                        for (int e = 0; e < EPV; ++e) f[e] = one(f[e], i0 + e);
+                    }
+                    stg16_cs(out + w * EPV, pack(f));
+                } else {
+                    for (int e = 0; e < EPV; ++e)
+                        if (i0 + e >= 0 && i0 + e < p.V) stf(dz + i0 + e, zero ? 0.f : one(ldf(z + i0 + e), i0 + e));
+                }
+            }
         }
-        stf(dz + v, d * p.inv_temp);
     }
+}
+
+// ------------------------------------------------------------------ launches
+template <typename T, int NT, bool ENT>
+int launch_row(const char* who, const LogpFwd& p, int ranks, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.T * ranks));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = p.k > 0 ? (kList + kSecond) * sizeof(unsigned long long) : 0;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, token_logp_row<T, NT, ENT>, p);
+    return check_launch(who);
+}
+
+template <typename T>
+int launch_fwd(const char* who, const LogpFwd& p, cudaStream_t st) {
+    const int64_t vecs = ceil_div(p.V, Vec<T>::N);
+    const bool ent = p.entropy != nullptr;
+    // few rows: each over a cluster of blocks, while a thread still gets two vectors
+    int ranks = 1;
+    while (ranks < 8 && p.T * ranks * 2 <= 2 * sm_count() && vecs >= 4 * ranks * kRowThreads) ranks *= 2;
+    if (vecs <= kShortRow)
+        return ent ? launch_row<T, 64, true>(who, p, 1, st) : launch_row<T, 64, false>(who, p, 1, st);
+    return ent ? launch_row<T, kRowThreads, true>(who, p, ranks, st) : launch_row<T, kRowThreads, false>(who, p, ranks, st);
+}
+
+template <typename T>
+int launch_bwd(const char* who, const LogpBwd& p, cudaStream_t st) {
+    const int64_t vecs = ceil_div(p.V, Vec<T>::N);
+    const uintptr_t az = reinterpret_cast<uintptr_t>(p.z), ad = reinterpret_cast<uintptr_t>(p.dz);
+    const bool same = (az - ad) % 16 == 0 && (p.T == 1 || (p.ld - p.ldd) * static_cast<int64_t>(sizeof(T)) % 16 == 0);
+    const int64_t y = std::max<int64_t>(1, std::min<int64_t>(65535, vecs / (2 * kUnroll * kRowThreads)));
+    const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>(y));
+    return same ? launch_early(who, token_logp_grad<T, true>, grid, kRowThreads, 0, st, p)
+                : launch_early(who, token_logp_grad<T, false>, grid, kRowThreads, 0, st, p);
 }
 
 int check_logits(const char* who, int64_t T, int64_t V, int64_t ld, float temperature, int dtype) {
@@ -198,10 +574,8 @@ extern "C" int liger_token_logp_fwd(const void* logits, int64_t ld, const int64_
         return fail(LIGER_ERR_ALIGN, "%s: tensors must be aligned to their elements", who);
     const LogpFwd p{logits, ld, tokens, T, V, ignore_index, 1.0f / temperature, logp, row_max, log_sum, entropy, top_logp, top_ids,
                     static_cast<int>(k)};
-    const dim3 grid(static_cast<unsigned>(T));
     cudaStream_t st = as_stream(stream);
-    return dtype == LIGER_F32 ? launch_early(who, token_logp_rows<float>, grid, kThreads, 0, st, p)
-                              : launch_early(who, token_logp_rows<__nv_bfloat16>, grid, kThreads, 0, st, p);
+    return dtype == LIGER_F32 ? launch_fwd<float>(who, p, st) : launch_fwd<__nv_bfloat16>(who, p, st);
 }
 
 extern "C" int liger_token_logp_bwd(const void* logits, int64_t ld, const int64_t* tokens, const float* row_max,
@@ -225,8 +599,6 @@ extern "C" int liger_token_logp_bwd(const void* logits, int64_t ld, const int64_
         return fail(LIGER_ERR_ALIGN, "%s: tensors must be aligned to their elements", who);
     const LogpBwd p{logits, ld, g_logp ? tokens : nullptr, row_max, log_sum, entropy, g_logp, g_entropy, T, V, ignore_index,
                     1.0f / temperature, dlogits, ldd};
-    const dim3 grid(static_cast<unsigned>(T));
     cudaStream_t st = as_stream(stream);
-    return dtype == LIGER_F32 ? launch_early(who, token_logp_bwd_rows<float>, grid, kThreads, 0, st, p)
-                              : launch_early(who, token_logp_bwd_rows<__nv_bfloat16>, grid, kThreads, 0, st, p);
+    return dtype == LIGER_F32 ? launch_bwd<float>(who, p, st) : launch_bwd<__nv_bfloat16>(who, p, st);
 }
