@@ -82,7 +82,8 @@ int liger_linear_act_fwd(const void* X, const void* W, const void* bias, const v
                          int64_t T, int64_t H, int64_t N, int act, int dtype, void* stream);
 
 /* Bytes of workspace liger_linear_act_bwd needs: dP where there is an
- * activation, and fp32 partial sums of db; 0 for arguments out of range. */
+ * activation, and fp32 partial sums of db of many tokens; 0 for arguments out of
+ * range. */
 size_t liger_linear_act_bwd_workspace(int64_t T, int64_t H, int64_t N, int act, int dtype);
 
 /* Backward, from dY [T, N] and pre as the forward kept it (not read, may be
@@ -92,9 +93,11 @@ size_t liger_linear_act_bwd_workspace(int64_t T, int64_t H, int64_t N, int act, 
  *   then W or X is not read).  relu'(0) = 0.  The gradient of the residual is dY.
  *   On the tensor cores dP is rounded to bf16 once, as an operand of both
  *   products (with act = 0 it is dY as it stands); db is summed in fp32 from
- *   the unrounded dP.  No output overlaps another tensor.
+ *   the unrounded dP.  No output overlaps another tensor; dX is written twice
+ *   (sums of dW may stand in it first).
  *   T = 0 writes zeros to dW and db.
- *   ws: at least liger_linear_act_bwd_workspace bytes, 256-byte aligned. */
+ *   ws: at least liger_linear_act_bwd_workspace bytes, 256-byte aligned (NULL
+ *   where that is 0). */
 int liger_linear_act_bwd(const void* dY, const void* X, const void* W, const void* pre, void* dX, void* dW, void* db,
                          void* ws, size_t ws_bytes, int64_t T, int64_t H, int64_t N, int act, int dtype, void* stream);
 

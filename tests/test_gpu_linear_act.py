@@ -245,7 +245,7 @@ def test_refusals(cuda_lib):
     with pytest.raises(L.LigerError):           # not 16-byte aligned
         L.liger_linear_act_fwd(buf[4:4 + 256].view(4, 64), W, Y)
     with pytest.raises(L.LigerError):           # no workspace, and no kept values
-        L.liger_linear_act_bwd(Y, X, W, X.clone(), None, None, None)
+        L.liger_linear_act_bwd(Y, X, W, X.clone(), None, None, None, pre=Y.half(), act="gelu")
     ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
     with pytest.raises(L.LigerError):
         L.liger_linear_act_bwd(Y, X, W, X.clone(), None, None, ws, act="gelu")

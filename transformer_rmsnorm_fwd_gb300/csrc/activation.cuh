@@ -80,21 +80,5 @@ __device__ __forceinline__ float act_slope(int act, float p) {
     }
 }
 
-// f[j] *= d act / dp (v[j]), the choice made once.
-template <bool FAST, int N>
-__device__ __forceinline__ void mul_slopes(int act, const float (&v)[N], float (&f)[N]) {
-    auto each = [&](auto a) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) f[j] *= act_slope<FAST>(decltype(a)::value, v[j]);
-    };
-    switch (act) {
-        case LIGER_ACT_RELU: each(std::integral_constant<int, LIGER_ACT_RELU>()); break;
-        case LIGER_ACT_GELU: each(std::integral_constant<int, LIGER_ACT_GELU>()); break;
-        case LIGER_ACT_GELU_TANH: each(std::integral_constant<int, LIGER_ACT_GELU_TANH>()); break;
-        case LIGER_ACT_SILU: each(std::integral_constant<int, LIGER_ACT_SILU>()); break;
-        default: break;
-    }
-}
-
 }  // namespace
 }  // namespace liger

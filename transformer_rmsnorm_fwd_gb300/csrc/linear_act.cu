@@ -7,78 +7,56 @@
 namespace liger {
 namespace {
 
-constexpr int kSumRows = 64;    // fewest rows per partial row of db
-constexpr int kMaxSums = 256;   // most partial rows of db
 constexpr int64_t kSmallTokens = 128;
+constexpr unsigned kDpShares = 8;   // most blocks of a cluster that share the rows of a column sum
+constexpr int64_t kDpLong = 2048, kDpParts = 64;
+constexpr int kDpRows = 4;
 
-int64_t rows_per_sum(int64_t T) { return std::max<int64_t>(kSumRows, ceil_div(T, kMaxSums)); }
+// dP = dY act'(P) and db, in one pass: a block takes some columns and its share of the rows, the blocks of a
+// cluster all rows of the same columns.  The column sums go from threads to the block over shared memory, and
+// over the cluster in the order of its blocks: no partial rows in device memory, no second kernel.
 
-// The same for bf16 in whole 16-byte vectors: a block takes 256 columns and a run of rows, 32 threads of 8
-// columns a row, 8 rows side by side.
-__global__ void __launch_bounds__(256) linear_dp_vec(const __nv_bfloat16* dy, const __half* pre, __nv_bfloat16* dp, float* part,
-                                                     int64_t rows, int cols, int64_t run, int act) {
-    __shared__ float red[8][256 + 4];
-    wait_for_stream();
-    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-    const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * 8;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * run, r1 = min(rows, r0 + run);
-    float s[8] = {};
-    if (col < cols) {
-        constexpr int U = 4;   // rows in flight
-        for (int64_t r = r0 + sl; r < r1; r += 8 * U) {
-            uint4 d[U], h[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (r + 8 * i < r1) {
-                    d[i] = ldg16_cs(dy + (r + 8 * i) * cols + col);
-                    if (dp != nullptr) h[i] = ldg16_cs(pre + (r + 8 * i) * cols + col);
-                }
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (r + 8 * i < r1) {
-                    float f[8];
-                    unpack(d[i], f);
-                    if (dp != nullptr) {
-                        const __half2* q = reinterpret_cast<const __half2*>(&h[i]);
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 w = __half22float2(q[e]);
-                            v[2 * e] = w.x;
-                            v[2 * e + 1] = w.y;
-                        }
-                        mul_slopes<true>(act, v, f);
-                        stg16(dp + (r + 8 * i) * cols + col, pack(f));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s[e] += f[e];
-                }
-        }
-    }
-    if (part == nullptr) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) red[sl][lane + 32 * e] = s[e];
+// Where there are more than kDpShares blocks' worth of rows, the blocks are no cluster: each leaves its sums as a partial row in
+// the workspace, and linear_db adds those in their order.
+
+// The cluster's column sums into db: `mine` holds this block's for columns [col0, col0 + n).
+template <typename T>
+__device__ __forceinline__ void join_db(const float* mine, T* db, float* part, int64_t col0, int n, int cols) {
+    const uint32_t ranks = blocks_in_cluster();
     __syncthreads();
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (c >= cols) return;
-    float t = 0.f;
+    if (part != nullptr) {
+        for (int i = threadIdx.x; i < n; i += blockDim.x)
+            if (col0 + i < cols) part[static_cast<int64_t>(blockIdx.y) * cols + col0 + i] = mine[i];
+        return;
+    }
+    if (ranks > 1) cluster_barrier();
+    if (block_in_cluster() == 0)
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            float v[kDpShares];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][(threadIdx.x >> 3) + 32 * (threadIdx.x & 7)];
-    part[static_cast<int64_t>(blockIdx.y) * cols + c] = t;
+            for (uint32_t q = 0; q < kDpShares; ++q)
+                if (q < ranks) v[q] = ranks > 1 ? peer_float(mine + i, q) : mine[i];
+#pragma unroll
+            for (uint32_t q = 1; q < kDpShares; ++q)
+                if (q < ranks) v[0] += v[q];
+            if (col0 + i < cols) stf(db + col0 + i, v[0]);
+        }
+    __syncwarp();
+    if (ranks > 1) cluster_barrier();   // no block exits while another reads its sums
 }
 
-// dP = dY act'(P) and the partial sums of db: a block takes 32 columns and a run of rows, 8 threads a column.
-// TP: type dP is kept in; dp NULL: not kept (dP is dY).
+// Any width: 32 columns a block, 8 threads a column.  TP: type dP is kept in; dp NULL: not kept (dP is dY).
 template <typename T, typename TPRE, typename TP>
-__global__ void __launch_bounds__(256) linear_dp(const T* dy, const TPRE* pre, TP* dp, float* part, int64_t rows, int cols,
-                                                 int64_t run, int act) {
-    __shared__ float red[8][33];
+__global__ void __launch_bounds__(256) linear_dp(const T* dy, const TPRE* pre, TP* dp, T* db, float* part, int64_t rows, int cols,
+                                                 int act) {
+    __shared__ float red[8][33], sums[32];
     wait_for_stream();
     const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * run, r1 = min(rows, r0 + run);
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 32, col = col0 + lane;
+    const int64_t r0 = rows * blockIdx.y / gridDim.y, r1 = rows * (blockIdx.y + 1) / gridDim.y;
     float s = 0.f;
     if (col < cols)
+#pragma unroll 4
         for (int64_t r = r0 + sl; r < r1; r += 8) {
             float d = ldf(dy + r * cols + col);
             if (dp != nullptr) {
@@ -87,26 +65,95 @@ __global__ void __launch_bounds__(256) linear_dp(const T* dy, const TPRE* pre, T
             }
             s += d;
         }
+    if (db == nullptr) return;
     red[sl][lane] = s;
     __syncthreads();
-    if (part != nullptr && sl == 0 && col < cols) {
+    if (sl == 0) {
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) t += red[i][lane];
-        part[static_cast<int64_t>(blockIdx.y) * cols + col] = t;
+        sums[lane] = t;
     }
+    join_db(sums, db, part, col0, 32, cols);
 }
 
-// db: the partial rows added in ascending order
+// bf16 in whole 16-byte vectors: LX threads of 8 columns a row, 256 / LX rows side by side, kDpRows of them in flight
+// a thread.
+template <int ACT, int LX>
+__global__ void __launch_bounds__(256, 3) linear_dp_vec(const __nv_bfloat16* dy, const __half* pre, __nv_bfloat16* dp,
+                                                        __nv_bfloat16* db, float* part, int64_t rows, int cols) {
+    constexpr int SL = 256 / LX, C = LX * 8;   // row slices, columns
+    __shared__ float red[SL][C + 4], sums[C];
+    wait_for_stream();
+    const int lane = threadIdx.x % LX, sl = threadIdx.x / LX;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * C, col = col0 + lane * 8;
+    const int64_t r0 = rows * blockIdx.y / gridDim.y, r1 = rows * (blockIdx.y + 1) / gridDim.y;
+    float s[8] = {};
+    if (col < cols) {
+        for (int64_t r = r0 + sl; r < r1; r += SL * kDpRows) {
+            uint4 d[kDpRows], h[kDpRows];
+#pragma unroll
+            for (int i = 0; i < kDpRows; ++i)
+                if (r + SL * i < r1) {
+                    d[i] = ldg16_cs(dy + (r + SL * i) * cols + col);
+                    if (ACT != LIGER_ACT_NONE) h[i] = ldg16_cs(pre + (r + SL * i) * cols + col);
+                }
+#pragma unroll
+            for (int i = 0; i < kDpRows; ++i)
+                if (r + SL * i < r1) {
+                    float f[8];
+                    unpack(d[i], f);
+                    if (ACT != LIGER_ACT_NONE) {
+                        const __half2* q = reinterpret_cast<const __half2*>(&h[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 w = __half22float2(q[e]);
+                            f[2 * e] *= act_slope<true>(ACT, w.x);
+                            f[2 * e + 1] *= act_slope<true>(ACT, w.y);
+                        }
+                        stg16(dp + (r + SL * i) * cols + col, pack(f));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] += f[e];
+                }
+        }
+    }
+    if (db == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4)
+        *reinterpret_cast<float4*>(&red[sl][lane * 8 + e]) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+    __syncthreads();
+    if (threadIdx.x < C) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < SL; ++i) t += red[i][threadIdx.x];
+        sums[threadIdx.x] = t;
+    }
+    join_db(sums, db, part, col0, C, cols);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(256) linear_db(const float* part, T* db, int parts, int cols) {
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+__global__ void __launch_bounds__(128) linear_db(const float* part, T* db, int parts, int cols) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
     wait_for_stream();
     if (col >= cols) return;
     float s = 0.f;
-#pragma unroll 8
+#pragma unroll 16
     for (int i = 0; i < parts; ++i) s += part[static_cast<int64_t>(i) * cols + col];
     stf(db + col, s);
+}
+
+// Blocks that share the rows of a column sum: a cluster of up to kDpShares with at least 32 rows each, or, from
+// kDpLong rows on, one for each 128 rows, kDpParts at most.
+struct DpShares {
+    unsigned blocks;
+    bool cluster;
+};
+DpShares dp_shares(int64_t rows) {
+    if (rows >= kDpLong) return {static_cast<unsigned>(std::min<int64_t>(kDpParts, ceil_div(rows, 128))), false};
+    unsigned n = kDpShares;
+    while (n > 1 && rows < 32 * static_cast<int64_t>(n)) n /= 2;
+    return {n, true};
 }
 
 bool on_tensor_cores(int64_t H, int64_t N, int dtype) {
@@ -128,13 +175,14 @@ bool off16(std::initializer_list<const void*> ps) {
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
-// bytes of dP in the workspace, and all of it
+// bytes of dP in the workspace, and of db's partial rows behind it
 size_t dp_bytes(int64_t T, int64_t H, int64_t N, int act, int dtype) {
     if (act == LIGER_ACT_NONE) return 0;
     return round256(static_cast<size_t>(T) * static_cast<size_t>(N) * (on_tensor_cores(H, N, dtype) ? 2 : 4));
 }
-size_t sum_bytes(int64_t T, int64_t N) {
-    return round256(static_cast<size_t>(ceil_div(T, rows_per_sum(T))) * static_cast<size_t>(N) * 4);
+size_t part_bytes(int64_t T, int64_t N) {
+    const DpShares s = dp_shares(T);
+    return s.cluster ? 0 : round256(static_cast<size_t>(s.blocks) * static_cast<size_t>(N) * 4);
 }
 
 template <typename T, typename TPRE>
@@ -196,7 +244,7 @@ int fwd_tc(const void* X, const void* W, const void* bias, const void* residual,
         p.pre = static_cast<__half*>(pre);
         p.act = act;
         p.err = err;
-        return launch_small<0>("linear_act_fwd", W, X, p, small_tokens(T), st);
+        return launch_small<0, 0>("linear_act_fwd", W, X, p, small_tokens(T), st);
     }
     CUtensorMap mX, mW;
     if ((rc = make_map(&mX, X, H, T, H, BK, BM))) return rc;
@@ -226,7 +274,15 @@ int grads_tc(const LinearBwd& a, const void* dP) {
     int* err = nullptr;
     int rc;
     if ((rc = lsw_err_word(&err))) return rc;
-    if (a.dW != nullptr) {
+    if (a.dW != nullptr && goes_small(a.N, a.H)) {
+        SmallParams p{};
+        p.F = H;
+        p.T = N;
+        p.K = T;
+        p.out = static_cast<__nv_bfloat16*>(a.dW);
+        p.err = err;
+        if ((rc = launch_small<1, 1>("linear_act_bwd dW", a.X, dP, p, 128, a.st))) return rc;
+    } else if (a.dW != nullptr) {
         CUtensorMap mP, mX;
         if ((rc = make_map(&mP, dP, N, T, N, MN_BOX, BK))) return rc;
         if ((rc = make_map(&mX, a.X, H, T, H, MN_BOX, BK))) return rc;
@@ -281,7 +337,7 @@ int grads_tc(const LinearBwd& a, const void* dP) {
         p.K = N;
         p.out = static_cast<__nv_bfloat16*>(a.dX);
         p.err = err;
-        return launch_small<1>("linear_act_bwd dX", a.W, dP, p, small_tokens(a.T), a.st);
+        return launch_small<1, 0>("linear_act_bwd dX", a.W, dP, p, small_tokens(a.T), a.st);
     }
     CUtensorMap mP, mW;
     if ((rc = make_map(&mP, dP, N, T, N, BK, BM))) return rc;
@@ -302,24 +358,37 @@ int bwd_typed(const LinearBwd& a) {
     const bool keep = a.act != LIGER_ACT_NONE;
     constexpr bool TC = sizeof(T) == 2 && sizeof(TP) == 2;   // bf16 in whole vectors, for the tensor cores
     if (keep || a.db != nullptr) {
-        const int64_t run = rows_per_sum(a.T);
-        const dim3 grid(static_cast<unsigned>(ceil_div(a.N, TC ? 256 : 32)), static_cast<unsigned>(ceil_div(a.T, run)));
-        float* part = a.db != nullptr ? a.part : nullptr;
+        const DpShares sh = dp_shares(a.T);
+        const bool wide = TC && a.N >= 2048;   // 256 columns a block, else 64
+        const dim3 grid(static_cast<unsigned>(ceil_div(a.N, !TC ? 32 : wide ? 256 : 64)), sh.blocks), cluster(1, sh.cluster ? sh.blocks : 1);
+        float* part = a.db != nullptr && !sh.cluster ? a.part : nullptr;
         const T* dy = static_cast<const T*>(a.dY);
         const TPRE* pre = static_cast<const TPRE*>(a.pre);
         TP* dp = static_cast<TP*>(keep ? a.dP : nullptr);
-        int rc;
-        if constexpr (TC)
-            rc = launch_early("linear_act_bwd dP", linear_dp_vec, grid, 256, 0, a.st, dy, pre, dp, part, a.T,
-                              static_cast<int>(a.N), run, a.act);
-        else
-            rc = launch_early("linear_act_bwd dP", linear_dp<T, TPRE, TP>, grid, 256, 0, a.st, dy, pre, dp, part, a.T,
-                              static_cast<int>(a.N), run, a.act);
+        T* db = static_cast<T*>(a.db);
+        const char* who = "linear_act_bwd dP";
+        int rc = LIGER_OK;
+        if constexpr (TC) {
+            auto go = [&](auto k) {
+                rc = launch_cluster(who, k, grid, cluster, 256, 0, a.st, dy, pre, dp, db, part, a.T, static_cast<int>(a.N));
+            };
+            switch (a.act) {
+                case LIGER_ACT_RELU: wide ? go(linear_dp_vec<LIGER_ACT_RELU, 32>) : go(linear_dp_vec<LIGER_ACT_RELU, 8>); break;
+                case LIGER_ACT_GELU: wide ? go(linear_dp_vec<LIGER_ACT_GELU, 32>) : go(linear_dp_vec<LIGER_ACT_GELU, 8>); break;
+                case LIGER_ACT_GELU_TANH:
+                    wide ? go(linear_dp_vec<LIGER_ACT_GELU_TANH, 32>) : go(linear_dp_vec<LIGER_ACT_GELU_TANH, 8>);
+                    break;
+                case LIGER_ACT_SILU: wide ? go(linear_dp_vec<LIGER_ACT_SILU, 32>) : go(linear_dp_vec<LIGER_ACT_SILU, 8>); break;
+                default: wide ? go(linear_dp_vec<LIGER_ACT_NONE, 32>) : go(linear_dp_vec<LIGER_ACT_NONE, 8>); break;
+            }
+        } else {
+            rc = launch_cluster(who, linear_dp<T, TPRE, TP>, grid, cluster, 256, 0, a.st, dy, pre, dp, db, part, a.T,
+                                static_cast<int>(a.N), a.act);
+        }
         if (rc) return rc;
-        if (a.db != nullptr)
-            if (int rc = launch_early("linear_act_bwd db", linear_db<T>, dim3(static_cast<unsigned>(ceil_div(a.N, 256))), 256, 0,
-                                      a.st, static_cast<const float*>(a.part), static_cast<T*>(a.db), static_cast<int>(grid.y),
-                                      static_cast<int>(a.N)))
+        if (part != nullptr)
+            if ((rc = launch_early(who, linear_db<T>, dim3(static_cast<unsigned>(ceil_div(a.N, 128))), 128, 0, a.st,
+                                   static_cast<const float*>(part), db, static_cast<int>(sh.blocks), static_cast<int>(a.N))))
                 return rc;
     }
     if constexpr (TC) return grads_tc(a, keep ? a.dP : a.dY);
@@ -357,7 +426,7 @@ extern "C" size_t liger_linear_act_bwd_workspace(int64_t T, int64_t H, int64_t N
     const bool good = check_sizes("linear_act_bwd_workspace", T, H, N, act, dtype) == LIGER_OK;
     clear_error();
     if (!good || T == 0) return 0;
-    return dp_bytes(T, H, N, act, dtype) + sum_bytes(T, N);
+    return dp_bytes(T, H, N, act, dtype) + part_bytes(T, N);
 }
 
 extern "C" int liger_linear_act_bwd(const void* dY, const void* X, const void* W, const void* pre, void* dX, void* dW, void* db,
@@ -378,10 +447,10 @@ extern "C" int liger_linear_act_bwd(const void* dY, const void* X, const void* W
     if (!dY || (dX && !W) || (dW && !X) || (act != LIGER_ACT_NONE && !pre))
         return fail(LIGER_ERR_NULL, "%s: dY is required, W for dX, X for dW, pre for an activation", who);
     const size_t need = liger_linear_act_bwd_workspace(T, H, N, act, dtype);
-    if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))
+    if (need > 0 && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255)))
         return fail(LIGER_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) required, got %zu", who, need, ws_bytes);
-    LinearBwd a{dY, X, W, pre, dX, dW, db, ws, nullptr, T, H, N, act, st};
-    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dp_bytes(T, H, N, act, dtype));
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dp_bytes(T, H, N, act, dtype));
+    const LinearBwd a{dY, X, W, pre, dX, dW, db, ws, part, T, H, N, act, st};
     if (dtype == LIGER_F32) return bwd_typed<float, float, float>(a);
     if (on_tensor_cores(H, N, dtype)) return bwd_typed<__nv_bfloat16, __half, __nv_bfloat16>(a);
     return bwd_typed<__nv_bfloat16, __half, float>(a);

@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 
 #include "activation.cuh"
+#include "cluster.cuh"
 #include "linear_fma.cuh"
 #include "tc_gemm.cuh"
 
@@ -25,6 +26,7 @@ namespace {
 
 constexpr int kSmallThreads = 192, kSmallWarps = kSmallThreads / 32;
 constexpr int kSmallRows = 128;   // features of a block
+constexpr int kSmallRanks = 8;    // most blocks of a cluster
 
 struct SmallParams {
     int F, T, K;                  // features (rows of Y's last dimension), tokens, sum length
@@ -50,20 +52,9 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ float4 ld_cluster16(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-    return r;
-}
-
-// A_MN: the weight's features are contiguous (dX = dP W), else its k is (Y = X W^T)
-template <int A_MN>
+// A_MN, B_MN: the features (tokens) of an operand are contiguous, else its k is: Y = X W^T 0, 0; dX = dP W 1, 0;
+// dW = dP^T X 1, 1, with the inputs as features, the outputs as "tokens" and the tokens as k.
+template <int A_MN, int B_MN>
 __global__ void __launch_bounds__(kSmallThreads, 2)
     linear_small(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const SmallParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -79,7 +70,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     volatile uint32_t* slot_ptr = reinterpret_cast<uint32_t*>(gbase + p.stages * stage_bytes + 16 * p.stages + 16);
     __shared__ int good;   // 0 where a wait has expired
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const uint32_t rank = block_in_cluster(), ranks = blocks_in_cluster();
     const int f0 = static_cast<int>(blockIdx.y) * kSmallRows, t0 = static_cast<int>(blockIdx.z) * p.nt;
     const int nkb = (p.K + BK - 1) / BK;   // at least one for every block of the cluster
     const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / ranks);
@@ -125,7 +116,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
                 } else {
                     tma_load_2d_hint(sa, &tmA, full_bar(s), kb * BK, f0, pol);
                 }
-                tma_load_2d_hint(sa + A_BYTES, &tmB, full_bar(s), kb * BK, t0, pol);
+                if (B_MN) {
+                    for (int j = 0; j < p.nt / MN_BOX; ++j)
+                        tma_load_2d_hint(sa + A_BYTES + j * MN_BOX_BYTES, &tmB, full_bar(s), t0 + j * MN_BOX, kb * BK, pol);
+                } else {
+                    tma_load_2d_hint(sa + A_BYTES, &tmB, full_bar(s), kb * BK, t0, pol);
+                }
                 if (++s == p.stages) {
                     s = 0;
                     ph ^= 1u;
@@ -140,8 +136,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = make_idesc(kSmallRows, p.nt, A_MN, 0);
+            const uint32_t idesc = make_idesc(kSmallRows, p.nt, A_MN, B_MN);
             const uint32_t a_lbo = A_MN ? MN_BOX_BYTES : 16u, a_kstep = A_MN ? UMMA_K * 128u : UMMA_K * 2u;
+            const uint32_t b_lbo = B_MN ? MN_BOX_BYTES : 16u, b_kstep = B_MN ? UMMA_K * 128u : UMMA_K * 2u;
             int s = 0;
             uint32_t ph = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -155,7 +152,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
                 const uint32_t sa = base + s * stage_bytes, sb = sa + A_BYTES;
 #pragma unroll
                 for (int k = 0; k < BK / UMMA_K; ++k)
-                    mma_bf16(tmem, smem_desc(sa + k * a_kstep, a_lbo, 1024u), smem_desc(sb + k * UMMA_K * 2u, 16u, 1024u), idesc,
+                    mma_bf16(tmem, smem_desc(sa + k * a_kstep, a_lbo, 1024u), smem_desc(sb + k * b_kstep, b_lbo, 1024u), idesc,
                              ((kb - kb0) | k) != 0 ? 1u : 0u);
                 mma_commit(empty_bar(s));
                 if (kb + 1 == kb1) mma_commit(done_bar);   // not reached after an expired wait: the epilogue's expires too
@@ -190,14 +187,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     }
     __syncthreads();
     const bool mine = good != 0;
-    if (ranks > 1) cluster_sync_all();
+    if (ranks > 1) cluster_barrier();
     bool all = mine;
     if (ranks > 1)
-        for (uint32_t r = 0; r < ranks; ++r) {
-            uint32_t g;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(g) : "r"(map_to_rank(smem_u32(&good), r)) : "memory");
-            all = all && g != 0;
-        }
+        for (uint32_t r = 0; r < ranks; ++r) all = all && peer_word(&good, r) != 0;
     const int f = f0 + lane * 4;
     const int nt = min(p.nt, p.T - t0);
     if (f < p.F) {   // F is a multiple of 8: four features are in or out together
@@ -207,40 +200,64 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
             b[0] = bf_lo(u.x); b[1] = bf_hi(u.x);
             b[2] = bf_lo(u.y); b[3] = bf_hi(u.y);
         }
-        for (int t = static_cast<int>(rank) + static_cast<int>(ranks) * warp; t < nt; t += static_cast<int>(ranks) * kSmallWarps) {
-            const int64_t o = static_cast<int64_t>(t0 + t) * p.F + f;
-            uint2 res = make_uint2(0, 0);
-            if (p.residual != nullptr) res = *reinterpret_cast<const uint2*>(p.residual + o);
-            const uint32_t at = base + static_cast<uint32_t>(t * kSmallRows + lane * 4) * 4u;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            for (uint32_t r = 0; r < ranks; ++r) {
-                const float4 s = ranks > 1 ? ld_cluster16(map_to_rank(at, r)) : *reinterpret_cast<const float4*>(part + t * kSmallRows + lane * 4);
-                v[0] += s.x;
-                v[1] += s.y;
-                v[2] += s.z;
-                v[3] += s.w;
+        // four tokens of a warp at a time, so that their loads are in flight together
+        constexpr int U = 4;
+        const int stride = static_cast<int>(ranks) * kSmallWarps;
+        for (int t = static_cast<int>(rank) + static_cast<int>(ranks) * warp; t < nt; t += U * stride) {
+            uint2 res[U];
+            float4 v[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                res[i] = make_uint2(0, 0);
+                if (p.residual != nullptr && t + i * stride < nt)
+                    res[i] = *reinterpret_cast<const uint2*>(p.residual + static_cast<int64_t>(t0 + t + i * stride) * p.F + f);
+            }
+            const float* at = part + t * kSmallRows + lane * 4;
+            if (ranks > 1) {   // the blocks' sums in their order; tokens past the tile read what stands there (inside the ring)
+#pragma unroll
+                for (int i = 0; i < U; ++i) v[i] = peer_float4(at + (t + i * stride < nt ? i * stride * kSmallRows : 0), 0);
+#pragma unroll 2
+                for (uint32_t r = 1; r < ranks; ++r)
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const float4 s = peer_float4(at + (t + i * stride < nt ? i * stride * kSmallRows : 0), r);
+                        v[i].x += s.x;
+                        v[i].y += s.y;
+                        v[i].z += s.z;
+                        v[i].w += s.w;
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    v[i] = *reinterpret_cast<const float4*>(at + (t + i * stride < nt ? i * stride * kSmallRows : 0));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = all ? v[i] + b[i] : __int_as_float(0x7FC00000);
-            if (p.pre != nullptr) {
-                __half h[4];
+            for (int i = 0; i < U; ++i) {
+                if (t + i * stride >= nt) break;
+                const int64_t o = static_cast<int64_t>(t0 + t + i * stride) * p.F + f;
+                float w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) keep_pre(h + i, v[i]);
-                *reinterpret_cast<uint2*>(p.pre + o) = *reinterpret_cast<const uint2*>(h);
-            }
+                for (int e = 0; e < 4; ++e) w[e] = all ? w[e] + b[e] : __int_as_float(0x7FC00000);
+                if (p.pre != nullptr) {
+                    __half h[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = act_value<true>(p.act, v[i]);
-            if (p.residual != nullptr) {
-                v[0] += bf_lo(res.x);
-                v[1] += bf_hi(res.x);
-                v[2] += bf_lo(res.y);
-                v[3] += bf_hi(res.y);
+                    for (int e = 0; e < 4; ++e) keep_pre(h + e, w[e]);
+                    *reinterpret_cast<uint2*>(p.pre + o) = *reinterpret_cast<const uint2*>(h);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = act_value<true>(p.act, w[e]);
+                if (p.residual != nullptr) {
+                    w[0] += bf_lo(res[i].x);
+                    w[1] += bf_hi(res[i].x);
+                    w[2] += bf_lo(res[i].y);
+                    w[3] += bf_hi(res[i].y);
+                }
+                *reinterpret_cast<uint2*>(p.out + o) = make_uint2(pack_bf2(w[0], w[1]), pack_bf2(w[2], w[3]));
             }
-            *reinterpret_cast<uint2*>(p.out + o) = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
         }
     }
     __syncwarp();
-    if (ranks > 1) cluster_sync_all();   // no block exits while another reads its sums
+    if (ranks > 1) cluster_barrier();   // no block exits while another reads its sums
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
@@ -249,52 +266,50 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 }
 
 // Tokens of a tile for T tokens: all of them up to 256 (the weight is read once), else equal tiles of at most `most`.
-inline int small_tile(int64_t T, int most) {
+inline int small_tile(int64_t T, int most, int unit) {
     const int64_t tiles = ceil_div(T, most);
-    return static_cast<int>(ceil_div(ceil_div(T, tiles), 16) * 16);
+    return static_cast<int>(ceil_div(ceil_div(T, tiles), unit) * unit);
 }
 
-// A: the weight's map base ([F, K] K-major, or [K, F] with A_MN), B [T, K].
-template <int A_MN>
+// A [F, K], or [K, F] with A_MN; B [T, K], or [K, T] with B_MN.
+template <int A_MN, int B_MN>
 int launch_small(const char* who, const void* A, const void* B, SmallParams p, int most_tokens, cudaStream_t st) {
-    p.nt = small_tile(p.T, most_tokens);
+    p.nt = small_tile(p.T, most_tokens, B_MN ? MN_BOX : 16);
     CUtensorMap ma, mb;
     int rc;
     if (A_MN) rc = make_map(&ma, A, p.F, p.K, p.F, MN_BOX, BK);
     else rc = make_map(&ma, A, p.K, p.F, p.K, BK, kSmallRows);
     if (rc) return rc;
-    if ((rc = make_map(&mb, B, p.K, p.T, p.K, BK, p.nt))) return rc;
+    if (B_MN) rc = make_map(&mb, B, p.T, p.K, p.T, MN_BOX, BK);
+    else rc = make_map(&mb, B, p.K, p.T, p.K, BK, p.nt);
+    if (rc) return rc;
     const int stage = A_BYTES + p.nt * BK * 2;
-    // two blocks on an SM while three stages of each fit
-    const int half = 112 * 1024, whole = 224 * 1024, over = 1024 + 256;
-    const bool two = 3 * stage + over <= half;
-    p.stages = std::min(12, ((two ? half : whole) - over) / stage);
+    const int64_t ft = ceil_div(p.F, kSmallRows), tt = ceil_div(p.T, p.nt), nkb = ceil_div(p.K, BK), sms = sm_count();
+    if (ft > 65535 || tt > 65535) return fail(LIGER_ERR_SHAPE, "%s: too many tiles", who);
     p.tmem_cols = 32;
     while (p.tmem_cols < p.nt) p.tmem_cols *= 2;
+    // K over `ranks` blocks a tile, so that the SM with the most blocks has the least to do, all of them resident at
+    // once where that can be: m blocks on an SM share its memory, three stages each, and its 512 TMEM columns
+    const int whole = 226 * 1024, over = 1024 + 256, extra = 2048;
+    int ranks = 1, m = 1;
+    double least = 1e30;
+    for (int r = 1; r <= kSmallRanks && nkb >= (r == 1 ? 1 : 4 * r); ++r) {
+        int64_t on = ceil_div(ft * tt * r, sms);
+        const int64_t fit = std::min<int64_t>({whole / (3 * stage + over + extra), 512 / p.tmem_cols, 4});
+        const double rounds = static_cast<double>(ceil_div(on, fit));
+        const double cost = static_cast<double>(on) / r + 0.02 * r + 0.1 * (rounds - 1);
+        if (cost < least) {
+            least = cost;
+            ranks = r;
+            m = static_cast<int>(std::min(on, fit));
+        }
+    }
+    p.stages = std::min(12, (whole / m - over - extra) / stage);
     const size_t smem = static_cast<size_t>(p.stages) * stage + over;
-    const int64_t ft = ceil_div(p.F, kSmallRows), tt = ceil_div(p.T, p.nt), nkb = ceil_div(p.K, BK);
-    if (ft > 65535 || tt > 65535) return fail(LIGER_ERR_SHAPE, "%s: too many tiles", who);
-    // K over as many blocks as fill the card once, four k-blocks at least each
-    int ranks = 1;
-    while (ranks < 8 && 2 * ranks * ft * tt <= (two ? 2 : 1) * static_cast<int64_t>(sm_count()) && nkb >= 8 * ranks) ranks *= 2;
-    constexpr auto k = linear_small<A_MN>;
+    constexpr auto k = linear_small<A_MN, B_MN>;
     if ((rc = allow_smem<k>())) return rc;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2] = {};
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(ranks), static_cast<unsigned>(ft), static_cast<unsigned>(tt));
-    cfg.blockDim = dim3(kSmallThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, k, ma, mb, static_cast<const SmallParams>(p));
-    return check_launch(who);
+    return launch_cluster(who, k, dim3(static_cast<unsigned>(ranks), static_cast<unsigned>(ft), static_cast<unsigned>(tt)),
+                          dim3(static_cast<unsigned>(ranks)), kSmallThreads, smem, st, ma, mb, p);
 }
 
 }  // namespace

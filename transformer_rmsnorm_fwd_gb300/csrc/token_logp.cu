@@ -2,9 +2,8 @@
 // alternatives and the gradient of the logits (formulas in liger_layer.h).
 #include <math.h>
 
-#include "common.cuh"
+#include "cluster.cuh"
 #include "liger_layer.h"
-#include "mbarrier.cuh"
 
 namespace liger {
 namespace {
@@ -33,37 +32,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// ---- a cluster of blocks on one row
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// the same shared object in block `rank` of the cluster
-__device__ __forceinline__ uint32_t peer(const void* p, int rank) {
-    uint32_t o;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(o) : "r"(smem_u32(p)), "r"(rank) : "memory");
-    return o;
-}
-__device__ __forceinline__ float peer_float(const float* p, int rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(p, rank)) : "memory");
-    return v;
-}
-__device__ __forceinline__ unsigned long long peer_key(const unsigned long long* p, int rank) {
-    unsigned long long v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
-    return v;
 }
 
 // A number whose unsigned order is that of the floats: -0 as +0, NaN above all.
@@ -194,7 +162,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p)
     __shared__ RowShared sh;
     extern __shared__ __align__(16) unsigned long long list[];   // [kList + kSecond] with k > 0
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+    const int rank = static_cast<int>(block_in_cluster()), ranks = static_cast<int>(blocks_in_cluster());
     wait_for_stream();
     const int64_t t = blockIdx.x / static_cast<unsigned>(ranks);
     const T* z = static_cast<const T*>(p.z) + t * p.ld;
@@ -376,7 +344,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p)
         }
     }
     __syncthreads();
-    if (ranks > 1) cluster_sync();
+    if (ranks > 1) cluster_barrier();
     if (rank == 0) {
         // the blocks' sums in their order, and their alternatives ranked again
         Sums all = sh.total;
@@ -425,7 +393,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p)
     }
     if (ranks > 1) {
         __syncwarp();
-        cluster_sync();   // no block exits while another reads from it
+        cluster_barrier();   // no block exits while another reads from it
     }
 }
 
@@ -500,22 +468,9 @@ __global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) 
 // ------------------------------------------------------------------ launches
 template <typename T, int NT, bool ENT>
 int launch_row(const char* who, const LogpFwd& p, int ranks, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2] = {};
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.T * ranks));
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = p.k > 0 ? (kList + kSecond) * sizeof(unsigned long long) : 0;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    cudaLaunchKernelEx(&cfg, token_logp_row<T, NT, ENT>, p);
-    return check_launch(who);
+    const size_t smem = p.k > 0 ? (kList + kSecond) * sizeof(unsigned long long) : 0;
+    return launch_cluster(who, token_logp_row<T, NT, ENT>, dim3(static_cast<unsigned>(p.T * ranks)), dim3(static_cast<unsigned>(ranks)),
+                          NT, smem, st, p);
 }
 
 template <typename T>
