@@ -45,10 +45,8 @@ __device__ __forceinline__ unsigned long long peer_key(const unsigned long long*
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t peer_word(const int* p, uint32_t rank) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer(p, rank)) : "memory");
-    return v;
+__device__ __forceinline__ void peer_store(int* p, uint32_t rank, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
 }
 
 // launch_early over clusters of `cluster` blocks (gridDim a multiple of it in each dimension)

@@ -38,7 +38,7 @@ __device__ __forceinline__ void fma_store(const FmaGemm& g, const FmaEpi<TO, TPR
 // buffers, the next ones loaded to registers while these are used.  FT = 128: 64 FMA for 16 values read (bound by FMA issue).  FT = 64,
 // for fewer outputs: K split over a cluster of blocks, whose tiles are joined in order over distributed shared memory.
 template <typename TA, typename TB, typename TO, typename TPRE, int FT>
-__global__ void __launch_bounds__(256, 2) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {
+__global__ void __launch_bounds__(256, FT == 64 ? 3 : 2) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {
     constexpr int kFK = 2048 / FT;
     constexpr int PT = FT / 16;             // outputs of a thread in each direction
     constexpr int LD = FT * kFK / 256;      // elements of an operand that a thread loads a step
@@ -155,9 +155,9 @@ int launch_fma_gemm(const char* who, const TA* A, const TB* B, const FmaGemm& g,
     auto tiles = [&](int ft) { return ceil_div(g.M, ft) * ceil_div(g.N, ft); };
     if (tiles(128) >= sm_count())
         return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128>, dim3(static_cast<unsigned>(tiles(128))), 256, 0, st, A, B, g, ep);
-    // K over as many blocks as give every SM about two, four steps at least each
+    // K over so many blocks that all of them are still resident at once (three on an SM), 64 k at least each
     int ranks = 1;
-    while (ranks < 8 && tiles(64) * ranks < 2 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
+    while (ranks < 8 && 2 * tiles(64) * ranks <= 3 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
     return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64>, dim3(static_cast<unsigned>(tiles(64) * ranks)),
                           dim3(static_cast<unsigned>(ranks)), 256, 0, st, A, B, g, ep);
 }

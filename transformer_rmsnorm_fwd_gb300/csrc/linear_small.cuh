@@ -186,11 +186,13 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
         }
     }
     __syncthreads();
-    const bool mine = good != 0;
-    if (ranks > 1) cluster_barrier();
-    bool all = mine;
-    if (ranks > 1)
-        for (uint32_t r = 0; r < ranks; ++r) all = all && peer_word(&good, r) != 0;
+    // (a wait that expired anywhere in the cluster shows in every block's word)
+    if (ranks > 1) {
+        if (good == 0 && threadIdx.x < ranks) peer_store(&good, threadIdx.x, 0);
+        __syncwarp();
+        cluster_barrier();
+    }
+    const bool all = good != 0;
     const int f = f0 + lane * 4;
     const int nt = min(p.nt, p.T - t0);
     if (f < p.F) {   // F is a multiple of 8: four features are in or out together
@@ -297,7 +299,7 @@ int launch_small(const char* who, const void* A, const void* B, SmallParams p, i
         int64_t on = ceil_div(ft * tt * r, sms);
         const int64_t fit = std::min<int64_t>({whole / (3 * stage + over + extra), 512 / p.tmem_cols, 4});
         const double rounds = static_cast<double>(ceil_div(on, fit));
-        const double cost = static_cast<double>(on) / r + 0.02 * r + 0.1 * (rounds - 1);
+        const double cost = static_cast<double>(on) / r + 0.05 * r + 0.1 * (rounds - 1);
         if (cost < least) {
             least = cost;
             ranks = r;
