@@ -2,6 +2,8 @@
 // alternatives and the gradient of the logits (formulas in liger_layer.h).
 #include <math.h>
 
+#include <type_traits>
+
 #include "cluster.cuh"
 #include "liger_layer.h"
 
@@ -79,12 +81,12 @@ __device__ __forceinline__ unsigned long long block_max_key(unsigned long long v
     return v;
 }
 
-// Running maximum with the sums relative to it.
+// Running maximum with the sums relative to it (c: log2 e / temperature).
 struct Sums {
     float m, s, u;
 };
-// The sums of `a` relative to a larger maximum m (c: log2 e / temperature).  The difference is held at -1e4,
-// where the factor is 0, so that 0 times it is not NaN.
+// The sums of `a` relative to a larger maximum m.  The difference is held at -1e4, where the factor is 0, so that 0 times it
+// is not NaN.
 __device__ __forceinline__ void raise(Sums& a, float m, float c) {
     const float d = max_nan((a.m - m) * c, -1e4f), f = ex2(d);
     a.u = fmaf(a.s, d, a.u) * f;
@@ -98,6 +100,40 @@ __device__ __forceinline__ void join(Sums& a, Sums b, float c) {
     a.s += b.s;
     a.u += b.u;
 }
+// The thread's sums while it runs: d is formed as f c - k by one fma, k = fl(m c), and so is off by e = m c - k (below
+// 2^-24 of m c) in every term alike, which is put right when the sums are read: with the sums s' and u' of those,
+// s = 2^-e s', u = 2^-e (u' - e s').  From kFarOut on (e would be no small number, or out of fp32's range as in a row
+// of nothing but the type's lowest values) d is (f - m) c, and e is 0.
+constexpr float kFarOut = 1e6f;
+struct Running {
+    float m, k;        // maximum, fl(m c)
+    float2 s, u;
+    __device__ __forceinline__ bool far() const { return !(fabsf(k) < kFarOut); }
+    __device__ __forceinline__ Sums read(float c) const {
+        const float e = far() ? 0.f : fmaf(m, c, -k), f = ex2(-e), sum = s.x + s.y;
+        return {m, sum * f, fmaf(-e, sum, u.x + u.y) * f};
+    }
+    __device__ __forceinline__ void set(const Sums& a, float c) {
+        m = a.m;
+        k = a.m * c;
+        const float e = far() ? 0.f : fmaf(m, c, -k), f = ex2(e);
+        s = make_float2(a.s * f, 0.f);
+        u = make_float2(fmaf(e, a.s, a.u) * f, 0.f);
+    }
+};
+
+// Largest element of a 16-byte vector, NaN above all; bf16 by packed comparisons.
+__device__ __forceinline__ float vec_max(const uint4& u, float) {
+    return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)), max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+__device__ __forceinline__ float vec_max(const uint4& u, __nv_bfloat16) {
+    auto larger = [](uint32_t a, uint32_t b) {
+        const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    };
+    const uint32_t m = larger(larger(u.x, u.y), larger(u.z, u.w));
+    return max_nan(bf_lo(m), bf_hi(m));
+}
 
 constexpr int kGroups = 64;         // groups of threads
 constexpr int kList = 2048;         // candidates of a block
@@ -109,31 +145,30 @@ constexpr int kShortRow = 256;      // rows of at most this many vectors: 64 thr
 template <typename T>
 struct RowVecs {
     const T* base;       // element 0 of vector 0 (aligned; up to EPV - 1 elements before the row)
-    int shift;
-    int64_t n, first, last, V;
+    int shift, n, first, last, V;
     __device__ RowVecs(const T* z, int64_t vocab) {
         constexpr int EPV = Vec<T>::N;
         const uintptr_t at = reinterpret_cast<uintptr_t>(z);
         shift = static_cast<int>((at & 15) / sizeof(T));
         base = z - shift;
-        V = vocab;
+        V = static_cast<int>(vocab);   // at most 2^30
         n = (V + shift + EPV - 1) / EPV;
         first = shift > 0 ? 1 : 0;
         last = (V + shift) / EPV;
     }
-    // the elements of vector v, -inf where it reaches past the row (nothing outside the row is read)
-    __device__ __forceinline__ void get(int64_t v, float (&f)[Vec<T>::N]) const {
+    // vector v, -inf where it reaches past the row (nothing outside the row is read)
+    __device__ __forceinline__ uint4 get(int v) const {
         constexpr int EPV = Vec<T>::N;
-        if (v >= first && v < last) {
-            unpack(ldg16(base + v * EPV), f);
-        } else {
+        if (v >= first && v < last) return ldg16(base + static_cast<int64_t>(v) * EPV);
+        float f[EPV];
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                const int64_t i = v * EPV + e - shift;
-                f[e] = i >= 0 && i < V ? ldf(base + v * EPV + e) : -INFINITY;
-            }
+        for (int e = 0; e < EPV; ++e) {
+            const int i = v * EPV + e - shift;
+            f[e] = i >= 0 && i < V ? ldf(base + i + shift) : -INFINITY;
         }
+        return pack(f);
     }
+    __device__ __forceinline__ void get(int v, float (&f)[Vec<T>::N]) const { unpack(get(v), f); }
 };
 
 // Finds the `k` largest of n keys (all different, none 0) by counting and leaves them in order in out[0 .. k).
@@ -167,7 +202,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p)
     const int64_t t = blockIdx.x / static_cast<unsigned>(ranks);
     const T* z = static_cast<const T*>(p.z) + t * p.ld;
     const RowVecs<T> row(z, p.V);
-    const int64_t v0 = row.n * rank / ranks, v1 = row.n * (rank + 1) / ranks;   // this block's vectors
+    const int v0 = static_cast<int>(static_cast<int64_t>(row.n) * rank / ranks);   // this block's vectors
+    const int v1 = static_cast<int>(static_cast<int64_t>(row.n) * (rank + 1) / ranks);
     const float c = p.inv_temp * kLog2e;
     // the token's logit, asked for early
     int64_t y = p.ignore;
@@ -176,99 +212,133 @@ __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p)
         y = p.tokens[t];
         if (y != p.ignore && y >= 0 && y < p.V) zy = ldf(z + y);
     }
-    Sums a{kLowest, 0.f, 0.f};
-    float best = -INFINITY;   // the thread's largest logit (NaN above all), and its vector
-    int64_t best_v = -1;
     const float2 c2 = make_float2(c, c);
-    auto take = [&](const float (&f)[kUnroll][EPV], int64_t v, int count) {
-        float gm = kLowest;
+    Running run;
+    run.set(Sums{kLowest, 0.f, 0.f}, c);
+    // the thread's largest logit (NaN above all), and its vector
+    float best = -INFINITY;
+    int best_v = v0 + tid < v1 ? v0 + tid : -1;
+    auto take = [&](const uint4 (&x)[kUnroll], int v, int count) {
+        float m[kUnroll];
+        m[0] = vec_max(x[0], T());
+        float gm = m[0];
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-            if (q >= count) break;
-            float m = f[q][0];
-#pragma unroll
-            for (int e = 1; e < EPV; ++e) m = max_nan(m, f[q][e]);
-            if (m > best || best_v < 0 || (m != m && best == best)) {
-                best = m;
-                best_v = v + q * NT;
+        for (int q = 1; q < kUnroll; ++q)
+            if (q < count) {
+                m[q] = vec_max(x[q], T());
+                gm = max_nan(gm, m[q]);
             }
-            gm = fmaxf(gm, m);
+        if (!(gm <= best)) {   // larger, or NaN; rare after the first vectors
+            if (best == best) {
+                best = gm;
+#pragma unroll
+                for (int q = kUnroll - 1; q >= 0; --q)   // the first of equal ones
+                    if (q < count && (m[q] == gm || m[q] != m[q])) best_v = v + q * NT;
+            }
+            if (gm > run.m) {
+                Sums a = run.read(c);
+                raise(a, gm, c);
+                run.set(a, c);
+            }
         }
-        if (gm > a.m) raise(a, gm, c);
-        const float2 nm = make_float2(-a.m, -a.m);
-        float2 s2 = make_float2(0.f, 0.f), u2 = make_float2(0.f, 0.f);
+        auto add = [&](auto far) {
+            const float2 nk = make_float2(-run.k, -run.k), nm = make_float2(-run.m, -run.m);
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-            if (q >= count) break;
+            for (int q = 0; q < kUnroll; ++q) {
+                if (q >= count) break;
+                float2 f[NP];
+                unpack2(x[q], f);
 #pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                float2 d = __fmul2_rn(__fadd2_rn(make_float2(f[q][2 * e], f[q][2 * e + 1]), nm), c2);
-                if (ENT) {   // a logit of -inf has d below any limit: held where 2^d is 0, so that d 2^d is not NaN
-                    d.x = max_nan(d.x, -200.f);
-                    d.y = max_nan(d.y, -200.f);
+                for (int e = 0; e < NP; ++e) {
+                    float2 d = decltype(far)::value ? __fmul2_rn(__fadd2_rn(f[e], nm), c2) : __ffma2_rn(f[e], c2, nk);
+                    if (ENT) {   // a logit of -inf has d below any limit: held where 2^d is 0, so that d 2^d is not NaN
+                        d.x = max_nan(d.x, -200.f);
+                        d.y = max_nan(d.y, -200.f);
+                    }
+                    const float2 w = make_float2(ex2(d.x), ex2(d.y));
+                    run.s = __fadd2_rn(run.s, w);
+                    if (ENT) run.u = __ffma2_rn(d, w, run.u);
                 }
-                const float2 x = make_float2(ex2(d.x), ex2(d.y));
-                s2 = __fadd2_rn(s2, x);
-                if (ENT) u2 = __ffma2_rn(d, x, u2);
             }
-        }
-        a.s += s2.x + s2.y;
-        if (ENT) a.u += u2.x + u2.y;
+        };
+        if (run.far()) add(std::true_type());
+        else add(std::false_type());
     };
-    int64_t v = v0 + tid;
-    for (; v + (kUnroll - 1) * NT < v1; v += kUnroll * NT) {
-        float f[kUnroll][EPV];
-        if (v >= row.first && v + (kUnroll - 1) * NT < row.last) {
-            uint4 x[kUnroll];
+    // groups of kUnroll vectors a thread, NT apart; the next group is asked for before this one is used
+    constexpr int STEP = kUnroll * NT;
+    auto fetch = [&](uint4 (&x)[kUnroll], int g0) {   // the block's group from vector g0 on
+        const int v = g0 + tid;
+        if (g0 >= row.first && g0 + STEP <= min(row.last, v1)) {
+            const uint4* at = reinterpret_cast<const uint4*>(row.base) + v;
 #pragma unroll
-            for (int q = 0; q < kUnroll; ++q) x[q] = ldg16(row.base + (v + q * NT) * EPV);
-#pragma unroll
-            for (int q = 0; q < kUnroll; ++q) unpack(x[q], f[q]);
+            for (int q = 0; q < kUnroll; ++q) x[q] = ldg16(at + q * NT);
         } else {
 #pragma unroll
-            for (int q = 0; q < kUnroll; ++q) row.get(v + q * NT, f[q]);
+            for (int q = 0; q < kUnroll; ++q)
+                if (v + q * NT < v1) x[q] = row.get(v + q * NT);
         }
-        take(f, v, kUnroll);
-    }
-    if (v < v1) {
-        float f[kUnroll][EPV];
-        int count = 0;
+    };
+    uint4 next[kUnroll];
+    fetch(next, v0);
+    int g0 = v0;
+    for (; g0 + STEP <= v1; g0 += STEP) {
+        uint4 x[kUnroll];
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q)
-            if (v + q * NT < v1) {
-                row.get(v + q * NT, f[q]);
-                count = q + 1;
-            }
-        take(f, v, count);
+        for (int q = 0; q < kUnroll; ++q) x[q] = next[q];
+        if (g0 + STEP < v1) fetch(next, g0 + STEP);
+        take(x, g0 + tid, kUnroll);
     }
-    // the block's sums
-    Sums w = a;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Sums b{__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o), __shfl_xor_sync(0xffffffffu, w.u, o)};
-        join(w, b, c);
-    }
-    if (lane == 0) sh.sums[warp] = w;
-    // its largest logit, and the groups' best, as keys: the order of the value, then the vector's index
+    if (g0 + tid < v1) take(next, g0 + tid, (v1 - g0 - tid + NT - 1) / NT);
+    Sums a = run.read(c);
+    // the warp's sums, and the groups' best logits as keys: the order of the value, then the vector's index
     const unsigned long long mine =
         best_v < 0 ? 0 : static_cast<unsigned long long>(order_of(best)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(best_v));
-    const unsigned long long top = block_max_key<NT>(mine, sh.red);   // (with two barriers)
+    constexpr int PER = NT / kGroups;   // neighbouring threads of a group
+    unsigned long long key = mine;
+    float wm = a.m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        if (o == PER && lane % PER == 0) sh.groups[tid / PER] = key;
+        key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+        wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+    }
+    raise(a, wm, c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+        if (ENT) a.u += __shfl_xor_sync(0xffffffffu, a.u, o);
+    }
+    if (lane == 0) {
+        sh.sums[warp] = a;
+        sh.red[warp] = key;
+    }
+    if (tid < LIGER_TOP_MAX) sh.best[tid] = 0;
     if (tid == 0) {
-        w = sh.sums[0];
-        for (int i = 1; i < NT / 32; ++i) join(w, sh.sums[i], c);
-        sh.total = w;
-        sh.row_max = value_of(static_cast<uint32_t>(top >> 32));
+        sh.bound = 0;
         sh.count = sh.count2 = 0;
     }
-    if (p.k > 0) {
-        constexpr int PER = NT / kGroups;   // neighbouring threads of a group
-        unsigned long long g = mine;
+    __syncthreads();
+    if (warp == NT / 32 - 1) {   // the last warp joins the warps' sums, in pairs that do not depend on anything but their number
+        Sums w = lane < NT / 32 ? sh.sums[lane] : Sums{kLowest, 0.f, 0.f};
+        unsigned long long top = lane < NT / 32 ? sh.red[lane] : 0;
+        float m = w.m;
 #pragma unroll
-        for (int o = PER / 2; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-        if (tid % PER == 0) sh.groups[tid / PER] = g;
-        if (tid < LIGER_TOP_MAX) sh.best[tid] = 0;
-        if (tid == 0) sh.bound = 0;
-        __syncthreads();
+        for (int o = NT / 64; o > 0; o >>= 1) {
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        raise(w, m, c);
+#pragma unroll
+        for (int o = NT / 64; o > 0; o >>= 1) {
+            w.s += __shfl_xor_sync(0xffffffffu, w.s, o);
+            w.u += __shfl_xor_sync(0xffffffffu, w.u, o);
+        }
+        if (lane == 0) {
+            sh.total = w;
+            sh.row_max = value_of(static_cast<uint32_t>(top >> 32));
+        }
+    }
+    if (p.k > 0) {
         if (tid < kGroups) {   // the k-th largest of the groups' (those without an element: 0, and not distinct)
             const unsigned long long x = sh.groups[tid];
             int above = 0;
@@ -281,18 +351,28 @@ __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p)
         const uint32_t bound_o = static_cast<uint32_t>(bound >> 32), bound_v = 0xFFFFFFFFu - static_cast<uint32_t>(bound);
         uint32_t hot = __ballot_sync(0xffffffffu, mine != 0 && mine >= bound);
         while (hot != 0) {   // the vectors of one thread at a time, over the warp
-            const int64_t vt = v0 + warp * 32 + (__ffs(hot) - 1);
+            const int vt = v0 + warp * 32 + (__ffs(hot) - 1);
             hot &= hot - 1;
-            for (int64_t x = vt + static_cast<int64_t>(lane) * NT; x < v1; x += 32 * NT) {
-                float f[EPV];
-                row.get(x, f);
+            for (int x0 = vt + lane * NT; x0 < v1; x0 += 64 * NT) {
+                uint4 w[2];
 #pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    const int64_t i = x * EPV + e - row.shift;
-                    const uint32_t o = order_of(f[e]);
-                    if (i >= 0 && i < p.V && (o > bound_o || (o == bound_o && (bound == 0 || static_cast<uint32_t>(x) <= bound_v)))) {
-                        const int at = atomicAdd(&sh.count, 1);   // in any order: the keys are ranked
-                        if (at < kList) list[at] = rank_key(f[e], static_cast<uint32_t>(i));
+                for (int h = 0; h < 2; ++h)
+                    if (x0 + h * 32 * NT < v1) w[h] = row.get(x0 + h * 32 * NT);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int x = x0 + h * 32 * NT;
+                    if (x >= v1 || order_of(vec_max(w[h], T())) < bound_o) continue;
+                    const bool level = bound == 0 || static_cast<uint32_t>(x) <= bound_v;
+                    float f[EPV];
+                    unpack(w[h], f);
+#pragma unroll
+                    for (int e = 0; e < EPV; ++e) {
+                        const int i = x * EPV + e - row.shift;
+                        const uint32_t o = order_of(f[e]);
+                        if (i >= 0 && i < row.V && (o > bound_o || (o == bound_o && level))) {
+                            const int at = atomicAdd(&sh.count, 1);   // in any order: the keys are ranked
+                            if (at < kList) list[at] = rank_key(f[e], static_cast<uint32_t>(i));
+                        }
                     }
                 }
             }
@@ -304,14 +384,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p)
             unsigned long long last = ~0ull;
             for (int i = 0; i < p.k; ++i) {
                 unsigned long long b = 0;
-                for (int64_t x = v0 + tid; x < v1; x += NT) {
+                for (int x = v0 + tid; x < v1; x += NT) {
                     float f[EPV];
                     row.get(x, f);
 #pragma unroll
                     for (int e = 0; e < EPV; ++e) {
-                        const int64_t j = x * EPV + e - row.shift;
+                        const int j = x * EPV + e - row.shift;
                         const unsigned long long key = rank_key(f[e], static_cast<uint32_t>(j));
-                        if (j >= 0 && j < p.V && key < last && key > b) b = key;
+                        if (j >= 0 && j < row.V && key < last && key > b) b = key;
                     }
                 }
                 last = block_max_key<NT>(b, sh.red);
@@ -436,7 +516,7 @@ __global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) 
     } else {
         const RowVecs<T> row(z, p.V);
         T* out = dz - row.shift;
-        const int64_t v0 = row.n * blockIdx.y / gridDim.y, v1 = row.n * (blockIdx.y + 1) / gridDim.y;
+        const int64_t v0 = static_cast<int64_t>(row.n) * blockIdx.y / gridDim.y, v1 = static_cast<int64_t>(row.n) * (blockIdx.y + 1) / gridDim.y;
         for (int64_t v = v0 + threadIdx.x; v < v1; v += kUnroll * kRowThreads) {
             uint4 x[kUnroll];
 #pragma unroll
