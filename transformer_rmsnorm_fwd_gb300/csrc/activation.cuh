@@ -12,24 +12,52 @@
 namespace liger {
 namespace {
 
+// FAST forms are for results that are rounded to bf16 next: the hardware's 2^x and reciprocal (relative errors near
+// 2^-22), and erfc by a published approximation.  The others use CUDA's functions.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Phi(p), the normal distribution function, as erfc(-p / sqrt 2) / 2: no cancellation for p < 0.
-__device__ __forceinline__ float normal_cdf(float p) { return 0.5f * erfcf(p * -0.70710678118654752f); }
+// FAST: erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0, off by at most 1.5e-7 (Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26); it needs e^(-p^2 / 2), which the density is formed from too.
+struct Normal {
+    float cdf, density;
+};
+template <bool FAST>
+__device__ __forceinline__ Normal normal(float p) {
+    if (!FAST) return {0.5f * erfcf(p * -0.70710678118654752f), 0.39894228040143268f * expf(-0.5f * p * p)};
+    const float e = fast_exp2(p * p * -0.72134752044448170f);   // log2(e) / 2
+    const float t = fast_rcp(fmaf(0.3275911f * 0.70710678118654752f, fabsf(p), 1.f));
+    float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    q = fmaf(q, t, 0.5f * 1.421413741f);
+    q = fmaf(q, t, 0.5f * -0.284496736f);
+    q = fmaf(q, t, 0.5f * 0.254829592f);
+    q *= t * e;   // Phi(-|p|)
+    return {p < 0.f ? q : 1.f - q, 0.39894228040143268f * e};
+}
 
 // 2 sqrt(2/pi) (p + 0.044715 p^3): gelu with tanh is p sigmoid of this, (1 + tanh a) / 2 = sigmoid(2 a)
 __device__ __forceinline__ float tanh_arg(float p) {
     return p * fmaf(2.f * 0.79788456080286536f * 0.044715f, p * p, 2.f * 0.79788456080286536f);
 }
-// FAST: the hardware exponential and reciprocal (for results that are rounded to bf16 next)
 template <bool FAST>
 __device__ __forceinline__ float sigmoid(float x) {
-    return FAST ? __fdividef(1.0f, 1.0f + __expf(-x)) : 1.0f / (1.0f + expf(-x));
+    return FAST ? fast_rcp(1.0f + fast_exp2(x * -1.4426950408889634f)) : 1.0f / (1.0f + expf(-x));
 }
 
 template <bool FAST>
 __device__ __forceinline__ float act_value(int act, float p) {
     switch (act) {
         case LIGER_ACT_RELU: return p > 0.f ? p : (p != p ? p : 0.f);
-        case LIGER_ACT_GELU: return p * normal_cdf(p);
+        case LIGER_ACT_GELU: return p * normal<FAST>(p).cdf;
         case LIGER_ACT_GELU_TANH: return p * sigmoid<FAST>(tanh_arg(p));
         case LIGER_ACT_SILU: return p * sigmoid<FAST>(p);
         default: return p;
@@ -64,10 +92,13 @@ template <bool FAST>
 __device__ __forceinline__ float act_slope(int act, float p) {
     switch (act) {
         case LIGER_ACT_RELU: return p > 0.f ? 1.f : (p != p ? p : 0.f);
-        case LIGER_ACT_GELU: return fmaf(p * 0.39894228040143268f, expf(-0.5f * p * p), normal_cdf(p));
+        case LIGER_ACT_GELU: {
+            const Normal n = normal<FAST>(p);
+            return fmaf(p, n.density, n.cdf);
+        }
         case LIGER_ACT_GELU_TANH: {
-            // s + p s (1 - s) d(arg)/dp; past 64 s is 0 or 1 (and p^2 may be infinite)
-            const float q = p > 64.f ? 64.f : p < -64.f ? -64.f : p;
+            // s + p s (1 - s) d(arg)/dp; past 64 s is 0 or 1, and p^2 may be infinite (not that of a half-precision p)
+            const float q = FAST ? p : p > 64.f ? 64.f : p < -64.f ? -64.f : p;
             const float s = sigmoid<FAST>(tanh_arg(q));
             const float d = fmaf(6.f * 0.79788456080286536f * 0.044715f, q * q, 2.f * 0.79788456080286536f);
             return fmaf(q * s * (1.f - s), d, s);

@@ -10,7 +10,7 @@ namespace {
 constexpr int64_t kSmallTokens = 128;
 constexpr unsigned kDpShares = 8;   // most blocks of a cluster that share the rows of a column sum
 constexpr int64_t kDpLong = 2048, kDpParts = 64;
-constexpr int kDpRows = 4;
+constexpr int kDpRows = 3;
 
 // dP = dY act'(P) and db, in one pass: a block takes some columns and its share of the rows, the blocks of a
 // cluster all rows of the same columns.  The column sums go from threads to the block over shared memory, and
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(256) linear_dp(const T* dy, const TPRE* pre, T
 // bf16 in whole 16-byte vectors: LX threads of 8 columns a row, 256 / LX rows side by side, kDpRows of them in flight
 // a thread.
 template <int ACT, int LX>
-__global__ void __launch_bounds__(256, 3) linear_dp_vec(const __nv_bfloat16* dy, const __half* pre, __nv_bfloat16* dp,
+__global__ void __launch_bounds__(256, 4) linear_dp_vec(const __nv_bfloat16* dy, const __half* pre, __nv_bfloat16* dp,
                                                         __nv_bfloat16* db, float* part, int64_t rows, int cols) {
     constexpr int SL = 256 / LX, C = LX * 8;   // row slices, columns
     __shared__ float red[SL][C + 4], sums[C];

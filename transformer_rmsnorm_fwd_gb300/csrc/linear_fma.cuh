@@ -155,9 +155,9 @@ int launch_fma_gemm(const char* who, const TA* A, const TB* B, const FmaGemm& g,
     auto tiles = [&](int ft) { return ceil_div(g.M, ft) * ceil_div(g.N, ft); };
     if (tiles(128) >= sm_count())
         return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128>, dim3(static_cast<unsigned>(tiles(128))), 256, 0, st, A, B, g, ep);
-    // K over so many blocks that all of them are still resident at once (three on an SM), 64 k at least each
+    // K over so many blocks that every SM has at most one, 64 k at least each
     int ranks = 1;
-    while (ranks < 8 && 2 * tiles(64) * ranks <= 3 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
+    while (ranks < 8 && 2 * tiles(64) * ranks <= sm_count() && g.K >= 128 * ranks) ranks *= 2;
     return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64>, dim3(static_cast<unsigned>(tiles(64) * ranks)),
                           dim3(static_cast<unsigned>(ranks)), 256, 0, st, A, B, g, ep);
 }
