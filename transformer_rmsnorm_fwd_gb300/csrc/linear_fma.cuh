@@ -34,132 +34,172 @@ __device__ __forceinline__ void fma_store(const FmaGemm& g, const FmaEpi<TO, TPR
     stf(ep.out + o, v);
 }
 
-// Tiles of FT x FT, 256 threads with FT / 16 squared outputs each, kFK k at a time (fp32: 8 KB of an operand) through two shared
-// buffers, the next ones loaded to registers while these are used.  FT = 128: 64 FMA for 16 values read (bound by FMA issue).  FT = 64,
-// for fewer outputs: K split over a cluster of blocks, whose tiles are joined in order over distributed shared memory.
-template <typename TA, typename TB, typename TO, typename TPRE, int FT>
-__global__ void __launch_bounds__(256, FT == 64 ? 3 : 2) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {
-    constexpr int kFK = 2048 / FT;
-    constexpr int PT = FT / 16;             // outputs of a thread in each direction
-    constexpr int LD = FT * kFK / 256;      // elements of an operand that a thread loads a step
-    struct Bufs {
-        float A[2][kFK][FT + 4], B[2][kFK][FT + 4];
-    };
-    constexpr int WORDS = sizeof(Bufs) / 4 > FT * FT ? sizeof(Bufs) / 4 : FT * FT;   // (the tile of sums: FT = 64 only)
-    __shared__ __align__(16) float mem[FT == 64 ? WORDS : sizeof(Bufs) / 4];
-    Bufs& s = *reinterpret_cast<Bufs*>(mem);
+// Tiles of FM x FN by 16 x 16 threads, FK k at a time through two shared buffers, the next ones loaded to registers while
+// these are used.  The arithmetic is on column pairs with the packed fp32x2 fma (single fmas stall on their register reads: 31
+// TFLOP/s at 2048^3 in 128 x 128 tiles); for that A's elements stand in shared memory twice, so that a pair is
+// read as it is needed.  Consecutive threads load consecutive
+// elements of an operand's contiguous dimension; inside the matrices without checks.
+//   128 x 128   where there are tiles enough for every SM
+//   64 x 64     fewer outputs: K split over a cluster of blocks, whose tiles are joined in order over distributed shared memory
+//   16 x 64     up to 16 rows, likewise
+template <int FM, int FN>
+struct FmaTile {
+    static constexpr int FK = FM == 128 ? 8 : 16;
+    static constexpr int SA = 2 * FM + 4, SB = FN + 4;   // words of a shared row of k
+    static constexpr int WORDS = 2 * FK * (SA + SB);
+};
+template <typename TA, typename TB, typename TO, typename TPRE, int FM, int FN>
+__global__ void __launch_bounds__(256, FM == 128 ? 2 : 3) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {
+    using Tile = FmaTile<FM, FN>;
+    constexpr int FK = Tile::FK, SA = Tile::SA, SB = Tile::SB, PM = FM / 16, PN = FN / 16;
+    constexpr int NA = FM * FK / 256, NB = FN * FK / 256;   // elements of an operand that a thread loads a step
+    __shared__ __align__(16) float mem[Tile::WORDS];   // two buffers of A, two of B; then the tile of sums
+    float* const sa = mem;
+    float* const sb = mem + 2 * FK * SA;
     const uint32_t rank = block_in_cluster(), ranks = blocks_in_cluster();
-    const unsigned tn = (static_cast<unsigned>(g.N) + FT - 1) / FT, tile = blockIdx.x / ranks, tile_m = tile / tn;
-    const int64_t m0 = static_cast<int64_t>(tile_m) * FT, n0 = static_cast<int64_t>(tile - tile_m * tn) * FT;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int steps = (g.K + kFK - 1) / kFK;
-    const int k0 = static_cast<int>(static_cast<int64_t>(steps) * rank / ranks) * kFK;
-    const int k1 = min(g.K, static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / ranks) * kFK);
+    const unsigned tn = (static_cast<unsigned>(g.N) + FN - 1) / FN, tile = blockIdx.x / ranks, tile_m = tile / tn;
+    const int64_t m0 = static_cast<int64_t>(tile_m) * FM, n0 = static_cast<int64_t>(tile - tile_m * tn) * FN;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int steps = (g.K + FK - 1) / FK;
+    const int k0 = static_cast<int>(static_cast<int64_t>(steps) * rank / ranks) * FK;
+    const int k1 = min(g.K, static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / ranks) * FK);
     wait_for_stream();
-    // consecutive threads take consecutive elements of each operand's contiguous dimension: element i of a thread
-    // stands im, ik further along
-    const bool ak = g.sak == 1, bn = g.sbn == 1;
-    const int tid = threadIdx.x;
-    const int am = ak ? tid / kFK : tid % FT, ka = ak ? tid % kFK : tid / FT, aim = ak ? 256 / kFK : 0, aik = ak ? 0 : 256 / FT;
-    const int nb = bn ? tid % FT : tid / kFK, kb = bn ? tid / FT : tid % kFK, bin = bn ? 0 : 256 / kFK, bik = bn ? 256 / FT : 0;
-    const TA* pa = A + (m0 + am) * g.sam + ka * g.sak;
-    const TB* pb = B + (n0 + nb) * g.sbn + kb * g.sbk;
-    const int64_t ai = aim * g.sam + aik * g.sak, bi = bin * g.sbn + bik * g.sbk;
-    float ra[LD], rb[LD];
+    // k contiguous: FK threads along k, the elements of a thread 256 / FK rows apart; else the rows' threads side by
+    // side, and 256 / F k apart
+    const bool ak = g.sak == 1, bk = g.sbk == 1;
+    const int am = ak ? tid / FK : tid % FM, ka = ak ? tid % FK : tid / FM, am_i = ak ? 256 / FK : 0, ka_i = ak ? 0 : 256 / FM;
+    const int bn = bk ? tid / FK : tid % FN, kb = bk ? tid % FK : tid / FN, bn_i = bk ? 256 / FK : 0, kb_i = bk ? 0 : 256 / FN;
+    const TA* pa = A + (m0 + am) * g.sam + (k0 + ka) * g.sak;   // this thread's first elements of the next step
+    const TB* pb = B + (n0 + bn) * g.sbn + (k0 + kb) * g.sbk;
+    const int64_t da = am_i * g.sam + ka_i * g.sak, db = bn_i * g.sbn + kb_i * g.sbk, step_a = FK * g.sak, step_b = FK * g.sbk;
+    const bool inside = m0 + FM <= g.M && n0 + FN <= g.N;
+    float ra[NA], rb[NB];
     auto fetch = [&](int k) {
-        const TA* qa = pa + k * g.sak;
-        const TB* qb = pb + k * g.sbk;
+        const TA* qa = pa;
+        const TB* qb = pb;
+        if (inside && k + FK <= k1) {
 #pragma unroll
-        for (int i = 0; i < LD; ++i) {
-            ra[i] = m0 + am + i * aim < g.M && k + ka + i * aik < k1 ? ldf(qa + i * ai) : 0.f;
-            rb[i] = n0 + nb + i * bin < g.N && k + kb + i * bik < k1 ? ldf(qb + i * bi) : 0.f;
+            for (int i = 0; i < NA; ++i, qa += da) ra[i] = ldf(qa);
+#pragma unroll
+            for (int i = 0; i < NB; ++i, qb += db) rb[i] = ldf(qb);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NA; ++i, qa += da) ra[i] = m0 + am + i * am_i < g.M && k + ka + i * ka_i < k1 ? ldf(qa) : 0.f;
+#pragma unroll
+            for (int i = 0; i < NB; ++i, qb += db) rb[i] = n0 + bn + i * bn_i < g.N && k + kb + i * kb_i < k1 ? ldf(qb) : 0.f;
         }
+        pa += step_a;
+        pb += step_b;
     };
+    // in shared memory: A's element at row k, its row's place twice; B's once
+    const int wa = ka * SA + 2 * am, wa_i = ka_i * SA + 2 * am_i, wb = kb * SB + bn, wb_i = kb_i * SB + bn_i;
     auto put = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < LD; ++i) {
-            s.A[buf][ka + i * aik][am + i * aim] = ra[i];
-            s.B[buf][kb + i * bik][nb + i * bin] = rb[i];
-        }
+        for (int i = 0; i < NA; ++i) *reinterpret_cast<float2*>(sa + buf * FK * SA + wa + i * wa_i) = make_float2(ra[i], ra[i]);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) sb[buf * FK * SB + wb + i * wb_i] = rb[i];
     };
-    // a thread's outputs: rows ty * 4 + (0 .. 3) of each half of 64 rows, columns tx * 4 + (0 .. 3) likewise
-    float acc[PT][PT] = {};
+    // a thread's outputs: rows ty * 4 + (0 .. 3) of each 64 rows (or row ty of 16), columns tx * 4 + (0 .. 3) of each 64
+    float2 acc[PM][PN / 2];
+#pragma unroll
+    for (int i = 0; i < PM; ++i)
+#pragma unroll
+        for (int j = 0; j < PN / 2; ++j) acc[i][j] = make_float2(0.f, 0.f);
     int buf = 0;
     fetch(k0);
     put(0);
     __syncthreads();
-    for (int k = k0; k < k1; k += kFK) {
-        const bool more = k + kFK < k1;
-        if (more) fetch(k + kFK);
+    for (int k = k0; k < k1; k += FK) {
+        const bool more = k + FK < k1;
+        if (more) fetch(k + FK);
+        const float* ca = sa + buf * FK * SA;
+        const float* cb = sb + buf * FK * SB;
 #pragma unroll
-        for (int kk = 0; kk < kFK; ++kk) {
-            float av[PT], bv[PT];
+        for (int kk = 0; kk < FK; ++kk) {
+            float2 av[PM], bv[PN / 2];
+            if constexpr (PM == 1) {
+                av[0] = *reinterpret_cast<const float2*>(ca + kk * SA + 2 * ty);
+            } else {
 #pragma unroll
-            for (int h = 0; h < PT / 4; ++h) {
-                *reinterpret_cast<float4*>(av + 4 * h) = *reinterpret_cast<const float4*>(&s.A[buf][kk][h * 64 + ty * 4]);
-                *reinterpret_cast<float4*>(bv + 4 * h) = *reinterpret_cast<const float4*>(&s.B[buf][kk][h * 64 + tx * 4]);
+                for (int i = 0; i < PM; i += 2) {
+                    const float4 q = *reinterpret_cast<const float4*>(ca + kk * SA + 2 * ((i / 4) * 64 + ty * 4 + i % 4));
+                    av[i] = make_float2(q.x, q.y);
+                    av[i + 1] = make_float2(q.z, q.w);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < PT; ++i)
+            for (int h = 0; h < PN / 4; ++h) {
+                const float4 q = *reinterpret_cast<const float4*>(cb + kk * SB + h * 64 + tx * 4);
+                bv[2 * h] = make_float2(q.x, q.y);
+                bv[2 * h + 1] = make_float2(q.z, q.w);
+            }
 #pragma unroll
-                for (int j = 0; j < PT; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+            for (int i = 0; i < PM; ++i)
+#pragma unroll
+                for (int j = 0; j < PN / 2; ++j) acc[i][j] = __ffma2_rn(av[i], bv[j], acc[i][j]);
         }
         if (more) put(buf ^ 1);   // last read before the barrier of the step before
         __syncthreads();
         buf ^= 1;
     }
-    if (FT == 64 && ranks > 1) {
-        // the tile into shared memory, and rows rank, rank + ranks, ... of the cluster's sums out of it
+    auto row_of = [&](int i) { return PM == 1 ? ty : (i / 4) * 64 + ty * 4 + i % 4; };
+    if constexpr (FM <= 64) {
+        if (ranks > 1) {
+            // the tile into shared memory, and rows rank, rank + ranks, ... of the cluster's sums out of it
+            static_assert(FM * FN <= Tile::WORDS, "the tile fits the buffers");
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(mem + (ty * 4 + i) * 64 + tx * 4) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        __syncthreads();
-        cluster_barrier();
-        for (int m = static_cast<int>(rank) + static_cast<int>(ranks) * ty; m < 64; m += static_cast<int>(ranks) * 16) {
-            if (m0 + m >= g.M) break;
-            float4 v[8];
+            for (int i = 0; i < PM; ++i)
+                *reinterpret_cast<float4*>(mem + row_of(i) * FN + tx * 4) = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+            __syncthreads();
+            cluster_barrier();
+            for (int m = static_cast<int>(rank) + static_cast<int>(ranks) * ty; m < FM && m0 + m < g.M; m += static_cast<int>(ranks) * 16) {
+                float4 v[8];
 #pragma unroll
-            for (uint32_t q = 0; q < 8; ++q)
-                if (q < ranks) v[q] = peer_float4(mem + m * 64 + tx * 4, q);
+                for (uint32_t q = 0; q < 8; ++q)
+                    if (q < ranks) v[q] = peer_float4(mem + m * FN + tx * 4, q);
 #pragma unroll
-            for (uint32_t q = 1; q < 8; ++q)
-                if (q < ranks) {
-                    v[0].x += v[q].x;
-                    v[0].y += v[q].y;
-                    v[0].z += v[q].z;
-                    v[0].w += v[q].w;
-                }
-            const float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                for (uint32_t q = 1; q < 8; ++q)
+                    if (q < ranks) {
+                        v[0].x += v[q].x;
+                        v[0].y += v[q].y;
+                        v[0].z += v[q].z;
+                        v[0].w += v[q].w;
+                    }
+                const float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n0 + tx * 4 + j < g.N) fma_store(g, ep, m0 + m, n0 + tx * 4 + j, o[j]);
+                for (int j = 0; j < 4; ++j)
+                    if (n0 + tx * 4 + j < g.N) fma_store(g, ep, m0 + m, n0 + tx * 4 + j, o[j]);
+            }
+            __syncwarp();
+            cluster_barrier();   // no block exits while another reads its sums
+            return;
         }
-        __syncwarp();
-        cluster_barrier();   // no block exits while another reads its sums
-        return;
     }
 #pragma unroll
-    for (int i = 0; i < PT; ++i) {
-        const int64_t m = m0 + (i / 4) * 64 + ty * 4 + i % 4;
+    for (int i = 0; i < PM; ++i) {
+        const int64_t m = m0 + row_of(i);
         if (m >= g.M) continue;
 #pragma unroll
-        for (int j = 0; j < PT; ++j) {
+        for (int j = 0; j < PN; ++j) {
             const int64_t n = n0 + (j / 4) * 64 + tx * 4 + j % 4;
-            if (n < g.N) fma_store(g, ep, m, n, acc[i][j]);
+            if (n < g.N) fma_store(g, ep, m, n, j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x);
         }
     }
 }
 
 template <typename TA, typename TB, typename TO, typename TPRE>
 int launch_fma_gemm(const char* who, const TA* A, const TB* B, const FmaGemm& g, const FmaEpi<TO, TPRE>& ep, cudaStream_t st) {
-    auto tiles = [&](int ft) { return ceil_div(g.M, ft) * ceil_div(g.N, ft); };
-    if (tiles(128) >= sm_count())
-        return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128>, dim3(static_cast<unsigned>(tiles(128))), 256, 0, st, A, B, g, ep);
-    // K over so many blocks that every SM has at most one, 64 k at least each
+    auto tiles = [&](int fm, int fn) { return ceil_div(g.M, fm) * ceil_div(g.N, fn); };
+    if (tiles(128, 128) >= sm_count())
+        return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128, 128>, dim3(static_cast<unsigned>(tiles(128, 128))), 256, 0, st, A, B,
+                            g, ep);
+    // K over so many blocks that all of them are still resident at once (three on an SM), 64 k at least each
+    const int64_t n = g.M <= 16 ? tiles(16, 64) : tiles(64, 64);
     int ranks = 1;
-    while (ranks < 8 && 2 * tiles(64) * ranks <= sm_count() && g.K >= 128 * ranks) ranks *= 2;
-    return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64>, dim3(static_cast<unsigned>(tiles(64) * ranks)),
-                          dim3(static_cast<unsigned>(ranks)), 256, 0, st, A, B, g, ep);
+    while (ranks < 8 && 2 * n * ranks <= 3 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
+    const dim3 grid(static_cast<unsigned>(n * ranks)), cluster(static_cast<unsigned>(ranks));
+    return g.M <= 16 ? launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 16, 64>, grid, cluster, 256, 0, st, A, B, g, ep)
+                     : launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
 }
 
 }  // namespace
