@@ -35,21 +35,22 @@ __device__ __forceinline__ void fma_store(const FmaGemm& g, const FmaEpi<TO, TPR
 }
 
 // Tiles of FM x FN by 16 x 16 threads, FK k at a time through two shared buffers, the next ones loaded to registers while
-// these are used.  The arithmetic is on column pairs with the packed fp32x2 fma (single fmas stall on their register reads: 31
-// TFLOP/s at 2048^3 in 128 x 128 tiles); for that A's elements stand in shared memory twice, so that a pair is
-// read as it is needed.  Consecutive threads load consecutive
+// these are used.  The arithmetic is on column pairs with the packed fp32x2 fma.  Consecutive threads load consecutive
 // elements of an operand's contiguous dimension; inside the matrices without checks.
-//   128 x 128   where there are tiles enough for every SM
-//   64 x 64     fewer outputs: K split over a cluster of blocks, whose tiles are joined in order over distributed shared memory
-//   16 x 64     up to 16 rows, likewise
+//   128 x 128   where there are tiles for every SM: 2048 x 2048 x 2048 in 411 us (42 TFLOP/s; the rounds of 256 tiles leave
+//               a sixth of the SMs' places empty), bound by fma issue beside the shared-memory reads
+//   64 x 64     fewer outputs: K split over a cluster of blocks, whose tiles are joined in order over distributed shared memory:
+//               300 x 257 x 1001 in 12.8 us, bound by the latencies of its few steps (in 128 x 64 tiles 15.3)
+//   16 x 64     up to 16 rows: 4 x 2048 x 2048 in 17.8 us, 32.9 in tiles of 64 rows
 template <int FM, int FN>
 struct FmaTile {
-    static constexpr int FK = FM == 128 ? 8 : 16;
-    static constexpr int SA = 2 * FM + 4, SB = FN + 4;   // words of a shared row of k
-    static constexpr int WORDS = 2 * FK * (SA + SB);
+    static constexpr int FK = 16;
+    static constexpr bool SPLIT = FM * FN <= 8192;   // its sums fit the shared memory, for a join over a cluster
+    static constexpr int SA = FM + 4, SB = FN + 4;   // words of a shared row of k
+    static constexpr int BUFS = 2 * FK * (SA + SB), WORDS = SPLIT && BUFS < FM * FN ? FM * FN : BUFS;
 };
 template <typename TA, typename TB, typename TO, typename TPRE, int FM, int FN>
-__global__ void __launch_bounds__(256, FM == 128 ? 2 : 3) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {
+__global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {
     using Tile = FmaTile<FM, FN>;
     constexpr int FK = Tile::FK, SA = Tile::SA, SB = Tile::SB, PM = FM / 16, PN = FN / 16;
     constexpr int NA = FM * FK / 256, NB = FN * FK / 256;   // elements of an operand that a thread loads a step
@@ -92,10 +93,10 @@ __global__ void __launch_bounds__(256, FM == 128 ? 2 : 3) fma_gemm(const TA* A, 
         pb += step_b;
     };
     // in shared memory: A's element at row k, its row's place twice; B's once
-    const int wa = ka * SA + 2 * am, wa_i = ka_i * SA + 2 * am_i, wb = kb * SB + bn, wb_i = kb_i * SB + bn_i;
+    const int wa = ka * SA + am, wa_i = ka_i * SA + am_i, wb = kb * SB + bn, wb_i = kb_i * SB + bn_i;
     auto put = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < NA; ++i) *reinterpret_cast<float2*>(sa + buf * FK * SA + wa + i * wa_i) = make_float2(ra[i], ra[i]);
+        for (int i = 0; i < NA; ++i) sa[buf * FK * SA + wa + i * wa_i] = ra[i];
 #pragma unroll
         for (int i = 0; i < NB; ++i) sb[buf * FK * SB + wb + i * wb_i] = rb[i];
     };
@@ -118,13 +119,16 @@ __global__ void __launch_bounds__(256, FM == 128 ? 2 : 3) fma_gemm(const TA* A, 
         for (int kk = 0; kk < FK; ++kk) {
             float2 av[PM], bv[PN / 2];
             if constexpr (PM == 1) {
-                av[0] = *reinterpret_cast<const float2*>(ca + kk * SA + 2 * ty);
+                const float q = ca[kk * SA + ty];
+                av[0] = make_float2(q, q);
             } else {
 #pragma unroll
-                for (int i = 0; i < PM; i += 2) {
-                    const float4 q = *reinterpret_cast<const float4*>(ca + kk * SA + 2 * ((i / 4) * 64 + ty * 4 + i % 4));
-                    av[i] = make_float2(q.x, q.y);
-                    av[i + 1] = make_float2(q.z, q.w);
+                for (int h = 0; h < PM / 4; ++h) {
+                    const float4 q = *reinterpret_cast<const float4*>(ca + kk * SA + h * 64 + ty * 4);
+                    av[4 * h] = make_float2(q.x, q.x);
+                    av[4 * h + 1] = make_float2(q.y, q.y);
+                    av[4 * h + 2] = make_float2(q.z, q.z);
+                    av[4 * h + 3] = make_float2(q.w, q.w);
                 }
             }
 #pragma unroll
@@ -143,10 +147,9 @@ __global__ void __launch_bounds__(256, FM == 128 ? 2 : 3) fma_gemm(const TA* A, 
         buf ^= 1;
     }
     auto row_of = [&](int i) { return PM == 1 ? ty : (i / 4) * 64 + ty * 4 + i % 4; };
-    if constexpr (FM <= 64) {
+    if constexpr (Tile::SPLIT) {
         if (ranks > 1) {
             // the tile into shared memory, and rows rank, rank + ranks, ... of the cluster's sums out of it
-            static_assert(FM * FN <= Tile::WORDS, "the tile fits the buffers");
 #pragma unroll
             for (int i = 0; i < PM; ++i)
                 *reinterpret_cast<float4*>(mem + row_of(i) * FN + tx * 4) = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
@@ -198,8 +201,8 @@ int launch_fma_gemm(const char* who, const TA* A, const TB* B, const FmaGemm& g,
     int ranks = 1;
     while (ranks < 8 && 2 * n * ranks <= 3 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
     const dim3 grid(static_cast<unsigned>(n * ranks)), cluster(static_cast<unsigned>(ranks));
-    return g.M <= 16 ? launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 16, 64>, grid, cluster, 256, 0, st, A, B, g, ep)
-                     : launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
+    if (g.M <= 16) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 16, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
+    return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
 }
 
 }  // namespace
