@@ -148,7 +148,7 @@ int liger_rope_scaled_bwd(const void* dq, const void* dk, void* dq_out, void* dk
 
 /* -------------------- token log-probabilities, entropy, alternatives
  * logits [T, V], row t at logits + t ld (ld >= V), dtype; with z = logits[t] /
- * temperature (> 0):
+ * temperature (at least 1e-30):
  *     row_max[t] = max_v logits[t, v]
  *     log_sum[t] = log sum_v exp(z_v - row_max[t] / temperature)
  *     logp[t] = z[tokens[t]] - row_max[t] / temperature - log_sum[t]

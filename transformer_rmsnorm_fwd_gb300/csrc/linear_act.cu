@@ -224,7 +224,9 @@ int64_t pair_tiles(int64_t M, int64_t N) {
     return ceil_div(M, static_cast<int64_t>(tc::TileCfg<1>::TM)) * ceil_div(N, static_cast<int64_t>(tc::BN));
 }
 // Whether T tokens by F features go in 128-feature tiles (linear_small.cuh) and not in 256 x 256 tiles of CTA pairs.
-bool goes_small(int64_t T, int64_t F) { return T <= kSmallTokens || 2 * pair_tiles(T, F) <= sm_count() / 2; }
+bool goes_small(int64_t T, int64_t F) {
+    return F <= 65535 * int64_t{tc::kSmallRows} && (T <= kSmallTokens || 2 * pair_tiles(T, F) <= sm_count() / 2);
+}
 int small_tokens(int64_t T) { return T <= 256 ? 256 : 128; }
 
 int fwd_tc(const void* X, const void* W, const void* bias, const void* residual, void* Y, void* pre, int64_t T, int64_t H,

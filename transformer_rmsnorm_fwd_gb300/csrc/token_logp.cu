@@ -580,8 +580,8 @@ int check_logits(const char* who, int64_t T, int64_t V, int64_t ld, float temper
     if (dtype != LIGER_F32 && dtype != LIGER_BF16) return fail(LIGER_ERR_DTYPE, "%s: dtype %d", who, dtype);
     if (T < 0 || T > 2147483647LL || V <= 0 || V > (1 << 30) || ld < V || ld > (int64_t{1} << 40))
         return fail(LIGER_ERR_SHAPE, "%s: T=%lld V=%lld ld=%lld", who, (long long)T, (long long)V, (long long)ld);
-    if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.0f / temperature))
-        return fail(LIGER_ERR_SHAPE, "%s: temperature must be > 0", who);
+    if (!(temperature >= 1e-30f) || !isfinite(temperature))   // (so that logits over it stay in range of the arithmetic)
+        return fail(LIGER_ERR_SHAPE, "%s: temperature must be at least 1e-30", who);
     return LIGER_OK;
 }
 bool off(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
