@@ -51,6 +51,8 @@ def _lib():
     if _loaded is None:
         import torch as t
         lib = _native.load()
+        if t.cuda.is_available():
+            t.cuda.init()       # the calls ask for the current device without it
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(lib, name)
             fn.argtypes = args
@@ -90,19 +92,15 @@ def _raise(dev, dtype, shape, t):
 def _like(dev, dtype, shape, *ts):
     """Those of the tensors that are given are contiguous, on device dev, of this dtype and shape."""
     for t in ts:
-        if t is not None and (t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev):
             _raise(dev, dtype, shape, t)
 
 
 def _hold(dev, dtype, n, *ts):
     """As _like, for any shape of n elements."""
     for t in ts:
-        if t is not None and (t.get_device() != dev or t.dtype is not dtype or t.numel() != n or not t.is_contiguous()):
+        if t is not None and (t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev):
             _raise(dev, dtype, (n,), t)
-
-
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _bytes(dev, ws):
@@ -125,13 +123,13 @@ def liger_layernorm_fwd(x, w, b, y, mean=None, rstd=None, eps: float = 1e-5):
 
     x, y [..., cols]; w, b [cols] or None; mean, rstd float32, one per row, or None.  y may be x."""
     lib = _loaded or _lib()
-    dev, dt = torch.cuda.current_device(), x.dtype
+    dev, dt = torch._C._cuda_getDevice(), x.dtype
     rows, cols = _rows(x)
     _like(dev, dt, x.shape, x, y)
     _like(dev, dt, x.shape[-1:], w, b)
     _hold(dev, torch.float32, rows, mean, rstd)
     _check(lib.liger_layernorm_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(y), _ptr(mean), _ptr(rstd), rows, cols, eps, _code(dt),
-                                   _raw_stream(dev)))
+                                   torch._C._cuda_getCurrentRawStream(dev)))
     return y
 
 
@@ -143,14 +141,14 @@ def liger_layernorm_bwd(dy, x, w, mean, rstd, dx, dw, db, ws, dres=None):
     """Backward of liger_layernorm_fwd: dx (plus dres, the gradient past the norm, if given), dw and db (each may be None).
     dx may be dy or dres."""
     lib = _loaded or _lib()
-    dev, dt = torch.cuda.current_device(), x.dtype
+    dev, dt = torch._C._cuda_getDevice(), x.dtype
     rows, cols = _rows(x)
     _like(dev, dt, x.shape, x, dy, dx, dres)
     _like(dev, dt, x.shape[-1:], w, dw, db)
     _hold(dev, torch.float32, rows, mean, rstd)
     pws, nws = _bytes(dev, ws)
     _check(lib.liger_layernorm_bwd(_ptr(dy), _ptr(dres), _ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw),
-                                   _ptr(db), pws, nws, rows, cols, _code(dt), _raw_stream(dev)))
+                                   _ptr(db), pws, nws, rows, cols, _code(dt), torch._C._cuda_getCurrentRawStream(dev)))
     return dx, dw, db
 
 
@@ -165,7 +163,7 @@ def liger_linear_act_fwd(X, W, Y, bias=None, residual=None, act: str = "none", p
     X [T, H], W [N, H], Y and residual [T, N], bias [N]; act "none", "relu", "gelu", "gelu_tanh" or "silu"; pre [T, N] or
     None: X W^T + bias kept for the backward, float16 for bfloat16 tensors, else float32.  residual may be Y."""
     lib = _loaded or _lib()
-    dev, dt = torch.cuda.current_device(), X.dtype
+    dev, dt = torch._C._cuda_getDevice(), X.dtype
     T, H = X.shape
     N = W.shape[0]
     _like(dev, dt, (T, H), X)
@@ -174,7 +172,7 @@ def liger_linear_act_fwd(X, W, Y, bias=None, residual=None, act: str = "none", p
     _like(dev, dt, (N,), bias)
     _like(dev, _kept_type(dt), (T, N), pre)
     _check(lib.liger_linear_act_fwd(_ptr(X), _ptr(W), _ptr(bias), _ptr(residual), _ptr(Y), _ptr(pre), T, H, N,
-                                    _choice(_ACTS, act, "act"), _code(dt), _raw_stream(dev)))
+                                    _choice(_ACTS, act, "act"), _code(dt), torch._C._cuda_getCurrentRawStream(dev)))
     return Y
 
 
@@ -186,7 +184,7 @@ def liger_linear_act_bwd(dY, X, W, dX, dW, db, ws, pre=None, act: str = "none"):
     """Backward of liger_linear_act_fwd: dX, dW and db (each may be None) from dY and what the forward kept in pre (None with
     act "none"); ws as liger_linear_act_bwd_workspace says.  The gradient of the residual is dY."""
     lib = _loaded or _lib()
-    dev, dt = torch.cuda.current_device(), X.dtype
+    dev, dt = torch._C._cuda_getDevice(), X.dtype
     T, H = X.shape
     N = W.shape[0]
     _like(dev, dt, (T, H), X, dX)
@@ -196,7 +194,7 @@ def liger_linear_act_bwd(dY, X, W, dX, dW, db, ws, pre=None, act: str = "none"):
     _like(dev, _kept_type(dt), (T, N), pre)
     pws, nws = _bytes(dev, ws)
     _check(lib.liger_linear_act_bwd(_ptr(dY), _ptr(X), _ptr(W), _ptr(pre), _ptr(dX), _ptr(dW), _ptr(db), pws, nws, T, H, N,
-                                    _choice(_ACTS, act, "act"), _code(dt), _raw_stream(dev)))
+                                    _choice(_ACTS, act, "act"), _code(dt), torch._C._cuda_getCurrentRawStream(dev)))
     return dX, dW, db
 
 
@@ -205,22 +203,25 @@ def _heads(dev, dt, t, B, S, D):
     """Head count and token stride of a [B, S, heads, D] view (or None: 0 heads)."""
     if t is None:
         return 0, 0
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != S or t.shape[3] != D:
-        raise ValueError(f"expected [batch, seq, heads, head_dim] = [{B}, {S}, heads, {D}], got {tuple(t.shape)}")
-    if t.get_device() != dev or t.dtype is not dt:
-        _raise(dev, dt, t.shape, t)
-    sb, ss, sh, sd = t.stride()
-    h = t.shape[2]
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 4:
+        raise ValueError(f"expected [batch, seq, heads, head_dim], got {tuple(shape)}")
+    b, s, h, d = shape
+    if b != B or s != S or d != D or t.get_device() != dev or t.dtype is not dt:
+        if b == B and s == S and d == D:
+            _raise(dev, dt, shape, t)
+        raise ValueError(f"expected [batch, seq, heads, head_dim] = [{B}, {S}, heads, {D}], got {tuple(shape)}")
+    sb, ss, sh, sd = strides
     if B == 0 or S == 0 or h == 0:
         return h, h * D
     if (sd != 1 and D > 1) or (sh != D and h > 1) or (S > 1 and B > 1 and sb != S * ss):
-        raise ValueError(f"heads must stand dense and tokens evenly apart (got strides {tuple(t.stride())})")
+        raise ValueError(f"heads must stand dense and tokens evenly apart (got strides {strides})")
     return h, ss if S > 1 else sb if B > 1 else h * D
 
 
 def _rope_scaled(fn, q, k, q_out, k_out, rotary_dim, pos, theta, pairing, scaling, factor, low, high, orig_len, attn_factor):
     lib = _loaded or _lib()
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     ref = q if q is not None else k
     if ref is None or ref.dim() != 4:
         raise ValueError("q or k is required, [batch, seq, heads, head_dim]")
@@ -228,14 +229,14 @@ def _rope_scaled(fn, q, k, q_out, k_out, rotary_dim, pos, theta, pairing, scalin
     B, S, _, D = ref.shape
     Hq, qs = _heads(dev, dt, q, B, S, D)
     Hk, ks = _heads(dev, dt, k, B, S, D)
-    Hqo, qos = _heads(dev, dt, q_out, B, S, D)
-    Hko, kos = _heads(dev, dt, k_out, B, S, D)
+    Hqo, qos = (Hq, qs) if q_out is q else _heads(dev, dt, q_out, B, S, D)
+    Hko, kos = (Hk, ks) if k_out is k else _heads(dev, dt, k_out, B, S, D)
     if Hqo != Hq or Hko != Hk:
         raise ValueError(f"outputs have {Hqo} and {Hko} heads, inputs {Hq} and {Hk}")
     _like(dev, torch.int32, (B, S), pos)
     _check(getattr(lib, fn)(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(pos), B, S, Hq, Hk, D, rotary_dim, qs, ks, qos,
                             kos, _choice(_PAIRINGS, pairing, "pairing"), theta, _choice(_SCALINGS, scaling, "scaling"), factor,
-                            low, high, orig_len, attn_factor, _code(dt), _raw_stream(dev)))
+                            low, high, orig_len, attn_factor, _code(dt), torch._C._cuda_getCurrentRawStream(dev)))
     return q_out, k_out
 
 
@@ -278,7 +279,7 @@ def liger_token_logp_fwd(logits, tokens, logp, row_max=None, log_sum=None, entro
     logits [T, V] with dense rows (any row stride); tokens int64 [T] with logp float32 [T], or both None; row_max, log_sum,
     entropy float32 [T] or None; top_logp float32 with top_ids int64 [T, k], or both None."""
     lib = _loaded or _lib()
-    dev, f32 = torch.cuda.current_device(), torch.float32
+    dev, f32 = torch._C._cuda_getDevice(), torch.float32
     T, V = logits.shape
     dt = logits.dtype
     ld = _logit_rows(dev, logits, T, V, dt)
@@ -293,7 +294,7 @@ def liger_token_logp_fwd(logits, tokens, logp, row_max=None, log_sum=None, entro
             top_ids = top_logp = None
     _check(lib.liger_token_logp_fwd(_ptr(logits), ld, _ptr(tokens), T, V, ignore_index, temperature, _ptr(logp),
                                     _ptr(row_max), _ptr(log_sum), _ptr(entropy), k, _ptr(top_logp), _ptr(top_ids), _code(dt),
-                                    _raw_stream(dev)))
+                                    torch._C._cuda_getCurrentRawStream(dev)))
     return logp
 
 
@@ -302,7 +303,7 @@ def liger_token_logp_bwd(logits, tokens, row_max, log_sum, g_logp, dlogits, entr
     """The gradient of the logits from g_logp and g_entropy (float32 [T], either may be None), with row_max, log_sum and
     entropy as liger_token_logp_fwd wrote them.  dlogits may be logits."""
     lib = _loaded or _lib()
-    dev, f32 = torch.cuda.current_device(), torch.float32
+    dev, f32 = torch._C._cuda_getDevice(), torch.float32
     T, V = logits.shape
     dt = logits.dtype
     ld, ldd = _logit_rows(dev, logits, T, V, dt), _logit_rows(dev, dlogits, T, V, dt)
@@ -310,5 +311,5 @@ def liger_token_logp_bwd(logits, tokens, row_max, log_sum, g_logp, dlogits, entr
     _hold(dev, f32, T, row_max, log_sum, entropy, g_logp, g_entropy)
     _check(lib.liger_token_logp_bwd(_ptr(logits), ld, _ptr(tokens), _ptr(row_max), _ptr(log_sum), _ptr(entropy),
                                     _ptr(g_logp), _ptr(g_entropy), T, V, ignore_index, temperature, _ptr(dlogits), ldd,
-                                    _code(dt), _raw_stream(dev)))
+                                    _code(dt), torch._C._cuda_getCurrentRawStream(dev)))
     return dlogits
