@@ -6,7 +6,10 @@ namespace liger {
 namespace {
 
 constexpr int kMaxPartRows = 1024;   // most partial rows of dw and of db
-constexpr size_t kFwdFlight = 64u * 1024u, kBwdFlight = 128u * 1024u;   // bytes of rows in flight on an SM that the rings aim at
+// Bytes of rows in flight on an SM that the rings aim at.  Forward of 32768 x 4096 bf16: 88 us with 32 KB, 85 with 64 to 192;
+// of 16384 x 8192 83, 83 and 88.  Backward: 192 KB where a row is 8 KB or more (16384 x 8192 bf16: 156 us, 167 with 64 or 128 KB;
+// 32768 x 4096: 155 and 158), 128 KB below (131072 x 512 bf16: 102 us, 104 with 192 KB).
+constexpr size_t kFwdFlight = 64u * 1024u, kBwdFlight = 128u * 1024u, kBwdFlightLong = 192u * 1024u;
 
 // ------------------------------------------------------------- any width
 // A block per row, elements strided over its threads; the row is read again from the caches for
@@ -324,24 +327,93 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, i
     }
 }
 
-// Rows that are no whole vectors: aligned windows around them (block_norm.cuh), EPT fixed columns a thread.
-template <typename T, int EPT, int NT>
-__global__ void __launch_bounds__(NT, 1) layer_norm_fwd_odd(LnFwd p, int nst, uint32_t wmax, int* err) {
+// Rows that are no whole vectors: aligned windows around them (block_norm.cuh).  A row starts `shift` elements into its
+// window; rows that lie a multiple of VEC apart have the same shift, and a block only takes such rows.  So the columns of
+// a thread's vectors stay the same from row to row, as do its weights, and only the first and the last vector of a
+// window, which the neighbouring rows share, go by elements.
+template <typename T> struct Span {
+    static constexpr int VEC = Vec<T>::N, NP = VEC / 2;
+    static constexpr uint32_t kAll = (1u << VEC) - 1u;
+    int shift, end, nv;   // the row is elements [shift, end) of its window of nv vectors
+    __device__ __forceinline__ Span(int64_t row, int64_t rows, int cols) {
+        shift = window_of<T>(row, rows, cols).shift;
+        end = shift + cols;
+        nv = (end + VEC - 1) / VEC;
+    }
+    // a bit for each element of vector v that is the row's
+    __device__ __forceinline__ uint32_t inside(int v) const {
+        const int lo = min(max(shift - v * VEC, 0), VEC), hi = min(max(end - v * VEC, 0), VEC);
+        return ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+    }
+    __device__ __forceinline__ void mask(uint32_t in, float2 (&f)[NP]) const {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            f[e].x = in >> (2 * e) & 1u ? f[e].x : 0.f;
+            f[e].y = in >> (2 * e + 1) & 1u ? f[e].y : 0.f;
+        }
+    }
+    // vector v of a row in global memory, by elements, 0 outside the row
+    __device__ __forceinline__ uint4 gather(const T* row, int v) const {
+        const uint32_t in = inside(v);
+        float f[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = in >> e & 1u ? ldf(row + v * VEC + e - shift) : 0.f;
+        return pack(f);
+    }
+    // the same from the row's window in shared memory
+    __device__ __forceinline__ uint4 take(const uint8_t* window, int v, uint32_t in) const {
+        uint4 u = *reinterpret_cast<const uint4*>(window + v * 16);
+        if (in == kAll) return u;
+        auto keep = [&](int i) {
+            if constexpr (VEC == 4) return in >> i & 1u ? 0xffffffffu : 0u;
+            else return (in >> (2 * i) & 1u ? 0xffffu : 0u) | (in >> (2 * i + 1) & 1u ? 0xffff0000u : 0u);
+        };
+        u.x &= keep(0);
+        u.y &= keep(1);
+        u.z &= keep(2);
+        u.w &= keep(3);
+        return u;
+    }
+    __device__ __forceinline__ void put(T* row, int v, uint32_t in, const float2 (&f)[NP]) const {
+        T* at = row - shift + v * VEC;
+        if (in == kAll) {
+            stg16_cs(at, pack2(f));
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            if (in >> (2 * e) & 1u) stf(at + 2 * e, f[e].x);
+            if (in >> (2 * e + 1) & 1u) stf(at + 2 * e + 1, f[e].y);
+        }
+    }
+    // The copy of the last row's window may stop short of its end: the elements behind go by plain stores, before the thread that
+    // asks for the copy arrives at its barrier.
+    static __device__ __forceinline__ void rest(uint8_t* window, const Window& win, const T* row, int cols) {
+        for (int c = win.tail; c < cols; ++c) reinterpret_cast<T*>(window)[win.shift + c] = row[c];
+    }
+};
+
+template <typename T, int VPT, int NT, int MB>
+__global__ void __launch_bounds__(NT, MB) layer_norm_fwd_odd(LnFwd p, int nst, uint32_t wmax, int* err) {
+    constexpr int VEC = Vec<T>::N, NP = VEC / 2;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ float red[2][NT / 32];
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    __shared__ __align__(16) float red[2][NT / 32];   // (slots of warps that the block has not hold 0)
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nt = blockDim.x;
     const uint32_t bars = smem_u32(sm + static_cast<size_t>(nst) * wmax);
     const T *x = static_cast<const T*>(p.x), *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
     T* y = static_cast<T*>(p.y);
     const float inv = 1.0f / static_cast<float>(p.cols);
     const int64_t step = gridDim.x;
     int64_t t = blockIdx.x;
+    const Span<T> span(t, p.rows, p.cols);
     auto issue = [&](int64_t row, int s) {
         const Window win = window_of<T>(row, p.rows, p.cols);
+        Span<T>::rest(sm + static_cast<size_t>(s) * wmax, win, x + row * p.cols, p.cols);
         mbar_expect_tx(bars + 8u * s, win.bytes);
         if (win.bytes > 0)
             bulk_g2s(smem_u32(sm + static_cast<size_t>(s) * wmax), static_cast<const uint8_t*>(p.x) + win.at, win.bytes, bars + 8u * s);
     };
+    if (tid < 2 * (NT / 32)) (&red[0][0])[tid] = 0.f;
     if (tid == 0)
         for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
     mbar_init_fence();
@@ -350,12 +422,14 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_fwd_odd(LnFwd p, int nst, ui
     if (tid == 0)
         for (int s = 0; s < nst; ++s)
             if (t + s * step < p.rows) issue(t + s * step, s);
-    float wf[EPT], bf[EPT];
+    uint4 cw[VPT], cb[VPT];
+    uint32_t in[VPT];   // 0: no vector of the row
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-        const int c = j * NT + tid;
-        wf[j] = w != nullptr && c < p.cols ? ldf(w + c) : 1.f;
-        bf[j] = b != nullptr && c < p.cols ? ldf(b + c) : 0.f;
+    for (int j = 0; j < VPT; ++j) {
+        in[j] = span.inside(j * nt + tid);
+        cw[j] = cb[j] = make_uint4(0, 0, 0, 0);
+        if (w != nullptr) cw[j] = span.gather(w, j * nt + tid);
+        if (b != nullptr) cb[j] = span.gather(b, j * nt + tid);
     }
     int turn = 0, s = 0;
     uint32_t ph = 0;
@@ -368,24 +442,25 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_fwd_odd(LnFwd p, int nst, ui
         return a;
     };
     for (; t < p.rows; t += step) {
-        const Window win = window_of<T>(t, p.rows, p.cols);
         ok = mbar_wait(bars + 8u * s, ph);
-        const T* xs = reinterpret_cast<const T*>(sm + static_cast<size_t>(s) * wmax) + win.shift;
+        const uint8_t* slot = sm + static_cast<size_t>(s) * wmax;
         const int64_t o = t * p.cols;
-        float f[EPT];
-        float sum = 0.f;
+        uint4 cx[VPT];
+        float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-            const int c = j * NT + tid;
-            f[j] = 0.f;
-            if (c < p.cols && ok) f[j] = c < win.tail ? ldf(xs + c) : ldf(x + o + c);
-            sum += f[j];
+        for (int j = 0; j < VPT; ++j) {
+            cx[j] = make_uint4(0, 0, 0, 0);
+            if (in[j] != 0 && ok) cx[j] = span.take(slot, j * nt + tid, in[j]);
+            float2 f[NP];
+            unpack2(cx[j], f);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) a = __fadd2_rn(a, f[e]);
         }
-        sum = warp_sum(sum);
+        float sum = warp_sum(a.x + a.y);
         if (lane == 0) red[turn][wid] = sum;
         ok = __syncthreads_and(ok ? 1 : 0) != 0;
         if (!ok) break;
-        if (tid == 0 && t + nst * step < p.rows) {   // every thread has its elements of the row
+        if (tid == 0 && t + nst * step < p.rows) {   // every thread has its vectors of the row
             fence_proxy_async_smem();
             issue(t + nst * step, s);
         }
@@ -394,20 +469,38 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_fwd_odd(LnFwd p, int nst, ui
             ph ^= 1u;
         }
         const float m = total() * inv;
-        sum = 0.f;
+        const float2 nm = make_float2(-m, -m);
+        a = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < EPT; ++j)
-            if (j * NT + tid < p.cols) {
-                f[j] -= m;
-                sum = fmaf(f[j], f[j], sum);
+        for (int j = 0; j < VPT; ++j)
+            if (in[j] != 0) {
+                float2 f[NP];
+                unpack2(cx[j], f);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) f[e] = __fadd2_rn(f[e], nm);
+                if (in[j] != Span<T>::kAll) span.mask(in[j], f);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) a = __ffma2_rn(f[e], f[e], a);
             }
-        sum = warp_sum(sum);
+        sum = warp_sum(a.x + a.y);
         if (lane == 0) red[turn][wid] = sum;
         __syncthreads();
         const float rs = inv_sqrt(fmaf(total(), inv, p.eps));
+        const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-        for (int j = 0; j < EPT; ++j)
-            if (j * NT + tid < p.cols) stf(y + o + j * NT + tid, fmaf(f[j] * rs, wf[j], bf[j]));
+        for (int j = 0; j < VPT; ++j)
+            if (in[j] != 0) {
+                float2 f[NP], g[NP], h[NP];
+                unpack2(cx[j], f);
+                unpack2(cw[j], g);
+                unpack2(cb[j], h);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    f[e] = __fmul2_rn(__fadd2_rn(f[e], nm), rs2);
+                    f[e] = w != nullptr ? __ffma2_rn(f[e], g[e], h[e]) : __fadd2_rn(f[e], h[e]);
+                }
+                span.put(y + o, j * nt + tid, in[j], f);
+            }
         if (tid == 0) {
             if (p.mean != nullptr) p.mean[t] = m;
             if (p.rstd != nullptr) p.rstd[t] = rs;
@@ -427,7 +520,7 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_fwd_odd(LnFwd p, int nst, ui
     }
     const float nan = __int_as_float(0x7FC00000);
     for (; t < p.rows; t += step) {
-        for (int c = tid; c < p.cols; c += NT) stf(y + t * p.cols + c, nan);
+        for (int c = tid; c < p.cols; c += nt) stf(y + t * p.cols + c, nan);
         if (tid == 0 && p.mean != nullptr) p.mean[t] = nan;
         if (tid == 0 && p.rstd != nullptr) p.rstd[t] = nan;
     }
@@ -691,12 +784,13 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_bwd_ring(LnBwd p, int tw, in
     }
 }
 
-// Rows that are no whole vectors: aligned windows around them (block_norm.cuh), EPT fixed columns a thread.
-template <typename T, int EPT, int NT>
-__global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, uint32_t wmax, int* err) {
+// Rows that are no whole vectors: windows of one shift a block, as in the forward.
+template <typename T, int VPT, int NT, int MB>
+__global__ void __launch_bounds__(NT, MB) layer_norm_bwd_odd(LnBwd p, int nst, uint32_t wmax, int* err) {
+    constexpr int VEC = Vec<T>::N, NP = VEC / 2;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ float red[2][2][NT / 32];
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    __shared__ float red[2][2][NT / 32];   // (slots of warps that the block has not hold 0)
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nt = blockDim.x;
     const T *dy = static_cast<const T*>(p.dy), *x = static_cast<const T*>(p.x), *dres = static_cast<const T*>(p.dres),
             *w = static_cast<const T*>(p.w);
     T* dx = static_cast<T*>(p.dx);
@@ -705,15 +799,21 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, ui
     const uint32_t bars = smem_u32(sm + static_cast<size_t>(nst) * slot_bytes);
     int64_t t = blockIdx.x;
     const int64_t step = gridDim.x;
+    const Span<T> span(t, p.rows, p.cols);
     auto issue = [&](int64_t row, int s) {
         const Window win = window_of<T>(row, p.rows, p.cols);
         const uint32_t bar = bars + 8u * s, dst = smem_u32(sm + static_cast<size_t>(s) * slot_bytes);
+        uint8_t* at = sm + static_cast<size_t>(s) * slot_bytes;
+        Span<T>::rest(at, win, dy + row * p.cols, p.cols);
+        Span<T>::rest(at + wmax, win, x + row * p.cols, p.cols);
+        if (res) Span<T>::rest(at + 2 * wmax, win, dres + row * p.cols, p.cols);
         mbar_expect_tx(bar, (res ? 3 : 2) * win.bytes);
         if (win.bytes == 0) return;
         bulk_g2s(dst, static_cast<const uint8_t*>(p.dy) + win.at, win.bytes, bar);
         bulk_g2s(dst + wmax, static_cast<const uint8_t*>(p.x) + win.at, win.bytes, bar);
         if (res) bulk_g2s(dst + 2 * wmax, static_cast<const uint8_t*>(p.dres) + win.at, win.bytes, bar);
     };
+    for (int i = tid; i < 4 * (NT / 32); i += nt) (&red[0][0][0])[i] = 0.f;
     if (tid == 0)
         for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
     mbar_init_fence();
@@ -722,11 +822,22 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, ui
     if (tid == 0)
         for (int s = 0; s < nst; ++s)
             if (t + s * step < p.rows) issue(t + s * step, s);
-    float wf[EPT], Sw[EPT], Sb[EPT];
+    uint4 cw[VPT];
+    uint32_t in[VPT];   // 0: no vector of the row
+    float2 Sw[VPT][NP], Sb[VPT][NP];
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-        wf[j] = w != nullptr && j * NT + tid < p.cols ? ldf(w + j * NT + tid) : 1.f;
-        Sw[j] = Sb[j] = 0.f;
+    for (int j = 0; j < VPT; ++j) {
+        in[j] = span.inside(j * nt + tid);
+        if (w != nullptr) {
+            cw[j] = span.gather(w, j * nt + tid);
+        } else {
+            float one[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) one[e] = 1.f;
+            cw[j] = pack(one);
+        }
+#pragma unroll
+        for (int e = 0; e < NP; ++e) Sw[j][e] = Sb[j][e] = make_float2(0.f, 0.f);
     }
     const float inv = 1.0f / static_cast<float>(p.cols);
     int s = 0, turn = 0;
@@ -739,29 +850,40 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, ui
             mn = p.mean[t + step];
             rn = p.rstd[t + step];
         }
-        const Window win = window_of<T>(t, p.rows, p.cols);
         ok = mbar_wait(bars + 8u * s, ph);
         const uint8_t* slot = sm + static_cast<size_t>(s) * slot_bytes;
         const int64_t o = t * p.cols;
-        auto get = [&](uint32_t so, const T* g, int c) {
-            return c < win.tail ? ldf(reinterpret_cast<const T*>(slot + so) + win.shift + c) : ldf(g + o + c);
-        };
-        float g[EPT], xh[EPT], r[EPT];
-        float s1 = 0.f, s2 = 0.f;
+        const float2 nm = make_float2(-m, -m), rs2 = make_float2(rs, rs);
+        uint4 cd[VPT], cx[VPT], cr[VPT];
+        float2 a1 = make_float2(0.f, 0.f), a2 = a1;
+        // a vector of the normalised row, 0 outside the row
+        auto normed = [&](const uint4& u, uint32_t in, float2 (&f)[NP]) {
+            unpack2(u, f);
 #pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-            const int c = j * NT + tid;
-            g[j] = xh[j] = r[j] = 0.f;
-            if (c >= p.cols || !ok) continue;
-            const float d = get(0, dy, c);
-            xh[j] = (get(wmax, x, c) - m) * rs;
-            if (res) r[j] = get(2 * wmax, dres, c);
-            g[j] = d * wf[j];
-            s1 += g[j];
-            s2 = fmaf(g[j], xh[j], s2);
-            Sw[j] = fmaf(d, xh[j], Sw[j]);
-            Sb[j] += d;
+            for (int e = 0; e < NP; ++e) f[e] = __fmul2_rn(__fadd2_rn(f[e], nm), rs2);
+            if (in != Span<T>::kAll) span.mask(in, f);
+        };
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * nt + tid;
+            if (in[j] == 0 || !ok) continue;
+            cd[j] = span.take(slot, v, in[j]);
+            cx[j] = span.take(slot + wmax, v, in[j]);
+            if (res) cr[j] = span.take(slot + 2 * wmax, v, in[j]);
+            float2 d[NP], h[NP], g[NP];
+            unpack2(cd[j], d);
+            unpack2(cw[j], g);
+            normed(cx[j], in[j], h);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                g[e] = __fmul2_rn(d[e], g[e]);
+                a1 = __fadd2_rn(a1, g[e]);
+                a2 = __ffma2_rn(g[e], h[e], a2);
+                Sw[j][e] = __ffma2_rn(d[e], h[e], Sw[j][e]);
+                Sb[j][e] = __fadd2_rn(Sb[j][e], d[e]);
+            }
         }
+        float s1 = a1.x + a1.y, s2 = a2.x + a2.y;
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) {
             s1 += __shfl_xor_sync(0xffffffffu, s1, i);
@@ -773,7 +895,7 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, ui
         }
         ok = __syncthreads_and(ok ? 1 : 0) != 0;
         if (!ok) break;
-        if (tid == 0 && t + nst * step < p.rows) {   // every thread has its elements of the row
+        if (tid == 0 && t + nst * step < p.rows) {   // every thread has its vectors of the row
             fence_proxy_async_smem();
             issue(t + nst * step, s);
         }
@@ -788,11 +910,22 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, ui
             s2 += red[turn][1][i];
         }
         turn ^= 1;
-        s1 *= inv;
-        s2 *= inv;
+        const float2 n1 = make_float2(-s1 * inv, -s1 * inv), n2 = make_float2(-s2 * inv, -s2 * inv);
 #pragma unroll
-        for (int j = 0; j < EPT; ++j)
-            if (j * NT + tid < p.cols) stf(dx + o + j * NT + tid, fmaf(rs, g[j] - s1 - xh[j] * s2, r[j]));
+        for (int j = 0; j < VPT; ++j) {
+            if (in[j] == 0) continue;
+            float2 d[NP], h[NP], g[NP], r[NP];
+            unpack2(cd[j], d);
+            unpack2(cw[j], g);
+            normed(cx[j], in[j], h);
+            if (res) unpack2(cr[j], r);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                d[e] = __ffma2_rn(h[e], n2, __ffma2_rn(d[e], g[e], n1));
+                d[e] = res ? __ffma2_rn(rs2, d[e], r[e]) : __fmul2_rn(rs2, d[e]);
+            }
+            span.put(dx + o, j * nt + tid, in[j], d);
+        }
     }
     float* pw = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
     float* pb = p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * p.cols : nullptr;
@@ -810,15 +943,17 @@ __global__ void __launch_bounds__(NT, 1) layer_norm_bwd_odd(LnBwd p, int nst, ui
             }
         }
         for (int64_t row = t; row < p.rows; row += step)
-            for (int c = tid; c < p.cols; c += NT) stf(dx + row * p.cols + c, nan);
+            for (int c = tid; c < p.cols; c += nt) stf(dx + row * p.cols + c, nan);
     }
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-        const int c = j * NT + tid;
-        if (c >= p.cols) continue;
-        if (pw != nullptr) pw[c] = ok ? Sw[j] : nan;
-        if (pb != nullptr) pb[c] = ok ? Sb[j] : nan;
-    }
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int col = (j * nt + tid) * VEC + e - span.shift;
+            if ((in[j] >> e & 1u) == 0) continue;
+            if (pw != nullptr) pw[col] = !ok ? nan : e % 2 ? Sw[j][e / 2].y : Sw[j][e / 2].x;
+            if (pb != nullptr) pb[col] = !ok ? nan : e % 2 ? Sb[j][e / 2].y : Sb[j][e / 2].x;
+        }
 }
 
 // dw (blockIdx.y 0) and db (1) from the partial rows: a block of 32 warps over 32 groups of V columns, warp w
@@ -901,17 +1036,24 @@ int fwd_ring(const LnFwd& p, int nvec, cudaStream_t st) {
     return fwd_ring_teams<T, VPT, NT, MB, 1>(p, tw, st);
 }
 
-template <typename T, int EPT, int NT>
-int fwd_odd(const LnFwd& p, cudaStream_t st) {
-    constexpr auto k = layer_norm_fwd_odd<T, EPT, NT>;
+// blocks of the odd kernels, whose rows must have one shift: the grid divides into whole vectors where a block takes
+// more than one row
+template <typename T> int64_t odd_grid(int64_t rows, int64_t most) {
+    return rows <= most ? rows : most / Vec<T>::N * Vec<T>::N;
+}
+
+template <typename T, int VPT, int NT, int MB>
+int fwd_odd(const LnFwd& p, int nvec, cudaStream_t st) {
+    const int threads = static_cast<int>(ceil_div(nvec, 32 * VPT)) * 32;
+    constexpr auto k = layer_norm_fwd_odd<T, VPT, NT, MB>;
     if (int rc = allow_smem<k>()) return rc;
     const size_t wmax = window_max(p.cols, sizeof(T)), smem = 3 * (wmax + 8);
     int per_sm = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, NT, smem);
-    const int64_t grid = std::min<int64_t>(p.rows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm));
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem);
+    const int64_t grid = odd_grid<T>(p.rows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm));
     int* err = nullptr;
     if (int rc = rmsnorm_err_word(&err)) return rc;
-    return launch_early("layernorm_fwd", k, dim3(static_cast<unsigned>(grid)), NT, smem, st, p, 3, static_cast<uint32_t>(wmax), err);
+    return launch_early("layernorm_fwd", k, dim3(static_cast<unsigned>(grid)), threads, smem, st, p, 3, static_cast<uint32_t>(wmax), err);
 }
 
 template <typename T>
@@ -928,12 +1070,14 @@ int run_fwd(const LnFwd& p, cudaStream_t st) {
         if (nvec <= 2048) return fwd_ring<T, 4, 512, 1, 0>(p, nvec, st);
     } else {
         if (p.cols <= 128) return fwd_team<T, 1, 4>(p, 1, st);
-        if (p.rows <= sm_count() && p.cols <= 2048) return fwd_team<T, 1, 4>(p, (p.cols + 127) / 128, st);
-        if (p.cols <= 512) return fwd_odd<T, 4, 128>(p, st);
-        if (p.cols <= 1024) return fwd_odd<T, 4, 256>(p, st);
-        if (p.cols <= 2048) return fwd_odd<T, 8, 256>(p, st);
-        if (p.cols <= 4096) return fwd_odd<T, 8, 512>(p, st);
-        if (p.cols <= 8192) return fwd_odd<T, 16, 512>(p, st);
+        const int nvec = (p.cols + 2 * EPV - 2) / EPV;   // of the longest window
+        // few threads a row and several rows on an SM hide a row's two barriers; what does not fit their registers takes more threads
+        if (nvec <= 64) return fwd_odd<T, 2, 32, 16>(p, nvec, st);     // 131072 x 333 bf16: 82 us, 101 with 4 vectors a thread
+        if (nvec <= 512) return fwd_odd<T, 4, 128, 4>(p, nvec, st);    // 65536 x 1001 bf16: 63 us, 70 with 2
+        if (nvec <= 576) return fwd_odd<T, 3, 192, 3>(p, nvec, st);    // 32768 x 4097 bf16: 124 us, 143 with 2
+        if (nvec <= 768) return fwd_odd<T, 2, 384, 2>(p, nvec, st);    // 16384 x 6001 bf16: 85 us, 102 with 3
+        if (nvec <= 1056) return fwd_odd<T, 3, 352, 2>(p, nvec, st);   // 16384 x 4097 fp32: 89 us, 120 with 2
+        if (nvec <= 2048) return fwd_odd<T, 4, 512, 1>(p, nvec, st);
     }
     const int64_t grid = std::min<int64_t>(p.rows, 8 * sm_count());
     return launch_early("layernorm_fwd", layer_norm_fwd_rows<T>, dim3(static_cast<unsigned>(grid)), 256, 0, st,
@@ -950,7 +1094,7 @@ int bwd_ring_teams(const LnBwd& p, int nvec, int teams, int64_t& grid, cudaStrea
     int per_sm = 0;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, teams * (slot + 8));
     per_sm = std::max(1, per_sm);
-    size_t nst = std::max<size_t>(1, std::min<size_t>(8, kBwdFlight / (per_sm * teams * slot)));
+    size_t nst = std::max<size_t>(1, std::min<size_t>(8, (nvec >= 512 ? kBwdFlightLong : kBwdFlight) / (per_sm * teams * slot)));
     if (nst == 1 && 2 * teams * (slot + 8) <= 220u * 1024u) nst = 2;
     // the sums of the teams go through the ring's memory at the end: 16 bytes a vector and element pair
     const size_t sums = teams > 1 ? static_cast<size_t>(nvec) * Vec<T>::N * 8 : 0;
@@ -969,19 +1113,20 @@ int bwd_ring(const LnBwd& p, int nvec, int64_t& grid, cudaStream_t st) {
     return bwd_ring_teams<T, VPT, NT, 1>(p, nvec, 1, grid, st);
 }
 
-template <typename T, int EPT, int NT>
-int bwd_odd(const LnBwd& p, int64_t& grid, cudaStream_t st) {
-    constexpr auto k = layer_norm_bwd_odd<T, EPT, NT>;
+template <typename T, int VPT, int NT, int MB>
+int bwd_odd(const LnBwd& p, int nvec, int64_t& grid, cudaStream_t st) {
+    const int threads = static_cast<int>(ceil_div(nvec, 32 * VPT)) * 32;
+    constexpr auto k = layer_norm_bwd_odd<T, VPT, NT, MB>;
     if (int rc = allow_smem<k>()) return rc;
     const size_t wmax = window_max(p.cols, sizeof(T)), slot = (p.dres != nullptr ? 3 : 2) * wmax + 8;
     int nst = 4;   // one row in use, three in flight
     while (nst > 2 && nst * slot > 200u * 1024u) --nst;
     int per_sm = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, NT, nst * slot);
-    grid = std::min<int64_t>({p.rows, kMaxPartRows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm)});
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, nst * slot);
+    grid = odd_grid<T>(p.rows, std::min<int64_t>(kMaxPartRows, static_cast<int64_t>(sm_count()) * std::max(1, per_sm)));
     int* err = nullptr;
     if (int rc = rmsnorm_err_word(&err)) return rc;
-    return launch_early("layernorm_bwd", k, dim3(static_cast<unsigned>(grid)), NT, nst * slot, st, p, nst,
+    return launch_early("layernorm_bwd", k, dim3(static_cast<unsigned>(grid)), threads, nst * slot, st, p, nst,
                         static_cast<uint32_t>(wmax), err);
 }
 
@@ -993,13 +1138,14 @@ int run_bwd(LnBwd p, void* dw, void* db, cudaStream_t st) {
     const int nvec = p.cols % EPV == 0 ? p.cols / EPV : 0;
     int64_t grid = 0;
     int rc;
-    if (nvec == 0 && p.cols >= 64 && p.cols <= 8192 && 2 * (streams * window_max(p.cols, sizeof(T)) + 8) <= 220u * 1024u) {
-        if (p.cols <= 256) rc = bwd_odd<T, 4, 64>(p, grid, st);
-        else if (p.cols <= 512) rc = bwd_odd<T, 4, 128>(p, grid, st);
-        else if (p.cols <= 1024) rc = bwd_odd<T, 4, 256>(p, grid, st);
-        else if (p.cols <= 2048) rc = bwd_odd<T, 8, 256>(p, grid, st);
-        else if (p.cols <= 4096) rc = bwd_odd<T, 8, 512>(p, grid, st);
-        else rc = bwd_odd<T, 16, 512>(p, grid, st);
+    const int longest = (p.cols + 2 * EPV - 2) / EPV;   // vectors of the longest window of an odd row
+    if (nvec == 0 && p.cols >= 64 && longest <= 2048 && 2 * (streams * window_max(p.cols, sizeof(T)) + 8) <= 220u * 1024u) {
+        if (longest <= 128) rc = bwd_odd<T, 1, 128, 5>(p, longest, grid, st);         // 131072 x 333 bf16: 156 us, 179 with 2 vectors a thread
+        else if (longest <= 256) rc = bwd_odd<T, 2, 128, 4>(p, longest, grid, st);    // 65536 x 2001 bf16: 188 us, 232 with 1
+        else if (longest <= 576) rc = bwd_odd<T, 3, 192, 2>(p, longest, grid, st);    // 32768 x 4097 bf16: 234 us, 326 with 2
+        else if (longest <= 1024) rc = bwd_odd<T, 2, 512, 1>(p, longest, grid, st);   // 16384 x 6001 bf16: 175 us, 292 with 3
+        else if (longest <= 1088) rc = bwd_odd<T, 2, 544, 1>(p, longest, grid, st);   // 16384 x 8191 bf16: 332 us, 344 with 3, 534 with 4
+        else rc = bwd_odd<T, 4, 512, 1>(p, longest, grid, st);
     } else if (nvec == 0 || nvec > 2048 || static_cast<size_t>(streams) * p.cols * sizeof(T) > 200u * 1024u) {
         const int64_t most = std::min<int64_t>({p.rows, kMaxPartRows, 4 * sm_count()});
         p.rows_per_block = ceil_div(p.rows, most);

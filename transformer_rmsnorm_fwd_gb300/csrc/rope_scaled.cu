@@ -12,7 +12,9 @@ namespace {
 
 constexpr int kMaxPairs = 256;   // rotary_dim <= 512
 constexpr int kThreads = 256;
-constexpr int64_t kStagedTokens = 512;   // fewer tokens go straight through registers
+// Fewer tokens go straight through registers.  32 + 8 heads of 128 bf16, half of each rotated, pairs across halves (neighbours), us:
+// 32 tokens 3.0 (3.2) staged, 3.3 (2.8) straight; 128: 3.1 (3.1), 3.3 (3.1); 512: 3.9 (3.6), 4.8 (5.4); 8192: 27 (26), 41 (46).
+constexpr int64_t kStagedTokens = 128;
 
 // inverse frequencies, by value in the kernel's parameters
 struct Freqs {

@@ -139,7 +139,9 @@ constexpr int kGroups = 64;         // groups of threads
 constexpr int kList = 2048;         // candidates of a block
 constexpr int kSecond = LIGER_TOP_MAX * kList / kGroups;   // ... that reach the second bound: k groups' shares at most
 constexpr int kUnroll = 4;          // vectors of a thread in flight
-constexpr int kShortRow = 256;      // rows of at most this many vectors: 64 threads
+// Many rows (kManyRows an SM) of at most kShortRow vectors: 64 threads a row, whose ends overlap better.  8192 rows of 1024 bf16
+// logits with 8 alternatives: 58 us, 86 with 256 threads; of 16384: 102 and 116; of 32768: 155 and 147; 304 rows of 4096: 9.4 and 7.6.
+constexpr int kShortRow = 2048, kManyRows = 6;
 
 // a row's vectors: vector v holds elements v EPV - shift + (0 .. EPV - 1); those in [first, last) are whole
 template <typename T>
@@ -557,10 +559,12 @@ template <typename T>
 int launch_fwd(const char* who, const LogpFwd& p, cudaStream_t st) {
     const int64_t vecs = ceil_div(p.V, Vec<T>::N);
     const bool ent = p.entropy != nullptr;
-    // few rows: each over a cluster of blocks, while a thread still gets two vectors
+    // Few rows: each over a cluster of blocks, while an SM has one of them and a thread more than 8 vectors.  128256 bf16 logits with 8
+    // alternatives, over 1, 2, 4, 8 blocks: one row 13.4, 10.3, 9.6, 9.5 us; 38 rows 14.1, 12.8, 10.7, 11.1; 76 rows 15.1, 12.7, 13.3,
+    // 20.0; 152 rows 15.6, 15.4, 21.7, 31.2.  32768 logits: one row 6.6, 7.9, 7.7, 8.5.
     int ranks = 1;
-    while (ranks < 8 && p.T * ranks * 2 <= 2 * sm_count() && vecs >= 4 * ranks * kRowThreads) ranks *= 2;
-    if (vecs <= kShortRow)
+    while (ranks < 8 && p.T * ranks * 2 <= sm_count() && vecs > 16 * ranks * kRowThreads) ranks *= 2;
+    if (vecs <= kShortRow && p.T >= kManyRows * sm_count())
         return ent ? launch_row<T, 64, true>(who, p, 1, st) : launch_row<T, 64, false>(who, p, 1, st);
     return ent ? launch_row<T, kRowThreads, true>(who, p, ranks, st) : launch_row<T, kRowThreads, false>(who, p, ranks, st);
 }
