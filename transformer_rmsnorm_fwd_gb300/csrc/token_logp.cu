@@ -564,7 +564,8 @@ int launch_fwd(const char* who, const LogpFwd& p, cudaStream_t st) {
     // 20.0; 152 rows 15.6, 15.4, 21.7, 31.2.  32768 logits: one row 6.6, 7.9, 7.7, 8.5.
     int ranks = 1;
     while (ranks < 8 && p.T * ranks * 2 <= sm_count() && vecs > 16 * ranks * kRowThreads) ranks *= 2;
-    if (vecs <= kShortRow && p.T >= kManyRows * sm_count())
+    // (64 threads for a row of few vectors too: among 256 threads too few of the groups that give the bound would hold any)
+    if (vecs < kRowThreads || (vecs <= kShortRow && p.T >= kManyRows * sm_count()))
         return ent ? launch_row<T, 64, true>(who, p, 1, st) : launch_row<T, 64, false>(who, p, 1, st);
     return ent ? launch_row<T, kRowThreads, true>(who, p, ranks, st) : launch_row<T, kRowThreads, false>(who, p, ranks, st);
 }
