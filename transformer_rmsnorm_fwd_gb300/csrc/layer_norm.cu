@@ -1,4 +1,9 @@
 // Layer norm, forward and backward (formulas in liger_layer.h).
+// A row's mean comes first and its variance from the differences to it, both in fp32 over values that stay in registers, so
+// that a row is read once and a large mean costs no digits.  The backward's two row sums, of dy w and of dy w xhat, are formed
+// in one pass, and dw and db as fp32 column sums in registers over all rows of a block; each block leaves them as a partial row,
+// added up in a fixed order.  What bounds all of it is HBM: two streams forward, three (four with dres) backward.  32768 x 4096
+// bf16: forward 85 us (0.93 of the copy rate), backward with dres 155 us (1.02); a few rows: the launch (4 rows: 2.3 us of kernel).
 #include "block_norm.cuh"
 #include "liger_layer.h"
 
@@ -1061,6 +1066,8 @@ int run_fwd(const LnFwd& p, cudaStream_t st) {
     constexpr int EPV = Vec<T>::N;
     if (p.cols % EPV == 0) {
         const int nvec = p.cols / EPV;
+        // A team to a row that it loads itself, up to one round of blocks; then the rings.  bf16, us by team and by ring: 152 x 4096 2.7,
+        // 2.9; 304 x 4096 3.6, 3.0; 608 x 1024 2.5, 2.9; 1216 x 1024 3.4, 3.1; 152 x 8192 3.1, 3.3; 608 x 8192 6.2, 5.1
         const int64_t few = static_cast<int64_t>(sm_count()) * std::max(1, 512 / std::max(nvec, 32));
         if (p.rows <= few && nvec <= 512) return fwd_team<T, EPV, 1>(p, (nvec + 31) / 32, st);
         if (p.rows <= few && nvec <= 2048) return fwd_team<T, EPV, 4>(p, (nvec + 127) / 128, st);

@@ -1,5 +1,10 @@
 // The projection with bias, activation and residual sum in its epilogue, and its
 // backward (formulas in liger_layer.h).
+// Y = act(X W^T + b) + R is one GEMM with the rest in its epilogue; the backward is one pass dP = dY act'(P) with db, then
+// dX = dP W and dW = dP^T X.  bf16 goes on the tensor cores, in 256 x 256 tiles of CTA pairs (tc_gemm.cuh) or, with few tiles, in
+// 128-feature tiles (linear_small.cuh); fp32 and sizes of no whole vectors on fp32 FMA (linear_fma.cuh).  8192 x 4096 x 11008 bf16
+// with gelu: forward 412 us (1790 TFLOP/s), dP and db 91, dW 390, dX 393: the tensor pipe under the power cap; 4 tokens: 19 us from
+// a cold L2, the weight's 90 MB.
 #include "activation.cuh"
 #include "linear_fma.cuh"
 #include "linear_small.cuh"
@@ -10,14 +15,14 @@ namespace {
 constexpr int64_t kSmallTokens = 128;
 constexpr unsigned kDpShares = 8;   // most blocks of a cluster that share the rows of a column sum
 constexpr int64_t kDpLong = 2048, kDpParts = 64;
-constexpr int kDpRows = 3;
+constexpr int kDpRows = 3;   // 8192 x 11008 with erf: 92 us, 210 with one row in flight and erff
 
 // dP = dY act'(P) and db, in one pass: a block takes some columns and its share of the rows, the blocks of a
 // cluster all rows of the same columns.  The column sums go from threads to the block over shared memory, and
 // over the cluster in the order of its blocks: no partial rows in device memory, no second kernel.
-
-// Where there are more than kDpShares blocks' worth of rows, the blocks are no cluster: each leaves its sums as a partial row in
-// the workspace, and linear_db adds those in their order.
+// From kDpLong rows on a cluster's blocks have too many each: more blocks, no cluster, each leaves its sums as a partial row in
+// the workspace, and linear_db adds those in their order.  2048 x 4096: 12.2 us so, 18.3 by clusters; 1024 x 4096 10.3 and 10.0;
+// 1111 x 520 6.1 and 4.3.
 
 // The cluster's column sums into db: `mine` holds this block's for columns [col0, col0 + n).
 template <typename T>
@@ -223,10 +228,17 @@ struct LinearBwd {
 int64_t pair_tiles(int64_t M, int64_t N) {
     return ceil_div(M, static_cast<int64_t>(tc::TileCfg<1>::TM)) * ceil_div(N, static_cast<int64_t>(tc::BN));
 }
-// Whether T tokens by F features go in 128-feature tiles (linear_small.cuh) and not in 256 x 256 tiles of CTA pairs.
+// Whether T tokens by F features go in 128-feature tiles (linear_small.cuh) and not in 256 x 256 tiles of CTA pairs: up to
+// 128 tokens, and where the pairs' tiles leave most of the SMs idle.  us in small tiles and in pairs', tokens x sum length x features:
+//   128 x 4096 x 11008 20.7, 26.9 (43 tiles of pairs)   256 x 4096 x 11008 35.1, 27.6 (43)   256 x 4096 x 4096 16.0, 24.9 (16)
+//   512 x 4096 x 4096  26.8, 24.9 (32)   600 x 4096 x 2048 18.7, 24.3 (24)   1024 x 1024 x 1024 9.7, 11.2 (16)
+//   2394 x 1600 x 696  16.1, 13.2 (30)   160 x 2048 x 8192 13.6, 15.7 (32)   1111 x 520 x 1384  10.5, 9.5 (30)
 bool goes_small(int64_t T, int64_t F) {
-    return F <= 65535 * int64_t{tc::kSmallRows} && (T <= kSmallTokens || 2 * pair_tiles(T, F) <= sm_count() / 2);
+    const int64_t pairs = sm_count() / 2;
+    return F <= 65535 * int64_t{tc::kSmallRows} && (T <= kSmallTokens || (T <= 256 ? 2 : 3) * pair_tiles(T, F) <= pairs);
 }
+// Tokens of a small tile: all of them up to 256 (256 x 4096 x 4096: 16.1 us, 17.4 in tiles of 128), else 128 (1024 x 2048 x 2048:
+// 16.9 us, 30.7 in tiles of 192; 700 x 2048 x 2048: 14.5, 13.3 in tiles of 192, 23.1 of 256).
 int small_tokens(int64_t T) { return T <= 256 ? 256 : 128; }
 
 int fwd_tc(const void* X, const void* W, const void* bias, const void* residual, void* Y, void* pre, int64_t T, int64_t H,
@@ -301,6 +313,8 @@ int grads_tc(const LinearBwd& a, const void* dP) {
         w.hint_a = HINT_EVICT_FIRST;
         w.hint_b = HINT_EVICT_LAST;   // X: reused by every row block
         w.early = 1;
+        // The last, partly filled round of tiles is split along the tokens over the idle pairs, their sums in dX, which is written after:
+        // 8192 x 4096 x 11008, dW and dX: 746 us, 789 with whole tiles; 8192 x 2048 x 5504: 225, 245
         const int64_t tiles = pair_tiles(N, H), pairs = sm_count() / 2, rem = tiles % pairs;
         const int64_t tile_bytes = int64_t{TileCfg<1>::TM} * BN * 4;
         const int64_t splits = a.dX == nullptr || rem == 0 ? 0

@@ -1,5 +1,10 @@
 // Log-probabilities of given tokens from logits, with the entropy, the top
 // alternatives and the gradient of the logits (formulas in liger_layer.h).
+// The forward reads a row once: a running maximum with the sums of e^(z - m) and of (z - m) e^(z - m) relative to it, raised where the
+// maximum rises, and the largest logit of each thread's vectors, from which the k-th largest of 64 groups bounds the alternatives:
+// only vectors that reach the bound are looked at again.  4096 rows of 128256 bf16 with 8 alternatives: 189 to 192 us, 0.81 of the
+// copy rate, without alternatives 159 (0.97): bound by HBM and, for the rest, by the ends of the rows (their barriers and ranking).
+// The gradient, 1500 x 32771 fp32: 58 us, the copy rate.  One row of 151936: 9.5 us, the latencies of one pass.
 #include <math.h>
 
 #include <type_traits>
