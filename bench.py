@@ -62,7 +62,7 @@ def parse_args(argv=None):
                    choices=["chain", "linear_ce", "linear_ce_two_pass", "rmsnorm_qkv_rope", "fused_linear_swiglu",
                             "fused_linear_swiglu_fwd_save", "fused_linear_swiglu_bwd_saved", "rmsnorm", "rope",
                             "swiglu", "block_norm", "swiglu_ckpt8", "fused_linear_swiglu_ckpt8", "linear_logp",
-                            "linear_policy"],
+                            "linear_policy", "layernorm", "linear_act", "rope_scaled", "token_logp"],
                    help="chain: the benchmark step (default); otherwise time that one operator alone at --seq "
                         "tokens (single-kernel profiling cases; prints a JSON line with ms per call)")
     p.add_argument("--chunk", type=int, default=0, help="--op linear_ce: token chunk (0 = automatic)")
@@ -1118,7 +1118,18 @@ def single_op(args):
         fn = lambda: L.liger_rmsnorm_qkv_rope_fwd(x, wn, Wq, Wk, Wv, q, k, v, ws, 1, S, HEADS, HEADS, HEAD_DIM,
                                                   eps=EPS, theta=THETA)
         flops = 2.0 * S * HIDDEN * N
-    elif op in ("rmsnorm", "rope", "swiglu", "block_norm", "swiglu_ckpt8"):
+    elif op == "linear_act":        # the MLP's first projection with bias and gelu, forward and backward
+        X, W = to_torch(normal(7, "op.lX", (S, HIDDEN), "bf16"), dev), to_torch(normal(7, "op.lW", (INTER, HIDDEN), "bf16", 0.0, 0.02), dev)
+        bl, dY = to_torch(normal(7, "op.lb", (INTER,), "bf16"), dev), to_torch(normal(7, "op.ld", (S, INTER), "bf16"), dev)
+        Y, pre = torch.empty(S, INTER, dtype=bf, device=dev), torch.empty(S, INTER, dtype=torch.float16, device=dev)
+        dX, dW, db = torch.empty_like(X), torch.empty_like(W), torch.empty_like(bl)
+        ws = torch.empty(L.liger_linear_act_bwd_workspace(S, HIDDEN, INTER, "gelu_tanh"), dtype=torch.uint8, device=dev)
+
+        def fn():
+            L.liger_linear_act_fwd(X, W, Y, bias=bl, act="gelu_tanh", pre=pre)
+            L.liger_linear_act_bwd(dY, X, W, dX, dW, db, ws, pre=pre, act="gelu_tanh")
+        flops = 6.0 * S * HIDDEN * INTER
+    elif op in ("rmsnorm", "rope", "swiglu", "block_norm", "swiglu_ckpt8", "layernorm", "rope_scaled", "token_logp"):
         # forward then backward, HBM-bound: report GB/s of the algorithmic bytes
         e = 2
         if op == "rmsnorm":
@@ -1153,6 +1164,36 @@ def single_op(args):
                 L.liger_block_norm_fwd(z, r, h, y, w, w, w, rz, rh, eps=EPS)
                 L.liger_block_norm_bwd(dh, dy, z, h, dr, dz, wsb, w, w, w, rz, rh, dwp, dg, dwn)
             nbytes = (4 + 6) * S * HIDDEN * e + 16 * S
+        elif op == "layernorm":
+            x, dy = to_torch(normal(7, "op.nx", (S, HIDDEN), "bf16"), dev), to_torch(normal(7, "op.nd", (S, HIDDEN), "bf16"), dev)
+            w, bn = to_torch(normal(7, "op.nw", (HIDDEN,), "bf16", 1.0, 0.1), dev), to_torch(normal(7, "op.nb", (HIDDEN,), "bf16"), dev)
+            y, dx, dw, db = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w), torch.empty_like(bn)
+            mean, rstd = torch.empty(S, device=dev), torch.empty(S, device=dev)
+            wsn = torch.empty(L.liger_layernorm_bwd_workspace(S, HIDDEN), dtype=torch.uint8, device=dev)
+
+            def fn():
+                L.liger_layernorm_fwd(x, w, bn, y, mean, rstd, EPS)
+                L.liger_layernorm_bwd(dy, x, w, mean, rstd, dx, dw, db, wsn)
+            nbytes = 5 * S * HIDDEN * e + 16 * S
+        elif op == "rope_scaled":       # half of each head turned, out of place
+            q, k = (to_torch(normal(7, f"op.s{c}", (1, S, HEADS, HEAD_DIM), "bf16"), dev) for c in "qk")
+            qo, ko = torch.empty_like(q), torch.empty_like(k)
+
+            def fn():
+                for turn in (L.liger_rope_scaled_fwd, L.liger_rope_scaled_bwd):
+                    turn(q, k, qo, ko, HEAD_DIM // 2, theta=THETA, scaling="yarn", factor=8.0, low=1.0, high=32.0, orig_len=8192)
+            nbytes = 2 * (2 * 2 * S * HEADS * HEAD_DIM * e)
+        elif op == "token_logp":        # scored with the entropy and 8 alternatives, then the gradient of the logits
+            z = to_torch(normal(7, "op.tz", (S, VOCAB), "bf16"), dev)
+            tok = torch.from_numpy(labels(7, "op.tt", S, VOCAB, 0.0)).to(dev)
+            logp, top_max, log_sum, ent, gl = (torch.ones(S, device=dev) for _ in range(5))
+            top, ids = torch.empty(S, 8, device=dev), torch.empty(S, 8, dtype=torch.int64, device=dev)
+            dz = torch.empty_like(z)
+
+            def fn():
+                L.liger_token_logp_fwd(z, tok, logp, top_max, log_sum, ent, top, ids)
+                L.liger_token_logp_bwd(z, tok, top_max, log_sum, gl, dz, entropy=ent, g_entropy=gl)
+            nbytes = 3 * S * VOCAB * e
         elif op == "swiglu_ckpt8":
             g, u, dy = (to_torch(normal(7, f"op.c{c}", (S, INTER), "bf16"), dev) for c in "gud")
             y, dg, du = torch.empty_like(g), torch.empty_like(g), torch.empty_like(g)
