@@ -4,7 +4,7 @@
 // maximum rises, and the largest logit of each thread's vectors, from which the k-th largest of 64 groups bounds the alternatives:
 // only vectors that reach the bound are looked at again.  4096 rows of 128256 bf16 with 8 alternatives: 189 to 192 us, 0.81 of the
 // copy rate, without alternatives 159 (0.97): bound by HBM and, for the rest, by the ends of the rows (their barriers and ranking).
-// The gradient, 1500 x 32771 fp32: 58 us, the copy rate.  One row of 151936: 9.5 us, the latencies of one pass.
+// The gradient, 4096 x 128256 bf16: 313 us (0.99); 1500 x 32771 fp32: 61 (0.95).  One row of 151936: 9.5 us, the latencies of one pass.
 #include <math.h>
 
 #include <type_traits>
@@ -144,9 +144,11 @@ constexpr int kGroups = 64;         // groups of threads
 constexpr int kList = 2048;         // candidates of a block
 constexpr int kSecond = LIGER_TOP_MAX * kList / kGroups;   // ... that reach the second bound: k groups' shares at most
 constexpr int kUnroll = 4;          // vectors of a thread in flight
-// Many rows (kManyRows an SM) of at most kShortRow vectors: 64 threads a row, whose ends overlap better.  8192 rows of 1024 bf16
-// logits with 8 alternatives: 58 us, 86 with 256 threads; of 16384: 102 and 116; of 32768: 155 and 147; 304 rows of 4096: 9.4 and 7.6.
-constexpr int kShortRow = 2048, kManyRows = 6;
+// Many rows (kManyRows an SM) of at most kShortRow vectors: 128 threads a row, whose ends overlap better; 64 for rows of few vectors,
+// of which 128 threads would hold too few groups for the bound.  us with 64, 128 and 256 threads, bf16, 8 alternatives: 8192 x 2048
+// 60, 58, 80; 8192 x 16384 101, 92, 115; 8192 x 32768 154, 128, 145; 4096 x 65536 173, 136, 111; 1024 x 8192 13.8, 13.0, 15.4;
+// 304 x 8192 10.5, 9.7, 7.7.
+constexpr int kShortRow = 5120, kManyRows = 6;
 
 // a row's vectors: vector v holds elements v EPV - shift + (0 .. EPV - 1); those in [first, last) are whole
 template <typename T>
@@ -504,6 +506,18 @@ __global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) 
     const int64_t t = blockIdx.x;
     const T* z = static_cast<const T*>(p.z) + t * p.ld;
     T* dz = static_cast<T*>(p.dz) + t * p.ldd;
+    // the first vectors are asked for before the row's scalars are known
+    const RowVecs<T> row(z, p.V);
+    const int64_t v0 = static_cast<int64_t>(row.n) * blockIdx.y / gridDim.y, v1 = static_cast<int64_t>(row.n) * (blockIdx.y + 1) / gridDim.y;
+    uint4 x[kUnroll];
+    auto load = [&](int64_t v) {
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            const int64_t w = v + q * kRowThreads;
+            if (w < v1 && w >= row.first && w < row.last) x[q] = ldg16(row.base + w * EPV);
+        }
+    };
+    if (VECS) load(v0 + threadIdx.x);
     const int64_t y = p.tokens != nullptr ? p.tokens[t] : p.ignore;
     const bool counts = p.g_logp != nullptr && y != p.ignore;
     float g = counts ? p.g_logp[t] : 0.f;
@@ -511,38 +525,47 @@ __global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) 
     const float h = p.g_entropy != nullptr ? p.g_entropy[t] : 0.f, H = p.g_entropy != nullptr ? p.entropy[t] : 0.f;
     const float m = p.row_max[t], ls = p.log_sum[t];
     const bool zero = (g == 0.f && h == 0.f) || (m == -INFINITY && g == g && h == h);
+    // dz = e^a (ch a + cg), and cy more at the token
+    const float ch = -h * p.inv_temp, cy = g * p.inv_temp, cg = fmaf(ch, H, -cy);
     auto one = [&](float zv, int64_t i) {
         const float a = max_nan(fmaf(zv - m, p.inv_temp, -ls), -1e4f);   // of -inf: held where e^a is 0
-        const float d = ex2(a * kLog2e) * fmaf(h, a + H, g);
-        return ((i == y ? g : 0.f) - d) * p.inv_temp;
+        const float d = ex2(a * kLog2e) * fmaf(ch, a, cg);
+        return i == y ? d + cy : d;
     };
     if constexpr (!VECS) {
         for (int64_t i = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; i < p.V; i += static_cast<int64_t>(gridDim.y) * kRowThreads)
             stf(dz + i, zero ? 0.f : one(ldf(z + i), i));
         return;
     } else {
-        const RowVecs<T> row(z, p.V);
         T* out = dz - row.shift;
-        const int64_t v0 = static_cast<int64_t>(row.n) * blockIdx.y / gridDim.y, v1 = static_cast<int64_t>(row.n) * (blockIdx.y + 1) / gridDim.y;
+        const float2 nm = make_float2(-m, -m), it = make_float2(p.inv_temp, p.inv_temp), nls = make_float2(-ls, -ls),
+                     l2e = make_float2(kLog2e, kLog2e), ch2 = make_float2(ch, ch), cg2 = make_float2(cg, cg);
         for (int64_t v = v0 + threadIdx.x; v < v1; v += kUnroll * kRowThreads) {
-            uint4 x[kUnroll];
-#pragma unroll
-            for (int q = 0; q < kUnroll; ++q) {
-                const int64_t w = v + q * kRowThreads;
-                if (!zero && w < v1 && w >= row.first && w < row.last) x[q] = ldg16(row.base + w * EPV);
-            }
+            if (!zero && v >= v0 + kUnroll * kRowThreads) load(v);
 #pragma unroll
             for (int q = 0; q < kUnroll; ++q) {
                 const int64_t w = v + q * kRowThreads, i0 = w * EPV - row.shift;
                 if (w >= v1) break;
                 if (w >= row.first && w < row.last) {
-                    float f[EPV] = {};
+                    float2 f[EPV / 2] = {};
                     if (!zero) {
-                        unpack(x[q], f);
+                        unpack2(x[q], f);
 #pragma unroll
-                        for (int e = 0; e < EPV; ++e) f[e] = one(f[e], i0 + e);
+                        for (int e = 0; e < EPV / 2; ++e) {
+                            float2 a = __ffma2_rn(__fadd2_rn(f[e], nm), it, nls);
+                            a = make_float2(max_nan(a.x, -1e4f), max_nan(a.y, -1e4f));
+                            const float2 b = __fmul2_rn(a, l2e);
+                            f[e] = __fmul2_rn(make_float2(ex2(b.x), ex2(b.y)), __ffma2_rn(ch2, a, cg2));
+                        }
+                        const int64_t at = y - i0;
+                        if (at >= 0 && at < EPV)
+#pragma unroll
+                            for (int e = 0; e < EPV / 2; ++e) {
+                                if (at == 2 * e) f[e].x += cy;
+                                if (at == 2 * e + 1) f[e].y += cy;
+                            }
                     }
-                    stg16_cs(out + w * EPV, pack(f));
+                    stg16_cs(out + w * EPV, pack2(f));
                 } else {
                     for (int e = 0; e < EPV; ++e)
                         if (i0 + e >= 0 && i0 + e < p.V) stf(dz + i0 + e, zero ? 0.f : one(ldf(z + i0 + e), i0 + e));
@@ -569,9 +592,9 @@ int launch_fwd(const char* who, const LogpFwd& p, cudaStream_t st) {
     // 20.0; 152 rows 15.6, 15.4, 21.7, 31.2.  32768 logits: one row 6.6, 7.9, 7.7, 8.5.
     int ranks = 1;
     while (ranks < 8 && p.T * ranks * 2 <= sm_count() && vecs > 16 * ranks * kRowThreads) ranks *= 2;
-    // (64 threads for a row of few vectors too: among 256 threads too few of the groups that give the bound would hold any)
-    if (vecs < kRowThreads || (vecs <= kShortRow && p.T >= kManyRows * sm_count()))
-        return ent ? launch_row<T, 64, true>(who, p, 1, st) : launch_row<T, 64, false>(who, p, 1, st);
+    if (vecs < kRowThreads) return ent ? launch_row<T, 64, true>(who, p, 1, st) : launch_row<T, 64, false>(who, p, 1, st);
+    if (vecs <= kShortRow && p.T >= kManyRows * sm_count())
+        return ent ? launch_row<T, 128, true>(who, p, 1, st) : launch_row<T, 128, false>(who, p, 1, st);
     return ent ? launch_row<T, kRowThreads, true>(who, p, ranks, st) : launch_row<T, kRowThreads, false>(who, p, ranks, st);
 }
 
@@ -580,7 +603,9 @@ int launch_bwd(const char* who, const LogpBwd& p, cudaStream_t st) {
     const int64_t vecs = ceil_div(p.V, Vec<T>::N);
     const uintptr_t az = reinterpret_cast<uintptr_t>(p.z), ad = reinterpret_cast<uintptr_t>(p.dz);
     const bool same = (az - ad) % 16 == 0 && (p.T == 1 || (p.ld - p.ldd) * static_cast<int64_t>(sizeof(T)) % 16 == 0);
-    const int64_t y = std::max<int64_t>(1, std::min<int64_t>(65535, vecs / (2 * kUnroll * kRowThreads)));
+    // 4 rounds of vectors a thread: 4096 x 128256 bf16 in 313 us, 334 with 2, 388 with 1, 314 with 8; few rows over more blocks
+    const int64_t fill = std::min<int64_t>(vecs / kRowThreads, ceil_div(2 * sm_count(), p.T));
+    const int64_t y = std::min<int64_t>(65535, std::max<int64_t>({1, fill, vecs / (4 * kUnroll * kRowThreads)}));
     const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>(y));
     return same ? launch_early(who, token_logp_grad<T, true>, grid, kRowThreads, 0, st, p)
                 : launch_early(who, token_logp_grad<T, false>, grid, kRowThreads, 0, st, p);
