@@ -96,6 +96,23 @@ def test_in_place_gives_the_same_bits(cuda_lib, dtype, rows, cols, alias):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(9001, 131), (7003, 333), (5001, 515), (3001, 1001), (2003, 1999), (2001, 2050), (1501, 4097), (901, 4099),
+                                       (903, 6001), (801, 8185), (801, 8191), (701, 12345), (607, 16001)])
+def test_many_rows_of_odd_width(cuda_lib, dtype, rows, cols):
+    """More rows than blocks: a block goes on to rows that start at the same place of their 16-byte windows."""
+    run_case(cuda_lib, dtype, rows, cols, seed=rows + cols)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(3001, 1001), (1501, 4097)])
+@pytest.mark.parametrize("alias", ["y dy", "y dres"])
+def test_many_rows_of_odd_width_in_place(cuda_lib, dtype, rows, cols, alias):
+    a = run_case(cuda_lib, dtype, rows, cols, seed=6)
+    b = run_case(cuda_lib, dtype, rows, cols, seed=6, in_place=alias)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("cols", [512, 777, 9000])
 def test_rows_far_from_zero_and_of_any_size(cuda_lib, dtype, cols):
     # a mean 300 times the spread: E x^2 - mean^2 would lose all of the variance's digits

@@ -1,4 +1,6 @@
 """Token log-probabilities, entropy and alternatives of logits against their formulas in 64 bits, and the gradient."""
+import math
+
 import pytest
 import torch
 
@@ -187,6 +189,41 @@ def test_nan_and_infinities_stay_in_their_rows(cuda_lib, dtype, V):
     assert bool(torch.isnan(o["top_logp"][1:3]).all())
     assert sorted([7, V // 2]) == o["top_ids"][1, :2].tolist() and int(o["top_ids"][2, 0]) == 9
     compare(z[:1], y[:1], 4, 1.0, {n: v[:1] for n, v in o.items()})
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V,k", [(300, 3), (2048, 8), (2100, 32), (20001, 5), (32771, 20)])
+def test_many_rows(cuda_lib, dtype, V, k):
+    """A batch large enough for fewer threads a row: against 64 bits, and odd rows against the same rows on their own."""
+    T = 1000
+    g = gen(V + k)
+    z = randn(g, T, V, std=2.5, dtype=dtype)
+    i = torch.arange(V, device="cuda")
+    odd = torch.tensor([0, 5, 151, 152, 500, 608, 777, 911, T - 1], device="cuda")
+    z[odd[0]] = 2.5                                     # all equal
+    z[odd[1]] = (i * 7919 % 3 == 0).to(dtype)           # two values
+    z[odd[2]] = NINF                                    # nothing left
+    z[odd[3], 1:] = NINF                                # one word left
+    z[odd[4]] = torch.where(i % 10 == 0, z[odd[4]], torch.tensor(torch.finfo(dtype).min, dtype=dtype, device="cuda"))
+    z[odd[5], V // 2] = float("nan")
+    z[odd[6], 9] = float("inf")
+    z[odd[7]] = (i.float() / V * 8).to(dtype)           # ascending
+    z[odd[8]] = ((i >= V // 2) & (i < V // 2 + 1500)).to(dtype) * 4
+    y = tokens_of(g, T, V)
+    y[odd[3]] = 0
+    o, alone = forward(z, y, k), forward(z[odd], y[odd], k)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[odd] = False
+    compare(z[rest], y[rest], k, 1.0, {n: v[rest] for n, v in o.items()})
+    c = _chain(V)                                       # each of the two is within c
+    for n, v in alone.items():
+        u = o[n][odd]
+        if n in ("top_ids", "row_max"):
+            assert torch.equal(u.nan_to_num(nan=-5.0), v.nan_to_num(nan=-5.0)), n
+            continue
+        live = torch.isfinite(v)
+        assert torch.equal(torch.isfinite(u), live) and torch.equal(torch.isnan(u), torch.isnan(v)), n
+        check(u[live], v[live].double(), 2 + 2 * v[live].double().abs() + (2 * math.log(V) if n == "entropy" else 0), 2 * c, n)
 
 
 def bwd_ref(z, y, m, ls, H, g, h, temp):
