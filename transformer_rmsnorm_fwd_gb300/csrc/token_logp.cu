@@ -525,12 +525,12 @@ __global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) 
     const float h = p.g_entropy != nullptr ? p.g_entropy[t] : 0.f, H = p.g_entropy != nullptr ? p.entropy[t] : 0.f;
     const float m = p.row_max[t], ls = p.log_sum[t];
     const bool zero = (g == 0.f && h == 0.f) || (m == -INFINITY && g == g && h == h);
-    // dz = e^a (ch a + cg), and cy more at the token
-    const float ch = -h * p.inv_temp, cy = g * p.inv_temp, cg = fmaf(ch, H, -cy);
+    // temperature dz = -e^a (h a + c), and g more at the token (scaled last: the sums of a row stay in range at any temperature)
+    const float c = fmaf(h, H, g);
     auto one = [&](float zv, int64_t i) {
         const float a = max_nan(fmaf(zv - m, p.inv_temp, -ls), -1e4f);   // of -inf: held where e^a is 0
-        const float d = ex2(a * kLog2e) * fmaf(ch, a, cg);
-        return i == y ? d + cy : d;
+        const float d = ex2(a * kLog2e) * fmaf(-h, a, -c);
+        return (i == y ? d + g : d) * p.inv_temp;
     };
     if constexpr (!VECS) {
         for (int64_t i = static_cast<int64_t>(blockIdx.y) * kRowThreads + threadIdx.x; i < p.V; i += static_cast<int64_t>(gridDim.y) * kRowThreads)
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) 
     } else {
         T* out = dz - row.shift;
         const float2 nm = make_float2(-m, -m), it = make_float2(p.inv_temp, p.inv_temp), nls = make_float2(-ls, -ls),
-                     l2e = make_float2(kLog2e, kLog2e), ch2 = make_float2(ch, ch), cg2 = make_float2(cg, cg);
+                     l2e = make_float2(kLog2e, kLog2e), nh = make_float2(-h, -h), nc = make_float2(-c, -c);
         for (int64_t v = v0 + threadIdx.x; v < v1; v += kUnroll * kRowThreads) {
             if (!zero && v >= v0 + kUnroll * kRowThreads) load(v);
 #pragma unroll
@@ -555,15 +555,17 @@ __global__ void __launch_bounds__(kRowThreads) token_logp_grad(const LogpBwd p) 
                             float2 a = __ffma2_rn(__fadd2_rn(f[e], nm), it, nls);
                             a = make_float2(max_nan(a.x, -1e4f), max_nan(a.y, -1e4f));
                             const float2 b = __fmul2_rn(a, l2e);
-                            f[e] = __fmul2_rn(make_float2(ex2(b.x), ex2(b.y)), __ffma2_rn(ch2, a, cg2));
+                            f[e] = __fmul2_rn(make_float2(ex2(b.x), ex2(b.y)), __ffma2_rn(nh, a, nc));
                         }
                         const int64_t at = y - i0;
                         if (at >= 0 && at < EPV)
 #pragma unroll
                             for (int e = 0; e < EPV / 2; ++e) {
-                                if (at == 2 * e) f[e].x += cy;
-                                if (at == 2 * e + 1) f[e].y += cy;
+                                if (at == 2 * e) f[e].x += g;
+                                if (at == 2 * e + 1) f[e].y += g;
                             }
+#pragma unroll
+                        for (int e = 0; e < EPV / 2; ++e) f[e] = __fmul2_rn(f[e], it);
                     }
                     stg16_cs(out + w * EPV, pack2(f));
                 } else {
