@@ -157,6 +157,17 @@ def test_backward_odd_and_fp32(cuda_lib, dtype, T, H, N, act):
     bwd_case(dtype, T, H, N, act=act, seed=T + H + N)
 
 
+@pytest.mark.parametrize("T,H,N", [(200, 200, 200), (17, 1600, 1999), (140, 2047, 131), (1024, 1024, 1001), (2000, 700, 300), (1599, 1601, 333),
+                                   (2043, 101, 2000), (2048, 2048, 2047)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_fma_tiles_of_all_shapes(cuda_lib, dtype, T, H, N):
+    """Products off the tensor cores large enough for each tile shape, with K split over clusters and whole."""
+    if dtype is BF and H % 8 == 0 and N % 8 == 0:
+        H += 1
+    fwd_case(dtype, T, H, N, act="silu", seed=T)
+    bwd_case(dtype, T, H, N, act="gelu_tanh", seed=T)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("want", [("dX",), ("dW",), ("db",), ("dX", "db"), ("dX", "dW")])

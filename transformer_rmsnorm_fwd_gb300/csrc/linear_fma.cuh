@@ -36,12 +36,10 @@ __device__ __forceinline__ void fma_store(const FmaGemm& g, const FmaEpi<TO, TPR
 
 // Tiles of FM x FN by 16 x 16 threads, FK k at a time through two shared buffers, the next ones loaded to registers while
 // these are used.  The arithmetic is on column pairs with the packed fp32x2 fma.  Consecutive threads load consecutive
-// elements of an operand's contiguous dimension; inside the matrices without checks.
-//   128 x 128   where there are tiles for every SM: 2048 x 2048 x 2048 in 411 us (42 TFLOP/s; the rounds of 256 tiles leave
-//               a sixth of the SMs' places empty), bound by fma issue beside the shared-memory reads
-//   64 x 64     fewer outputs: K split over a cluster of blocks, whose tiles are joined in order over distributed shared memory:
-//               300 x 257 x 1001 in 12.8 us, bound by the latencies of its few steps (in 128 x 64 tiles 15.3)
-//   16 x 64     up to 16 rows: 4 x 2048 x 2048 in 17.8 us, 32.9 in tiles of 64 rows
+// elements of an operand's contiguous dimension; inside the matrices without checks.  K is split over a cluster of blocks,
+// whose tiles are joined in order over distributed shared memory (not for 128 x 128, whose sums do not fit).  Bound by fma issue
+// beside the shared-memory reads, the less the larger the tile, and by how evenly the blocks fill the SMs (fma_us below).
+// 16 x 64: up to 16 rows; 4 x 2048 x 2048 in 17.8 us, 32.9 in tiles of 64 rows.
 template <int FM, int FN>
 struct FmaTile {
     static constexpr int FK = 16;
@@ -74,6 +72,11 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
     const TB* pb = B + (n0 + bn) * g.sbn + (k0 + kb) * g.sbk;
     const int64_t da = am_i * g.sam + ka_i * g.sak, db = bn_i * g.sbn + kb_i * g.sbk, step_a = FK * g.sak, step_b = FK * g.sbk;
     const bool inside = m0 + FM <= g.M && n0 + FN <= g.N;
+    uint32_t va = 0, vb = 0;   // which of this thread's rows and columns are inside
+#pragma unroll
+    for (int i = 0; i < NA; ++i) va |= m0 + am + i * am_i < g.M ? 1u << i : 0u;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) vb |= n0 + bn + i * bn_i < g.N ? 1u << i : 0u;
     float ra[NA], rb[NB];
     auto fetch = [&](int k) {
         const TA* qa = pa;
@@ -83,11 +86,16 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
             for (int i = 0; i < NA; ++i, qa += da) ra[i] = ldf(qa);
 #pragma unroll
             for (int i = 0; i < NB; ++i, qb += db) rb[i] = ldf(qb);
+        } else if (k + FK <= k1) {
+#pragma unroll
+            for (int i = 0; i < NA; ++i, qa += da) ra[i] = va >> i & 1u ? ldf(qa) : 0.f;
+#pragma unroll
+            for (int i = 0; i < NB; ++i, qb += db) rb[i] = vb >> i & 1u ? ldf(qb) : 0.f;
         } else {
 #pragma unroll
-            for (int i = 0; i < NA; ++i, qa += da) ra[i] = m0 + am + i * am_i < g.M && k + ka + i * ka_i < k1 ? ldf(qa) : 0.f;
+            for (int i = 0; i < NA; ++i, qa += da) ra[i] = (va >> i & 1u) && k + ka + i * ka_i < k1 ? ldf(qa) : 0.f;
 #pragma unroll
-            for (int i = 0; i < NB; ++i, qb += db) rb[i] = n0 + bn + i * bn_i < g.N && k + kb + i * kb_i < k1 ? ldf(qb) : 0.f;
+            for (int i = 0; i < NB; ++i, qb += db) rb[i] = (vb >> i & 1u) && k + kb + i * kb_i < k1 ? ldf(qb) : 0.f;
         }
         pa += step_a;
         pb += step_b;
@@ -190,19 +198,47 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
     }
 }
 
+// What `blocks` blocks of a tile shape take with K split over `ranks` of them, in us, from measurements: the SM with the most
+// blocks has their k to do, at a lower rate where it has one block alone, and each block's start, join and end.  Measured (and by
+// this, with 3 for the launch), in 64 x 64 over 1, 2, 4, 8 blocks: 1024^3 72, 77, 71, 80 (76, 78, 73, 83); 2000 x 700 x 300 53, 42,
+// 38, 44 (54, 42, 40, 42); 100 x 1000 x 1000 49, 28, 16, 13 (50, 28, 16, 14); in 128 x 64: 1024^3 84, 71, 70, 74 (100, 68, 72, 74);
+// 1600^3 299, 251, 224, 253 (293, 250, 235, 255), in 64 x 64 over 4 240 (258), in 128 x 128 347 (324); 2048^3 in 128 x 128 411 (412).
+struct FmaShape {
+    int m, n;
+    double us_k, alone, us_block;
+};
+constexpr FmaShape kFmaShapes[3] = {{64, 64, 0.0342, 1.33, 1.35}, {128, 64, 0.059, 1.57, 2.2}, {128, 128, 0.098, 1.15, 3.9}};
+inline double fma_us(const FmaShape& s, int64_t blocks, int ranks, int K) {
+    const int64_t on = ceil_div(blocks, static_cast<int64_t>(sm_count()));
+    const double k = on == 1 ? s.alone * 16 * static_cast<double>(ceil_div(ceil_div(K, 16), ranks)) : static_cast<double>(K) / ranks;
+    return static_cast<double>(on) * (s.us_k * k + s.us_block);
+}
+
 template <typename TA, typename TB, typename TO, typename TPRE>
 int launch_fma_gemm(const char* who, const TA* A, const TB* B, const FmaGemm& g, const FmaEpi<TO, TPRE>& ep, cudaStream_t st) {
     auto tiles = [&](int fm, int fn) { return ceil_div(g.M, fm) * ceil_div(g.N, fn); };
-    if (tiles(128, 128) >= sm_count())
-        return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128, 128>, dim3(static_cast<unsigned>(tiles(128, 128))), 256, 0, st, A, B,
-                            g, ep);
-    // K over so many blocks that all of them are still resident at once (three on an SM), 64 k at least each
-    const int64_t n = g.M <= 16 ? tiles(16, 64) : tiles(64, 64);
-    int ranks = 1;
-    while (ranks < 8 && 2 * n * ranks <= 3 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
-    const dim3 grid(static_cast<unsigned>(n * ranks)), cluster(static_cast<unsigned>(ranks));
-    if (g.M <= 16) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 16, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
-    return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
+    if (g.M <= 16) {   // K over so many blocks that all of them are still resident at once (three on an SM), 64 k at least each
+        const int64_t n = tiles(16, 64);
+        int ranks = 1;
+        while (ranks < 8 && 2 * n * ranks <= 3 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
+        return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 16, 64>, dim3(static_cast<unsigned>(n * ranks)),
+                              dim3(static_cast<unsigned>(ranks)), 256, 0, st, A, B, g, ep);
+    }
+    int shape = 0, ranks = 1;
+    double least = 1e30;
+    for (int i = 0; i < 3; ++i)
+        for (int r = 1; r <= (i == 2 ? 1 : 8) && (r == 1 || g.K >= 24 * r); r *= 2) {
+            const double us = fma_us(kFmaShapes[i], tiles(kFmaShapes[i].m, kFmaShapes[i].n) * r, r, g.K);
+            if (us < least) {
+                least = us;
+                shape = i;
+                ranks = r;
+            }
+        }
+    const dim3 grid(static_cast<unsigned>(tiles(kFmaShapes[shape].m, kFmaShapes[shape].n) * ranks)), cluster(static_cast<unsigned>(ranks));
+    if (shape == 0) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
+    if (shape == 1) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 128, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
+    return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128, 128>, grid, 256, 0, st, A, B, g, ep);
 }
 
 }  // namespace
