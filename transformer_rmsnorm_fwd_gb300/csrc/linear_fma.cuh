@@ -24,13 +24,14 @@ struct FmaEpi {
     int act;
 };
 
+// one output: the sum v with its column's bias, `res` the residual there
 template <typename TO, typename TPRE>
-__device__ __forceinline__ void fma_store(const FmaGemm& g, const FmaEpi<TO, TPRE>& ep, int64_t m, int64_t n, float v) {
+__device__ __forceinline__ void fma_store(const FmaGemm& g, const FmaEpi<TO, TPRE>& ep, int64_t m, int64_t n, float v, float bias, float res) {
     const int64_t o = m * g.N + n;
-    if (ep.bias != nullptr) v += ldf(ep.bias + n);
+    v += bias;
     if (ep.pre != nullptr) keep_pre(ep.pre + o, v);
     v = act_value<false>(ep.act, v);
-    if (ep.residual != nullptr) v += ldf(ep.residual + o);
+    if (ep.residual != nullptr) v += res;
     stf(ep.out + o, v);
 }
 
@@ -155,6 +156,11 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
         buf ^= 1;
     }
     auto row_of = [&](int i) { return PM == 1 ? ty : (i / 4) * 64 + ty * 4 + i % 4; };
+    // the bias and the residual are asked for ahead of the stores, behind which their loads would wait (the residual may be the output)
+    auto col_of = [&](int j) { return n0 + (j / 4) * 64 + tx * 4 + j % 4; };
+    float bias[PN];
+#pragma unroll
+    for (int j = 0; j < PN; ++j) bias[j] = ep.bias != nullptr && col_of(j) < g.N ? ldf(ep.bias + col_of(j)) : 0.f;
     if constexpr (Tile::SPLIT) {
         if (ranks > 1) {
             // the tile into shared memory, and rows rank, rank + ranks, ... of the cluster's sums out of it
@@ -165,6 +171,10 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
             cluster_barrier();
             for (int m = static_cast<int>(rank) + static_cast<int>(ranks) * ty; m < FM && m0 + m < g.M; m += static_cast<int>(ranks) * 16) {
                 float4 v[8];
+                float res[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    res[j] = ep.residual != nullptr && col_of(j) < g.N ? ldf(ep.residual + (m0 + m) * g.N + col_of(j)) : 0.f;
 #pragma unroll
                 for (uint32_t q = 0; q < 8; ++q)
                     if (q < ranks) v[q] = peer_float4(mem + m * FN + tx * 4, q);
@@ -179,22 +189,31 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
                 const float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (n0 + tx * 4 + j < g.N) fma_store(g, ep, m0 + m, n0 + tx * 4 + j, o[j]);
+                    if (col_of(j) < g.N) fma_store(g, ep, m0 + m, col_of(j), o[j], bias[j], res[j]);
             }
             __syncwarp();
             cluster_barrier();   // no block exits while another reads its sums
             return;
         }
     }
+    constexpr int ROWS = PM < 4 ? PM : PM == 4 ? 4 : 2;
 #pragma unroll
-    for (int i = 0; i < PM; ++i) {
-        const int64_t m = m0 + row_of(i);
-        if (m >= g.M) continue;
+    for (int i0 = 0; i0 < PM; i0 += ROWS) {
+        float res[ROWS][PN];
 #pragma unroll
-        for (int j = 0; j < PN; ++j) {
-            const int64_t n = n0 + (j / 4) * 64 + tx * 4 + j % 4;
-            if (n < g.N) fma_store(g, ep, m, n, j % 2 ? acc[i][j / 2].y : acc[i][j / 2].x);
-        }
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < PN; ++j) {
+                const int64_t m = m0 + row_of(i0 + i), n = col_of(j);
+                res[i][j] = ep.residual != nullptr && m < g.M && n < g.N ? ldf(ep.residual + m * g.N + n) : 0.f;
+            }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < PN; ++j) {
+                const int64_t m = m0 + row_of(i0 + i), n = col_of(j);
+                if (m < g.M && n < g.N) fma_store(g, ep, m, n, j % 2 ? acc[i0 + i][j / 2].y : acc[i0 + i][j / 2].x, bias[j], res[i][j]);
+            }
     }
 }
 
