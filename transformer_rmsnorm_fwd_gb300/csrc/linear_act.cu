@@ -193,26 +193,21 @@ size_t part_bytes(int64_t T, int64_t N) {
 template <typename T, typename TPRE>
 int fwd_fma(const void* X, const void* W, FmaEpi<T, TPRE> e, int64_t Tn, int64_t H, int64_t N, cudaStream_t st) {
     FmaGemm g{static_cast<int>(Tn), static_cast<int>(N), static_cast<int>(H), H, 1, 1, H};
-    return launch_fma_gemm("linear_act_fwd", static_cast<const T*>(X), static_cast<const T*>(W), g, e, st);
+    return launch_fma_gemm("linear_act_fwd", FmaJob<T, T, T, TPRE>{static_cast<const T*>(X), static_cast<const T*>(W), g, e}, st);
 }
 
 // dX = dP W and dW = dP^T X from dP [T, N] in TP
 template <typename T, typename TP>
 int grads_fma(const TP* dP, const void* X, const void* W, void* dX, void* dW, int64_t Tn, int64_t H, int64_t N,
               cudaStream_t st) {
-    if (dX != nullptr) {
-        FmaEpi<T, float> e{};
-        e.out = static_cast<T*>(dX);
-        FmaGemm g{static_cast<int>(Tn), static_cast<int>(H), static_cast<int>(N), N, 1, H, 1};
-        if (int rc = launch_fma_gemm("linear_act_bwd dX", dP, static_cast<const T*>(W), g, e, st)) return rc;
-    }
-    if (dW != nullptr) {
-        FmaEpi<T, float> e{};
-        e.out = static_cast<T*>(dW);
-        FmaGemm g{static_cast<int>(N), static_cast<int>(H), static_cast<int>(Tn), 1, N, H, 1};
-        if (int rc = launch_fma_gemm("linear_act_bwd dW", dP, static_cast<const T*>(X), g, e, st)) return rc;
-    }
-    return LIGER_OK;
+    FmaEpi<T, float> ex{}, ew{};
+    ex.out = static_cast<T*>(dX);
+    ew.out = static_cast<T*>(dW);
+    const FmaJob<TP, T, T, float> x{dP, static_cast<const T*>(W), {static_cast<int>(Tn), static_cast<int>(H), static_cast<int>(N), N, 1, H, 1}, ex};
+    const FmaJob<TP, T, T, float> w{dP, static_cast<const T*>(X), {static_cast<int>(N), static_cast<int>(H), static_cast<int>(Tn), 1, N, H, 1}, ew};
+    if (dX != nullptr && dW != nullptr) return launch_fma_two("linear_act_bwd dX, dW", x, w, st);
+    if (dX != nullptr) return launch_fma_gemm("linear_act_bwd dX", x, st);
+    return dW != nullptr ? launch_fma_gemm("linear_act_bwd dW", w, st) : LIGER_OK;
 }
 
 struct LinearBwd {

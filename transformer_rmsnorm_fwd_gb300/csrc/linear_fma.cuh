@@ -48,8 +48,17 @@ struct FmaTile {
     static constexpr int SA = FM + 4, SB = FN + 4;   // words of a shared row of k
     static constexpr int BUFS = 2 * FK * (SA + SB), WORDS = SPLIT && BUFS < FM * FN ? FM * FN : BUFS;
 };
-template <typename TA, typename TB, typename TO, typename TPRE, int FM, int FN>
-__global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, const TB* B, FmaGemm g, FmaEpi<TO, TPRE> ep) {
+// A launch holds one product or two that do not depend on each other (JOBS): the blocks from `first` on are the second's.
+template <typename TA, typename TB, typename TO, typename TPRE>
+struct FmaJob {
+    const TA* A;
+    const TB* B;
+    FmaGemm g;
+    FmaEpi<TO, TPRE> ep;
+};
+template <typename TA, typename TB, typename TO, typename TPRE, int FM, int FN, int JOBS>
+__global__ void __launch_bounds__(256, FN == 128 ? 2 : 3)
+    fma_gemm(const FmaJob<TA, TB, TO, TPRE> job0, const FmaJob<TA, TB, TO, TPRE> job1, unsigned first) {
     using Tile = FmaTile<FM, FN>;
     constexpr int FK = Tile::FK, SA = Tile::SA, SB = Tile::SB, PM = FM / 16, PN = FN / 16;
     constexpr int NA = FM * FK / 256, NB = FN * FK / 256;   // elements of an operand that a thread loads a step
@@ -57,7 +66,12 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
     float* const sa = mem;
     float* const sb = mem + 2 * FK * SA;
     const uint32_t rank = block_in_cluster(), ranks = blocks_in_cluster();
-    const unsigned tn = (static_cast<unsigned>(g.N) + FN - 1) / FN, tile = blockIdx.x / ranks, tile_m = tile / tn;
+    const bool second = JOBS == 2 && blockIdx.x >= first;
+    const FmaGemm g = second ? job1.g : job0.g;
+    const FmaEpi<TO, TPRE> ep = second ? job1.ep : job0.ep;
+    const TA* const A = second ? job1.A : job0.A;
+    const TB* const B = second ? job1.B : job0.B;
+    const unsigned tn = (static_cast<unsigned>(g.N) + FN - 1) / FN, tile = (blockIdx.x - (second ? first : 0)) / ranks, tile_m = tile / tn;
     const int64_t m0 = static_cast<int64_t>(tile_m) * FM, n0 = static_cast<int64_t>(tile - tile_m * tn) * FN;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int steps = (g.K + FK - 1) / FK;
@@ -217,8 +231,8 @@ __global__ void __launch_bounds__(256, FN == 128 ? 2 : 3) fma_gemm(const TA* A, 
     }
 }
 
-// What `blocks` blocks of a tile shape take with K split over `ranks` of them, in us, from measurements: the SM with the most
-// blocks has their k to do, at a lower rate where it has one block alone, and each block's start, join and end.  Measured (and by
+// What the blocks of a tile shape take with K split over `ranks` of them, in us, from measurements: the SM with the most blocks
+// has their k to do, at a lower rate where it has one block alone, and each block's start, join and end.  Measured (and by
 // this, with 3 for the launch), in 64 x 64 over 1, 2, 4, 8 blocks: 1024^3 72, 77, 71, 80 (76, 78, 73, 83); 2000 x 700 x 300 53, 42,
 // 38, 44 (54, 42, 40, 42); 100 x 1000 x 1000 49, 28, 16, 13 (50, 28, 16, 14); in 128 x 64: 1024^3 84, 71, 70, 74 (100, 68, 72, 74);
 // 1600^3 299, 251, 224, 253 (293, 250, 235, 255), in 64 x 64 over 4 240 (258), in 128 x 128 347 (324); 2048^3 in 128 x 128 411 (412).
@@ -227,37 +241,73 @@ struct FmaShape {
     double us_k, alone, us_block;
 };
 constexpr FmaShape kFmaShapes[3] = {{64, 64, 0.0342, 1.33, 1.35}, {128, 64, 0.059, 1.57, 2.2}, {128, 128, 0.098, 1.15, 3.9}};
-inline double fma_us(const FmaShape& s, int64_t blocks, int ranks, int K) {
-    const int64_t on = ceil_div(blocks, static_cast<int64_t>(sm_count()));
-    const double k = on == 1 ? s.alone * 16 * static_cast<double>(ceil_div(ceil_div(K, 16), ranks)) : static_cast<double>(K) / ranks;
-    return static_cast<double>(on) * (s.us_k * k + s.us_block);
+struct FmaPlan {
+    int shape = 0, ranks = 1;
+    double us = 1e30;
+};
+inline int64_t fma_tiles(const FmaShape& s, const FmaGemm& g) { return ceil_div(g.M, s.m) * static_cast<int64_t>(ceil_div(g.N, s.n)); }
+// the plan for one product, or for two in one launch (in 64 x 64: in larger tiles the second product's parameters spill)
+inline FmaPlan fma_plan(const FmaGemm& g0, const FmaGemm* g1) {
+    FmaPlan best;
+    for (int i = 0; i < (g1 != nullptr ? 1 : 3); ++i)
+        for (int r = 1; r <= (i == 2 ? 1 : 8); r *= 2) {
+            const FmaShape& s = kFmaShapes[i];
+            const int64_t n0 = fma_tiles(s, g0) * r, n1 = g1 != nullptr ? fma_tiles(s, *g1) * r : 0;
+            const int64_t on = ceil_div(n0 + n1, static_cast<int64_t>(sm_count()));
+            bool enough = true;
+            auto us = [&](int K) {
+                enough = enough && (r == 1 || K >= 24 * r);
+                return s.us_k * (on == 1 ? s.alone * 16 * static_cast<double>(ceil_div(ceil_div(K, 16), r)) : static_cast<double>(K) / r) + s.us_block;
+            };
+            const double u0 = us(g0.K), u1 = g1 != nullptr ? us(g1->K) : 0.0;
+            // the SM's share of the work, and no less than its longest block beside two others
+            const double t = on == 1 ? std::max(u0, u1)
+                                     : std::max(static_cast<double>(on) * (n0 * u0 + n1 * u1) / static_cast<double>(n0 + n1),
+                                                static_cast<double>(std::min<int64_t>(on, 3)) * std::max(u0, u1) * (g1 != nullptr ? 1.0 : 0.0));
+            if (enough && t < best.us) best = {i, r, t};
+        }
+    return best;
 }
 
 template <typename TA, typename TB, typename TO, typename TPRE>
-int launch_fma_gemm(const char* who, const TA* A, const TB* B, const FmaGemm& g, const FmaEpi<TO, TPRE>& ep, cudaStream_t st) {
-    auto tiles = [&](int fm, int fn) { return ceil_div(g.M, fm) * ceil_div(g.N, fn); };
-    if (g.M <= 16) {   // K over so many blocks that all of them are still resident at once (three on an SM), 64 k at least each
-        const int64_t n = tiles(16, 64);
-        int ranks = 1;
-        while (ranks < 8 && 2 * n * ranks <= 3 * sm_count() && g.K >= 128 * ranks) ranks *= 2;
-        return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 16, 64>, dim3(static_cast<unsigned>(n * ranks)),
-                              dim3(static_cast<unsigned>(ranks)), 256, 0, st, A, B, g, ep);
-    }
-    int shape = 0, ranks = 1;
-    double least = 1e30;
-    for (int i = 0; i < 3; ++i)
-        for (int r = 1; r <= (i == 2 ? 1 : 8) && (r == 1 || g.K >= 24 * r); r *= 2) {
-            const double us = fma_us(kFmaShapes[i], tiles(kFmaShapes[i].m, kFmaShapes[i].n) * r, r, g.K);
-            if (us < least) {
-                least = us;
-                shape = i;
-                ranks = r;
-            }
+int launch_fma_plan(const char* who, const FmaJob<TA, TB, TO, TPRE>& a, const FmaPlan& plan, cudaStream_t st) {
+    const FmaShape& s = kFmaShapes[plan.shape];
+    const unsigned first = static_cast<unsigned>(fma_tiles(s, a.g) * plan.ranks);
+    const dim3 grid(first), cluster(static_cast<unsigned>(plan.ranks));
+    if (plan.shape == 0) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64, 1>, grid, cluster, 256, 0, st, a, a, first);
+    if (plan.shape == 1) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 128, 64, 1>, grid, cluster, 256, 0, st, a, a, first);
+    return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128, 128, 1>, grid, 256, 0, st, a, a, first);
+}
+
+template <typename TA, typename TB, typename TO, typename TPRE>
+int launch_fma_gemm(const char* who, const FmaJob<TA, TB, TO, TPRE>& a, cudaStream_t st) {
+    if (a.g.M > 16) return launch_fma_plan(who, a, fma_plan(a.g, nullptr), st);
+    // K over so many blocks that all of them are still resident at once (three on an SM), 64 k at least each
+    const int64_t n = ceil_div(a.g.N, 64);
+    int ranks = 1;
+    while (ranks < 8 && 2 * n * ranks <= 3 * sm_count() && a.g.K >= 128 * ranks) ranks *= 2;
+    return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 16, 64, 1>, dim3(static_cast<unsigned>(n * ranks)), dim3(static_cast<unsigned>(ranks)),
+                          256, 0, st, a, a, static_cast<unsigned>(n * ranks));
+}
+
+// Two products that do not depend on each other, in one launch where that is estimated to take less (well less, where their sums
+// differ much in length: the estimate is poor there): both are bound by the latencies of their few steps, and share them.
+template <typename TA, typename TB, typename TO, typename TPRE>
+int launch_fma_two(const char* who, const FmaJob<TA, TB, TO, TPRE>& a, const FmaJob<TA, TB, TO, TPRE>& b, cudaStream_t st) {
+    if (a.g.M > 16 && b.g.M > 16) {
+        const bool longer = a.g.K >= b.g.K;   // the longer blocks start first
+        const FmaJob<TA, TB, TO, TPRE>&p = longer ? a : b, &q = longer ? b : a;
+        const FmaPlan both = fma_plan(p.g, &q.g);
+        const double margin = 2 * static_cast<int64_t>(q.g.K) >= p.g.K ? 1.0 : 0.85;
+        if (both.us < margin * (fma_plan(a.g, nullptr).us + fma_plan(b.g, nullptr).us + 3.0)) {
+            const unsigned first = static_cast<unsigned>(fma_tiles(kFmaShapes[0], p.g) * both.ranks);
+            return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64, 2>,
+                                  dim3(first + static_cast<unsigned>(fma_tiles(kFmaShapes[0], q.g) * both.ranks)),
+                                  dim3(static_cast<unsigned>(both.ranks)), 256, 0, st, p, q, first);
         }
-    const dim3 grid(static_cast<unsigned>(tiles(kFmaShapes[shape].m, kFmaShapes[shape].n) * ranks)), cluster(static_cast<unsigned>(ranks));
-    if (shape == 0) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 64, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
-    if (shape == 1) return launch_cluster(who, fma_gemm<TA, TB, TO, TPRE, 128, 64>, grid, cluster, 256, 0, st, A, B, g, ep);
-    return launch_early(who, fma_gemm<TA, TB, TO, TPRE, 128, 128>, grid, 256, 0, st, A, B, g, ep);
+    }
+    if (int rc = launch_fma_gemm(who, a, st)) return rc;
+    return launch_fma_gemm(who, b, st);
 }
 
 }  // namespace
