@@ -200,6 +200,7 @@ struct RowShared {
     int count, count2;
 };
 
+// 1024 threads on an SM with 63 registers each: 4096 x 128256 bf16 with 8 alternatives in 189 us; 1280 with 48 (which spill) 218.
 template <typename T, int NT, bool ENT>
 __global__ void __launch_bounds__(NT, 1024 / NT) token_logp_row(const LogpFwd p) {
     constexpr int EPV = Vec<T>::N, NP = EPV / 2;
