@@ -71,8 +71,8 @@ int liger_layernorm_bwd(const void* dy, const void* dres, const void* x, const v
  *   are kept as its largest, where every derivative here has its limit), fp32
  *   for fp32.
  *   All tensors 16-byte aligned.  residual may be Y; no other overlap.
- *   bf16 with H and N multiples of 8 runs on the tensor cores; fp32, and bf16
- *   of other sizes, in fp32 FMA.  T = 0 does nothing. */
+ *   bf16 with H and N multiples of 8, 64 or more, runs on the tensor cores;
+ *   fp32, and bf16 of other sizes, in fp32 FMA.  T = 0 does nothing. */
 #define LIGER_ACT_NONE 0
 #define LIGER_ACT_RELU 1
 #define LIGER_ACT_GELU 2
