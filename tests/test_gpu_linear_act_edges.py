@@ -1,0 +1,64 @@
+"""The projection's activations at the edges of their types: sums near 0, where half precision ends."""
+import pytest
+import torch
+
+from layer_util import act as act_of, gen, randn
+from train_util import check
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+# few tokens and 128-feature tiles, tiles of CTA pairs (96 of them), fp32 FMA for bf16 and for fp32
+PATHS = [(BF, 4, 64, 72), (BF, 300, 128, 264), (BF, 3000, 64, 2048), (BF, 9, 33, 40), (BF, 200, 70, 90), (F32, 30, 24, 40)]
+
+
+def code(dtype):
+    import transformer_rmsnorm_fwd_gb300 as L
+    return L.LIGER_BF16 if dtype is BF else L.LIGER_F32
+
+
+def small_sums(g, dtype, T, H, N):
+    """X with one power of two (2^-100 to 2^-20, the same in every row that has it at h) a row and W of small whole numbers: every
+    sum is that power times one of them, exactly."""
+    at = torch.arange(T, device="cuda") % H
+    power = 2.0 ** torch.randint(-100, -19, (H,), device="cuda", generator=g).double()
+    X = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    X[torch.arange(T, device="cuda"), at] = power[at]
+    W = torch.randint(-3, 4, (N, H), device="cuda", generator=g).to(dtype)
+    return X.to(dtype), W
+
+
+@pytest.mark.parametrize("dtype,T,H,N", PATHS)
+def test_relu_of_tiny_sums_keeps_its_gradient(cuda_lib, dtype, T, H, N):
+    import transformer_rmsnorm_fwd_gb300 as L
+    g = gen(T + N)
+    X, W = small_sums(g, dtype, T, H, N)
+    p = X.double() @ W.double().T
+    Y, pre = torch.empty(T, N, dtype=dtype, device="cuda"), torch.empty(T, N, dtype=torch.float16 if dtype is BF else F32, device="cuda")
+    L.liger_linear_act_fwd(X, W, Y, act="relu", pre=pre)
+    assert torch.equal(Y, p.clamp(min=0).to(dtype))
+    assert torch.equal(torch.sign(pre.double()), torch.sign(p))
+    dY = torch.randint(-3, 4, (T, N), device="cuda", generator=g).to(dtype)
+    dX, dW, db = torch.empty_like(X), torch.empty_like(W), torch.empty(N, dtype=dtype, device="cuda")
+    ws = torch.empty(L.liger_linear_act_bwd_workspace(T, H, N, "relu", code(dtype)), dtype=torch.uint8, device="cuda")
+    L.liger_linear_act_bwd(dY, X, W, dX, dW, db, ws, pre=pre, act="relu")
+    dp = dY.double() * (p > 0)
+    # whole numbers, and whole numbers times one power of two: exact before the one rounding
+    assert torch.equal(dX, (dp @ W.double()).to(dtype)) and torch.equal(db, dp.sum(0).to(dtype))
+    assert torch.equal(dW, (dp.T @ X.double()).to(dtype)) and bool(dW.any())
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype,T,H,N", PATHS)
+def test_smooth_activations_of_tiny_sums(cuda_lib, dtype, T, H, N, act):
+    """The value kept for a sum below 2^-24 is at most 2^-24 off, and with slopes' derivatives of at most 1 so is the slope: of one
+    half, 2^-23 of it beside the 32 roundings of its arithmetic."""
+    import transformer_rmsnorm_fwd_gb300 as L
+    g = gen(T + N + 1)
+    X, W = small_sums(g, dtype, T, H, N)
+    Y, pre = torch.empty(T, N, dtype=dtype, device="cuda"), torch.empty(T, N, dtype=torch.float16 if dtype is BF else F32, device="cuda")
+    L.liger_linear_act_fwd(X, W, Y, act=act, pre=pre)
+    dY, db = randn(g, T, N, dtype=dtype), torch.empty(N, dtype=dtype, device="cuda")
+    ws = torch.empty(L.liger_linear_act_bwd_workspace(T, H, N, act, code(dtype)), dtype=torch.uint8, device="cuda")
+    L.liger_linear_act_bwd(dY, X, W, None, None, db, ws, pre=pre, act=act)
+    dp = dY.double() * act_of(act, X.double() @ W.double().T)[1]
+    check(db, dp.sum(0), dp.abs().sum(0), T / 64 + 300 + 34, "db")

@@ -82,9 +82,11 @@ __device__ __forceinline__ void act_values(int act, float (&v)[32]) {
 
 // What the backward's slope is formed from (kept by the forward): half precision beside bf16 tensors, fp32 beside fp32.
 __device__ __forceinline__ void keep_pre(float* p, float v) { *p = v; }
-// half precision holds up to 65504: larger values (where every activation's slope has its limit) as that; NaN stays
+// Half precision holds 2^-24 to 65504.  Larger values (where every activation's slope has its limit) are kept as that.  Smaller
+// ones but 0 as 2^-24, with their sign: relu's slope jumps at 0, and the others' are the same there to within 1e-7.  NaN stays.
 __device__ __forceinline__ void keep_pre(__half* p, float v) {
-    *p = __float2half_rn(v > 65504.f ? 65504.f : v < -65504.f ? -65504.f : v);
+    constexpr float most = 65504.f, least = 0x1p-24f;
+    *p = __float2half_rn(v > 0.f ? fminf(fmaxf(v, least), most) : v < 0.f ? fmaxf(fminf(v, -least), -most) : v);
 }
 
 // d act / dp
