@@ -62,3 +62,38 @@ def test_smooth_activations_of_tiny_sums(cuda_lib, dtype, T, H, N, act):
     L.liger_linear_act_bwd(dY, X, W, None, None, db, ws, pre=pre, act=act)
     dp = dY.double() * act_of(act, X.double() @ W.double().T)[1]
     check(db, dp.sum(0), dp.abs().sum(0), T / 64 + 300 + 34, "db")
+
+
+def far_points(n):
+    """n values of bf16 over [-12, 12], close together near 0 too."""
+    half = n // 2
+    p = torch.cat((torch.linspace(-12, 12, n - half, dtype=torch.float64), 12 * torch.linspace(-1, 1, half, dtype=torch.float64) ** 5))
+    return p.to(BF).double().cuda()
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype,T,H,N", [(BF, 1, 64, 4000), (BF, 300, 128, 2000), (BF, 3000, 64, 2048), (BF, 3, 33, 1001), (F32, 5, 24, 2000)])
+def test_activations_of_far_sums_relative_to_themselves(cuda_lib, dtype, T, H, N, act):
+    """A result that is small because its activation is (p far below 0) has its type's relative error.  Before the rounding to it
+    the exponent of e, at most 88 in fp32's range, is off by up to 4 roundings of its size, and there are up to 40 of the result's:
+    400 of 2^-24.  The hardware's functions leave out what is below 2^-126, here times 12."""
+    import transformer_rmsnorm_fwd_gb300 as L
+    p = far_points(N)
+    X, W = torch.zeros(T, H, dtype=dtype, device="cuda"), torch.zeros(N, H, dtype=dtype, device="cuda")
+    X[:, 0], W[:, 0] = 1.0, p.to(dtype)
+    Y, pre = torch.empty(T, N, dtype=dtype, device="cuda"), torch.empty(T, N, dtype=torch.float16 if dtype is BF else F32, device="cuda")
+    L.liger_linear_act_fwd(X, W, Y, act=act, pre=pre)
+    y, s = act_of(act, p)
+    u = torch.finfo(dtype).eps / 2
+    rel = 400 * 2.0 ** -24
+    assert bool(((Y.double() - y).abs() <= (u + rel) * y.abs() + 2.0 ** -122).all())
+    # one row's slope comes out as db; its two terms may cancel
+    dY, db = torch.ones(1, N, dtype=dtype, device="cuda"), torch.empty(N, dtype=dtype, device="cuda")
+    ws = torch.empty(L.liger_linear_act_bwd_workspace(1, H, N, act, code(dtype)) + 256, dtype=torch.uint8, device="cuda")
+    L.liger_linear_act_bwd(dY, X[:1].contiguous(), W, None, None, db, ws, pre=pre[:1].contiguous(), act=act)
+    value = y / torch.where(p == 0, 1.0, p)
+    terms = value.abs() + (s - value).abs()
+    # (a sum below 2^-14 was kept in steps of 2^-24; what the functions leave out below 2^-126 counts p times the derivative of the
+    # exponent here, in gelu with tanh at 12: 12 (1.596 + 0.2141 * 144) = 389 < 2^9)
+    floor = 2.0 ** -24 * (p.abs() < 2.0 ** -14) + 2.0 ** -117
+    assert bool(((db.double() - s).abs() <= u * s.abs() + rel * terms + floor).all())
