@@ -88,7 +88,8 @@ template <int ACT, int LX>
 __global__ void __launch_bounds__(256, 4) linear_dp_vec(const __nv_bfloat16* dy, const __half* pre, __nv_bfloat16* dp,
                                                         __nv_bfloat16* db, float* part, int64_t rows, int cols) {
     constexpr int SL = 256 / LX, C = LX * 8;   // row slices, columns
-    __shared__ float red[SL][C + 4], sums[C];
+    __shared__ __align__(16) float red[SL][C + 4];
+    __shared__ float sums[C];
     wait_for_stream();
     const int lane = threadIdx.x % LX, sl = threadIdx.x / LX;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * C, col = col0 + lane * 8;

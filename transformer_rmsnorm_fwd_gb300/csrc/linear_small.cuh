@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = all ? w[e] + b[e] : __int_as_float(0x7FC00000);
                 if (p.pre != nullptr) {
-                    __half h[4];
+                    alignas(8) __half h[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) keep_pre(h + e, w[e]);
                     *reinterpret_cast<uint2*>(p.pre + o) = *reinterpret_cast<const uint2*>(h);

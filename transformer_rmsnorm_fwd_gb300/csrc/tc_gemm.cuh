@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (ep.pre16 != nullptr) {
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
-                                __half h[8];
+                                alignas(16) __half h[8];
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) keep_pre(h + e, v[g * 8 + e]);
                                 sts16(s_pre + stage_slot<4>(lane, g), *reinterpret_cast<const uint4*>(h));
@@ -1183,7 +1183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 for (int g2 = 0; g2 < 2; ++g2) {
                                     const int g = hh * 2 + g2;   // 8 pairs: columns j + 8 g
                                     const int o = j + g * 8;
-                                    float cs[8], sn[8], ba[8], bb[8], y1[8], y2[8];
+                                    alignas(16) float cs[8], sn[8], ba[8], bb[8], y1[8], y2[8];
 #pragma unroll
                                     for (int h = 0; h < 2; ++h) {
                                         const uint4 c4 = gc4[g2 * 2 + h], s4 = gs4[g2 * 2 + h];
@@ -1228,7 +1228,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                                 for (int g = 0; g < 4; ++g) {
                                     const int o = j + g * 8;
-                                    float ba[8], y[8];
+                                    alignas(16) float ba[8], y[8];
                                     *reinterpret_cast<float4*>(ba) = __ldg(reinterpret_cast<const float4*>(bh + o));
                                     *reinterpret_cast<float4*>(ba + 4) =
                                         __ldg(reinterpret_cast<const float4*>(bh + o + 4));

@@ -191,9 +191,11 @@ __device__ __forceinline__ void rank_keys(const unsigned long long* keys, int n,
     }
 }
 
-struct RowShared {
-    unsigned long long best[LIGER_TOP_MAX];   // this block's k largest keys in order (0: no more)
-    unsigned long long groups[kGroups], red[kRowThreads / 32], bound;
+struct alignas(16) RowShared {   // (the keys by pairs too, should a loop over them be read so)
+    alignas(16) unsigned long long best[LIGER_TOP_MAX];   // this block's k largest keys in order (0: no more)
+    alignas(16) unsigned long long groups[kGroups];
+    alignas(16) unsigned long long red[kRowThreads / 32];
+    unsigned long long bound;
     Sums sums[kRowThreads / 32];
     Sums total;
     float row_max;
