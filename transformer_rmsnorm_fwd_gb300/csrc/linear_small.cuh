@@ -19,7 +19,6 @@
 
 #include "activation.cuh"
 #include "cluster.cuh"
-#include "linear_fma.cuh"
 #include "tc_gemm.cuh"
 
 namespace liger {

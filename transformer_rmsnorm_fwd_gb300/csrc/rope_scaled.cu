@@ -79,22 +79,12 @@ __global__ void __launch_bounds__(kThreads) rope_scaled_elems(const RopeScaled a
 
 // ------------------------------------------------------------- pieces of 16 bytes
 // Where heads, their rotated part and its halves are whole pieces of P elements: P consecutive elements of
-// one type move as one access (16 bytes, or less: P = 1 is a single element, or a pair of neighbours).
+// one type move as one access: 16 bytes, or two elements.
 template <typename T, int P> struct Chunk {
     static_assert(P == Vec<T>::N, "16 bytes");
     float f[P];
     __device__ __forceinline__ void get(const T* p) { unpack(*reinterpret_cast<const uint4*>(p), f); }
     __device__ __forceinline__ void put(T* p) const { *reinterpret_cast<uint4*>(p) = pack(f); }
-};
-template <> struct Chunk<float, 1> {
-    float f[1];
-    __device__ __forceinline__ void get(const float* p) { f[0] = *p; }
-    __device__ __forceinline__ void put(float* p) const { *p = f[0]; }
-};
-template <> struct Chunk<__nv_bfloat16, 1> {
-    float f[1];
-    __device__ __forceinline__ void get(const __nv_bfloat16* p) { f[0] = ldf(p); }
-    __device__ __forceinline__ void put(__nv_bfloat16* p) const { stf(p, f[0]); }
 };
 template <> struct Chunk<float, 2> {
     float f[2];
@@ -234,7 +224,6 @@ __global__ void __launch_bounds__(kThreads) rope_scaled_staged(const RopeScaled 
 
 // ------------------------------------------------------------- straight from global memory
 // Few tokens, or in place with a part of the heads that stays: a thread moves whole chunks itself.
-// C: chunk of the copied rest (in elements).
 template <typename T, bool INTER, int P>
 __global__ void __launch_bounds__(kThreads) rope_scaled_chunks(const RopeScaled a, const __grid_constant__ Freqs f) {
     constexpr int APU = INTER ? P / 2 : P;
@@ -272,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) rope_scaled_chunks(const RopeScaled 
     }
 }
 
-// f_i of every pair in double precision; false if the scaling gives a frequency that is no positive number
+// f_i of every pair in double precision; false if the scaling gives a frequency that is no finite number
 bool frequencies(Freqs& f, int R, double theta, int scaling, double factor, double low, double high, double orig_len) {
     const int half = R / 2;
     const double two_pi = 6.283185307179586;
