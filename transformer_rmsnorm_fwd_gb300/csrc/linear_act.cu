@@ -273,6 +273,7 @@ int fwd_tc(const void* X, const void* W, const void* bias, const void* residual,
     e.hint_b = HINT_EVICT_FIRST;   // W: streamed once per group of rows
     e.m_group = static_cast<int>(ceil_div(rows_in_l2(H, T), static_cast<int64_t>(TileCfg<1>::TM)));
     e.early = 1;
+    e.nan_unfinished = 1;
     return launch_gemm<0, 0, EPI_LINEAR, 1>(mX, mW, e.M, e.N, static_cast<int>(H), e, st);
 }
 
@@ -309,6 +310,7 @@ int grads_tc(const LinearBwd& a, const void* dP) {
         w.hint_a = HINT_EVICT_FIRST;
         w.hint_b = HINT_EVICT_LAST;   // X: reused by every row block
         w.early = 1;
+        w.nan_unfinished = 1;
         // The last, partly filled round of tiles is split along the tokens over the idle pairs, their sums in dX, which is written after:
         // 8192 x 4096 x 11008, dW and dX: 746 us, 789 with whole tiles; 8192 x 2048 x 5504: 225, 245
         const int64_t tiles = pair_tiles(N, H), pairs = sm_count() / 2, rem = tiles % pairs;
@@ -362,6 +364,7 @@ int grads_tc(const LinearBwd& a, const void* dP) {
     d.ldo = H;
     d.raster = RASTER_N_GROUPS;
     d.early = 1;
+    d.nan_unfinished = 1;
     return launch_gemm<0, 1, EPI_STORE, 1>(mP, mW, T, H, N, d, a.st);
 }
 

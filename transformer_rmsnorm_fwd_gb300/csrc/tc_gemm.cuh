@@ -194,6 +194,9 @@ struct EpiParams {
     const __nv_bfloat16* bias16;
     __half* pre16;
     int act;
+    // After an expired wait the epilogue writes NaN into what it did not finish of `out` (and pre16, or a split tile's sums);
+    // else that is left as it was.
+    int nan_unfinished;
     int m_group;   // row blocks that one sweep over all columns takes (they stay in L2)
     int early;     // set up while the kernel before still runs (barriers, TMEM), as launch_early; CTA pairs only
 };
@@ -483,6 +486,21 @@ __device__ __forceinline__ uint4 pack_bf8(const float* f) {
 // one-time attribute set in one unit never stands in for another's.
 namespace {
 
+// NaN for what an epilogue warp did not finish: the 32 rows from r0 on of the tile whose first row and column are m0 and n0, of the
+// outputs or, with `sums`, of that item's sums [., BN].
+__device__ __noinline__ void unfinished_rows(float* sums, __nv_bfloat16* out, __half* pre, int64_t ldo, int M, int N, int m0, int r0,
+                                             int n0, int lane) {
+    for (int r = r0; r < r0 + 32 && m0 + r < M; ++r) {
+        const int64_t at = static_cast<int64_t>(m0 + r) * ldo + n0;
+        for (int c = lane; c < BN; c += 32) {
+            if (sums != nullptr) sums[r * BN + c] = __int_as_float(0x7FC00000);
+            if (sums != nullptr || n0 + c >= N) continue;
+            out[at + c] = __ushort_as_bfloat16(0x7FC0);
+            if (pre != nullptr) pre[at + c] = __ushort_as_half(0x7E00);
+        }
+    }
+}
+
 template <int A_MN, int B_MN, int EPI, int PAIR = 0, int MODE = MODE_PLAIN>
 __global__ void __launch_bounds__(THREADS, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -499,6 +517,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * Cfg::ST + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * Cfg::ST + 2 + a); };
     const uint32_t slot = bar0 + 8u * (2 * Cfg::ST + 4);
+    const uint32_t spare_bar = slot + 8u;   // of MMAs that end without a result
     uint32_t* slot_ptr = reinterpret_cast<uint32_t*>(gbase + Cfg::ST * Cfg::STAGE_L + 8 * (2 * Cfg::ST + 4));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -539,6 +558,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(tfull_bar(a), 1);
             mbar_init(tempty_bar(a), PAIR ? 8 : 4);   // the epilogue warps of both CTAs
         }
+        mbar_init(spare_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&tmA);
         prefetch_map(&tmB);
@@ -737,9 +757,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 commit(tfull_bar(as));
             }
             if (!ok && any) {
-                // wait for the MMAs already issued: commit to a free barrier and wait on it
-                commit(tfull_bar(it & 1));
-                mbar_wait(tfull_bar(it & 1), ((it >> 1) & 1));
+                // wait for the MMAs already issued, by a barrier that tells the epilogue nothing: this tile's sums are not whole
+                commit(spare_bar);
+                mbar_wait(spare_bar, 0);
             }
         }
     } else {
@@ -791,6 +811,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(as), aphase));
             if (!got) {
                 if (lane == 0) atomicExch(ep.err, ERR_EPI_TMEM);
+                if ((EPI == EPI_LINEAR || EPI == EPI_STORE || EPI == EPI_ACCUM) && ep.nan_unfinished) {
+                    for (; t < items; t += nunits) {
+                        const int place = item(t, tile, kb0, kb1);
+                        tile_mn(tile, mi, ni);
+                        unfinished_rows(place >= 0 ? ep.kpart + static_cast<int64_t>(place) * ep.kpart_rows * BN : nullptr, ep.out, ep.pre16,
+                                        ep.ldo, ep.M, ep.N, mi * Cfg::TM, static_cast<int>(crank) * BM + q * 32, ni * BN, lane);
+                    }
+                }
                 break;
             }
             tc_fence_after();
