@@ -1,6 +1,12 @@
 // Layer norm, forward and backward (formulas in liger_layer.h).
 // A row's mean comes first and its variance from the differences to it, both in fp32 over values that stay in registers, so
-// that a row is read once and a large mean costs no digits.  The backward's two row sums, of dy w and of dy w xhat, are formed
+// that a row is read once.  The mean m is rounded, and so is the sum it comes from, by what may be many steps of the differences
+// x - m where the mean is large.  fp32 rows with a mean above twice their deviation: the differences' own mean `off` is what is
+// missing, the mean is m + off, the variance mean((x - m)^2) - off^2, and y is formed from x - m - off, so that a large mean costs
+// the forward no digits (of 1000 deviations: y off by 1e-4 without, 1e-6 with).  Formed in every row it would cost a seventh of the
+// time of wide ones; so only rows that need it pay (16384 x 8192 165 us, 205 where all do; 32768 x 4096 177 and 184).  bf16 rows:
+// m is off by some 2^-14 of the inputs' own rounding, and nothing is formed.  The backward has the mean as it is stored, in fp32.
+// The backward's two row sums, of dy w and of dy w xhat, are formed
 // in one pass, and dw and db as fp32 column sums in registers over all rows of a block; each block leaves them as a partial row,
 // added up in a fixed order.  What bounds all of it is HBM: two streams forward, three (four with dres) backward.  32768 x 4096
 // bf16: forward 85 us (0.93 of the copy rate), backward with dres 155 us (1.02); a few rows: the launch (4 rows: 2.3 us of kernel).
@@ -15,6 +21,18 @@ constexpr int kMaxPartRows = 1024;   // most partial rows of dw and of db
 // of 16384 x 8192 83, 83 and 88.  Backward: 192 KB where a row is 8 KB or more (16384 x 8192 bf16: 156 us, 167 with 64 or 128 KB;
 // 32768 x 4096: 155 and 158), 128 KB below (131072 x 512 bf16: 102 us, 104 with 192 KB).
 constexpr size_t kFwdFlight = 64u * 1024u, kBwdFlight = 128u * 1024u, kBwdFlightLong = 192u * 1024u;
+
+// Whether the differences' own mean is formed (above) for a row of mean m and mean square `square` of its differences to it
+template <typename T> constexpr bool kOffset = sizeof(T) == 4;
+template <typename T>
+__device__ __forceinline__ bool far_off(float m, float square) {
+    return kOffset<T> && m * m > 4.f * square;
+}
+// The variance from the mean square of x - m and the mean `off` of x - m (at least 0; NaN stays)
+__device__ __forceinline__ float variance(float square, float off) {
+    const float v = fmaf(-off, off, square);
+    return v < 0.f ? 0.f : v;
+}
 
 // ------------------------------------------------------------- any width
 // A block per row, elements strided over its threads; the row is read again from the caches for
@@ -35,14 +53,21 @@ __global__ void __launch_bounds__(256) layer_norm_fwd_rows(const T* x, const T* 
             const float d = ldf(xr + j) - m;
             s = fmaf(d, d, s);
         }
-        const float rs = 1.0f / sqrtf(block_sum(s, sh) / n + eps);
+        float square = block_sum(s, sh) / n, off = 0.f;
+        if (far_off<T>(m, square)) {
+            s = 0.f;
+            for (int j = threadIdx.x; j < cols; j += blockDim.x) s += ldf(xr + j) - m;
+            off = block_sum(s, sh) / n;
+            square = variance(square, off);
+        }
+        const float rs = 1.0f / sqrtf(square + eps);
         T* yr = y + r * cols;
         for (int j = threadIdx.x; j < cols; j += blockDim.x) {
-            const float h = (ldf(xr + j) - m) * rs;
+            const float h = (kOffset<T> ? ldf(xr + j) - m - off : ldf(xr + j) - m) * rs;
             stf(yr + j, fmaf(h, w != nullptr ? ldf(w + j) : 1.f, b != nullptr ? ldf(b + j) : 0.f));
         }
         if (threadIdx.x == 0) {
-            if (mean != nullptr) mean[r] = m;
+            if (mean != nullptr) mean[r] = kOffset<T> ? m + off : m;
             if (rstd != nullptr) rstd[r] = rs;
         }
     }
@@ -78,7 +103,7 @@ struct LnFwd {
 // mean of the squared differences go over the team by shuffles and one named barrier each.
 template <typename T, int VEC, int VPT>
 __global__ void __launch_bounds__(512) layer_norm_fwd_team(LnFwd p, int tw) {
-    __shared__ float red[2][16];
+    __shared__ float red[3][16];   // sums of the values, of the differences' squares, of the differences
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int team = warp / tw, wt = warp - team * tw, teams = (blockDim.x >> 5) / tw;
     const int tt = wt * 32 + lane, nt = tw * 32;   // thread of the team, threads of the team
@@ -86,12 +111,10 @@ __global__ void __launch_bounds__(512) layer_norm_fwd_team(LnFwd p, int tw) {
     const T *x = static_cast<const T*>(p.x), *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
     T* y = static_cast<T*>(p.y);
     const float inv = 1.0f / static_cast<float>(p.cols);
-    int turn = 0;
-    auto team_sum = [&](float v) {
+    auto team_sum = [&](int k, float v) {
         v = warp_sum(v);
         if (tw == 1) return v;
-        float* sh = red[turn & 1] + team * tw;   // written again only after a barrier that follows every read of it
-        ++turn;
+        float* sh = red[k] + team * tw;   // written again only after another barrier, which follows every read of it
         if (lane == 0) sh[wt] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(nt) : "memory");
         float s = 0.f;
@@ -122,7 +145,7 @@ __global__ void __launch_bounds__(512) layer_norm_fwd_team(LnFwd p, int tw) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) s += f[e];
             }
-        const float m = team_sum(s) * inv;
+        const float m = team_sum(0, s) * inv;
         s = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
@@ -132,14 +155,28 @@ __global__ void __launch_bounds__(512) layer_norm_fwd_team(LnFwd p, int tw) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) s = fmaf(f[e] - m, f[e] - m, s);
             }
-        const float rs = inv_sqrt(fmaf(team_sum(s), inv, p.eps));
+        float square = team_sum(1, s) * inv, off = 0.f;
+        if (far_off<T>(m, square)) {
+            s = 0.f;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (live[j]) {
+                    float f[VEC];
+                    cx[j].get(f);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) s += f[e] - m;
+                }
+            off = team_sum(2, s) * inv;
+            square = variance(square, off);
+        }
+        const float rs = inv_sqrt(square + p.eps);
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
             if (live[j]) {
                 float f[VEC], g[VEC];
                 cx[j].get(f);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) f[e] = (f[e] - m) * rs;
+                for (int e = 0; e < VEC; ++e) f[e] = (kOffset<T> ? f[e] - m - off : f[e] - m) * rs;
                 if (w != nullptr) {
                     cw[j].get(g);
 #pragma unroll
@@ -153,7 +190,7 @@ __global__ void __launch_bounds__(512) layer_norm_fwd_team(LnFwd p, int tw) {
                 Piece<T, VEC>::put(y + o + static_cast<int64_t>(j * nt + tt) * VEC, f);
             }
         if (tt == 0) {
-            if (p.mean != nullptr) p.mean[t] = m;
+            if (p.mean != nullptr) p.mean[t] = kOffset<T> ? m + off : m;
             if (p.rstd != nullptr) p.rstd[t] = rs;
         }
     }
@@ -183,7 +220,8 @@ template <typename T, int VPT, int NT, int MB, int ONE>
 __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, int nst, int* err) {
     constexpr int VEC = Vec<T>::N, NP = VEC / 2;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ __align__(16) float red[2][NT / 32 + 4][4];   // rows of 4: a team starts on a multiple of 4 warps or is a warp alone
+    // sums of the values, of the differences' squares, of the differences; rows of 4: a team starts on a multiple of 4 warps or is a warp alone
+    __shared__ __align__(16) float red[3][NT / 32 + 4][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (ONE) tw = blockDim.x >> 5;
     const int team = ONE ? 0 : warp / tw, wt = warp - team * tw, teams = ONE ? 1 : (blockDim.x >> 5) / tw;
@@ -201,7 +239,7 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, i
         mbar_expect_tx(bars + 8u * s, rb);
         bulk_g2s(smem_u32(ring + static_cast<size_t>(s) * rb), x + row * p.cols, rb, bars + 8u * s);
     };
-    for (int i = threadIdx.x; i < 2 * (NT / 32 + 4) * 4; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+    for (int i = threadIdx.x; i < 3 * (NT / 32 + 4) * 4; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
     if (tt == 0)
         for (int s = 0; s < nst; ++s) mbar_init(bars + 8u * s, 1);
     mbar_init_fence();
@@ -220,23 +258,21 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, i
         if (live[j] && w != nullptr) cw[j] = ldg16(w + c);
         if (live[j] && b != nullptr) cb[j] = ldg16(b + c);
     }
-    int turn = 0;
     const int at0 = ONE ? 0 : team * ((tw + 3) & ~3);
-    // Team-wide sum in two halves: gather() brings the warps' sums together and says whether every thread
-    // of the team got its row (one team barrier), total() adds them up.
-    auto gather = [&](float& v, bool& ok) {
+    // Team-wide sum in two halves: gather() brings the warps' sums together in place k and says whether every thread
+    // of the team got its row (one team barrier), total() adds them up.  A place is written again only after another barrier.
+    auto gather = [&](int k, float& v, bool& ok) {
         v = warp_sum(v);
         if (!ONE && tw == 1) {
             ok = __all_sync(0xffffffffu, ok);
             return;
         }
-        if (lane == 0) (&red[turn][0][0])[at0 + wt] = v;
+        if (lane == 0) (&red[k][0][0])[at0 + wt] = v;
         ok = ONE ? __syncthreads_and(ok ? 1 : 0) != 0 : team_all(team, nt, ok);
     };
-    auto total = [&](float v) {
+    auto total = [&](int k, float v) {
         if (!ONE && tw == 1) return v;
-        const float4* q = reinterpret_cast<const float4*>(&red[turn][0][0] + at0);   // slots past the team's warps hold 0
-        turn ^= 1;
+        const float4* q = reinterpret_cast<const float4*>(&red[k][0][0] + at0);   // slots past the team's warps hold 0
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < (NT / 32 + 3) / 4; ++i)
@@ -264,9 +300,9 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, i
             for (int e = 0; e < NP; ++e) a = __fadd2_rn(a, f[e]);
         }
         float sum = a.x + a.y;
-        gather(sum, ok);
+        gather(0, sum, ok);
         if (!ok) break;
-        const float m = total(sum) * inv;
+        const float m = total(0, sum) * inv;
         if (tt == 0 && t + nst * step < p.rows) {   // every thread of the team has read the slot
             fence_proxy_async_smem();
             issue(t + nst * step, s);
@@ -290,9 +326,25 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, i
             }
         sum = a.x + a.y;
         bool same = true;
-        gather(sum, same);
-        const float rs = inv_sqrt(fmaf(total(sum), inv, p.eps));
-        const float2 rs2 = make_float2(rs, rs);
+        gather(1, sum, same);
+        float square = total(1, sum) * inv, off = 0.f;
+        if (far_off<T>(m, square)) {
+            a = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (live[j]) {
+                    float2 f[NP];
+                    unpack2(cx[j], f);
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) a = __fadd2_rn(a, __fadd2_rn(f[e], nm));
+                }
+            sum = a.x + a.y;
+            gather(2, sum, same);
+            off = total(2, sum) * inv;
+            square = variance(square, off);
+        }
+        const float rs = inv_sqrt(square + p.eps);
+        const float2 rs2 = make_float2(rs, rs), no2 = make_float2(-off * rs, -off * rs);   // (x - m) rstd - off rstd
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
             if (live[j]) {
@@ -302,13 +354,14 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_ring(LnFwd p, int tw, i
                 unpack2(cb[j], h);
 #pragma unroll
                 for (int e = 0; e < NP; ++e) {
-                    f[e] = __fmul2_rn(__fadd2_rn(f[e], nm), rs2);
+                    f[e] = __fadd2_rn(f[e], nm);
+                    f[e] = kOffset<T> ? __ffma2_rn(f[e], rs2, no2) : __fmul2_rn(f[e], rs2);
                     f[e] = w != nullptr ? __ffma2_rn(f[e], g[e], h[e]) : __fadd2_rn(f[e], h[e]);
                 }
                 stg16_cs(y + t * p.cols + static_cast<int64_t>(j * nt + tt) * VEC, pack2(f));
             }
         if (tt == 0) {
-            if (p.mean != nullptr) p.mean[t] = m;
+            if (p.mean != nullptr) p.mean[t] = kOffset<T> ? m + off : m;
             if (p.rstd != nullptr) p.rstd[t] = rs;
         }
     }
@@ -439,6 +492,10 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_odd(LnFwd p, int nst, u
     int turn = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true;
+    auto put = [&](float v) {
+        v = warp_sum(v);
+        if (lane == 0) red[turn][wid] = v;
+    };
     auto total = [&]() {
         float a = 0.f;
 #pragma unroll
@@ -461,8 +518,7 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_odd(LnFwd p, int nst, u
 #pragma unroll
             for (int e = 0; e < NP; ++e) a = __fadd2_rn(a, f[e]);
         }
-        float sum = warp_sum(a.x + a.y);
-        if (lane == 0) red[turn][wid] = sum;
+        put(a.x + a.y);
         ok = __syncthreads_and(ok ? 1 : 0) != 0;
         if (!ok) break;
         if (tid == 0 && t + nst * step < p.rows) {   // every thread has its vectors of the row
@@ -475,23 +531,41 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_odd(LnFwd p, int nst, u
         }
         const float m = total() * inv;
         const float2 nm = make_float2(-m, -m);
+        auto differences = [&](int j, float2 (&f)[NP]) {   // 0 outside the row
+            unpack2(cx[j], f);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) f[e] = __fadd2_rn(f[e], nm);
+            if (in[j] != Span<T>::kAll) span.mask(in[j], f);
+        };
         a = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
             if (in[j] != 0) {
                 float2 f[NP];
-                unpack2(cx[j], f);
-#pragma unroll
-                for (int e = 0; e < NP; ++e) f[e] = __fadd2_rn(f[e], nm);
-                if (in[j] != Span<T>::kAll) span.mask(in[j], f);
+                differences(j, f);
 #pragma unroll
                 for (int e = 0; e < NP; ++e) a = __ffma2_rn(f[e], f[e], a);
             }
-        sum = warp_sum(a.x + a.y);
-        if (lane == 0) red[turn][wid] = sum;
+        put(a.x + a.y);
         __syncthreads();
-        const float rs = inv_sqrt(fmaf(total(), inv, p.eps));
-        const float2 rs2 = make_float2(rs, rs);
+        float square = total() * inv, off = 0.f;
+        if (far_off<T>(m, square)) {
+            a = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (in[j] != 0) {
+                    float2 f[NP];
+                    differences(j, f);
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) a = __fadd2_rn(a, f[e]);
+                }
+            put(a.x + a.y);
+            __syncthreads();
+            off = total() * inv;
+            square = variance(square, off);
+        }
+        const float rs = inv_sqrt(square + p.eps);
+        const float2 rs2 = make_float2(rs, rs), no2 = make_float2(-off * rs, -off * rs);   // (x - m) rstd - off rstd
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
             if (in[j] != 0) {
@@ -501,13 +575,14 @@ __global__ void __launch_bounds__(NT, MB) layer_norm_fwd_odd(LnFwd p, int nst, u
                 unpack2(cb[j], h);
 #pragma unroll
                 for (int e = 0; e < NP; ++e) {
-                    f[e] = __fmul2_rn(__fadd2_rn(f[e], nm), rs2);
+                    f[e] = __fadd2_rn(f[e], nm);
+                    f[e] = kOffset<T> ? __ffma2_rn(f[e], rs2, no2) : __fmul2_rn(f[e], rs2);
                     f[e] = w != nullptr ? __ffma2_rn(f[e], g[e], h[e]) : __fadd2_rn(f[e], h[e]);
                 }
                 span.put(y + o, j * nt + tid, in[j], f);
             }
         if (tid == 0) {
-            if (p.mean != nullptr) p.mean[t] = m;
+            if (p.mean != nullptr) p.mean[t] = kOffset<T> ? m + off : m;
             if (p.rstd != nullptr) p.rstd[t] = rs;
         }
     }
