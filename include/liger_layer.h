@@ -69,8 +69,8 @@ int liger_layernorm_bwd(const void* dy, const void* dres, const void* x, const v
  *   pre [T, N] or NULL: P kept for the backward of the activation, IEEE half
  *   precision for bf16 tensors (8 times finer than bf16 down to 2^-14, in steps of
  *   2^-24 below; values past its range are kept as its largest, where every
- *   derivative here has its limit, and values but 0 below 2^-24 as that with their
- *   sign, which decides relu's derivative), fp32 for fp32.
+ *   derivative here has its limit, and with relu, whose derivative their sign
+ *   decides, positive ones below 2^-24 as that), fp32 for fp32.
  *   All tensors 16-byte aligned.  residual may be Y; no other overlap.
  *   bf16 with H and N multiples of 8, 64 or more, runs on the tensor cores;
  *   fp32, and bf16 of other sizes, in fp32 FMA.  T = 0 does nothing. */

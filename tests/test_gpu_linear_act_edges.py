@@ -36,7 +36,7 @@ def test_relu_of_tiny_sums_keeps_its_gradient(cuda_lib, dtype, T, H, N):
     Y, pre = torch.empty(T, N, dtype=dtype, device="cuda"), torch.empty(T, N, dtype=torch.float16 if dtype is BF else F32, device="cuda")
     L.liger_linear_act_fwd(X, W, Y, act="relu", pre=pre)
     assert torch.equal(Y, p.clamp(min=0).to(dtype))
-    assert torch.equal(torch.sign(pre.double()), torch.sign(p))
+    assert torch.equal(pre > 0, p > 0) and not bool(torch.isnan(pre).any())
     dY = torch.randint(-3, 4, (T, N), device="cuda", generator=g).to(dtype)
     dX, dW, db = torch.empty_like(X), torch.empty_like(W), torch.empty(N, dtype=dtype, device="cuda")
     ws = torch.empty(L.liger_linear_act_bwd_workspace(T, H, N, "relu", code(dtype)), dtype=torch.uint8, device="cuda")
@@ -50,8 +50,8 @@ def test_relu_of_tiny_sums_keeps_its_gradient(cuda_lib, dtype, T, H, N):
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("dtype,T,H,N", PATHS)
 def test_smooth_activations_of_tiny_sums(cuda_lib, dtype, T, H, N, act):
-    """The value kept for a sum below 2^-24 is at most 2^-24 off, and with slopes' derivatives of at most 1 so is the slope: of one
-    half, 2^-23 of it beside the 32 roundings of its arithmetic."""
+    """The value kept for a sum below 2^-14 is at most 2^-25 off, and with slopes' derivatives of at most 1 so is the slope: of one
+    half, 2^-24 of it beside the 32 roundings of its arithmetic."""
     import transformer_rmsnorm_fwd_gb300 as L
     g = gen(T + N + 1)
     X, W = small_sums(g, dtype, T, H, N)

@@ -86,12 +86,24 @@ __device__ __forceinline__ void act_values(int act, float (&v)[32]) {
 }
 
 // What the backward's slope is formed from (kept by the forward): half precision beside bf16 tensors, fp32 beside fp32.
-__device__ __forceinline__ void keep_pre(float* p, float v) { *p = v; }
-// Half precision holds 2^-24 to 65504.  Larger values (where every activation's slope has its limit) are kept as that.  Smaller
-// ones but 0 as 2^-24, with their sign: relu's slope jumps at 0, and the others' are the same there to within 1e-7.  NaN stays.
-__device__ __forceinline__ void keep_pre(__half* p, float v) {
-    constexpr float most = 65504.f, least = 0x1p-24f;
-    *p = __float2half_rn(v > 0.f ? fminf(fmaxf(v, least), most) : v < 0.f ? fmaxf(fminf(v, -least), -most) : v);
+// Half precision holds 2^-24 to 65504.  Larger values (where every activation's slope has its limit) are kept as that, NaN as NaN.
+// Smaller ones round to 0, which only relu's slope tells from them: there a positive sum is lifted to 2^-24 (RELU).  Both limits
+// for all elements by comparisons took the forward of 8192 x 4096 x 11008 with gelu from 489 us to 571; the saturating conversion of
+// pairs takes what a plain one does.
+constexpr float kLeastHalf = 0x1p-24f;
+template <bool RELU>
+__device__ __forceinline__ uint32_t kept_pair(float lo, float hi) {
+    if (RELU) {
+        lo = lo > 0.f ? fmaxf(lo, kLeastHalf) : lo;
+        hi = hi > 0.f ? fmaxf(hi, kLeastHalf) : hi;
+    }
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void keep_pre(int, float* p, float v) { *p = v; }
+__device__ __forceinline__ void keep_pre(int act, __half* p, float v) {
+    *p = __ushort_as_half(static_cast<unsigned short>(act == LIGER_ACT_RELU ? kept_pair<true>(v, 0.f) : kept_pair<false>(v, 0.f)));
 }
 
 // d act / dp

@@ -29,7 +29,7 @@ template <typename TO, typename TPRE>
 __device__ __forceinline__ void fma_store(const FmaGemm& g, const FmaEpi<TO, TPRE>& ep, int64_t m, int64_t n, float v, float bias, float res) {
     const int64_t o = m * g.N + n;
     v += bias;
-    if (ep.pre != nullptr) keep_pre(ep.pre + o, v);
+    if (ep.pre != nullptr) keep_pre(ep.act, ep.pre + o, v);
     v = act_value<false>(ep.act, v);
     if (ep.residual != nullptr) v += res;
     stf(ep.out + o, v);

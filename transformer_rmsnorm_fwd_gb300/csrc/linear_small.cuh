@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = all ? w[e] + b[e] : __int_as_float(0x7FC00000);
                 if (p.pre != nullptr) {
-                    alignas(8) __half h[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) keep_pre(h + e, w[e]);
-                    *reinterpret_cast<uint2*>(p.pre + o) = *reinterpret_cast<const uint2*>(h);
+                    const bool relu = p.act == LIGER_ACT_RELU;
+                    *reinterpret_cast<uint2*>(p.pre + o) =
+                        relu ? make_uint2(kept_pair<true>(w[0], w[1]), kept_pair<true>(w[2], w[3]))
+                             : make_uint2(kept_pair<false>(w[0], w[1]), kept_pair<false>(w[2], w[3]));
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = act_value<true>(p.act, w[e]);

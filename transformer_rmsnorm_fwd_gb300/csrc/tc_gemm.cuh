@@ -960,13 +960,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         __syncwarp();   // the previous block's row runs have been read
                         if (ep.src != nullptr) stage_block<4>(s_res, lane, res);
                         if (ep.pre16 != nullptr) {
+                            auto keep = [&](auto relu) {
+                                constexpr bool R = decltype(relu)::value;
 #pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                alignas(16) __half h[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) keep_pre(h + e, v[g * 8 + e]);
-                                sts16(s_pre + stage_slot<4>(lane, g), *reinterpret_cast<const uint4*>(h));
-                            }
+                                for (int g = 0; g < 4; ++g) {
+                                    const float* f = v + g * 8;
+                                    sts16(s_pre + stage_slot<4>(lane, g), make_uint4(kept_pair<R>(f[0], f[1]), kept_pair<R>(f[2], f[3]),
+                                                                                    kept_pair<R>(f[4], f[5]), kept_pair<R>(f[6], f[7])));
+                                }
+                            };
+                            if (ep.act == LIGER_ACT_RELU) keep(std::true_type());
+                            else keep(std::false_type());
                         }
                         act_values<true>(ep.act, v);
                         if (ep.src != nullptr) {
