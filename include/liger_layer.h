@@ -16,9 +16,9 @@
  * nothing, and can be captured in a CUDA graph after a first call on the device.
  * Results are the same from run to run on one device (sums in a fixed order,
  * no atomics).  A bounded wait that expires in a kernel (see liger.h) leaves
- * NaN in the outputs that it did not finish; liger_device_status names the
- * layer norm's as RMSNorm's, the projection's as FusedLinearSwiGLU's and the
- * rotation's as RoPE's.
+ * NaN in the outputs that it did not finish; the layer norm's is recorded with
+ * RMSNorm's, the projection's with FusedLinearSwiGLU's and the rotation's with
+ * RoPE's, and liger_device_status names both.
  */
 #ifndef LIGER_LAYER_H
 #define LIGER_LAYER_H

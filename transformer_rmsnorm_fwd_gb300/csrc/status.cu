@@ -64,8 +64,9 @@ int max_smem_optin() {
 // one thread (atomic exchange), the values landing in g_taken for the copy
 // back to the host.
 constexpr int kWords = 4;
-static const char* const kFamily[kWords] = {"RMSNorm (staged kernels)", "FusedLinearSwiGLU",
-                                            "fused RMSNorm+QKV+RoPE", "RoPE (staged kernel)"};
+// the operators that share a word, all of them named: which one it was the caller knows from what it queued
+static const char* const kFamily[kWords] = {"RMSNorm, block norms or layer norm", "FusedLinearSwiGLU or projections with bias and activation",
+                                            "fused RMSNorm+QKV+RoPE", "RoPE or scaled RoPE"};
 
 struct Words {
     int* w[kWords];
