@@ -38,6 +38,11 @@ struct RopeScaled {
     float m, sign;
 };
 
+// A pair by its (cos, sin), with the roundings written out: every path below gives the same bits.
+__device__ __forceinline__ float2 turned(float a, float b, float2 r) {
+    return make_float2(fmaf(a, r.x, -__fmul_rn(b, r.y)), fmaf(b, r.x, __fmul_rn(a, r.y)));
+}
+
 // A block takes npos tokens: their angles into shared memory, then a thread per pair or copied element.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_scaled_elems(const RopeScaled a, const __grid_constant__ Freqs f) {
@@ -66,11 +71,10 @@ __global__ void __launch_bounds__(kThreads) rope_scaled_elems(const RopeScaled a
         T* dst = isq ? static_cast<T*>(a.q_out) + t * a.qo_ts + static_cast<int64_t>(h) * a.D
                      : static_cast<T*>(a.k_out) + t * a.ko_ts + static_cast<int64_t>(h - a.Hq) * a.D;
         if (j < half) {
-            const float2 r = cs[pp * half + j];
             const int ia = a.inter ? 2 * j : j, ib = a.inter ? 2 * j + 1 : j + half;
-            const float x0 = ldf(src + ia), x1 = ldf(src + ib);
-            stf(dst + ia, x0 * r.x - x1 * r.y);
-            stf(dst + ib, x1 * r.x + x0 * r.y);
+            const float2 y = turned(ldf(src + ia), ldf(src + ib), cs[pp * half + j]);
+            stf(dst + ia, y.x);
+            stf(dst + ib, y.y);
         } else if (isq ? a.copy_q : a.copy_k) {
             dst[a.R + j - half] = src[a.R + j - half];
         }
@@ -112,18 +116,16 @@ __device__ __forceinline__ void turn(Chunk<T, P>& a, Chunk<T, P>& b, const float
     if (INTER) {
 #pragma unroll
         for (int i = 0; i < P / 2; ++i) {
-            const float2 r = cs[i * apart];
-            const float x0 = a.f[2 * i], x1 = a.f[2 * i + 1];
-            a.f[2 * i] = x0 * r.x - x1 * r.y;
-            a.f[2 * i + 1] = x1 * r.x + x0 * r.y;
+            const float2 y = turned(a.f[2 * i], a.f[2 * i + 1], cs[i * apart]);
+            a.f[2 * i] = y.x;
+            a.f[2 * i + 1] = y.y;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const float2 r = cs[i * apart];
-            const float x0 = a.f[i], x1 = b.f[i];
-            a.f[i] = x0 * r.x - x1 * r.y;
-            b.f[i] = x1 * r.x + x0 * r.y;
+            const float2 y = turned(a.f[i], b.f[i], cs[i * apart]);
+            a.f[i] = y.x;
+            b.f[i] = y.y;
         }
     }
 }
