@@ -97,3 +97,20 @@ def test_activations_of_far_sums_relative_to_themselves(cuda_lib, dtype, T, H, N
     # exponent here, in gelu with tanh at 12: 12 (1.596 + 0.2141 * 144) = 389 < 2^9)
     floor = 2.0 ** -24 * (p.abs() < 2.0 ** -14) + 2.0 ** -117
     assert bool(((db.double() - s).abs() <= u * s.abs() + rel * terms + floor).all())
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("T,H,N", [(4, 64, 72), (300, 128, 264), (3000, 64, 2048), (9, 33, 40), (200, 70, 90)])
+def test_sums_that_overflow_keep_their_limits_slope(cuda_lib, T, H, N, act):
+    """Infinite sums of bf16 tensors are kept as half precision's largest, where every slope is 0 or 1."""
+    import transformer_rmsnorm_fwd_gb300 as L
+    X, W = torch.full((T, H), 1e30, dtype=BF, device="cuda"), torch.full((N, H), 1e30, dtype=BF, device="cuda")
+    W[::2] *= -1
+    Y, pre = torch.empty(T, N, dtype=BF, device="cuda"), torch.empty(T, N, dtype=torch.float16, device="cuda")
+    L.liger_linear_act_fwd(X, W, Y, act=act, pre=pre)
+    assert bool((Y[:, 1::2] == float("inf")).all())
+    assert bool((pre[:, 1::2] == 65504.0).all()) and bool((pre[:, ::2] == -65504.0).all())
+    dY, db = torch.ones(T, N, dtype=BF, device="cuda"), torch.empty(N, dtype=BF, device="cuda")
+    ws = torch.empty(L.liger_linear_act_bwd_workspace(T, H, N, act), dtype=torch.uint8, device="cuda")
+    L.liger_linear_act_bwd(dY, X, W, None, None, db, ws, pre=pre, act=act)
+    assert not db[::2].any() and bool((db[1::2] == torch.tensor(T, dtype=BF)).all())
